@@ -43,6 +43,10 @@ EXPORTED = [
     "mmdit_double_block_bwd_saved", "mmdit_single_block_fwd_train", "mmdit_single_block_bwd_saved",
     "mmdit_modulation_batched_fwd", "mmdit_conditioning_workspace_size",
     "mmdit_conditioning_fwd", "mmdit_flux_workspace_size", "mmdit_flux_forward",
+    "mmdit_add_rmsnorm_fwd", "mmdit_add_rmsnorm_bwd_workspace_size", "mmdit_add_rmsnorm_bwd",
+    "mmdit_fp8_block_cast", "mmdit_fp8_block_linear_workspace_size", "mmdit_fp8_block_linear_fwd",
+    "mmdit_fp8_block_linear_bwd_workspace_size", "mmdit_fp8_block_linear_bwd",
+    "mmdit_rope_config", "mmdit_rope_fwd", "mmdit_rope_bwd",
 ]
 
 
@@ -127,6 +131,17 @@ class FluxW(C.Structure):
                 ("w_out", VP), ("b_out", VP)]
 
 
+class RopeCfg(C.Structure):
+    _fields_ = [("rot_dim", I32), ("interleaved", I32), ("mscale", F32), ("reserved", I32),
+                ("turns", C.c_uint64 * 256)]
+
+
+class RopeView(C.Structure):
+    _fields_ = [("ptr", VP), ("stride_b", I64), ("stride_s", I64), ("stride_h", I64)]
+
+
+ROPE_SCALINGS = ("none", "linear", "by_parts")  # mmdit_rope_scaling
+PROPE, PVIEW, F64 = C.POINTER(RopeCfg), C.POINTER(RopeView), C.c_double
 PCOND, PFLUXC, PFLUXW = C.POINTER(CondW), C.POINTER(FluxConfig), C.POINTER(FluxW)
 
 _SIGS = {
@@ -192,6 +207,19 @@ _SIGS = {
     "mmdit_conditioning_fwd": (C.c_int, [I32, I32, I32, I32, I32, PCOND, VP, VP, VP, VP, VP, SZ, VP]),
     "mmdit_flux_workspace_size": (SZ, [PFLUXC]),
     "mmdit_flux_forward": (C.c_int, [PFLUXC, PFLUXW, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
+    "mmdit_add_rmsnorm_fwd": (C.c_int, [I32, I32, I32, I32, F32, VP, I64, VP, VP, VP, VP, VP, VP, VP, VP]),
+    "mmdit_add_rmsnorm_bwd_workspace_size": (SZ, [I32, I32]),
+    "mmdit_add_rmsnorm_bwd": (C.c_int, [I32, I32, I32, I32, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
+    "mmdit_fp8_block_cast": (C.c_int, [I32, I32, I32, I32, VP, VP, VP, VP, VP, VP]),
+    "mmdit_fp8_block_linear_workspace_size": (SZ, [I32, I32, I32]),
+    "mmdit_fp8_block_linear_fwd": (C.c_int, [I32, I32, I32, VP, VP, VP, VP, VP, VP, I32, VP, SZ, VP]),
+    "mmdit_fp8_block_linear_bwd_workspace_size": (SZ, [I32, I32, I32]),
+    "mmdit_fp8_block_linear_bwd": (C.c_int, [I32, I32, I32, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
+    "mmdit_rope_config": (C.c_int, [PROPE, I32, I32, F64, I32, F64, F64, F64, F64, F64]),
+    "mmdit_rope_fwd": (C.c_int, [I32, PROPE, I32, I32, I32, I32, PVIEW, PVIEW, I32, PVIEW, PVIEW, VP, I64, VP, VP,
+                                 VP]),
+    "mmdit_rope_bwd": (C.c_int, [I32, PROPE, I32, I32, I32, I32, PVIEW, PVIEW, I32, PVIEW, PVIEW, VP, I64, VP, VP,
+                                 VP]),
 }
 
 _lib = None
@@ -755,3 +783,212 @@ def mmdit_fp8_attention_fwd(q, k, v, scale_q, scale_k, scale_v, out, ws=None, st
                                           _ptr(scale_k), _ptr(scale_v), _ptr(out), _ptr(ws), ws.numel(),
                                           _stream(stream)))
     return ws
+
+
+# ----------------------------------------------------------------------------- language-model operators
+def _tiles(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _ld16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def _arg(name, t, dev, dtype, *shape):
+    """The address of one dense tensor argument of an operator, after checking it (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+        return t.data_ptr()
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _launch(name, dev, stream, *args):
+    """Calls entry point `name` with device `dev` current, on `stream` or on that device's current stream."""
+    lib = _lib or load()
+    # the raw handle of the current stream, without the Stream object torch.cuda.current_stream would build
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(lib, name)(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib, name)(*args, raw)
+    if status != MMDIT_OK:
+        raise MMDitError(status, last_error())
+
+
+def _device(t):
+    """The device of a call's first tensor; host tensors are refused as _ptr refuses them."""
+    if not t.is_cuda:
+        _ptr(t)
+    return t.device
+
+
+def _workspace_arg(ws, dev, nbytes):
+    """The caller's workspace, or a new one of nbytes(); its size and alignment are the library's to check."""
+    if ws is None:
+        return workspace(nbytes(), dev)
+    if ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, the call's tensors are on {dev}")
+    return ws
+
+
+def mmdit_add_rmsnorm_fwd(x, gain, residual=None, h=None, y=None, y_q=None, s_y=None, rstd=None, eps=1e-6,
+                          stream=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) gain, in x's type and/or as E4M3 codes y_q (uint8)
+    with 1 x 128 scales s_y [ceil(D/128), R].  x [R, D] bf16 or fp32 (rows may be strided); residual and h
+    [R, D] in x's type, or fp32 for a bf16 x; rstd [R] fp32 for the backward."""
+    dev, dt, f32 = _device(x), x.dtype, torch.float32
+    act = act_of(x)
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError("x must be [R, D] with dense rows")
+    R, D = x.shape
+    rdt = dt if residual is None else residual.dtype
+    if rdt is not dt and rdt is not f32:
+        raise TypeError(f"residual has dtype {rdt}, expected {dt} or float32")
+    ldx = x.stride(0) if R > 1 else _ld16(D)
+    _launch("mmdit_add_rmsnorm_fwd", dev, stream, act, int(rdt is f32), R, D, float(eps), x.data_ptr(), ldx,
+            _arg("residual", residual, dev, rdt, R, D), _arg("gain", gain, dev, dt, D), _arg("h", h, dev, rdt, R, D),
+            _arg("y", y, dev, dt, R, D), _arg("y_q", y_q, dev, torch.uint8, R, D),
+            _arg("s_y", s_y, dev, f32, _tiles(D), R), _arg("rstd", rstd, dev, f32, R))
+
+
+def mmdit_add_rmsnorm_bwd_workspace_size(rows, dim) -> int:
+    return load().mmdit_add_rmsnorm_bwd_workspace_size(rows, dim)
+
+
+def mmdit_add_rmsnorm_bwd(dy, h, gain, rstd, dh, dh_in=None, dx=None, dgain=None, ws=None, stream=None):
+    """Gradients of mmdit_add_rmsnorm_fwd: dh [R, D] (of x and of the residual, in h's type; may be dh_in),
+    dx the same in dy's type, dgain [D] fp32; dh_in is the gradient reaching h past the norm."""
+    dev, dt, hdt, f32 = _device(dy), dy.dtype, h.dtype, torch.float32
+    act = act_of(dy)
+    if hdt is not dt and hdt is not f32:
+        raise TypeError(f"h has dtype {hdt}, expected {dt} or float32")
+    R, D = dy.shape
+    ws = _workspace_arg(ws, dev, lambda: mmdit_add_rmsnorm_bwd_workspace_size(R, D))
+    _launch("mmdit_add_rmsnorm_bwd", dev, stream, act, int(hdt is f32), R, D, _arg("dy", dy, dev, dt, R, D),
+            _arg("h", h, dev, hdt, R, D), _arg("gain", gain, dev, dt, D), _arg("rstd", rstd, dev, f32, R),
+            _arg("dh_in", dh_in, dev, hdt, R, D), _arg("dh", dh, dev, hdt, R, D), _arg("dx", dx, dev, dt, R, D),
+            _arg("dgain", dgain, dev, f32, D), ws.data_ptr(), ws.numel())
+    return ws
+
+
+def mmdit_fp8_block_cast(x, q=None, s=None, q_t=None, s_t=None, square=False, stream=None):
+    """E4M3 codes (uint8) of x [R, C] with block scales: 1 x 128 tiles (q, s [ceil(C/128), R]; transposed
+    q_t [C, R rounded up to 16], s_t [ceil(R/128), C]) or, with square, 128 x 128 tiles (s [ceil(R/128),
+    ceil(C/128)], codes q and/or q_t)."""
+    dev, u8, f32 = _device(x), torch.uint8, torch.float32
+    R, Cc = x.shape
+    s_shape = (_tiles(R), _tiles(Cc)) if square else (_tiles(Cc), R)
+    _launch("mmdit_fp8_block_cast", dev, stream, act_of(x), int(bool(square)), R, Cc, _arg("x", x, dev, x.dtype, R, Cc),
+            _arg("q", q, dev, u8, R, Cc), _arg("s", s, dev, f32, *s_shape), _arg("q_t", q_t, dev, u8, Cc, _ld16(R)),
+            _arg("s_t", s_t, dev, f32, _tiles(R), Cc))
+
+
+def mmdit_fp8_block_linear_workspace_size(M, N, K) -> int:
+    return load().mmdit_fp8_block_linear_workspace_size(M, N, K)
+
+
+def mmdit_fp8_block_linear_fwd(x_q, s_x, w_q, s_w, b, y, ws=None, stream=None):
+    """y [M, N] (bf16 or fp32) = x W^T + b on E4M3 codes x_q [M, K] (s_x [ceil(K/128), M]) and w_q [N, K]
+    (s_w [ceil(N/128), ceil(K/128)]); b [N] bf16 or None."""
+    dev, u8, f32 = _device(x_q), torch.uint8, torch.float32
+    M, K = x_q.shape
+    N = w_q.shape[0]
+    ws = _workspace_arg(ws, dev, lambda: mmdit_fp8_block_linear_workspace_size(M, N, K))
+    _launch("mmdit_fp8_block_linear_fwd", dev, stream, M, N, K, _arg("x_q", x_q, dev, u8, M, K),
+            _arg("s_x", s_x, dev, f32, _tiles(K), M), _arg("w_q", w_q, dev, u8, N, K),
+            _arg("s_w", s_w, dev, f32, _tiles(N), _tiles(K)), _arg("b", b, dev, torch.bfloat16, N),
+            _arg("y", y, dev, y.dtype, M, N), int(act_of(y) == MMDIT_F32), ws.data_ptr(), ws.numel())
+    return ws
+
+
+def mmdit_fp8_block_linear_bwd_workspace_size(M, N, K) -> int:
+    return load().mmdit_fp8_block_linear_bwd_workspace_size(M, N, K)
+
+
+def mmdit_fp8_block_linear_bwd(dy, w_t=None, s_w=None, x_t=None, s_xt=None, dx=None, dw=None, db=None, ws=None,
+                               stream=None):
+    """Gradients of mmdit_fp8_block_linear_fwd from dy [M, N] bf16: dx [M, K] bf16 from the transposed weight
+    codes w_t [K, N rounded up to 16] and s_w; dw [N, K] fp32 from the transposed activation codes x_t
+    [K, M rounded up to 16] and s_xt [ceil(M/128), K]; db [N] fp32.  Gradients that are None are not
+    computed, and their operands not read."""
+    dev, u8, f32, b16 = _device(dy), torch.uint8, torch.float32, torch.bfloat16
+    M, N = dy.shape
+    K = next((t.shape[i] for t, i in ((w_t, 0), (x_t, 0), (dx, 1), (dw, 1)) if t is not None), 16)
+    ws = _workspace_arg(ws, dev, lambda: mmdit_fp8_block_linear_bwd_workspace_size(M, N, K))
+    _launch("mmdit_fp8_block_linear_bwd", dev, stream, M, N, K, _arg("dy", dy, dev, b16, M, N),
+            _arg("w_t", w_t, dev, u8, K, _ld16(N)), _arg("s_w", s_w, dev, f32, _tiles(N), _tiles(K)),
+            _arg("x_t", x_t, dev, u8, K, _ld16(M)), _arg("s_xt", s_xt, dev, f32, _tiles(M), K),
+            _arg("dx", dx, dev, b16, M, K), _arg("dw", dw, dev, f32, N, K), _arg("db", db, dev, f32, N),
+            ws.data_ptr(), ws.numel())
+    return ws
+
+
+def make_rope_cfg(rot_dim, theta=10000.0, interleaved=True, scaling="none", factor=1.0, orig_len=0.0, low=1.0,
+                  high=4.0, mscale=1.0) -> RopeCfg:
+    """Frequencies of rotary positions (mmdit_rope_config); scaling "none", "linear" or "by_parts"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {ROPE_SCALINGS}, got {scaling!r}")
+    cfg = RopeCfg()
+    _check(load().mmdit_rope_config(C.byref(cfg), rot_dim, int(bool(interleaved)), float(theta),
+                                    ROPE_SCALINGS.index(scaling), float(factor), float(orig_len), float(low),
+                                    float(high), float(mscale)))
+    return cfg
+
+
+def _rope_view(name, t, dev, dtype, shape):
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    sb, ss, sh, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
+        raise ValueError(f"{name}: the elements of a head must be adjacent")
+    return RopeView(t.data_ptr(), sb if shape[0] > 1 else 0, ss if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
+
+
+def _rope(name, cfg, q, q_out, k, k_out, positions, cos, sin, stream):
+    dev, dt = _device(q), q.dtype
+    act = act_of(q)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, S, H, d]")
+    B, S, Hq, d = q.shape
+    vq, vqo = _rope_view("q", q, dev, dt, q.shape), _rope_view("q_out", q_out, dev, dt, q.shape)
+    vk = vko = None
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[2]
+        shape = torch.Size((B, S, Hk, d))
+        vk, vko = _rope_view("k", k, dev, dt, shape), _rope_view("k_out", k_out, dev, dt, shape)
+    pb = 0
+    if positions is not None:
+        if positions.device != dev or positions.dtype is not torch.int64:
+            raise TypeError(f"positions must be int64 on {dev}")
+        if positions.shape == (B, S) and (S <= 1 or positions.stride(1) == 1):
+            pb = positions.stride(0) if B > 1 else 0
+        elif positions.shape != (S,) or (S > 1 and positions.stride(0) != 1):
+            raise ValueError(f"positions must be [{B}, {S}] or [{S}] with dense rows")
+    pairs = cfg.rot_dim // 2
+    _launch(name, dev, stream, act, cfg, B, S, d, Hq, vq, vqo, Hk, vk, vko,
+            None if positions is None else positions.data_ptr(), pb, _arg("cos", cos, dev, torch.float32, B, S, pairs),
+            _arg("sin", sin, dev, torch.float32, B, S, pairs))
+
+
+def mmdit_rope_fwd(cfg: RopeCfg, q, q_out, k=None, k_out=None, positions=None, cos=None, sin=None, stream=None):
+    """q and k [B, S, H, d] (views of any strides with adjacent head elements) rotated into q_out, k_out (the
+    inputs themselves for in place) at int64 positions [B, S] or [S], or by cos / sin tables [B, S, rot/2]."""
+    _rope("mmdit_rope_fwd", cfg, q, q_out, k, k_out, positions, cos, sin, stream)
+
+
+def mmdit_rope_bwd(cfg: RopeCfg, dq, dq_out, k=None, k_out=None, positions=None, cos=None, sin=None, stream=None):
+    """The gradient of mmdit_rope_fwd: dq (and k = dk) [B, S, H, d] of the rotated heads into those of q and k."""
+    _rope("mmdit_rope_bwd", cfg, dq, dq_out, k, k_out, positions, cos, sin, stream)

@@ -1,6 +1,7 @@
 // api.cu -- the C ABI of libmmdit.so (declared in include/mmdit.h): argument validation,
 // workspace planning and the launch sequences of each entry point.  No device memory is
 // allocated here; every buffer comes from the caller.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -8,6 +9,7 @@
 
 #include <algorithm>
 #include <array>
+#include <cmath>
 #include <initializer_list>
 #include <vector>
 
@@ -2506,6 +2508,314 @@ mmdit_status mmdit_flux_forward(const mmdit_flux_config* cfg, const mmdit_flux_w
   }
   return final_layer_body(d, cfg->channels, img_rows, vec, w->w_ada, w->b_ada, w->w_out, w->b_out, pred,
                           workspace, st);
+}
+
+// ----------------------------------------------------------------------------- language-model operators
+static mmdit_status check_norm(int32_t act, int32_t rows, int32_t dim, int step, const char* what) {
+  if (act != MMDIT_F32 && act != MMDIT_BF16) return fail(MMDIT_ERR_INVALID_ARG, "%s: bad act %d", what, act);
+  if (rows < 0 || dim < 1) return fail(MMDIT_ERR_INVALID_ARG, "%s: bad shape (%d rows of %d)", what, rows, dim);
+  if (dim % step != 0 || dim > 16384)
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: dim must be a multiple of %d, at most 16384 (got %d)", what, step, dim);
+  return MMDIT_OK;
+}
+
+mmdit_status mmdit_add_rmsnorm_fwd(int32_t act, int32_t res_f32, int32_t rows, int32_t dim, float eps, const void* x,
+                                   int64_t ldx, const void* residual, const void* gain, void* h, void* y, void* y_q,
+                                   float* s_y, float* rstd, void* stream) {
+  mmdit_status s = check_norm(act, rows, dim, y_q ? 16 : 8, "RMSNorm");
+  if (s != MMDIT_OK) return s;
+  if (!(eps >= 0.f)) return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: eps must not be negative");
+  if (ldx < dim || ldx % (16 / static_cast<int64_t>(elt_bytes(act))) != 0)
+    return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: rows of x must be 16-byte multiples apart, at least dim elements");
+  if (rows == 0) return MMDIT_OK;
+  if ((s = check_ptrs({x, gain}, "RMSNorm")) != MMDIT_OK) return s;
+  if (!aligned16(residual) || !aligned16(h) || !aligned16(y) || !aligned16(y_q))
+    return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: a residual or output is not 16-byte aligned");
+  if (h && !residual) return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: h needs a residual (without one it is x)");
+  if (!y && !y_q) return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: neither y nor y_q is given");
+  if ((y_q == nullptr) != (s_y == nullptr)) return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: y_q and s_y go together");
+  if (y == x || y == residual || h == x || (h && h == y))
+    return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: only h may alias an input, and only the residual");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  pdl_begin_call();
+  ProfScope ps_("add_rmsnorm", st);
+  MMDIT_CUDA(launch_add_rmsnorm_fwd(act, res_f32 ? 1 : 0, rows, dim, eps, x, ldx, residual, gain, h, y,
+                                    static_cast<uint8_t*>(y_q), s_y, rstd, st),
+             "RMSNorm");
+  return MMDIT_OK;
+}
+
+size_t mmdit_add_rmsnorm_bwd_workspace_size(int32_t rows, int32_t dim) {
+  if (rows < 1 || dim < 1) return kStatusBytes;
+  Carver c;
+  c.take(static_cast<size_t>(add_rmsnorm_bwd_blocks(rows)) * dim * sizeof(float));
+  return c.off;
+}
+
+mmdit_status mmdit_add_rmsnorm_bwd(int32_t act, int32_t res_f32, int32_t rows, int32_t dim, const void* dy,
+                                   const void* h, const void* gain, const float* rstd, const void* dh_in, void* dh,
+                                   void* dx, float* dgain, void* workspace, size_t workspace_bytes, void* stream) {
+  mmdit_status s = check_norm(act, rows, dim, 8, "RMSNorm backward");
+  if (s != MMDIT_OK) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, mmdit_add_rmsnorm_bwd_workspace_size(rows, dim))) != MMDIT_OK)
+    return s;
+  if (!aligned16(dh_in) || !aligned16(dx) || !aligned16(dgain))
+    return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm backward: dh_in, dx or dgain is not 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (dgain) MMDIT_CUDA(cudaMemsetAsync(dgain, 0, static_cast<size_t>(dim) * sizeof(float), st), "dgain clear");
+    return MMDIT_OK;
+  }
+  if ((s = check_ptrs({dy, h, gain, dh}, "RMSNorm backward")) != MMDIT_OK) return s;
+  if (!rstd) return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm backward: NULL rstd");
+  if (dh == dy || dh == h || dx == dy || dx == h || (dx && (dx == dh || dx == dh_in)))
+    return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm backward: only dh may alias an input, and only dh_in");
+  pdl_begin_call();
+  ProfScope ps_("add_rmsnorm_bwd", st);
+  MMDIT_CUDA(launch_add_rmsnorm_bwd(act, res_f32 ? 1 : 0, rows, dim, dy, h, gain, rstd, dh_in, dh, dx, dgain,
+                                    at<float>(workspace, kStatusBytes), st),
+             "RMSNorm backward");
+  return MMDIT_OK;
+}
+
+mmdit_status mmdit_fp8_block_cast(int32_t act, int32_t square, int32_t rows, int32_t cols, const void* x, void* q,
+                                  float* s, void* q_t, float* s_t, void* stream) {
+  if (act != MMDIT_F32 && act != MMDIT_BF16) return fail(MMDIT_ERR_INVALID_ARG, "block cast: bad act %d", act);
+  if (square != 0 && square != 1) return fail(MMDIT_ERR_INVALID_ARG, "block cast: square must be 0 or 1");
+  if (rows < 0 || cols < 1) return fail(MMDIT_ERR_INVALID_ARG, "block cast: bad shape %d x %d", rows, cols);
+  if (cols % 16 != 0) return fail(MMDIT_ERR_UNSUPPORTED, "block cast: cols must be a multiple of 16 (got %d)", cols);
+  if (rows > (1 << 30) || cols > (1 << 30)) return fail(MMDIT_ERR_UNSUPPORTED, "block cast: more than 2^30 rows or columns");
+  if (rows == 0) return MMDIT_OK;
+  mmdit_status st_ = check_ptrs({x}, "block cast");
+  if (st_ != MMDIT_OK) return st_;
+  if (!q && !q_t) return fail(MMDIT_ERR_INVALID_ARG, "block cast: neither q nor q_t is given");
+  if (!aligned16(q) || !aligned16(q_t)) return fail(MMDIT_ERR_INVALID_ARG, "block cast: codes not 16-byte aligned");
+  if ((q || square) && !s) return fail(MMDIT_ERR_INVALID_ARG, "block cast: NULL s");
+  if (square ? s_t != nullptr : (q_t == nullptr) != (s_t == nullptr))
+    return fail(MMDIT_ERR_INVALID_ARG, "block cast: s_t goes with q_t, and only where square is 0");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  pdl_begin_call();
+  ProfScope ps_("fp8_block_cast", st);
+  MMDIT_CUDA(launch_block_cast(act, square, rows, cols, x, static_cast<uint8_t*>(q), cols, s, static_cast<uint8_t*>(q_t),
+                               static_cast<int64_t>(round_up(rows, 16)), s_t, nullptr, nullptr, st),
+             "block cast");
+  return MMDIT_OK;
+}
+
+static mmdit_status check_block_linear(int32_t M, int32_t N, int32_t K, const char* what) {
+  if (M < 0 || N < 1 || K < 1) return fail(MMDIT_ERR_INVALID_ARG, "%s: bad shape M=%d N=%d K=%d", what, M, N, K);
+  if (N % 8 != 0 || K % 16 != 0)
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: N must be a multiple of 8 and K of 16 (N=%d, K=%d)", what, N, K);
+  if (M > (1 << 30) || N > (1 << 23) || K > (1 << 23))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: M must be at most 2^30, N and K at most 2^23", what);
+  return MMDIT_OK;
+}
+
+size_t mmdit_fp8_block_linear_workspace_size(int32_t, int32_t, int32_t) { return kStatusBytes; }
+
+mmdit_status mmdit_fp8_block_linear_fwd(int32_t M, int32_t N, int32_t K, const void* x, const float* s_x, const void* w,
+                                        const float* s_w, const void* b, void* y, int32_t y_f32, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  mmdit_status s = check_block_linear(M, N, K, "block FP8 linear");
+  if (s != MMDIT_OK) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, kStatusBytes)) != MMDIT_OK) return s;
+  if (M == 0) return MMDIT_OK;
+  if ((s = check_ptrs({x, w, y}, "block FP8 linear")) != MMDIT_OK) return s;
+  if (!s_x || !s_w) return fail(MMDIT_ERR_INVALID_ARG, "block FP8 linear: NULL scale");
+  if (!aligned16(b)) return fail(MMDIT_ERR_INVALID_ARG, "block FP8 linear: bias is not 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  pdl_begin_call();
+  ProfScope ps_("fp8_block_linear", st);
+  BlockGemm g;
+  g.M = M, g.N = N, g.K = K, g.A = static_cast<const uint8_t*>(x), g.B = static_cast<const uint8_t*>(w);
+  g.lda = g.ldb = K, g.sa = s_x, g.sb = s_w, g.sb_n = (K + 127) / 128, g.sb_k = 1;
+  g.bias = static_cast<const __nv_bfloat16*>(b), g.out = y, g.out_f32 = y_f32 ? 1 : 0;
+  MMDIT_CUDA(launch_gemm_block(g, status_word(workspace), 1, st), "block FP8 linear");
+  return MMDIT_OK;
+}
+
+}  // extern "C"
+
+namespace {
+struct BlockBwdPlan {
+  size_t g, sg, gt, sgt, part, total;
+  int64_t ldn, ldm;
+};
+BlockBwdPlan plan_block_linear_bwd(int M, int N) {
+  BlockBwdPlan p;
+  const size_t m = static_cast<size_t>(M), n = static_cast<size_t>(N), tm = (m + 127) / 128, tn = (n + 127) / 128;
+  p.ldn = static_cast<int64_t>(round_up(n, 16)), p.ldm = static_cast<int64_t>(round_up(m, 16));
+  Carver c;
+  p.g = c.take(m * static_cast<size_t>(p.ldn)), p.sg = c.take(tn * m * 4);
+  p.gt = c.take(n * static_cast<size_t>(p.ldm)), p.sgt = c.take(tm * n * 4);
+  p.part = c.take(tm * n * 4);
+  p.total = c.off;
+  return p;
+}
+}  // namespace
+
+extern "C" {
+
+size_t mmdit_fp8_block_linear_bwd_workspace_size(int32_t M, int32_t N, int32_t) {
+  if (M < 1 || N < 1) return kStatusBytes;
+  return plan_block_linear_bwd(M, N).total;
+}
+
+mmdit_status mmdit_fp8_block_linear_bwd(int32_t M, int32_t N, int32_t K, const void* dy, const void* w_t,
+                                        const float* s_w, const void* x_t, const float* s_xt, void* dx, float* dw,
+                                        float* db, void* workspace, size_t workspace_bytes, void* stream) {
+  mmdit_status s = check_block_linear(M, N, K, "block FP8 linear backward");
+  if (s != MMDIT_OK) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, mmdit_fp8_block_linear_bwd_workspace_size(M, N, K))) != MMDIT_OK)
+    return s;
+  if (!aligned16(dw) || !aligned16(db))
+    return fail(MMDIT_ERR_INVALID_ARG, "block FP8 linear backward: dw or db is not 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    MMDIT_CUDA(cudaMemsetAsync(workspace, 0, 4, st), "status clear");
+    if (dw) MMDIT_CUDA(cudaMemsetAsync(dw, 0, static_cast<size_t>(N) * K * 4, st), "dW clear");
+    if (db) MMDIT_CUDA(cudaMemsetAsync(db, 0, static_cast<size_t>(N) * 4, st), "db clear");
+    return MMDIT_OK;
+  }
+  if (!dx && !dw && !db) return fail(MMDIT_ERR_INVALID_ARG, "block FP8 linear backward: no output is given");
+  if ((s = check_ptrs({dy}, "block FP8 linear backward")) != MMDIT_OK) return s;
+  if (dx && (s = check_ptrs({dx, w_t}, "block FP8 linear backward dx")) != MMDIT_OK) return s;
+  if (dw && (s = check_ptrs({x_t}, "block FP8 linear backward dw")) != MMDIT_OK) return s;
+  if ((dx && !s_w) || (dw && !s_xt)) return fail(MMDIT_ERR_INVALID_ARG, "block FP8 linear backward: NULL scale");
+  const BlockBwdPlan p = plan_block_linear_bwd(M, N);
+  pdl_begin_call();
+  ProfScope ps_("fp8_block_linear_bwd", st);
+  uint32_t* status = status_word(workspace);
+  MMDIT_CUDA(launch_block_cast(MMDIT_BF16, 0, M, N, dy, dx ? at<uint8_t>(workspace, p.g) : nullptr, p.ldn,
+                               at<float>(workspace, p.sg), dw ? at<uint8_t>(workspace, p.gt) : nullptr, p.ldm,
+                               at<float>(workspace, p.sgt), db ? at<float>(workspace, p.part) : nullptr, status, st),
+             "gradient cast");
+  const int tiles_m = (M + 127) / 128, tiles_k = (K + 127) / 128;
+  if (dx) {
+    // contracted over N: slice j of N, block of K i -> s_w[j, i]
+    BlockGemm g;
+    g.M = M, g.N = K, g.K = N, g.A = at<uint8_t>(workspace, p.g), g.B = static_cast<const uint8_t*>(w_t);
+    g.lda = g.ldb = p.ldn, g.sa = at<float>(workspace, p.sg), g.sb = s_w, g.sb_n = 1, g.sb_k = tiles_k;
+    g.out = dx;
+    MMDIT_CUDA(launch_gemm_block(g, status, 0, st), "block FP8 dgrad");
+  }
+  if (dw) {
+    BlockGemm g;
+    g.M = N, g.N = K, g.K = M, g.A = at<uint8_t>(workspace, p.gt), g.B = static_cast<const uint8_t*>(x_t);
+    g.lda = g.ldb = p.ldm, g.sa = at<float>(workspace, p.sgt), g.sb = s_xt, g.row_b = 1;
+    g.out = dw, g.out_f32 = 1;
+    MMDIT_CUDA(launch_gemm_block(g, status, 0, st), "block FP8 wgrad");
+  }
+  if (db) MMDIT_CUDA(launch_colsum_finish(at<float>(workspace, p.part), tiles_m, N, db, st), "db column sums");
+  return MMDIT_OK;
+}
+
+mmdit_status mmdit_rope_config(mmdit_rope_cfg* cfg, int32_t rot_dim, int32_t interleaved, double theta, int32_t scaling,
+                               double factor, double orig_len, double low, double high, double mscale) {
+  if (!cfg) return fail(MMDIT_ERR_INVALID_ARG, "rope config: cfg is NULL");
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 512)
+    return fail(MMDIT_ERR_UNSUPPORTED, "rope config: rot_dim must be even, 2 to 512 (got %d)", rot_dim);
+  if (scaling < MMDIT_ROPE_SCALE_NONE || scaling > MMDIT_ROPE_SCALE_BY_PARTS)
+    return fail(MMDIT_ERR_INVALID_ARG, "rope config: unknown scaling %d", scaling);
+  if (!(theta >= 1.0) || !std::isfinite(theta) || !std::isfinite(mscale))
+    return fail(MMDIT_ERR_INVALID_ARG, "rope config: theta must be at least 1, theta and mscale finite");
+  if (scaling != MMDIT_ROPE_SCALE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(MMDIT_ERR_INVALID_ARG, "rope config: factor must be at least 1 and finite");
+  if (scaling == MMDIT_ROPE_SCALE_BY_PARTS &&
+      (!(orig_len > 0.0) || !(high > low) || !std::isfinite(orig_len) || !std::isfinite(high) || !std::isfinite(low)))
+    return fail(MMDIT_ERR_INVALID_ARG, "rope config: by parts needs orig_len > 0 and high > low");
+  memset(cfg, 0, sizeof(*cfg));
+  cfg->rot_dim = rot_dim, cfg->interleaved = interleaved ? 1 : 0, cfg->mscale = static_cast<float>(mscale);
+  const double two_pi = 6.283185307179586476925;
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    double f = pow(theta, -2.0 * j / rot_dim);
+    if (scaling == MMDIT_ROPE_SCALE_LINEAR) {
+      f /= factor;
+    } else if (scaling == MMDIT_ROPE_SCALE_BY_PARTS) {
+      const double g = std::min(std::max((orig_len * f / two_pi - low) / (high - low), 0.0), 1.0);
+      f *= g + (1.0 - g) / factor;
+    }
+    cfg->turns[j] = static_cast<uint64_t>(ldexp(f / two_pi, 64));  // f <= 1: below 2^62
+  }
+  return MMDIT_OK;
+}
+
+}  // extern "C"
+
+namespace {
+mmdit_status check_view(const mmdit_rope_view* v, int64_t unit, const char* name) {
+  if (!v || !v->ptr) return fail(MMDIT_ERR_INVALID_ARG, "rope: %s is NULL", name);
+  if (!aligned16(v->ptr)) return fail(MMDIT_ERR_INVALID_ARG, "rope: %s is not 16-byte aligned", name);
+  for (int64_t st : {v->stride_b, v->stride_s, v->stride_h})
+    if (st < 0 || st % unit != 0)
+      return fail(MMDIT_ERR_INVALID_ARG, "rope: %s's strides must be multiples of 16 bytes, not negative", name);
+  return MMDIT_OK;
+}
+
+mmdit_status rope_call(int32_t act, const mmdit_rope_cfg* cfg, int32_t batch, int32_t seq, int32_t head_dim,
+                       int32_t heads_q, const mmdit_rope_view* q, const mmdit_rope_view* q_out, int32_t heads_k,
+                       const mmdit_rope_view* k, const mmdit_rope_view* k_out, const int64_t* positions,
+                       int64_t pos_bstride, const float* cos, const float* sin, int transposed, void* stream) {
+  if (act != MMDIT_F32 && act != MMDIT_BF16) return fail(MMDIT_ERR_INVALID_ARG, "rope: bad act %d", act);
+  if (!cfg) return fail(MMDIT_ERR_INVALID_ARG, "rope: cfg is NULL");
+  if (cfg->rot_dim < 2 || cfg->rot_dim % 2 != 0 || cfg->rot_dim > 512)
+    return fail(MMDIT_ERR_INVALID_ARG, "rope: cfg was not filled by mmdit_rope_config");
+  if (batch < 0 || seq < 0 || heads_q < 0 || heads_k < 0) return fail(MMDIT_ERR_INVALID_ARG, "rope: negative size");
+  if (head_dim % 8 != 0 || head_dim < 8 || head_dim > 512)
+    return fail(MMDIT_ERR_UNSUPPORTED, "rope: head_dim must be a multiple of 8, at most 512 (got %d)", head_dim);
+  if (cfg->rot_dim > head_dim)
+    return fail(MMDIT_ERR_INVALID_ARG, "rope: rot_dim %d exceeds head_dim %d", cfg->rot_dim, head_dim);
+  if (static_cast<int64_t>(heads_q) + heads_k > 65536) return fail(MMDIT_ERR_UNSUPPORTED, "rope: more than 65536 heads");
+  if (static_cast<int64_t>(batch) * seq == 0) return MMDIT_OK;
+  const bool tables = cos || sin;
+  if (tables ? (!cos || !sin || positions) : !positions)
+    return fail(MMDIT_ERR_INVALID_ARG, "rope: give positions, or both cos and sin");
+  if (pos_bstride < 0) return fail(MMDIT_ERR_INVALID_ARG, "rope: negative pos_bstride");
+  if ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0 || !aligned16(cos) || !aligned16(sin))
+    return fail(MMDIT_ERR_INVALID_ARG, "rope: positions, cos or sin is not aligned");
+  const int64_t unit = 16 / static_cast<int64_t>(elt_bytes(act));
+  mmdit_rope_view in[2] = {}, out[2] = {};
+  int heads[2] = {heads_q, k ? heads_k : 0};
+  const mmdit_rope_view *vi[2] = {q, k}, *vo[2] = {q_out, k_out};
+  for (int i = 0; i < 2; ++i) {
+    if (i == 1 && !k) {
+      if (k_out) return fail(MMDIT_ERR_INVALID_ARG, "rope: k_out without k");
+      break;
+    }
+    if (heads[i] == 0) continue;
+    mmdit_status s = check_view(vi[i], unit, i ? "k" : "q");
+    if (s != MMDIT_OK || (s = check_view(vo[i], unit, i ? "k_out" : "q_out")) != MMDIT_OK) return s;
+    in[i] = *vi[i], out[i] = *vo[i];
+    if (in[i].ptr == out[i].ptr && (in[i].stride_b != out[i].stride_b || in[i].stride_s != out[i].stride_s ||
+                                    in[i].stride_h != out[i].stride_h))
+      return fail(MMDIT_ERR_INVALID_ARG, "rope: in place needs the same strides");
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  pdl_begin_call();
+  ProfScope ps_(transposed ? "rope_bwd" : "rope", st);
+  MMDIT_CUDA(launch_rope_apply(act, *cfg, batch, seq, head_dim, in, out, heads, positions, pos_bstride, cos, sin,
+                               transposed, st),
+             "rope");
+  return MMDIT_OK;
+}
+}  // namespace
+
+extern "C" {
+
+mmdit_status mmdit_rope_fwd(int32_t act, const mmdit_rope_cfg* cfg, int32_t batch, int32_t seq, int32_t head_dim,
+                            int32_t heads_q, const mmdit_rope_view* q, const mmdit_rope_view* q_out, int32_t heads_k,
+                            const mmdit_rope_view* k, const mmdit_rope_view* k_out, const int64_t* positions,
+                            int64_t pos_bstride, const float* cos, const float* sin, void* stream) {
+  return rope_call(act, cfg, batch, seq, head_dim, heads_q, q, q_out, heads_k, k, k_out, positions, pos_bstride, cos,
+                   sin, 0, stream);
+}
+
+mmdit_status mmdit_rope_bwd(int32_t act, const mmdit_rope_cfg* cfg, int32_t batch, int32_t seq, int32_t head_dim,
+                            int32_t heads_q, const mmdit_rope_view* q, const mmdit_rope_view* q_out, int32_t heads_k,
+                            const mmdit_rope_view* k, const mmdit_rope_view* k_out, const int64_t* positions,
+                            int64_t pos_bstride, const float* cos, const float* sin, void* stream) {
+  return rope_call(act, cfg, batch, seq, head_dim, heads_q, q, q_out, heads_k, k, k_out, positions, pos_bstride, cos,
+                   sin, 1, stream);
 }
 
 }  // extern "C"

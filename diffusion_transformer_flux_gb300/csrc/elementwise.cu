@@ -1091,7 +1091,11 @@ cudaError_t launch_colsum(int act, const void* in, int R, int C, float* part, in
                           static_cast<const float*>(in), R, C, part);
   if (e_ != cudaSuccess) return e_;
   count_launch();
-  e_ = launch_pdl(colsum_finish_kernel, dim3((C + 31) / 32), dim3(32, 32), 0, stream, part, chunks, C, out);
+  return launch_colsum_finish(part, chunks, C, out, stream);
+}
+
+cudaError_t launch_colsum_finish(const float* part, int chunks, int C, float* out, cudaStream_t stream) {
+  const cudaError_t e_ = launch_pdl(colsum_finish_kernel, dim3((C + 31) / 32), dim3(32, 32), 0, stream, part, chunks, C, out);
   if (e_ != cudaSuccess) return e_;
   count_launch();
   return cudaGetLastError();

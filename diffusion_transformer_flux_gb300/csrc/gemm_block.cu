@@ -1,0 +1,665 @@
+// gemm_block.cu -- matrix products of E4M3 codes with a scale for each block of 128 along K:
+//   C[m, n] = sum over 128-wide slices j of K of  (A_j B_j^T)[m, n] / (s_a[j, m] s_b(j, n))  + bias[n]
+// A [M, K] and B [N, K] hold codes (rows of lda, ldb bytes), s_a [ceil(K/128), M]; B's scale is one per
+// 128 x 128 tile (a weight) or one per row and slice, [ceil(K/128), N] (the second operand of a weight
+// gradient).  Each slice's product is a sum of at most 128 products of E4M3 codes in the tensor core's
+// float32 accumulator; it is taken out of tensor memory, scaled and added in float32 registers in slice
+// order, so the result is the same from call to call.
+//
+// block_pair_kernel (many rows): 256 x 256 output tiles on CTA pairs (tcgen05 cta_group::2), as in
+// gemm_pair.cuh: each CTA stages its 128 rows of A and 128 rows of B, 32 KB per slice.  A slice is 512
+// cycles of the pair's tensor cores.  Two TMEM buffers of 256 columns take the slices in turn; in the
+// 512 cycles that the tensor cores spend on one, eight warps read the other (a row and 128 columns per
+// thread), multiply by the slice's factor and add to 128 float32 registers per thread, two at a time
+// (fma.rn.f32x2).  The pair halves what each SM has to read of B, which is what a single CTA's 128 x 256
+// tile is bound by.
+//
+// block_stream_kernel (few rows): B's bytes are the cost, so the roles are turned: 128 rows of B are the
+// MMA's M side and NT = 16 .. 128 rows of A its N side, and the CTAs of a cluster split K, so that every
+// SM streams its share of B through a ring of TMA stages.  The partial sums meet in shared memory of the
+// cluster (each CTA adds up its own columns, in rank order): no workspace, no atomics, the same bits
+// every time.
+//
+// Every wait is bounded (common.cuh); after one gives up the remaining barriers are still met, so no
+// thread is left behind.
+#include <atomic>
+
+#include "gemm_kernel.cuh"
+
+namespace mmdit {
+namespace {
+
+constexpr int kSlice = 128;  // K of a scale block: 128 codes = one 128-byte swizzled row
+constexpr int kPairStages = 6;
+constexpr int kPairStageBytes = 2 * kSlice * kSlice;  // this CTA's 128 rows of A and of B
+constexpr int kPairThreads = 128 + 512;               // producer, MMA issuer, two idle warps; 16 promotion warps
+constexpr int kPairRowB = 16 * 2 * 64;                // per promotion warp: two slices' factors of its columns
+constexpr int kPairSmem = kPairStages * kPairStageBytes + kPairRowB * 4 + 256 + 1024;
+// 640 threads start with 96 registers (61440); the promotion warpgroups take 112, the other one keeps 32
+constexpr int kPairFewRegs = 32, kPairManyRegs = 112;
+static_assert(128 * kPairFewRegs + 512 * kPairManyRegs <= kPairThreads * 96, "register shares");
+constexpr int kPairN = 256;
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+
+// mbar_wait that tries the barrier a few hundred times before it first reads the timer: the waits here
+// recur every slice, and a timer read costs more than the slice's hand-over.
+__device__ __forceinline__ bool slice_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_test(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort, status, kErrGemmWait);
+}
+
+// slice_wait by a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return __all_sync(0xffffffffu, slice_wait(bar, parity, abort, status)) != 0;
+}
+
+// One lane of a converged warp.  The MMA and TMA loops below run on whole warps and let one lane issue:
+// descriptors and counters then stay in uniform registers, which a loop that only one lane walks cannot
+// use (each MMA would first move its operands there: 450 instead of 100 cycles for a slice's four).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Moves registers between the warpgroups of a CTA: the sum of the shares is what the launch gave.
+template <int R>
+__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+struct BlockArgs {
+  const float* sa;   // [num_kb, M]
+  const float* sb;   // tile scales: (n / 128) * sb_n + kb * sb_k; row scales: kb * N + n
+  int64_t sb_n, sb_k;
+  const __nv_bfloat16* bias;
+  void* out;         // [M, N]
+  int M, N, num_kb;
+  uint32_t* status;
+  int clear;         // 1: this kernel is the call's first and clears the status word
+};
+
+template <typename TO>
+__device__ __forceinline__ void store_row(TO* dst, const __nv_bfloat16* bias, int n, int N, float (&v)[32]) {
+  if (n + 32 <= N) {
+    if (bias) {
+      float b[32];
+      load32(bias + n, b);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += b[i];
+    }
+    store32(dst + n, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (n + i < N) {
+      const float r = v[i] + (bias ? __bfloat162float(bias[n + i]) : 0.f);
+      if constexpr (sizeof(TO) == 2)
+        dst[n + i] = __float2bfloat16(r);
+      else
+        dst[n + i] = r;
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- many rows
+template <bool ROW_B, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    block_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                      const __grid_constant__ BlockArgs a) {
+  constexpr uint32_t kIdesc = make_idesc<kKindF8>(256, 128);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* row_b = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes);  // [16 warps][2][64]
+  uint64_t* full = reinterpret_cast<uint64_t*>(row_b + kPairRowB);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* pfull = empty + kPairStages;  // [buffer][half]
+  uint64_t* pempty = pfull + 4;
+  uint64_t* drain = pempty + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int num_kb = a.num_kb;
+  const int tiles_m = (a.M + 255) / 256, tiles_n = (a.N + kPairN - 1) / kPairN;
+  const int tiles = tiles_m * tiles_n;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int b = 0; b < 4; ++b) mbar_init(&pfull[b], 1), mbar_init(&pempty[b], 16);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+
+  if (warp < 4) {
+    regs_fewer<kPairFewRegs>();
+    if (warp == 0) {
+      // ---------------- TMA producer (both CTAs; the bytes complete on the leader's barrier).  Half h
+      // of the tile's columns is rows 64 h .. 64 h + 63 of both CTAs' B.
+      if (elect_one()) {
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_b);
+      }
+      const uint32_t full_leader = mapa_shared(smem_addr(full), 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0, parities = 0;  // bit s: stage s was filled, and with which parity last
+      bool ok = true;
+      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+        const int m0 = (tile % tiles_m) * 256 + static_cast<int>(rank) * 128;
+        const int n0 = (tile / tiles_m) * kPairN + static_cast<int>(rank) * 64;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          ok = warp_wait(&empty[stage], phase ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          uint8_t* st = smem + stage * kPairStageBytes;
+          const uint32_t bar = full_leader + static_cast<uint32_t>(stage * sizeof(uint64_t));
+          if (elect_one()) {
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
+            tma_load_2d_pair(st, &tm_a, bar, kb * kSlice, m0);
+            tma_load_2d_pair(st + kSlice * kSlice, &tm_b, bar, kb * kSlice, n0);
+            tma_load_2d_pair(st + kSlice * kSlice + 64 * kSlice, &tm_b, bar, kb * kSlice, n0 + 128);
+          }
+          __syncwarp();
+          issued |= 1u << stage;
+          parities = (parities & ~(1u << stage)) | (phase << stage);
+          if (++stage == kPairStages) stage = 0, phase ^= 1;
+        }
+      }
+      if (*abort_flag && leader) {
+        // a bounded chance for the copies already issued to land before the pair exits
+        int never = 0;
+        for (int s = 0; s < kPairStages; ++s)
+          if (issued >> s & 1) mbar_wait(&full[s], parities >> s & 1, &never, a.status, 0);
+      }
+    } else if (warp == 1 && leader) {
+      // ---------------- MMA issuer: slice `it` of this pair's walk into TMEM buffer it & 1, one half of
+      // the columns after the other
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+        for (int kb = 0; ok && kb < num_kb; ++kb, ++it) {
+          const uint32_t b = it & 1, parity = ((it >> 1) & 1) ^ 1;
+          ok = warp_wait(&full[stage], phase, abort_flag, a.status);
+          if (!ok) break;
+          const uint64_t da = sdesc_kmajor_sw128(smem_addr(smem + stage * kPairStageBytes));
+          const uint64_t db = sdesc_kmajor_sw128(smem_addr(smem + stage * kPairStageBytes + kSlice * kSlice));
+#pragma unroll
+          for (uint32_t h = 0; h < 2; ++h) {
+            if (ok) ok = warp_wait(&pempty[2 * b + h], parity, abort_flag, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            // a descriptor's address field counts 16 bytes: a K step is 2, 64 rows are 512
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma_pair<kKindF8>(tmem + b * 256u + h * 128u, da + 2 * k, db + 2 * k + h * 512, kIdesc, k > 0 ? 1u : 0u);
+              tc_commit_pair_mc(&pfull[2 * b + h], 0x3);
+              if (h == 1) tc_commit_pair_mc(&empty[stage], 0x3);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (++stage == kPairStages) stage = 0, phase ^= 1;
+        }
+      }
+      if (*abort_flag) {
+        int never = 0;
+        if (elect_one()) tc_commit_pair(drain);
+        __syncwarp();
+        mbar_wait(drain, 0, &never, a.status, 0);
+      }
+    }
+  } else {
+    regs_more<kPairManyRegs>();
+    // ---------------- promotion: warp w reads TMEM lanes 32 (w % 4) .. (its row) and 64 columns, half
+    // h = g / 2 of each buffer, g its warp group
+    const int quarter = warp & 3, g = (warp - 4) >> 2, h = g >> 1;
+    const int row = quarter * 32 + lane;
+    const uint32_t pempty_leader = mapa_shared(smem_addr(&pempty[h]), 0);
+    const uint32_t t_base = tmem + static_cast<uint32_t>(g * 64) + (static_cast<uint32_t>(quarter * 32) << 16);
+    float* my_row_b = row_b + (warp - 4) * 128;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = pair; tile < tiles; tile += pairs) {
+      const int m = (tile % tiles_m) * 256 + static_cast<int>(rank) * 128 + row;
+      const int ng = (tile / tiles_m) * kPairN + g * 64;
+      const bool row_ok = m < a.M;
+      // the slice's factor 1 / (s_a s_b): the scales of slice kb + 2 are fetched while slice kb is
+      // taken out, those of kb + 1 are turned into a factor after it
+      const float* pa = a.sa + (row_ok ? m : 0);
+      const float* pb = ROW_B ? a.sb : a.sb + static_cast<int64_t>(ng < a.N ? ng >> 7 : 0) * a.sb_n;
+      const int64_t b_step = ROW_B ? static_cast<int64_t>(a.N) : a.sb_k;
+      const int nb0 = ng + 2 * lane < a.N ? ng + 2 * lane : 0, nb1 = ng + 2 * lane + 1 < a.N ? ng + 2 * lane + 1 : 0;
+      uint64_t acc[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc[i] = 0;
+      float f, sa1, sb1 = 1.f, sb1x = 1.f;
+      auto fetch = [&](int kb) {
+        if (kb >= num_kb) return;
+        sa1 = __ldg(pa + static_cast<int64_t>(kb) * a.M);
+        if constexpr (ROW_B) {
+          sb1 = __ldg(pb + kb * b_step + nb0), sb1x = __ldg(pb + kb * b_step + nb1);
+        } else {
+          sb1 = __ldg(pb + kb * b_step);
+        }
+      };
+      auto factor = [&](uint32_t slot) {
+        if constexpr (ROW_B) {
+          f = fast_rcp(sa1);
+          *reinterpret_cast<float2*>(my_row_b + slot * 64 + 2 * lane) = make_float2(fast_rcp(sb1), fast_rcp(sb1x));
+          __syncwarp();
+        } else {
+          f = fast_rcp(sa1) * fast_rcp(sb1);
+        }
+      };
+      fetch(0);
+      factor(it & 1);
+      fetch(1);
+      for (int kb = 0; kb < num_kb; ++kb, ++it) {
+        const uint32_t b = it & 1;
+        if (ok) ok = warp_wait(&pfull[2 * b + h], (it >> 1) & 1, abort_flag, a.status);
+        if (!ok) continue;
+        tc_fence_after();
+        const uint64_t f2 = f32x2(f, f);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+          tmem_ld32_wait(t_base + b * 256u + static_cast<uint32_t>(c * 32), p);
+          if (c == 1) {  // this warp has read its part of the half buffer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(pempty_leader + b * 2 * static_cast<uint32_t>(sizeof(uint64_t)));
+          }
+          if constexpr (ROW_B) {
+            const float4* rb = reinterpret_cast<const float4*>(my_row_b + b * 64 + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 w = rb[i];
+              acc[c * 16 + 2 * i] = ffma2(pack2(p[4 * i], p[4 * i + 1]), fmul2(f32x2(w.x, w.y), f2), acc[c * 16 + 2 * i]);
+              acc[c * 16 + 2 * i + 1] =
+                  ffma2(pack2(p[4 * i + 2], p[4 * i + 3]), fmul2(f32x2(w.z, w.w), f2), acc[c * 16 + 2 * i + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c * 16 + i] = ffma2(pack2(p[2 * i], p[2 * i + 1]), f2, acc[c * 16 + i]);
+          }
+        }
+        if (kb + 1 < num_kb) factor((it + 1) & 1);
+        fetch(kb + 2);
+      }
+      if (ok && row_ok) {
+        TO* dst = static_cast<TO*>(a.out) + static_cast<int64_t>(m) * a.N;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f32x2_split(acc[c * 16 + i], v[2 * i], v[2 * i + 1]);
+          if (ng + c * 32 < a.N) store_row<TO>(dst, a.bias, ng + c * 32, a.N, v);
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------------------------------- few rows
+template <int NT>
+struct StreamCfg {
+  static constexpr int kStageBytes = kSlice * kSlice + NT * kSlice;
+  static constexpr int kStages = 100 * 1024 / kStageBytes;      // two CTAs to an SM
+  static constexpr int kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr int kFacSlices = 8;                          // slices whose factors are held at a time
+  static constexpr int kSmem = kStages * kStageBytes + 2 * kFacSlices * NT * 4 + 256 + 1024;
+  static_assert(NT * 128 * 4 <= kStages * kStageBytes, "the partial sums reuse the stage ring");
+};
+constexpr int kStreamThreads = 64 + 128;
+
+template <int NT, bool ROW_B, typename TO>
+__global__ void __launch_bounds__(kStreamThreads)
+    block_stream_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                        const __grid_constant__ BlockArgs a) {
+  using Cfg = StreamCfg<NT>;
+  constexpr uint32_t kIdesc = make_idesc<kKindF8>(128, NT);
+  constexpr int kFac = Cfg::kFacSlices;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* fac = reinterpret_cast<float*>(smem + Cfg::kStages * Cfg::kStageBytes);  // [2][kFac][NT]
+  uint64_t* full = reinterpret_cast<uint64_t*>(fac + 2 * kFac * NT);
+  uint64_t* empty = full + Cfg::kStages;
+  uint64_t* pfull = empty + Cfg::kStages;
+  uint64_t* pempty = pfull + 2;
+  uint64_t* drain = pempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = gridDim.x, rank = blockIdx.x;  // the cluster spans gridDim.x
+  const int n0 = blockIdx.y * 128, m0 = blockIdx.z * NT;
+  // this CTA's slices
+  const int per = a.num_kb / splits, rest = a.num_kb - per * splits;
+  const int kb0 = rank * per + (rank < rest ? rank : rest);
+  const int num = per + (rank < rest ? 1 : 0);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&pfull[b], 1), mbar_init(&pempty[b], 4);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  if (a.clear && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.status = 0;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, a.status); };
+  float acc[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = 0.f;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ---------------- TMA producer
+    if (elect_one()) {
+      tma_prefetch_desc(&tm_a);
+      tma_prefetch_desc(&tm_b);
+    }
+    int issued = 0, s = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < num; ++i) {
+      if (!wait(&empty[s], phase ^ 1u)) break;
+      uint8_t* st = smem + s * Cfg::kStageBytes;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+        tma_load_2d(st, &tm_b, &full[s], (kb0 + i) * kSlice, n0);
+        tma_load_2d(st + kSlice * kSlice, &tm_a, &full[s], (kb0 + i) * kSlice, m0);
+      }
+      __syncwarp();
+      issued = i + 1;
+      if (++s == Cfg::kStages) s = 0, phase ^= 1u;
+    }
+    if (*abort_flag) {
+      int never = 0;
+      for (int t = issued - Cfg::kStages > 0 ? issued - Cfg::kStages : 0; t < issued; ++t)
+        mbar_wait(&full[t % Cfg::kStages], static_cast<uint32_t>(t / Cfg::kStages) & 1u, &never, a.status, 0);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer: slice i into TMEM buffer i & 1
+    int s = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < num; ++i) {
+      const int b = i & 1;
+      if (!wait(&full[s], phase)) break;
+      if (!wait(&pempty[b], (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u)) break;
+      tc_fence_after();
+      const uint64_t dw = sdesc_kmajor_sw128(smem_addr(smem + s * Cfg::kStageBytes));
+      const uint64_t dx = sdesc_kmajor_sw128(smem_addr(smem + s * Cfg::kStageBytes + kSlice * kSlice));
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma<kKindF8>(tmem + static_cast<uint32_t>(b * NT), dw + 2 * k, dx + 2 * k, kIdesc, k > 0 ? 1u : 0u);
+        tc_commit(&empty[s]);
+        tc_commit(&pfull[b]);
+      }
+      __syncwarp();
+      if (++s == Cfg::kStages) s = 0, phase ^= 1u;
+    }
+    if (*abort_flag) {
+      int never = 0;
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      mbar_wait(drain, 0, &never, a.status, 0);
+    }
+  } else {
+    // ---------------- promotion: thread = one row of B, NT columns (rows of A)
+    const int quarter = warp & 3, row = quarter * 32 + lane, tp = static_cast<int>(threadIdx.x) - 64;
+    const uint32_t t_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    // factors of kFac slices at a time: entry (slice, column) by thread (slice * NT + column) % 128
+    constexpr int kPer = kFac * NT / 128;
+    float next[kPer];
+    auto fetch = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int e = tp + u * 128, i = i0 + e / NT, m = m0 + e % NT;
+        next[u] = 1.f;
+        if (i < num && m < a.M) {
+          next[u] = fast_rcp(__ldg(a.sa + static_cast<int64_t>(kb0 + i) * a.M + m));
+          if constexpr (!ROW_B) next[u] *= fast_rcp(__ldg(a.sb + static_cast<int64_t>(blockIdx.y) * a.sb_n + (kb0 + i) * a.sb_k));
+        }
+      }
+    };
+    fetch(0);
+    float sb_next = 1.f;
+    const bool n_ok = n0 + row < a.N;
+    if constexpr (ROW_B)
+      if (n_ok && num > 0) sb_next = __ldg(a.sb + static_cast<int64_t>(kb0) * a.N + n0 + row);
+    for (int i = 0; i < num; ++i) {
+      const int b = i & 1, slot = i % kFac, buf = (i / kFac) & 1;
+      if (slot == 0) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) fac[buf * kFac * NT + tp + u * 128] = next[u];
+        fetch(i + kFac);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
+      float fr = 1.f;
+      if constexpr (ROW_B) {
+        fr = fast_rcp(sb_next);
+        if (n_ok && i + 1 < num) sb_next = __ldg(a.sb + static_cast<int64_t>(kb0 + i + 1) * a.N + n0 + row);
+      }
+      if (ok) ok = wait(&pfull[b], static_cast<uint32_t>(i >> 1) & 1u);
+      if (!ok) continue;
+      tc_fence_after();
+      const float* f = fac + (buf * kFac + slot) * NT;
+#pragma unroll
+      for (int c = 0; c < NT; c += 16) {
+        uint32_t p[16];
+        tmem_ld16_wait(t_base + static_cast<uint32_t>(b * NT + c), p);
+        if (c + 16 == NT) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pempty[b]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 w = *reinterpret_cast<const float4*>(f + c + 4 * q);
+          const float w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[c + 4 * q + e] = fmaf(__uint_as_float(p[4 * q + e]), ROW_B ? w4[e] * fr : w4[e], acc[c + 4 * q + e]);
+        }
+      }
+    }
+  }
+
+  auto put = [&](int m, int n, float v) {
+    if (m >= a.M || n >= a.N) return;
+    if (a.bias) v += __bfloat162float(a.bias[n]);
+    TO* dst = static_cast<TO*>(a.out) + static_cast<int64_t>(m) * a.N + n;
+    if constexpr (sizeof(TO) == 2)
+      *dst = __float2bfloat16(v);
+    else
+      *dst = v;
+  };
+  const int tp = static_cast<int>(threadIdx.x) - 64, row = (warp & 3) * 32 + lane;
+  if (splits == 1) {
+    if (warp >= 2 && ok) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) put(m0 + t, n0 + row, acc[t]);
+    }
+  } else {
+    // CTA q of the cluster adds up columns [q cols, (q + 1) cols) of every CTA's partial sums, which
+    // the others write into its stage ring once all of them are done with theirs
+    const int cols = NT / splits;
+    __syncthreads();
+    cluster_sync();
+    if (warp >= 2) {
+      const uint32_t base = smem_addr(smem);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int q = t / cols, lc = t - q * cols;
+        const uint32_t dst = mapa_shared(base + static_cast<uint32_t>(((rank * cols + lc) * 128 + row) * 4), static_cast<uint32_t>(q));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(acc[t]) : "memory");
+      }
+    }
+    cluster_sync();
+    if (warp >= 2 && ok) {
+      const float* part = reinterpret_cast<const float*>(smem);
+      for (int lc = 0; lc < cols; ++lc) {
+        float v = 0.f;
+        for (int r = 0; r < splits; ++r) v += part[(r * cols + lc) * 128 + row];
+        put(m0 + rank * cols + lc, n0 + row, v);
+      }
+    }
+  }
+  (void)tp;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------------------------- host
+// Whether a kernel's dynamic shared memory size has been set on a device (one flag per kernel and device).
+struct Configured {
+  std::atomic<uint64_t> devices{0};
+};
+
+template <typename F>
+cudaError_t configure(F kern, int smem, Configured& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  done.devices.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
+
+bool code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, int64_t ld, int box_rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(k), static_cast<uint64_t>(rows)};
+  const uint64_t stride[1] = {static_cast<uint64_t>(ld)};
+  const uint32_t box[2] = {static_cast<uint32_t>(kSlice), static_cast<uint32_t>(box_rows)};
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, stride, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool ROW_B, typename TO>
+cudaError_t run_pair(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream) {
+  CUtensorMap ta, tb;
+  if (!code_map(&ta, p.A, p.M, p.K, p.lda, 128) || !code_map(&tb, p.B, p.N, p.K, p.ldb, 64)) return cudaErrorInvalidValue;
+  auto kern = block_pair_kernel<ROW_B, TO>;
+  static Configured done;
+  cudaError_t e = configure(kern, kPairSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + kPairN - 1) / kPairN);
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  const int pairs = static_cast<int>(tiles < num_sms() / 2 ? tiles : num_sms() / 2);
+  e = launch_pdl(kern, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, stream, ta, tb, a);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <int NT, bool ROW_B, typename TO>
+cudaError_t run_stream(const BlockGemm& p, const BlockArgs& a, int splits, cudaStream_t stream) {
+  using Cfg = StreamCfg<NT>;
+  CUtensorMap ta, tb;
+  if (!code_map(&ta, p.A, p.M, p.K, p.lda, NT) || !code_map(&tb, p.B, p.N, p.K, p.ldb, 128)) return cudaErrorInvalidValue;
+  auto kern = block_stream_kernel<NT, ROW_B, TO>;
+  static Configured done;
+  cudaError_t e = configure(kern, Cfg::kSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits), attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(splits, (p.N + 127) / 128, (p.M + NT - 1) / NT);
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_next_launch() ? 2 : 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, ta, tb, a)) != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <bool ROW_B, typename TO>
+cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream) {
+  if (p.M > 128) return run_pair<ROW_B, TO>(p, a, stream);
+  const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + nt - 1) / nt);
+  int splits = 1;
+  while (splits < 8 && tiles * splits < num_sms() && 4 * splits <= a.num_kb) splits *= 2;
+  switch (nt) {
+    case 16: return run_stream<16, ROW_B, TO>(p, a, splits, stream);
+    case 32: return run_stream<32, ROW_B, TO>(p, a, splits, stream);
+    case 64: return run_stream<64, ROW_B, TO>(p, a, splits, stream);
+    default: return run_stream<128, ROW_B, TO>(p, a, splits, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_block(const BlockGemm& p, uint32_t* status, int clear_status, cudaStream_t stream) {
+  if (p.M <= 0 || p.N <= 0) return cudaSuccess;
+  if (p.K <= 0) return cudaErrorInvalidValue;
+  BlockArgs a;
+  a.sa = p.sa, a.sb = p.sb, a.sb_n = p.sb_n, a.sb_k = p.sb_k;
+  a.bias = p.bias, a.out = p.out, a.M = p.M, a.N = p.N, a.num_kb = (p.K + kSlice - 1) / kSlice;
+  a.status = status, a.clear = clear_status;
+  if (p.row_b) return p.out_f32 ? run_any<true, float>(p, a, stream) : cudaErrorInvalidValue;
+  return p.out_f32 ? run_any<false, float>(p, a, stream) : run_any<false, __nv_bfloat16>(p, a, stream);
+}
+
+}  // namespace mmdit

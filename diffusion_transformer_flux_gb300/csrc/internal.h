@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/mmdit.h"
+
 namespace mmdit {
 
 // Epilogues of the tensor-core GEMM  C[M, N] = A[M, K] * W[N, K]^T (fp32 accumulation).
@@ -193,6 +195,47 @@ cudaError_t launch_blockwise_linear(int M, int N, int K, const __nv_bfloat16* x,
                                     const __nv_bfloat16* bias, __nv_bfloat16* y, void* scratch, uint32_t* status,
                                     cudaStream_t stream);
 
+// block_cast.cu: E4M3 codes of x [rows, cols] (act 0 fp32, 1 bf16; cols a multiple of 8) with block
+// scales.  square = 0: q [rows, ldq] in 1 x 128 tiles with s [ceil(cols/128), rows], and/or the transpose
+// qt [cols, ldt] in 1 x 128 tiles of x's columns with st [ceil(rows/128), cols]; square = 1: 128 x 128
+// tiles, s [ceil(rows/128), ceil(cols/128)], codes to q and/or qt.  ldt is rows rounded up to 16 (zeros
+// behind column `rows`).  part: null, or [ceil(rows/128), cols] receiving each 128-row block's column
+// sums of x.  status: null, or a status word to clear.
+cudaError_t launch_block_cast(int act, int square, int rows, int cols, const void* x, uint8_t* q, int64_t ldq, float* s,
+                              uint8_t* qt, int64_t ldt, float* st, float* part, uint32_t* status, cudaStream_t stream);
+// gemm_block.cu: out [M, N] = sum over 128-wide slices j of K of (A_j B_j^T) / (sa[j, m] sb(j, n)) + bias,
+// A [M, K] and B [N, K] E4M3 codes in rows of lda, ldb bytes (multiples of 16), sa [ceil(K/128), M]; sb is
+// one scale per 128 x 128 tile at (n / 128) sb_n + j sb_k, or with row_b (out_f32 only) [ceil(K/128), N].
+// N % 8 == 0.
+struct BlockGemm {
+  int M = 0, N = 0, K = 0;
+  const uint8_t *A = nullptr, *B = nullptr;
+  int64_t lda = 0, ldb = 0;
+  const float *sa = nullptr, *sb = nullptr;
+  int64_t sb_n = 0, sb_k = 0;
+  int row_b = 0;
+  const __nv_bfloat16* bias = nullptr;
+  void* out = nullptr;  // bf16, or fp32 with out_f32
+  int out_f32 = 0;
+};
+cudaError_t launch_gemm_block(const BlockGemm& p, uint32_t* status, int clear_status, cudaStream_t stream);
+// rmsnorm.cu: h = x + res, y = h g / sqrt(mean(h^2) + eps), and its backward (see the file's header).
+// T is the activation type, the residual's type is fp32 with res_f32 (or act 0), else T.  dim a
+// multiple of 8, at most 16384; part: add_rmsnorm_bwd_blocks(rows) * dim floats (with dgain).
+int add_rmsnorm_bwd_blocks(int rows);
+cudaError_t launch_add_rmsnorm_fwd(int act, int res_f32, int rows, int dim, float eps, const void* x, int64_t ldx,
+                                   const void* res, const void* gain, void* h, void* y, uint8_t* yq, float* sy,
+                                   float* rstd, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_bwd(int act, int res_f32, int rows, int dim, const void* dy, const void* h,
+                                   const void* gain, const float* rstd, const void* dh_in, void* dh, void* dx,
+                                   float* dgain, float* part, cudaStream_t stream);
+// rope_apply.cu: q and k (in[0], in[1]: [batch, seq, heads, head_dim] at the views' strides) rotated
+// into out; cos/sin tables [batch, seq, rot_dim / 2] or null (then positions pos[b * pos_bstride + s]).
+cudaError_t launch_rope_apply(int act, const mmdit_rope_cfg& cfg, int batch, int seq, int head_dim,
+                              const mmdit_rope_view in[2], const mmdit_rope_view out[2], const int heads[2],
+                              const int64_t* pos, int64_t pos_bstride, const float* cos, const float* sin,
+                              int transposed, cudaStream_t stream);
+
 // mxfp8.cu: MXFP8 casts (E4M3 elements, one E8M0 scale per 32 consecutive elements along K).
 // Each job casts src [rows, K] (bf16, K % 32 == 0) and writes the represented values P * 2^e
 // as bf16 into deq (may be src itself), and, when not null, the E4M3 codes [rows, K] and the
@@ -320,6 +363,8 @@ cudaError_t launch_transpose_pad(int act, const void* in, int R, int C, int ld_o
 // [chunks, C], then summed in chunk order.
 cudaError_t launch_colsum(int act, const void* in, int R, int C, float* part, int chunks, float* out,
                           cudaStream_t stream);
+// The second half of launch_colsum: out[c] = sum over chunks of part [chunks, C] in chunk order.
+cudaError_t launch_colsum_finish(const float* part, int chunks, int C, float* out, cudaStream_t stream);
 // vec = v32 (+ g[b] w_g + b_g when g != NULL), written in the activation type.
 cudaError_t launch_vec_finish(int act, const float* v32, const float* g, const void* wg,
                               const void* bg, int batch, int dim, void* vec, cudaStream_t stream);

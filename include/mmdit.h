@@ -683,6 +683,146 @@ mmdit_status mmdit_flux_forward(const mmdit_flux_config *cfg, const mmdit_flux_w
                                 const float *guidance, const float *rope_cos, const float *rope_sin,
                                 float *pred, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Language-model operators: what a text model beside the blocks (an encoder of prompts, or a
+ * transformer trained or served with the same library) needs around them.  Root-mean-square norm
+ * of the residual stream with an E4M3 output, linear layers on E4M3 codes with a scale for each
+ * block of 128 (weights cast once, activations where they are produced) with their gradients, and
+ * rotary positions for long contexts.  [API] §Normalization, RMSNorm; [FP8] §Configuration,
+ * fp8_recipe "blockwise"; [ARCH] §Mathematical formulation, 3D RoPE mathematics (the rotation).
+ *
+ * Block scales.  A tile of values v with largest magnitude amax is stored as the E4M3 codes
+ * E4M3(v s) (v s in float32, rounded to nearest even, saturating) with s = min(448 (1 / amax), 2^100)
+ * (reciprocal and product each rounded to float32), 1 for a tile of zeros; a code c stands for c / s.  NaN elements stay
+ * NaN and do not enter amax; an infinite element makes s zero and its tile's products NaN.
+ * Activations use 1 x 128 tiles, s [ceil(C/128), R] for values [R, C] (the layout of
+ * mmdit_fp8_blockwise_linear_fwd's s_x); weights 128 x 128 tiles, s [ceil(R/128), ceil(C/128)].  The
+ * last tile of a row or column may be short. */
+
+/* Residual addition and RMSNorm, row by row (one pass over memory):
+ *   h = x + residual (rounded to the residual's type),  r = 1 / sqrt(mean(h^2) + eps),  y = h r gain
+ *   x [rows, dim] of type `act`, rows ldx elements apart (16-byte multiples, >= dim);
+ *   residual NULL (then h = x), or [rows, dim] of type `act`, fp32 with res_f32 != 0;
+ *   gain [dim] of type `act`;
+ *   h: NULL, or [rows, dim] of the residual's type receiving h (needs residual; may alias it);
+ *   y: NULL, or [rows, dim] of type `act`; y_q: NULL, or the E4M3 codes of the float32 y [rows, dim]
+ *   in 1 x 128 tiles, with s_y [ceil(dim/128), rows]; rstd: NULL, or r [rows] fp32 (for the backward).
+ * float32 statistics.  dim a multiple of 8 (16 with y_q), at most 16384.  No workspace. */
+mmdit_status mmdit_add_rmsnorm_fwd(int32_t act, int32_t res_f32, int32_t rows, int32_t dim, float eps,
+                                   const void *x, int64_t ldx, const void *residual, const void *gain,
+                                   void *h, void *y, void *y_q, float *s_y, float *rstd, void *stream);
+
+/* Its gradients (the chain rule; the cast's rounding passes gradients through unchanged):
+ *   dh = r (dy gain - n mean(dy gain n)) + dh_in,  n = h r;   dgain = sum over rows of dy n
+ *   dy [rows, dim] of type `act`: the gradient of y; h, rstd: as the forward left them (h is x itself
+ *   without a residual), h of type `act`, or fp32 with res_f32 != 0;
+ *   dh_in: NULL, or the gradient that reaches h past the norm (h's type);
+ *   dh [rows, dim] of h's type: the gradient of x and of the residual (may alias dh_in);
+ *   dx: NULL, or the same gradient in type `act` (for an fp32 residual stream whose x is bf16);
+ *   dgain: NULL, or [dim] fp32 (written; fixed order, deterministic).
+ * rows == 0 zeroes dgain.  dim as for the forward.
+ * workspace >= mmdit_add_rmsnorm_bwd_workspace_size(rows, dim). */
+size_t mmdit_add_rmsnorm_bwd_workspace_size(int32_t rows, int32_t dim);
+mmdit_status mmdit_add_rmsnorm_bwd(int32_t act, int32_t res_f32, int32_t rows, int32_t dim, const void *dy,
+                                   const void *h, const void *gain, const float *rstd, const void *dh_in,
+                                   void *dh, void *dx, float *dgain, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* E4M3 codes with block scales, from one read of x [rows, cols] (type `act`):
+ *   square = 0 (activations, gradients): q [rows, cols] in 1 x 128 tiles of the rows with s
+ *   [ceil(cols/128), rows], and/or, for a product that contracts over the rows, q_t [cols, ld] in
+ *   1 x 128 tiles of the columns with s_t [ceil(rows/128), cols];
+ *   square = 1 (weights): 128 x 128 tiles with s [ceil(rows/128), ceil(cols/128)], the same codes as
+ *   q [rows, cols] and/or q_t [cols, ld] (s_t must be NULL).
+ * ld = rows rounded up to 16; the codes behind column `rows` of q_t are written as zeros.  q or q_t
+ * may be NULL (not both; without q, square = 0 needs no s).  cols a multiple of 16.  No workspace. */
+mmdit_status mmdit_fp8_block_cast(int32_t act, int32_t square, int32_t rows, int32_t cols, const void *x,
+                                  void *q, float *s, void *q_t, float *s_t, void *stream);
+
+/* Linear layer on E4M3 codes with block scales: y = x W^T + b,
+ *   y[m, n] = sum over 128-wide slices j of K of (x_j W_j^T)[m, n] / (s_x[j, m] s_w[n / 128, j]) + b[n]
+ *   x [M, K] codes, s_x [ceil(K/128), M] (1 x 128 tiles); w [N, K] codes, s_w [ceil(N/128),
+ *   ceil(K/128)] (128 x 128 tiles); b [N] bf16 or NULL; y [M, N] bf16, or fp32 with y_f32 != 0.
+ * Each slice is summed on the tensor cores in float32 and scaled into float32 sums in a fixed order:
+ * the same bits from call to call.  1 / (s_x s_w) has to be finite in float32 (the amax of the two
+ * tiles multiply to less than 6e43).  N a multiple of 8, K of 16; M == 0 is a no-op.
+ * workspace >= mmdit_fp8_block_linear_workspace_size(M, N, K) (the status word). */
+size_t mmdit_fp8_block_linear_workspace_size(int32_t M, int32_t N, int32_t K);
+mmdit_status mmdit_fp8_block_linear_fwd(int32_t M, int32_t N, int32_t K, const void *x, const float *s_x,
+                                        const void *w, const float *s_w, const void *b, void *y,
+                                        int32_t y_f32, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/* Its gradients.  dy [M, N] bf16 is cast here, once per direction, G in 1 x 128 tiles of its rows and
+ * G' in 1 x 128 tiles of its columns (the recipe of mmdit_fp8_block_cast):
+ *   dx = G W [M, K] bf16 (NULL: not computed), from w_t [K, ldn] = the transposed codes of W
+ *   (mmdit_fp8_block_cast with square = 1, q_t) and the forward's s_w;
+ *   dw = G'^T X [N, K] fp32 (NULL: not computed), from x_t [K, ldm], s_xt [ceil(M/128), K] = the
+ *   transposed codes and scales of x (square = 0, q_t, s_t);
+ *   db = column sums of dy [N] fp32 (NULL: not computed), fixed order.
+ * ldn, ldm: N, M rounded up to 16.  Written, not accumulated; deterministic.  N a multiple of 8, K of
+ * 16; M == 0 zeroes dw and db.
+ * workspace >= mmdit_fp8_block_linear_bwd_workspace_size(M, N, K). */
+size_t mmdit_fp8_block_linear_bwd_workspace_size(int32_t M, int32_t N, int32_t K);
+mmdit_status mmdit_fp8_block_linear_bwd(int32_t M, int32_t N, int32_t K, const void *dy, const void *w_t,
+                                        const float *s_w, const void *x_t, const float *s_xt, void *dx,
+                                        float *dw, float *db, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/* Rotary positions.  Pair j < rot_dim / 2 of a head's first rot_dim elements is (2j, 2j + 1) with
+ * interleaved != 0, (j, j + rot_dim / 2) without; a pair (a, b) of the token at position p becomes
+ * mscale (a cos t - b sin t, a sin t + b cos t), t = p f_j; elements from rot_dim on pass unchanged.
+ * mmdit_rope_config fills *cfg on the host (once per model) with f_j = theta^(-2j/rot_dim), changed
+ * for contexts longer than the trained one as `scaling` says:
+ *   MMDIT_ROPE_SCALE_NONE      f_j
+ *   MMDIT_ROPE_SCALE_LINEAR    f_j / factor (positions interpolated)
+ *   MMDIT_ROPE_SCALE_BY_PARTS  f_j (g + (1 - g) / factor), g = clamp((orig_len f_j / 2 pi - low) /
+ *                              (high - low), 0, 1): pairs that turn more than `high` times within
+ *                              orig_len keep their frequency, those below `low` are interpolated
+ * turns[j] is f_j / 2 pi in units of 2^-64: the phase of an integer position is exact modulo a turn.
+ * rot_dim even, 2 to 512; theta >= 1, factor >= 1, high > low, orig_len > 0 (BY_PARTS); mscale finite. */
+typedef enum mmdit_rope_scaling {
+  MMDIT_ROPE_SCALE_NONE = 0,
+  MMDIT_ROPE_SCALE_LINEAR = 1,
+  MMDIT_ROPE_SCALE_BY_PARTS = 2
+} mmdit_rope_scaling;
+typedef struct mmdit_rope_cfg {
+  int32_t rot_dim;
+  int32_t interleaved;
+  float mscale;
+  int32_t reserved;
+  uint64_t turns[256];
+} mmdit_rope_cfg;
+mmdit_status mmdit_rope_config(mmdit_rope_cfg *cfg, int32_t rot_dim, int32_t interleaved, double theta,
+                               int32_t scaling, double factor, double orig_len, double low, double high,
+                               double mscale);
+
+/* q and k rotated (k may be NULL: q alone).  A view is element (b, s, h, i) of a tensor
+ * [batch, seq, heads, head_dim] of type `act` at ptr + b stride_b + s stride_s + h stride_h + i
+ * (strides in elements, multiples of 16 bytes, >= 0): token-major, head-major and packed q|k|v layouts
+ * alike.  An output may be the input itself (same ptr and strides: in place) and must not overlap it
+ * otherwise.  Angles come from positions [batch, seq] int64 (pos_bstride elements between samples, 0:
+ * the same for all; any sign, exact far into a context) or from tables cos, sin [batch, seq,
+ * rot_dim / 2] fp32, 16-byte aligned, as rope3d_freqs writes them: exactly one of the two.  cfg and the
+ * views are host memory.  head_dim a multiple of 8, at most 512, >= cfg->rot_dim; float32 arithmetic.
+ * batch * seq == 0 is a no-op.  No workspace. */
+typedef struct mmdit_rope_view {
+  void *ptr;
+  int64_t stride_b, stride_s, stride_h;
+} mmdit_rope_view;
+mmdit_status mmdit_rope_fwd(int32_t act, const mmdit_rope_cfg *cfg, int32_t batch, int32_t seq,
+                            int32_t head_dim, int32_t heads_q, const mmdit_rope_view *q,
+                            const mmdit_rope_view *q_out, int32_t heads_k, const mmdit_rope_view *k,
+                            const mmdit_rope_view *k_out, const int64_t *positions, int64_t pos_bstride,
+                            const float *cos, const float *sin, void *stream);
+/* Its gradient: the views are the gradients of the rotated q and k in, of q and k out (the transposed
+ * rotation). */
+mmdit_status mmdit_rope_bwd(int32_t act, const mmdit_rope_cfg *cfg, int32_t batch, int32_t seq,
+                            int32_t head_dim, int32_t heads_q, const mmdit_rope_view *q,
+                            const mmdit_rope_view *q_out, int32_t heads_k, const mmdit_rope_view *k,
+                            const mmdit_rope_view *k_out, const int64_t *positions, int64_t pos_bstride,
+                            const float *cos, const float *sin, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

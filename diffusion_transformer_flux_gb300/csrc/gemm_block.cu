@@ -7,12 +7,16 @@
 // order, so the result is the same from call to call.
 //
 // block_pair_kernel (many rows): 256 x 256 output tiles on CTA pairs (tcgen05 cta_group::2), as in
-// gemm_pair.cuh: each CTA stages its 128 rows of A and 128 rows of B, 32 KB per slice.  A slice is 512
-// cycles of the pair's tensor cores.  Two TMEM buffers of 256 columns take the slices in turn; in the
-// 512 cycles that the tensor cores spend on one, eight warps read the other (a row and 128 columns per
-// thread), multiply by the slice's factor and add to 128 float32 registers per thread, two at a time
-// (fma.rn.f32x2).  The pair halves what each SM has to read of B, which is what a single CTA's 128 x 256
-// tile is bound by.
+// gemm_pair.cuh: each CTA stages its 128 rows of A and 128 rows of B, 32 KB per slice.  A slice's product
+// is 256 columns of TMEM, so two fit, and a buffer comes back to the MMA only after eight warps have read
+// it.  What bounds the kernel is that round trip (MMA, commit, TMEM loads, arrival at the leader: about
+// 2000 cycles for two slices of 512 each), so it is cut into halves of 128 columns with an MMA issuer, a
+// warpgroup and barriers of their own; the arrivals carry no release at cluster scope, the waits read no
+// timer, a warp's scales come through a ring of asynchronous copies, and the issuers run on whole warps.
+// Each promotion thread holds a row's 128 float32 sums in registers (setmaxnreg moves them over from the
+// other warpgroup).  8192^3: 493 us, 2.23 PFLOP/s; 4608 x 12288 x 4096 with bias: 225 us, 2.06 PFLOP/s
+// (the same loop without the multiply-adds: 420 and 196 us, without reading TMEM either: 332 and 156 us;
+// with one N = 256 MMA and barrier per slice 558 and 256 us).
 //
 // block_stream_kernel (few rows): B's bytes are the cost, so the roles are turned: 128 rows of B are the
 // MMA's M side and NT = 16 .. 128 rows of A its N side, and the CTAs of a cluster split K, so that every
@@ -30,26 +34,15 @@ namespace mmdit {
 namespace {
 
 constexpr int kSlice = 128;  // K of a scale block: 128 codes = one 128-byte swizzled row
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 4;  // more only spread the pairs apart in L2: 8192^3 takes 493 us with 4, 507 with 5, 514 with 6, 522 with 3
 constexpr int kPairStageBytes = 2 * kSlice * kSlice;  // this CTA's 128 rows of A and of B
-constexpr int kPairThreads = 128 + 512;               // producer, MMA issuer, two idle warps; 16 promotion warps
-constexpr int kPairRowB = 16 * 2 * 64;                // per promotion warp: two slices' factors of its columns
-constexpr int kPairSmem = kPairStages * kPairStageBytes + kPairRowB * 4 + 256 + 1024;
-// 640 threads start with 96 registers (61440); the promotion warpgroups take 112, the other one keeps 32
-constexpr int kPairFewRegs = 32, kPairManyRegs = 112;
-static_assert(128 * kPairFewRegs + 512 * kPairManyRegs <= kPairThreads * 96, "register shares");
+constexpr int kPairThreads = 128 + 256;               // producer, two MMA issuers, an idle warp; 8 promotion warps
+constexpr int kRing = 4, kRingFloats = 32 + 128;      // per promotion warp: slices whose scales are held, floats of one
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 8 * kRing * kRingFloats * 4 + 256 + 1024;
+// 384 threads start with 168 registers (64512); the promotion warpgroups take 232, the other one keeps 40
+constexpr int kPairFewRegs = 40, kPairManyRegs = 232;
+static_assert(128 * kPairFewRegs + 256 * kPairManyRegs <= kPairThreads * 168, "register shares");
 constexpr int kPairN = 256;
-
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
 
 // mbar_wait that tries the barrier a few hundred times before it first reads the timer: the waits here
 // recur every slice, and a timer read costs more than the slice's hand-over.
@@ -73,6 +66,14 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+
+// Four bytes copied to shared memory while the thread goes on; groups of them are awaited in order.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Moves registers between the warpgroups of a CTA: the sum of the shares is what the launch gave.
 template <int R>
@@ -124,13 +125,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* row_b = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes);  // [16 warps][2][64]
-  uint64_t* full = reinterpret_cast<uint64_t*>(row_b + kPairRowB);
+  float* rings = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes);  // [8 warps][kRing][kRingFloats]
+  uint64_t* full = reinterpret_cast<uint64_t*>(rings + 8 * kRing * kRingFloats);
   uint64_t* empty = full + kPairStages;
   uint64_t* pfull = empty + kPairStages;  // [buffer][half]
   uint64_t* pempty = pfull + 4;
   uint64_t* drain = pempty + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t rank = cluster_ctarank();
@@ -142,9 +143,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-    for (int b = 0; b < 4; ++b) mbar_init(&pfull[b], 1), mbar_init(&pempty[b], 16);
-    mbar_init(drain, 1);
+    for (int s = 0; s < kPairStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 2);
+    for (int b = 0; b < 4; ++b) mbar_init(&pfull[b], 1), mbar_init(&pempty[b], 8);
+    mbar_init(&drain[0], 1), mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
@@ -201,131 +202,134 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int s = 0; s < kPairStages; ++s)
           if (issued >> s & 1) mbar_wait(&full[s], parities >> s & 1, &never, a.status, 0);
       }
-    } else if (warp == 1 && leader) {
-      // ---------------- MMA issuer: slice `it` of this pair's walk into TMEM buffer it & 1, one half of
-      // the columns after the other
+    } else if ((warp == 1 || warp == 2) && leader) {
+      // ---------------- MMA issuers: slice `it` of this pair's walk into TMEM buffer it & 1, warp 1 + h
+      // for half h of the columns
+      const uint32_t h = static_cast<uint32_t>(warp - 1);
       int stage = 0;
       uint32_t phase = 0;
       uint32_t it = 0;
       bool ok = true;
       for (int tile = pair; ok && tile < tiles; tile += pairs) {
-        for (int kb = 0; ok && kb < num_kb; ++kb, ++it) {
-          const uint32_t b = it & 1, parity = ((it >> 1) & 1) ^ 1;
-          ok = warp_wait(&full[stage], phase, abort_flag, a.status);
+        for (int kb = 0; kb < num_kb; ++kb, ++it) {
+          const uint32_t b = it & 1;
+          ok = warp_wait(&full[stage], phase, abort_flag, a.status) &&
+               warp_wait(&pempty[2 * b + h], ((it >> 1) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
+          tc_fence_after();
+          // a descriptor's address field counts 16 bytes: a K step is 2
           const uint64_t da = sdesc_kmajor_sw128(smem_addr(smem + stage * kPairStageBytes));
-          const uint64_t db = sdesc_kmajor_sw128(smem_addr(smem + stage * kPairStageBytes + kSlice * kSlice));
+          const uint64_t db = sdesc_kmajor_sw128(smem_addr(smem + stage * kPairStageBytes + kSlice * kSlice + h * 64 * kSlice));
+          if (elect_one()) {
 #pragma unroll
-          for (uint32_t h = 0; h < 2; ++h) {
-            if (ok) ok = warp_wait(&pempty[2 * b + h], parity, abort_flag, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            // a descriptor's address field counts 16 bytes: a K step is 2, 64 rows are 512
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tc_mma_pair<kKindF8>(tmem + b * 256u + h * 128u, da + 2 * k, db + 2 * k + h * 512, kIdesc, k > 0 ? 1u : 0u);
-              tc_commit_pair_mc(&pfull[2 * b + h], 0x3);
-              if (h == 1) tc_commit_pair_mc(&empty[stage], 0x3);
-            }
-            __syncwarp();
+            for (int k = 0; k < 4; ++k)
+              tc_mma_pair<kKindF8>(tmem + b * 256u + h * 128u, da + 2 * k, db + 2 * k, kIdesc, k > 0 ? 1u : 0u);
+            tc_commit_pair_mc(&pfull[2 * b + h], 0x3);
+            tc_commit_pair_mc(&empty[stage], 0x3);
           }
-          if (!ok) break;
+          __syncwarp();
           if (++stage == kPairStages) stage = 0, phase ^= 1;
         }
       }
       if (*abort_flag) {
         int never = 0;
-        if (elect_one()) tc_commit_pair(drain);
+        if (elect_one()) tc_commit_pair(&drain[h]);
         __syncwarp();
-        mbar_wait(drain, 0, &never, a.status, 0);
+        mbar_wait(&drain[h], 0, &never, a.status, 0);
       }
     }
   } else {
     regs_more<kPairManyRegs>();
-    // ---------------- promotion: warp w reads TMEM lanes 32 (w % 4) .. (its row) and 64 columns, half
-    // h = g / 2 of each buffer, g its warp group
-    const int quarter = warp & 3, g = (warp - 4) >> 2, h = g >> 1;
+    // ---------------- promotion: warp w reads TMEM lanes 32 (w % 4) .. (its row) and the 128 columns of
+    // half h of each buffer, h its warpgroup
+    const int quarter = warp & 3, h = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t pempty_leader = mapa_shared(smem_addr(&pempty[h]), 0);
-    const uint32_t t_base = tmem + static_cast<uint32_t>(g * 64) + (static_cast<uint32_t>(quarter * 32) << 16);
-    float* my_row_b = row_b + (warp - 4) * 128;
+    const uint32_t t_base = tmem + static_cast<uint32_t>(h * 128) + (static_cast<uint32_t>(quarter * 32) << 16);
+    const float* my_ring = rings + (warp - 4) * kRing * kRingFloats;
+    const uint32_t ring = smem_addr(my_ring);
     uint32_t it = 0;
     bool ok = true;
     for (int tile = pair; tile < tiles; tile += pairs) {
       const int m = (tile % tiles_m) * 256 + static_cast<int>(rank) * 128 + row;
-      const int ng = (tile / tiles_m) * kPairN + g * 64;
+      const int ng = (tile / tiles_m) * kPairN + h * 128;
       const bool row_ok = m < a.M;
-      // the slice's factor 1 / (s_a s_b): the scales of slice kb + 2 are fetched while slice kb is
-      // taken out, those of kb + 1 are turned into a factor after it
+      // the scales of slice kb come through this warp's ring of kRing slots in shared memory, copied
+      // kRing - 1 slices ahead: lane l's row scale, and its column scales (the tile's one scale, or of
+      // columns l, l + 32, l + 64, l + 96)
       const float* pa = a.sa + (row_ok ? m : 0);
       const float* pb = ROW_B ? a.sb : a.sb + static_cast<int64_t>(ng < a.N ? ng >> 7 : 0) * a.sb_n;
       const int64_t b_step = ROW_B ? static_cast<int64_t>(a.N) : a.sb_k;
-      const int nb0 = ng + 2 * lane < a.N ? ng + 2 * lane : 0, nb1 = ng + 2 * lane + 1 < a.N ? ng + 2 * lane + 1 : 0;
-      uint64_t acc[32];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i] = 0;
-      float f, sa1, sb1 = 1.f, sb1x = 1.f;
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
       auto fetch = [&](int kb) {
-        if (kb >= num_kb) return;
-        sa1 = __ldg(pa + static_cast<int64_t>(kb) * a.M);
-        if constexpr (ROW_B) {
-          sb1 = __ldg(pb + kb * b_step + nb0), sb1x = __ldg(pb + kb * b_step + nb1);
-        } else {
-          sb1 = __ldg(pb + kb * b_step);
+        if (kb < num_kb) {
+          const uint32_t slot = ring + static_cast<uint32_t>((kb % kRing) * kRingFloats + lane) * 4u;
+          copy_async4(slot, pa + static_cast<int64_t>(kb) * a.M);
+#pragma unroll
+          for (int e = 0; e < (ROW_B ? 4 : 1); ++e) {
+            const int n = ROW_B ? ng + 32 * e + lane : 0;
+            copy_async4(slot + 128u * (1 + e), pb + kb * b_step + (n < a.N ? n : 0));
+          }
         }
+        copy_async_commit();
       };
-      auto factor = [&](uint32_t slot) {
-        if constexpr (ROW_B) {
-          f = fast_rcp(sa1);
-          *reinterpret_cast<float2*>(my_row_b + slot * 64 + 2 * lane) = make_float2(fast_rcp(sb1), fast_rcp(sb1x));
-          __syncwarp();
-        } else {
-          f = fast_rcp(sa1) * fast_rcp(sb1);
-        }
+      auto factor = [&](int kb) {
+        copy_async_wait<kRing - 2>();
+        const float* v = my_ring + (kb % kRing) * kRingFloats;
+        if constexpr (ROW_B) __syncwarp();  // the other lanes' columns
+        return ROW_B ? fast_rcp(v[lane]) : fast_rcp(v[lane]) * fast_rcp(v[32 + lane]);
       };
-      fetch(0);
-      factor(it & 1);
-      fetch(1);
+#pragma unroll
+      for (int i = 0; i < kRing - 1; ++i) fetch(i);
       for (int kb = 0; kb < num_kb; ++kb, ++it) {
         const uint32_t b = it & 1;
         if (ok) ok = warp_wait(&pfull[2 * b + h], (it >> 1) & 1, abort_flag, a.status);
         if (!ok) continue;
         tc_fence_after();
-        const uint64_t f2 = f32x2(f, f);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[32];
-          tmem_ld32_wait(t_base + b * 256u + static_cast<uint32_t>(c * 32), p);
-          if (c == 1) {  // this warp has read its part of the half buffer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote_relaxed(pempty_leader + b * 2 * static_cast<uint32_t>(sizeof(uint64_t)));
-          }
+        const uint32_t t = t_base + b * 256u;
+        uint32_t p0[32], p1[32];
+        tmem_ld32(t, p0);
+        tmem_ld32(t + 32u, p1);
+        const float f = factor(kb);  // while the loads are on their way
+        auto add = [&](int c, const uint32_t(&p)[32]) {
           if constexpr (ROW_B) {
-            const float4* rb = reinterpret_cast<const float4*>(my_row_b + b * 64 + c * 32);
+            const float4* rb = reinterpret_cast<const float4*>(my_ring + (kb % kRing) * kRingFloats + 32 + c * 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 w = rb[i];
-              acc[c * 16 + 2 * i] = ffma2(pack2(p[4 * i], p[4 * i + 1]), fmul2(f32x2(w.x, w.y), f2), acc[c * 16 + 2 * i]);
-              acc[c * 16 + 2 * i + 1] =
-                  ffma2(pack2(p[4 * i + 2], p[4 * i + 3]), fmul2(f32x2(w.z, w.w), f2), acc[c * 16 + 2 * i + 1]);
+              const float w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[c * 32 + 4 * i + e] = fmaf(__uint_as_float(p[4 * i + e]), fast_rcp(w4[e]) * f, acc[c * 32 + 4 * i + e]);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c * 16 + i] = ffma2(pack2(p[2 * i], p[2 * i + 1]), f2, acc[c * 16 + i]);
+            for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(p[i]), f, acc[c * 32 + i]);
           }
-        }
-        if (kb + 1 < num_kb) factor((it + 1) & 1);
-        fetch(kb + 2);
+        };
+        tmem_ld_deps64(p0, p1);
+        add(0, p0);
+        tmem_ld32(t + 64u, p0);
+        add(1, p1);
+        tmem_ld32(t + 96u, p1);
+        tmem_ld_deps64(p0, p1);
+        // this warp has read its part of the half buffer
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(pempty_leader + b * 2 * static_cast<uint32_t>(sizeof(uint64_t)));
+        add(2, p0);
+        add(3, p1);
+        fetch(kb + kRing - 1);
       }
       if (ok && row_ok) {
         TO* dst = static_cast<TO*>(a.out) + static_cast<int64_t>(m) * a.N;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 4; ++c) {
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) f32x2_split(acc[c * 16 + i], v[2 * i], v[2 * i + 1]);
+          for (int i = 0; i < 32; ++i) v[i] = acc[c * 32 + i];
           if (ng + c * 32 < a.N) store_row<TO>(dst, a.bias, ng + c * 32, a.N, v);
         }
       }

@@ -18,11 +18,17 @@
 // (the same loop without the multiply-adds: 420 and 196 us, without reading TMEM either: 332 and 156 us;
 // with one N = 256 MMA and barrier per slice 558 and 256 us).
 //
-// block_stream_kernel (few rows): B's bytes are the cost, so the roles are turned: 128 rows of B are the
-// MMA's M side and NT = 16 .. 128 rows of A its N side, and the CTAs of a cluster split K, so that every
-// SM streams its share of B through a ring of TMA stages.  The partial sums meet in shared memory of the
-// cluster (each CTA adds up its own columns, in rank order): no workspace, no atomics, the same bits
-// every time.
+// block_stream_kernel (tens of rows, or too few tiles for the pairs): B's bytes are the cost, so the roles are
+// turned: 128 rows of B are the MMA's M side and 32 or 64 rows of A its N side, four slices' products in TMEM,
+// and the CTAs of a cluster split K, so that every SM streams its share of B through a ring of TMA stages.  The
+// partial sums meet in shared memory of the cluster (each CTA adds up its own columns, in rank order): no
+// workspace, no atomics, the same bits every time.  48 x 4096 x 14336: 17.7 us, 3.4 TB/s; its fixed part (start,
+// first bytes, two cluster barriers) is 4 us.
+//
+// block_few_kernel (up to 16 rows): B streams through rings of asynchronous copies that every warp keeps for
+// itself, straight into the register layout of mma.sync.  At these sizes the tensor cores' rate does not count
+// and the latency does: no TMEM to allocate, no barrier and no cluster between the first copy and the sums.
+// 1 x 12288 x 4096: 11.2 us, 4.5 TB/s, of which 2 are the launch; 1 x 1024 x 1024: 2.2 us.
 //
 // Every wait is bounded (common.cuh); after one gives up the remaining barriers are still met, so no
 // thread is left behind.
@@ -70,6 +76,10 @@ __device__ __forceinline__ bool elect_one() {
 // Four bytes copied to shared memory while the thread goes on; groups of them are awaited in order.
 __device__ __forceinline__ void copy_async4(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or zeros where `ok` is false (the source is then not read).
+__device__ __forceinline__ void copy_async16(uint32_t dst, const uint8_t* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -349,9 +359,11 @@ template <int NT>
 struct StreamCfg {
   static constexpr int kStageBytes = kSlice * kSlice + NT * kSlice;
   static constexpr int kStages = 100 * 1024 / kStageBytes;      // two CTAs to an SM
-  static constexpr int kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr int kBufs = 4;                               // slices' products in TMEM
+  static constexpr int kTmemCols = kBufs * NT;
   static constexpr int kFacSlices = 8;                          // slices whose factors are held at a time
   static constexpr int kSmem = kStages * kStageBytes + 2 * kFacSlices * NT * 4 + 256 + 1024;
+  static_assert(NT == 32 || NT == 64, "columns of a tile");
   static_assert(NT * 128 * 4 <= kStages * kStageBytes, "the partial sums reuse the stage ring");
 };
 constexpr int kStreamThreads = 64 + 128;
@@ -370,8 +382,8 @@ __global__ void __launch_bounds__(kStreamThreads)
   uint64_t* full = reinterpret_cast<uint64_t*>(fac + 2 * kFac * NT);
   uint64_t* empty = full + Cfg::kStages;
   uint64_t* pfull = empty + Cfg::kStages;
-  uint64_t* pempty = pfull + 2;
-  uint64_t* drain = pempty + 2;
+  uint64_t* pempty = pfull + Cfg::kBufs;
+  uint64_t* drain = pempty + Cfg::kBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -385,7 +397,7 @@ __global__ void __launch_bounds__(kStreamThreads)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-    for (int b = 0; b < 2; ++b) mbar_init(&pfull[b], 1), mbar_init(&pempty[b], 4);
+    for (int b = 0; b < Cfg::kBufs; ++b) mbar_init(&pfull[b], 1), mbar_init(&pempty[b], 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -434,13 +446,13 @@ __global__ void __launch_bounds__(kStreamThreads)
         mbar_wait(&full[t % Cfg::kStages], static_cast<uint32_t>(t / Cfg::kStages) & 1u, &never, a.status, 0);
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer: slice i into TMEM buffer i & 1
+    // ---------------- MMA issuer: slice i into TMEM buffer i % kBufs
     int s = 0;
     uint32_t phase = 0;
     for (int i = 0; i < num; ++i) {
-      const int b = i & 1;
+      const int b = i % Cfg::kBufs;
       if (!wait(&full[s], phase)) break;
-      if (!wait(&pempty[b], (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u)) break;
+      if (!wait(&pempty[b], (static_cast<uint32_t>(i / Cfg::kBufs) & 1u) ^ 1u)) break;
       tc_fence_after();
       const uint64_t dw = sdesc_kmajor_sw128(smem_addr(smem + s * Cfg::kStageBytes));
       const uint64_t dx = sdesc_kmajor_sw128(smem_addr(smem + s * Cfg::kStageBytes + kSlice * kSlice));
@@ -484,7 +496,7 @@ __global__ void __launch_bounds__(kStreamThreads)
     if constexpr (ROW_B)
       if (n_ok && num > 0) sb_next = __ldg(a.sb + static_cast<int64_t>(kb0) * a.N + n0 + row);
     for (int i = 0; i < num; ++i) {
-      const int b = i & 1, slot = i % kFac, buf = (i / kFac) & 1;
+      const int b = i % Cfg::kBufs, slot = i % kFac, buf = (i / kFac) & 1;
       if (slot == 0) {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) fac[buf * kFac * NT + tp + u * 128] = next[u];
@@ -496,27 +508,37 @@ __global__ void __launch_bounds__(kStreamThreads)
         fr = fast_rcp(sb_next);
         if (n_ok && i + 1 < num) sb_next = __ldg(a.sb + static_cast<int64_t>(kb0 + i + 1) * a.N + n0 + row);
       }
-      if (ok) ok = wait(&pfull[b], static_cast<uint32_t>(i >> 1) & 1u);
+      if (ok) ok = wait(&pfull[b], static_cast<uint32_t>(i / Cfg::kBufs) & 1u);
       if (!ok) continue;
       tc_fence_after();
       const float* f = fac + (buf * kFac + slot) * NT;
+      const uint32_t t = t_base + static_cast<uint32_t>(b * NT);
+      auto add = [&](int c, const auto& p) {
 #pragma unroll
-      for (int c = 0; c < NT; c += 16) {
-        uint32_t p[16];
-        tmem_ld16_wait(t_base + static_cast<uint32_t>(b * NT + c), p);
-        if (c + 16 == NT) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&pempty[b]);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < static_cast<int>(sizeof(p) / 16); ++q) {
           const float4 w = *reinterpret_cast<const float4*>(f + c + 4 * q);
           const float w4[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             acc[c + 4 * q + e] = fmaf(__uint_as_float(p[4 * q + e]), ROW_B ? w4[e] * fr : w4[e], acc[c + 4 * q + e]);
         }
+      };
+      auto release = [&]() {  // this warp has read the buffer
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pempty[b]);
+      };
+      if constexpr (NT == 32) {
+        uint32_t p[32];
+        tmem_ld32_wait(t, p);
+        release();
+        add(0, p);
+      } else {
+        uint32_t p0[32], p1[32];
+        tmem_ld64_wait(t, p0, p1);
+        release();
+        add(0, p0);
+        add(32, p1);
       }
     }
   }
@@ -530,7 +552,7 @@ __global__ void __launch_bounds__(kStreamThreads)
     else
       *dst = v;
   };
-  const int tp = static_cast<int>(threadIdx.x) - 64, row = (warp & 3) * 32 + lane;
+  const int row = (warp & 3) * 32 + lane;
   if (splits == 1) {
     if (warp >= 2 && ok) {
 #pragma unroll
@@ -538,35 +560,163 @@ __global__ void __launch_bounds__(kStreamThreads)
     }
   } else {
     // CTA q of the cluster adds up columns [q cols, (q + 1) cols) of every CTA's partial sums, which
-    // the others write into its stage ring once all of them are done with theirs
-    const int cols = NT / splits;
+    // the others write into its stage ring once all of them are done with theirs: part [rank][cols / 4]
+    // [row][4], so that a warp's 16-byte stores and loads are contiguous
+    const int shift = __ffs(NT / splits) - 1, cols = 1 << shift;
     __syncthreads();
     cluster_sync();
     if (warp >= 2) {
-      const uint32_t base = smem_addr(smem);
+      const uint32_t base = smem_addr(smem) + static_cast<uint32_t>((rank << shift) * 512 + row * 16);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int q = t / cols, lc = t - q * cols;
-        const uint32_t dst = mapa_shared(base + static_cast<uint32_t>(((rank * cols + lc) * 128 + row) * 4), static_cast<uint32_t>(q));
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(acc[t]) : "memory");
+      for (int t = 0; t < NT; t += 4) {
+        const uint32_t dst = mapa_shared(base + static_cast<uint32_t>((t & (cols - 1)) * 512), static_cast<uint32_t>(t >> shift));
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(acc[t]), "f"(acc[t + 1]),
+                     "f"(acc[t + 2]), "f"(acc[t + 3])
+                     : "memory");
       }
     }
     cluster_sync();
     if (warp >= 2 && ok) {
-      const float* part = reinterpret_cast<const float*>(smem);
-      for (int lc = 0; lc < cols; ++lc) {
-        float v = 0.f;
-        for (int r = 0; r < splits; ++r) v += part[(r * cols + lc) * 128 + row];
-        put(m0 + rank * cols + lc, n0 + row, v);
+      const float4* part = reinterpret_cast<const float4*>(smem) + row;
+      for (int c = 0; c < cols; c += 4) {
+        float4 v = part[c * 32];
+        for (int r = 1; r < splits; ++r) {
+          const float4 w = part[((r << shift) + c) * 32];
+          v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        }
+        const int m = m0 + (rank << shift) + c;
+        put(m, n0 + row, v.x), put(m + 1, n0 + row, v.y), put(m + 2, n0 + row, v.z), put(m + 3, n0 + row, v.w);
       }
     }
   }
-  (void)tp;
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------------------------- a few rows
+// D (16 x 8, float32) += A (16 x 32) B (8 x 32)^T of E4M3 codes held in registers.
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A CTA computes 16 rows of B against up to 8 CT rows of A; its 8 warps take the slices of K in turn.  Lane
+// (g, q) = (lane / 4, lane % 4) of a warp copies 16 bytes at byte 16 q of both 64-byte halves of a slice, of
+// rows g and g + 8 of B and of rows g, g + 8, .. of A: the four words of a copy are the lane's fragments of two
+// MMAs, whose order along K is the same for both operands and otherwise free.  The copies land in a ring of
+// kStages slices per warp in shared memory, in the lane's own places: no lane reads another's, so the ring
+// needs no barrier, and every warp has kStages - 1 slices on their way while it works on one.  Three CTAs to
+// an SM (72 or 64 KB) measured best: at 1 x 12288 x 4096 three stages take 11.2 us, two 11.2, four 13.4; at 16
+// rows (CT = 2) two take 14.3, three 16.0.  D holds
+// rows g, g + 8 and columns 2 q, 2 q + 1.
+constexpr int kFewWarps = 8;
+constexpr int kFewMaxSlices = 256;  // the factors 1 / (s_a s_b) of all slices are formed once, in shared memory
+template <int CT>
+struct FewCfg {
+  static constexpr int kStages = CT == 1 ? 3 : 2;
+  static constexpr int kStageBytes = (4 + 2 * CT) * 512;  // 16-byte pieces of 32 lanes
+  static constexpr int kRingBytes = kFewWarps * kStages * kStageBytes;
+  static int smem(int num_kb) { return kRingBytes + num_kb * 8 * CT * 4; }
+};
+
+template <int CT, typename TO>
+__global__ void __launch_bounds__(32 * kFewWarps) block_few_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
+                                                                    int K, const BlockArgs a) {
+  using Cfg = FewCfg<CT>;
+  constexpr int kOut = 16 * 8 * CT;
+  extern __shared__ __align__(128) uint8_t few_smem[];
+  float* fac = reinterpret_cast<float*>(few_smem + Cfg::kRingBytes);  // [num_kb][8 CT]
+  static_assert(kFewWarps * kOut * 4 <= Cfg::kRingBytes, "the partial sums reuse the ring");
+  pdl_wait();
+  pdl_trigger();
+  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int n0 = blockIdx.x * 16;
+  const uint32_t ring = smem_addr(few_smem) + static_cast<uint32_t>(warp * Cfg::kStages * Cfg::kStageBytes + lane * 16);
+  const uint8_t* pb = B + static_cast<int64_t>(n0 + g) * K + 16 * q;
+  const uint8_t* pa = A + static_cast<int64_t>(g) * K + 16 * q;
+  const bool hi_ok = n0 + 8 < a.N;  // N is a multiple of 8: rows g are there
+  const int64_t row8 = static_cast<int64_t>(8) * K;
+  auto fetch = [&](int i) {  // this warp's i-th slice
+    const int kb = warp + i * kFewWarps;
+    if (kb < a.num_kb) {
+      const uint32_t dst = ring + static_cast<uint32_t>((i % Cfg::kStages) * Cfg::kStageBytes);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = kb * kSlice + 64 * h;
+        const bool ok = at + 16 * q < K;  // K is a multiple of 16
+        copy_async16(dst + h * 512u, ok ? pb + at : B, ok);
+        copy_async16(dst + (2 + h) * 512u, ok && hi_ok ? pb + row8 + at : B, ok && hi_ok);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const bool m_ok = ok && 8 * c + g < a.M;
+          copy_async16(dst + (4 + 2 * c + h) * 512u, m_ok ? pa + c * row8 + at : A, m_ok);
+        }
+      }
+    }
+    copy_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < Cfg::kStages - 1; ++i) fetch(i);
+  const float* sb = a.sb + static_cast<int64_t>(n0 >> 7) * a.sb_n;  // the rows of a CTA lie in one tile
+  for (int i = threadIdx.x; i < a.num_kb * 8 * CT; i += 32 * kFewWarps) {
+    const int kb = i / (8 * CT), m = i % (8 * CT);
+    fac[i] = m < a.M ? fast_rcp(__ldg(a.sa + static_cast<int64_t>(kb) * a.M + m)) * fast_rcp(__ldg(sb + kb * a.sb_k)) : 0.f;
+  }
+  __syncthreads();
+  float acc[CT][4];
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+  for (int i = 0, kb = warp; kb < a.num_kb; ++i, kb += kFewWarps) {
+    fetch(i + Cfg::kStages - 1);
+    copy_async_wait<Cfg::kStages - 1>();
+    const uint8_t* st = few_smem + (warp * Cfg::kStages + i % Cfg::kStages) * Cfg::kStageBytes + lane * 16;
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(st + j * 512);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x = *reinterpret_cast<const uint4*>(st + (4 + 2 * c + h) * 512);
+        mma_e4m3(d, w[h].x, w[2 + h].x, w[h].y, w[2 + h].y, x.x, x.y);
+        mma_e4m3(d, w[h].z, w[2 + h].z, w[h].w, w[2 + h].w, x.z, x.w);
+      }
+      const float2 f = *reinterpret_cast<const float2*>(fac + (kb * CT + c) * 8 + 2 * q);
+      acc[c][0] = fmaf(d[0], f.x, acc[c][0]), acc[c][1] = fmaf(d[1], f.y, acc[c][1]);
+      acc[c][2] = fmaf(d[2], f.x, acc[c][2]), acc[c][3] = fmaf(d[3], f.y, acc[c][3]);
+    }
+  }
+  // the warps' sums, added in warp order; entry (column, row)
+  copy_async_wait<0>();
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(few_smem);
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[warp * kOut + (8 * c + 2 * q + (e & 1)) * 16 + g + 8 * (e >> 1)] = acc[c][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kOut; i += 32 * kFewWarps) {
+    const int m = i / 16, n = n0 + i % 16;
+    if (m >= a.M || n >= a.N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int s = 0; s < kFewWarps; ++s) v += red[s * kOut + i];
+    if (a.bias) v += __bfloat162float(a.bias[n]);
+    TO* dst = static_cast<TO*>(a.out) + static_cast<int64_t>(m) * a.N + n;
+    if constexpr (sizeof(TO) == 2)
+      *dst = __float2bfloat16(v);
+    else
+      *dst = v;
   }
 }
 
@@ -638,19 +788,36 @@ cudaError_t run_stream(const BlockGemm& p, const BlockArgs& a, int splits, cudaS
   return cudaGetLastError();
 }
 
+template <int CT, typename TO>
+cudaError_t run_few(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream) {
+  auto kern = block_few_kernel<CT, TO>;
+  static Configured done;
+  cudaError_t e = configure(kern, FewCfg<CT>::smem(kFewMaxSlices), done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3((p.N + 15) / 16), dim3(32 * kFewWarps), FewCfg<CT>::smem(a.num_kb), stream, p.A, p.B, p.K, a);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
+}
+
+// Which kernel.  Few rows: up to 16 rows of A the weights' bytes and the launch are the cost (1 x 6144 x 4096:
+// 6.7 us against 9.4 in the stream kernel, 1 x 1024 x 1024: 2.2 against 4.8; at 32 rows a CTA would read twice as
+// much of A as of B, 22 us against 15 at 32 x 12288 x 4096).  Many rows: the pair kernel once its tiles occupy
+// about half of the pairs (32 tiles: 512 x 4096 x 4096 23 us against 25; 16 tiles: 256 x 4096 x 4096 23 against 18).
+// Between them the stream kernel, K split while two CTAs to an SM still hold every CTA of the launch (48 x 4096 x
+// 14336: 61, 35, 21, 18 us on 1, 2, 4, 8; 32 x 12288 x 4096, 96 tiles: 17.7, 15.0, 18.9 on 1, 2, 4).
 template <bool ROW_B, typename TO>
 cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream) {
-  if (p.M > 128) return run_pair<ROW_B, TO>(p, a, stream);
-  const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  if constexpr (!ROW_B)
+    if (p.M <= 16 && a.num_kb <= kFewMaxSlices && p.lda == p.K && p.ldb == p.K)
+      return p.M <= 8 ? run_few<1, TO>(p, a, stream) : run_few<2, TO>(p, a, stream);
+  const int64_t pair_tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + kPairN - 1) / kPairN);
+  if (pair_tiles >= num_sms() / 5) return run_pair<ROW_B, TO>(p, a, stream);
+  const int nt = p.M <= 32 ? 32 : 64;
   const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + nt - 1) / nt);
   int splits = 1;
-  while (splits < 8 && tiles * splits < num_sms() && 4 * splits <= a.num_kb) splits *= 2;
-  switch (nt) {
-    case 16: return run_stream<16, ROW_B, TO>(p, a, splits, stream);
-    case 32: return run_stream<32, ROW_B, TO>(p, a, splits, stream);
-    case 64: return run_stream<64, ROW_B, TO>(p, a, splits, stream);
-    default: return run_stream<128, ROW_B, TO>(p, a, splits, stream);
-  }
+  while (splits < 8 && 2 * splits <= a.num_kb && tiles * 2 * splits <= 2 * num_sms()) splits *= 2;
+  return nt == 32 ? run_stream<32, ROW_B, TO>(p, a, splits, stream) : run_stream<64, ROW_B, TO>(p, a, splits, stream);
 }
 
 }  // namespace

@@ -814,7 +814,7 @@ def _launch(name, dev, stream, *args):
     lib = _lib or load()
     # the raw handle of the current stream, without the Stream object torch.cuda.current_stream would build
     raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         status = getattr(lib, name)(*args, raw)
     else:
         with torch.cuda.device(dev):

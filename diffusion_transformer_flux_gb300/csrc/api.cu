@@ -2546,9 +2546,9 @@ mmdit_status mmdit_add_rmsnorm_fwd(int32_t act, int32_t res_f32, int32_t rows, i
 }
 
 size_t mmdit_add_rmsnorm_bwd_workspace_size(int32_t rows, int32_t dim) {
-  if (rows < 1 || dim < 1) return kStatusBytes;
+  if (rows < 1 || dim < 8 || dim % 8 != 0) return kStatusBytes;
   Carver c;
-  c.take(static_cast<size_t>(add_rmsnorm_bwd_blocks(rows)) * dim * sizeof(float));
+  c.take(static_cast<size_t>(add_rmsnorm_bwd_parts(rows, dim)) * dim * sizeof(float));
   return c.off;
 }
 
@@ -2766,6 +2766,7 @@ mmdit_status rope_call(int32_t act, const mmdit_rope_cfg* cfg, int32_t batch, in
   if (cfg->rot_dim > head_dim)
     return fail(MMDIT_ERR_INVALID_ARG, "rope: rot_dim %d exceeds head_dim %d", cfg->rot_dim, head_dim);
   if (static_cast<int64_t>(heads_q) + heads_k > 65536) return fail(MMDIT_ERR_UNSUPPORTED, "rope: more than 65536 heads");
+  if (batch > 65535) return fail(MMDIT_ERR_UNSUPPORTED, "rope: batch must be at most 65535 (got %d)", batch);
   if (static_cast<int64_t>(batch) * seq == 0) return MMDIT_OK;
   const bool tables = cos || sin;
   if (tables ? (!cos || !sin || positions) : !positions)

@@ -221,8 +221,8 @@ struct BlockGemm {
 cudaError_t launch_gemm_block(const BlockGemm& p, uint32_t* status, int clear_status, cudaStream_t stream);
 // rmsnorm.cu: h = x + res, y = h g / sqrt(mean(h^2) + eps), and its backward (see the file's header).
 // T is the activation type, the residual's type is fp32 with res_f32 (or act 0), else T.  dim a
-// multiple of 8, at most 16384; part: add_rmsnorm_bwd_blocks(rows) * dim floats (with dgain).
-int add_rmsnorm_bwd_blocks(int rows);
+// multiple of 8, at most 16384; part: add_rmsnorm_bwd_parts(rows, dim) * dim floats (with dgain).
+int add_rmsnorm_bwd_parts(int rows, int dim);
 cudaError_t launch_add_rmsnorm_fwd(int act, int res_f32, int rows, int dim, float eps, const void* x, int64_t ldx,
                                    const void* res, const void* gain, void* h, void* y, uint8_t* yq, float* sy,
                                    float* rstd, cudaStream_t stream);

@@ -22,16 +22,17 @@ namespace {
 
 constexpr int kNormMaxThreads = 512;
 
-// Sum over the CTA's threads, the same in every thread; `red` holds one float per warp, and the
-// caller alternates between two of them so that one barrier per call is enough.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// Sum over the blockDim.x threads of a row, the same in each of them.  `red` holds one float per warp of the
+// CTA; a caller with several sums alternates between two of them, so that one barrier per sum is enough.
+__device__ __forceinline__ float row_sum(float v, float* red) {
   v = warp_sum(v);
   const int warps = blockDim.x >> 5;
-  if (warps == 1) return v;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if (warps == 1) return v;  // blockDim.x a multiple of 32: the row is this warp
+  float* mine = red + threadIdx.y * warps;
+  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
   __syncthreads();
   float t = 0.f;
-  for (int i = 0; i < warps; ++i) t += red[i];
+  for (int i = 0; i < warps; ++i) t += mine[i];
   return t;
 }
 
@@ -54,10 +55,12 @@ struct NormFwdArgs {
 
 template <typename T, typename TR, int NC>
 __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_fwd_kernel(const NormFwdArgs a) {
-  __shared__ float red[2][kNormMaxThreads / 32];
+  __shared__ float red[kNormMaxThreads / 32];
   pdl_wait();
+  pdl_trigger();
   const int chunks = a.dim >> 3;
-  const int64_t row = blockIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool row_ok = row < a.rows;  // the rows behind the last take part in the barrier alone
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const TR* res = a.res ? static_cast<const TR*>(a.res) + row * a.dim : nullptr;
   float v[NC][8];
@@ -66,7 +69,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_fwd_kernel(const 
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
-    if (c < chunks) {
+    if (row_ok && c < chunks) {
       rx[i].load(x + 8 * c);
       if (res) rr[i].load(res + 8 * c);
     }
@@ -75,7 +78,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_fwd_kernel(const 
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
-    if (c < chunks) {
+    if (row_ok && c < chunks) {
       rx[i].to_f32(v[i]);
       if (res) {
         float w[8];
@@ -91,12 +94,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_fwd_kernel(const 
       for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
     }
   }
-  const float r = 1.f / sqrtf(block_sum(ss, red[0]) / static_cast<float>(a.dim) + a.eps);
-  if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
+  const float r = 1.f / sqrtf(row_sum(ss, red) / static_cast<float>(a.dim) + a.eps);
+  if (a.rstd && row_ok && threadIdx.x == 0) a.rstd[row] = r;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
-    const bool in = c < chunks;
+    const bool in = row_ok && c < chunks;
     if (in) {
       float g[8];
       load8(static_cast<const T*>(a.gain) + 8 * c, g);
@@ -128,75 +131,116 @@ struct NormBwdArgs {
   int rows, dim;
 };
 
-// CTA b takes rows b, b + gridDim.x, ... and keeps its share of dg in registers.
-template <typename T, typename TR, int NC>
-__global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
-  __shared__ float red[2][kNormMaxThreads / 32];
+// A CTA holds blockDim.y groups of blockDim.x threads; group k of all groups takes rows k, k + groups, ... and
+// keeps its share of dg in registers.  A row's operands stay packed as they were loaded while the row's sum is
+// formed (12 registers per 8 bf16 elements instead of 24 float32 ones) and the next row's are already on
+// their way, so two CTAs to an SM keep the memory busy: 4095 x 5120 bf16 in 32.8 us, 5.1 TB/s, the sums of dg and
+// their second kernel included (floats kept across the sum, no prefetch: 60 us).
+template <typename T, typename TR, int NC, int MAX>
+__global__ void __launch_bounds__(MAX, MAX <= 320 ? 2 : 1) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  __shared__ float red[2][MAX / 32];
+  __shared__ float sums[NC == 1 ? 2048 : 1];
   pdl_wait();
+  pdl_trigger();
   const int chunks = a.dim >> 3;
   const float inv_dim = 1.f / static_cast<float>(a.dim);
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * blockDim.y, group = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   float dg[NC][8];
 #pragma unroll
   for (int i = 0; i < NC; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[i][e] = 0.f;
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+  struct Row {
+    Raw8<T> dy[NC];
+    Raw8<TR> h[NC], in[NC];
+    float r;
+  };
+  auto load = [&](int64_t row, Row& x) {
+    if (row >= a.rows) return;
     const int64_t off = row * a.dim;
-    Raw8<T> rdy[NC];
-    Raw8<TR> rh[NC], rin[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
       if (c < chunks) {
-        rdy[i].load(static_cast<const T*>(a.dy) + off + 8 * c);
-        rh[i].load(static_cast<const TR*>(a.h) + off + 8 * c);
-        if (a.dh_in) rin[i].load(static_cast<const TR*>(a.dh_in) + off + 8 * c);
+        x.dy[i].load(static_cast<const T*>(a.dy) + off + 8 * c);
+        x.h[i].load(static_cast<const TR*>(a.h) + off + 8 * c);
+        if (a.dh_in) x.in[i].load(static_cast<const TR*>(a.dh_in) + off + 8 * c);
       }
     }
-    const float r = __ldg(a.rstd + row);
-    float av[NC][8], nv[NC][8];
+    x.r = __ldg(a.rstd + row);
+  };
+  Row cur, next;
+  load(group, cur);
+  int turn = 0;
+  // every group of a CTA makes the same number of turns: the row's sum is a barrier of the whole CTA
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.rows; base += groups, turn ^= 1) {
+    const int64_t row = base + threadIdx.y;
+    if constexpr (NC <= 2) load(row + groups, next);
     float dot = 0.f;
+    if (row < a.rows) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      if (c < chunks) {
-        float g[8], dy[8];
-        load8(static_cast<const T*>(a.gain) + 8 * c, g);
-        rdy[i].to_f32(dy);
-        rh[i].to_f32(nv[i]);
+      for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < chunks) {
+          float g[8], dy[8], n[8];
+          load8(static_cast<const T*>(a.gain) + 8 * c, g);
+          cur.dy[i].to_f32(dy);
+          cur.h[i].to_f32(n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          nv[i][e] *= r;
-          dg[i][e] = fmaf(dy[e], nv[i][e], dg[i][e]);
-          av[i][e] = dy[e] * g[e];
-          dot = fmaf(av[i][e], nv[i][e], dot);
+          for (int e = 0; e < 8; ++e) {
+            const float t = dy[e] * (n[e] * cur.r);
+            dg[i][e] += t;
+            dot = fmaf(t, g[e], dot);
+          }
         }
       }
     }
-    const float mean = block_sum(dot, red[turn]) * inv_dim;
+    const float mean = row_sum(dot, red[turn]) * inv_dim;
+    if (row < a.rows) {
+      const int64_t off = row * a.dim;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      if (c < chunks) {
-        float d[8], in[8];
-        if (a.dh_in) rin[i].to_f32(in);
+      for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < chunks) {
+          float g[8], dy[8], n[8], d[8];
+          load8(static_cast<const T*>(a.gain) + 8 * c, g);
+          cur.dy[i].to_f32(dy);
+          cur.h[i].to_f32(n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          d[e] = r * (av[i][e] - nv[i][e] * mean);
-          if (a.dh_in) d[e] += in[e];
+          for (int e = 0; e < 8; ++e) d[e] = cur.r * (dy[e] * g[e] - n[e] * cur.r * mean);
+          if (a.dh_in) {
+            float in[8];
+            cur.in[i].to_f32(in);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] += in[e];
+          }
+          store8(static_cast<TR*>(a.dh) + off + 8 * c, d);
+          if (a.dx) store8(static_cast<T*>(a.dx) + off + 8 * c, d);
         }
-        store8(static_cast<TR*>(a.dh) + off + 8 * c, d);
-        if (a.dx) store8(static_cast<T*>(a.dx) + off + 8 * c, d);
       }
+    }
+    if constexpr (NC <= 2)
+      cur = next;
+    else
+      load(row + groups, cur);
+  }
+  if (!a.part) return;
+  if constexpr (NC == 1) {
+    if (blockDim.y > 1) {  // the CTA's groups first, in order
+      float* mine = sums + (threadIdx.y * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mine[e] = dg[0][e];
+      __syncthreads();
+      if (threadIdx.y > 0) return;
+      for (int k = 1; k < static_cast<int>(blockDim.y); ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dg[0][e] += mine[k * blockDim.x * 8 + e];
     }
   }
-  if (a.part) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int c = threadIdx.x + i * blockDim.x;
-      if (c < chunks) store8(a.part + static_cast<int64_t>(blockIdx.x) * a.dim + 8 * c, dg[i]);
-    }
+  for (int i = 0; i < NC; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    if (c < chunks) store8(a.part + static_cast<int64_t>(blockIdx.x) * a.dim + 8 * c, dg[i]);
   }
 }
 
@@ -209,25 +253,47 @@ inline int norm_nc(int chunks, int most) {
   return 4;
 }
 
+// Rows to a CTA: short rows share one of 256 threads (16384 x 256 in CTAs of one warp: 10.6 us, of eight rows 6.2).
+inline int norm_rows(int threads) { return threads < 256 ? 256 / threads : 1; }
+
 template <typename T, typename TR>
 cudaError_t run_fwd(const NormFwdArgs& a, cudaStream_t stream) {
-  const int chunks = a.dim / 8, nc = norm_nc(chunks, 256), threads = norm_threads(chunks, nc);
+  const int chunks = a.dim / 8, nc = norm_nc(chunks, 256), threads = norm_threads(chunks, nc), rows = norm_rows(threads);
   auto kern = nc == 1 ? add_rmsnorm_fwd_kernel<T, TR, 1> : nc == 2 ? add_rmsnorm_fwd_kernel<T, TR, 2> : add_rmsnorm_fwd_kernel<T, TR, 4>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(a.rows)), dim3(threads), 0, stream, a);
+  return launch_pdl(kern, dim3(static_cast<unsigned>((a.rows + static_cast<int64_t>(rows) - 1) / rows)), dim3(threads, rows), 0,
+                    stream, a);
+}
+
+// The backward's launch: chunks per thread, threads of a row, rows of a CTA and CTAs: as many as stay resident
+// (four to an SM with one chunk per thread, two with two), each with its sums of dg.
+struct BwdShape {
+  int nc, threads, rows, grid;
+};
+BwdShape bwd_shape(int rows, int dim) {
+  BwdShape s;
+  const int chunks = dim / 8;
+  s.nc = chunks <= 256 ? 1 : chunks <= 2 * kNormMaxThreads ? 2 : 4;
+  s.threads = norm_threads(chunks, s.nc);
+  s.rows = norm_rows(s.threads);
+  const int ctas = (rows + s.rows - 1) / s.rows, most = (s.nc == 1 ? 4 : 2) * num_sms();
+  s.grid = ctas < most ? ctas : most;
+  return s;
 }
 
 template <typename T, typename TR>
-cudaError_t run_bwd(const NormBwdArgs& a, int grid, cudaStream_t stream) {
-  const int chunks = a.dim / 8, nc = norm_nc(chunks, 256), threads = norm_threads(chunks, nc);
-  auto kern = nc == 1 ? add_rmsnorm_bwd_kernel<T, TR, 1> : nc == 2 ? add_rmsnorm_bwd_kernel<T, TR, 2> : add_rmsnorm_bwd_kernel<T, TR, 4>;
-  return launch_pdl(kern, dim3(grid), dim3(threads), 0, stream, a);
+cudaError_t run_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t stream) {
+  auto kern = s.nc == 1                       ? add_rmsnorm_bwd_kernel<T, TR, 1, 256>
+              : s.nc == 2 && s.threads <= 256 ? add_rmsnorm_bwd_kernel<T, TR, 2, 256>
+              : s.nc == 2 && s.threads <= 320 ? add_rmsnorm_bwd_kernel<T, TR, 2, 320>
+              : s.nc == 2                     ? add_rmsnorm_bwd_kernel<T, TR, 2, kNormMaxThreads>
+                                              : add_rmsnorm_bwd_kernel<T, TR, 4, kNormMaxThreads>;
+  return launch_pdl(kern, dim3(s.grid), dim3(s.threads, s.rows), 0, stream, a);
 }
 
 }  // namespace
 
-int add_rmsnorm_bwd_blocks(int rows) {
-  const int most = 4 * num_sms();
-  return rows < most ? rows : most;
+int add_rmsnorm_bwd_parts(int rows, int dim) {
+  return bwd_shape(rows, dim).grid;
 }
 
 cudaError_t launch_add_rmsnorm_fwd(int act, int res_f32, int rows, int dim, float eps, const void* x, int64_t ldx,
@@ -247,14 +313,14 @@ cudaError_t launch_add_rmsnorm_bwd(int act, int res_f32, int rows, int dim, cons
                                    const void* gain, const float* rstd, const void* dh_in, void* dh, void* dx,
                                    float* dgain, float* part, cudaStream_t stream) {
   if (rows <= 0) return cudaSuccess;
-  const int grid = add_rmsnorm_bwd_blocks(rows);
+  const BwdShape s = bwd_shape(rows, dim);
   const NormBwdArgs a{dy, h, gain, rstd, dh_in, dh, dx, dgain ? part : nullptr, rows, dim};
-  cudaError_t e = act == 0 ? run_bwd<float, float>(a, grid, stream)
-                  : res_f32 ? run_bwd<__nv_bfloat16, float>(a, grid, stream)
-                            : run_bwd<__nv_bfloat16, __nv_bfloat16>(a, grid, stream);
+  cudaError_t e = act == 0 ? run_bwd<float, float>(a, s, stream)
+                  : res_f32 ? run_bwd<__nv_bfloat16, float>(a, s, stream)
+                            : run_bwd<__nv_bfloat16, __nv_bfloat16>(a, s, stream);
   if (e != cudaSuccess) return e;
   count_launch();
-  if (dgain) return launch_colsum_finish(part, grid, dim, dgain, stream);
+  if (dgain) return launch_colsum_finish(part, s.grid, dim, dgain, stream);
   return cudaGetLastError();
 }
 

@@ -11,12 +11,16 @@
 // angle (negative positions included); its upper 32 bits feed sincospi.  The frequencies' own rounding
 // (2^-53 relative, from the host's double) is then all that is left: 2^-36 of a turn at position 2^20.
 //
-// Bound by memory: each element read and written once.  A CTA takes TT tokens, its threads first form
-// the tokens' cos and sin in shared memory (once for all heads), then rotate all heads of q and k in
-// pieces of V elements per half (16-byte accesses for V = 8): interleaved pieces hold whole pairs;
-// half pieces are a run of V first elements and the V second ones.  V is the largest of 8, 4, 2, 1 that
-// divides rot_dim / 2.  A piece is read before it is written by the same thread, so the rotation may be
-// done in place.
+// Bound by memory: each element read and written once.  Thread (x, y, z) of a CTA takes piece x of heads y,
+// y + blockDim.y, ... of token z: interleaved pieces are 8 elements, half pieces a run of V first elements and the
+// V second ones, V the largest of 8, 4, 2, 1 that divides rot_dim / 2; the pieces behind rot_dim pass.  The first
+// heads' loads are on their way while the CTA forms its tokens' cos and sin in shared memory, once for all
+// heads.  A CTA holds as many heads as it has threads for, and more tokens where a token has few: 2 x 4608
+// tokens of 32 + 8 heads of 128, interleaved, in 32.8 us, 5.7 TB/s (a CTA that walks four tokens in turn: 75 us,
+// one list of items with divided indices: 51, 64-bit divisions of the token alone: 41).  A piece is read before it is written by the same thread, so the rotation may be done
+// in place.
+#include <algorithm>
+
 #include "../../include/mmdit.h"
 #include "internal.h"
 #include "rowwise.cuh"
@@ -24,7 +28,8 @@
 namespace mmdit {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;     // of a CTA where a head has at most as many pieces
+constexpr int kRopeMaxThreads = 512;  // head_dim 512 with V = 1 has up to 511
 
 template <int P>
 struct RopeTurns {
@@ -37,7 +42,6 @@ struct RopeArgs {
   const int64_t* pos;
   int64_t pos_bstride;
   const float *cos, *sin;  // [batch, seq, pairs] tables, or null
-  int64_t tokens;          // batch * seq
   int seq, head_dim, rot_dim;
   float mscale, sign;      // sign -1 for the gradient
 };
@@ -74,98 +78,137 @@ __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
   }
 }
 
-template <typename T, int V, bool INTER, int P>
-__global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const RopeArgs a, const __grid_constant__ RopeTurns<P> turns,
-                                                                  int tt) {
-  extern __shared__ float table[];  // [tt][2][pairs]
-  pdl_wait();
-  const int pairs = a.rot_dim >> 1;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tt;
-  const int n_tok = a.tokens - t0 < tt ? static_cast<int>(a.tokens - t0) : tt;
-  for (int i = threadIdx.x; i < n_tok * pairs; i += kRopeThreads) {
-    const int t = i / pairs, j = i - t * pairs;
-    const int64_t tok = t0 + t;
-    float c, s;
-    if (a.cos) {
-      c = __ldg(a.cos + tok * pairs + j), s = __ldg(a.sin + tok * pairs + j);
-    } else {
-      const int64_t b = tok / a.seq;
-      const int64_t p = __ldg(a.pos + b * a.pos_bstride + (tok - b * a.seq));
-      const uint64_t phase = static_cast<uint64_t>(p) * turns.f[j];
-      // the signed fraction of a turn in half turns: [-1, 1)
-      sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);
-    }
-    table[(2 * t) * pairs + j] = c * a.mscale;
-    table[(2 * t + 1) * pairs + j] = s * a.mscale * a.sign;
-  }
-  __syncthreads();
-  // pieces of a head: rotated ones, then the ones that pass
-  const int turned = INTER ? (a.rot_dim + V - 1) / V : pairs / V;
-  const int per_head = turned + (INTER ? a.head_dim / V - turned : (a.head_dim - a.rot_dim) / V);
-  const int heads = a.heads[0] + a.heads[1];
-  const int items = n_tok * heads * per_head;
-  for (int i = threadIdx.x; i < items; i += kRopeThreads) {
-    const int hh = i / per_head, piece = i - hh * per_head;
-    const int t = hh / heads, h0 = hh - t * heads;
-    const int which = h0 >= a.heads[0];
-    const int h = which ? h0 - a.heads[0] : h0;
-    const int64_t tok = t0 + t, b = tok / a.seq, s = tok - b * a.seq;
-    const mmdit_rope_view &vi = a.in[which], &vo = a.out[which];
-    const T* src = static_cast<const T*>(vi.ptr) + b * vi.stride_b + s * vi.stride_s + h * vi.stride_h;
-    T* dst = static_cast<T*>(vo.ptr) + b * vo.stride_b + s * vo.stride_s + h * vo.stride_h;
-    const float* cs = table + (2 * t) * pairs;
-    const float* sn = cs + pairs;
-    float x[V];
-    if constexpr (INTER) {
-      load_v<T, V>(src + piece * V, x);
+// A piece as loaded: packed for the 16-byte ones, so that several fit a thread's registers.
+template <typename T, int V>
+struct Piece {
+  float v[V];
+  __device__ __forceinline__ void load(const T* p) { load_v<T, V>(p, v); }
+  __device__ __forceinline__ void to_f32(float (&x)[V]) const {
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        const int j = piece * (V / 2) + e;
-        if (j < pairs) {
-          const float u = x[2 * e], w = x[2 * e + 1];
-          x[2 * e] = u * cs[j] - w * sn[j];
-          x[2 * e + 1] = u * sn[j] + w * cs[j];
+    for (int i = 0; i < V; ++i) x[i] = v[i];
+  }
+};
+template <>
+struct Piece<__nv_bfloat16, 8> : Raw8<__nv_bfloat16> {};
+
+template <typename T, int V, bool INTER, int P>
+__global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_apply_kernel(const RopeArgs a, const __grid_constant__ RopeTurns<P> turns) {
+  extern __shared__ float table[];  // [tokens of the CTA][2][stride]
+  constexpr int kU = INTER ? 4 : 2;          // heads in flight
+  constexpr int kPairs = INTER ? V / 2 : V;  // pairs of a piece
+  pdl_wait();
+  pdl_trigger();
+  const int pairs = a.rot_dim >> 1, stride = (pairs + 3) & ~3;
+  const int b = blockIdx.y, s0 = blockIdx.x * blockDim.z, s = s0 + threadIdx.z;  // the grid is (token groups, batch)
+  const int piece = threadIdx.x, turned = INTER ? (a.rot_dim + V - 1) / V : pairs / V;
+  const bool turn = piece < turned;
+  const int at = INTER || turn ? piece * V : a.rot_dim + (piece - turned) * V;
+  // where head 0 of q (and of k, as far before it as q has heads) has this piece
+  const int hq = a.heads[0];
+  auto base = [&](const mmdit_rope_view& v, int before) {
+    return static_cast<T*>(v.ptr) + b * v.stride_b + s * v.stride_s - before * v.stride_h + at;
+  };
+  const T *src_q = base(a.in[0], 0), *src_k = base(a.in[1], hq);
+  T *dst_q = base(a.out[0], 0), *dst_k = base(a.out[1], hq);
+  const int heads = s < a.seq ? hq + a.heads[1] : 0;
+  const float* cs = table + 2 * threadIdx.z * stride + piece * kPairs;
+  const float* sn = cs + stride;
+  for (int h0 = threadIdx.y, first = 1; first || h0 < heads; h0 += kU * blockDim.y, first = 0) {
+    Piece<T, V> x[kU], y[INTER ? 1 : kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int h = h0 + u * blockDim.y;
+      if (h < heads) {
+        const T* p = h < hq ? src_q + h * a.in[0].stride_h : src_k + h * a.in[1].stride_h;
+        x[u].load(p);
+        if constexpr (!INTER)
+          if (turn) y[u].load(p + pairs);
+      }
+    }
+    if (first) {
+      const int threads = blockDim.x * blockDim.y * blockDim.z;
+      const int tid = (threadIdx.z * blockDim.y + threadIdx.y) * blockDim.x + threadIdx.x;
+      for (int i = tid; i < static_cast<int>(blockDim.z) * pairs; i += threads) {
+        const int t = i / pairs, j = i - t * pairs;
+        if (s0 + t >= a.seq) break;
+        float c, w;
+        if (a.cos) {
+          const int64_t row = (static_cast<int64_t>(b) * a.seq + s0 + t) * pairs + j;
+          c = __ldg(a.cos + row), w = __ldg(a.sin + row);
+        } else {
+          const int64_t pos = __ldg(a.pos + b * a.pos_bstride + s0 + t);
+          const uint64_t phase = static_cast<uint64_t>(pos) * turns.f[j];
+          // the signed fraction of a turn in half turns: [-1, 1)
+          sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &w, &c);
+        }
+        table[2 * t * stride + j] = c * a.mscale;
+        table[(2 * t + 1) * stride + j] = w * a.mscale * a.sign;
+      }
+      __syncthreads();
+    }
+    // the piece's cos and sin: in registers for all heads where they are few, else read at each use (16 more
+    // registers would cost a quarter of the resident CTAs)
+    float c[kPairs], n[kPairs];
+    if (INTER && turn) {
+      load_v<float, kPairs>(cs, c);
+      load_v<float, kPairs>(sn, n);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int h = h0 + u * blockDim.y;
+      if (h >= heads) continue;
+      T* out = h < hq ? dst_q + h * a.out[0].stride_h : dst_k + h * a.out[1].stride_h;
+      float v[V], w[V];
+      x[u].to_f32(v);
+      if (turn) {
+        if constexpr (INTER) {
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            if (piece * kPairs + e < pairs) {  // the last piece may end behind rot_dim
+              const float p = v[2 * e], q = v[2 * e + 1];
+              v[2 * e] = p * c[e] - q * n[e], v[2 * e + 1] = p * n[e] + q * c[e];
+            }
+          }
+        } else {
+          y[u].to_f32(w);
+          load_v<float, kPairs>(cs, c);
+          load_v<float, kPairs>(sn, n);
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            const float p = v[e], q = w[e];
+            v[e] = p * c[e] - q * n[e], w[e] = p * n[e] + q * c[e];
+          }
+          store_v<T, V>(out + pairs, w);
         }
       }
-      store_v<T, V>(dst + piece * V, x);
-    } else if (piece < turned) {
-      float y[V];
-      load_v<T, V>(src + piece * V, x);
-      load_v<T, V>(src + pairs + piece * V, y);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float c = cs[piece * V + e], w = sn[piece * V + e];
-        const float u = x[e];
-        x[e] = u * c - y[e] * w;
-        y[e] = u * w + y[e] * c;
-      }
-      store_v<T, V>(dst + piece * V, x);
-      store_v<T, V>(dst + pairs + piece * V, y);
-    } else {
-      const int at = a.rot_dim + (piece - turned) * V;
-      load_v<T, V>(src + at, x);
-      store_v<T, V>(dst + at, x);
+      store_v<T, V>(out, v);
     }
   }
 }
 
 template <typename T, int P>
-cudaError_t run_rope(const mmdit_rope_cfg& cfg, const RopeArgs& a, cudaStream_t stream) {
+cudaError_t run_rope(const mmdit_rope_cfg& cfg, const RopeArgs& a, int batch, cudaStream_t stream) {
   RopeTurns<P> turns;
   const int pairs = cfg.rot_dim / 2;
   for (int j = 0; j < P; ++j) turns.f[j] = j < pairs ? cfg.turns[j] : 0;
-  // A CTA per token while they are few; four tokens to a CTA once every SM has its fill
-  const int tt = a.tokens >= 32 * static_cast<int64_t>(num_sms()) ? 4 : 1;
-  const int64_t grid = (a.tokens + tt - 1) / tt;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const int v = pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : pairs % 2 == 0 ? 2 : 1;
   auto kern = cfg.interleaved ? rope_apply_kernel<T, 8, true, P>
               : v == 8        ? rope_apply_kernel<T, 8, false, P>
               : v == 4        ? rope_apply_kernel<T, 4, false, P>
               : v == 2        ? rope_apply_kernel<T, 2, false, P>
                               : rope_apply_kernel<T, 1, false, P>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kRopeThreads),
-                    static_cast<size_t>(tt) * 2 * pairs * sizeof(float), stream, a, turns, tt);
+  // pieces of a head, heads of a CTA (each thread takes as many as it keeps in flight) and tokens of a CTA,
+  // one while there are too few of them to fill the SMs
+  const int turned = cfg.interleaved ? (cfg.rot_dim + 7) / 8 : pairs / v;
+  const int pieces = cfg.interleaved ? a.head_dim / 8 : turned + (a.head_dim - cfg.rot_dim) / v;
+  const int heads = a.heads[0] + a.heads[1], most = kRopeThreads / pieces > 0 ? kRopeThreads / pieces : 1;
+  const int flight = cfg.interleaved ? 4 : 2, per = (heads + flight - 1) / flight, y = per < most ? per : most;
+  const int64_t tokens = static_cast<int64_t>(batch) * a.seq;
+  int64_t z = kRopeThreads / (pieces * y);
+  z = std::max<int64_t>(1, std::min<int64_t>({z, 8, a.seq, tokens / (4 * num_sms())}));
+  const dim3 grid(static_cast<unsigned>((a.seq + z - 1) / z), static_cast<unsigned>(batch));
+  return launch_pdl(kern, grid, dim3(pieces, y, static_cast<unsigned>(z)),
+                    static_cast<size_t>(z) * 2 * ((pairs + 3) / 4 * 4) * sizeof(float), stream, a, turns);
 }
 
 }  // namespace
@@ -177,13 +220,13 @@ cudaError_t launch_rope_apply(int act, const mmdit_rope_cfg& cfg, int batch, int
   RopeArgs a;
   for (int i = 0; i < 2; ++i) a.in[i] = in[i], a.out[i] = out[i], a.heads[i] = heads[i];
   a.pos = pos, a.pos_bstride = pos_bstride, a.cos = cos, a.sin = sin;
-  a.tokens = static_cast<int64_t>(batch) * seq, a.seq = seq, a.head_dim = head_dim, a.rot_dim = cfg.rot_dim;
+  a.seq = seq, a.head_dim = head_dim, a.rot_dim = cfg.rot_dim;
   a.mscale = cfg.mscale, a.sign = transposed ? -1.f : 1.f;
-  if (a.tokens == 0 || heads[0] + heads[1] == 0) return cudaSuccess;
+  if (batch == 0 || seq == 0 || heads[0] + heads[1] == 0) return cudaSuccess;
   // the frequencies travel as a kernel argument: 512 bytes for the usual heads, 2 KB for wide ones
   const bool few = cfg.rot_dim <= 128;
-  const cudaError_t e = act == 1 ? (few ? run_rope<__nv_bfloat16, 64>(cfg, a, stream) : run_rope<__nv_bfloat16, 256>(cfg, a, stream))
-                                 : (few ? run_rope<float, 64>(cfg, a, stream) : run_rope<float, 256>(cfg, a, stream));
+  const cudaError_t e = act == 1 ? (few ? run_rope<__nv_bfloat16, 64>(cfg, a, batch, stream) : run_rope<__nv_bfloat16, 256>(cfg, a, batch, stream))
+                                 : (few ? run_rope<float, 64>(cfg, a, batch, stream) : run_rope<float, 256>(cfg, a, batch, stream));
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();

@@ -805,7 +805,7 @@ mmdit_status mmdit_rope_config(mmdit_rope_cfg *cfg, int32_t rot_dim, int32_t int
  * the same for all; any sign, exact far into a context) or from tables cos, sin [batch, seq,
  * rot_dim / 2] fp32, 16-byte aligned, as rope3d_freqs writes them: exactly one of the two.  cfg and the
  * views are host memory.  head_dim a multiple of 8, at most 512, >= cfg->rot_dim; float32 arithmetic.
- * batch * seq == 0 is a no-op.  No workspace. */
+ * batch at most 65535; batch * seq == 0 is a no-op.  No workspace. */
 typedef struct mmdit_rope_view {
   void *ptr;
   int64_t stride_b, stride_s, stride_h;

@@ -409,6 +409,9 @@ def rope_check(got, x, cos, sin, rot, inter, mscale, transposed, act):
     (1, 9, 2, 1, 256, 256, True, "bf16", "by_parts", 10 ** 9, False),
     (1, 3, 1, 1, 512, 512, False, "f32", "linear", (1 << 40) + 7, True),
     (1, 6, 2, 1, 128, 64, True, "bf16", "none", -20, False),
+    (1, 5, 9, 3, 512, 510, False, "bf16", "none", 3, False),    # the most pieces to a head
+    (2, 3, 1, 1, 512, 2, False, "f32", "none", 3, True),
+    (1, 2, 70, 10, 64, 64, True, "bf16", "none", 11, True),
     (5, 1000, 2, 1, 64, 64, False, "bf16", "none", 0, True),    # four tokens to a CTA
 ])
 def test_rope(B, S, Hq, Hk, d, rot, inter, act, scaling, start, head_major):

@@ -115,7 +115,8 @@ def test_workspace_sizes(lib):
     assert floor <= L.mmdit_fp8_block_linear_bwd_workspace_size(M, N, 512) <= floor + 256 * 6
     assert L.mmdit_fp8_block_linear_bwd_workspace_size(0, N, 512) == 256
     assert L.mmdit_add_rmsnorm_bwd_workspace_size(0, 64) == 256
-    assert L.mmdit_add_rmsnorm_bwd_workspace_size(3, 64) == 256 + 3 * 64 * 4
+    # at least one CTA's sums of dgain, at most one row's per row
+    assert 256 + 64 * 4 <= L.mmdit_add_rmsnorm_bwd_workspace_size(3, 64) <= 256 + 3 * 64 * 4
     assert L.mmdit_add_rmsnorm_bwd_workspace_size(1 << 20, 4096) < 64 << 20
 
 
@@ -166,7 +167,7 @@ def _rope(lib, fn="mmdit_rope_fwd", act=1, cfg="ok", batch=1, seq=4, d=64, hq=2,
     (INVALID, dict(q=None)), (INVALID, dict(qo=None)), (INVALID, dict(ko=None)), (INVALID, dict(k=None)),
     (INVALID, dict(q=(A + 8, 512, 128, 64))), (INVALID, dict(q=(A, 512, 128, 60))), (INVALID, dict(qo=(B_, 512, -128, 64))),
     (INVALID, dict(qo=(A, 512, 64, 256))), (INVALID, dict(pos=None)), (INVALID, dict(cos=E_, sin=F_)),
-    (INVALID, dict(pos=None, cos=E_)), (INVALID, dict(pb=-4)), (UNSUPPORTED, dict(hq=65536, hk=1)),
+    (INVALID, dict(pos=None, cos=E_)), (INVALID, dict(pb=-4)), (UNSUPPORTED, dict(hq=65536, hk=1)), (UNSUPPORTED, dict(batch=65536)),
     (INVALID, dict(pos=E_ + 4)), (INVALID, dict(pos=None, cos=E_ + 2, sin=F_)),
 ])
 def test_rope_refusals(lib, fn, status, kw):

@@ -50,6 +50,12 @@ constexpr int kPairFewRegs = 40, kPairManyRegs = 232;
 static_assert(128 * kPairFewRegs + 256 * kPairManyRegs <= kPairThreads * 168, "register shares");
 constexpr int kPairN = 256;
 
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // mbar_wait that tries the barrier a few hundred times before it first reads the timer: the waits here
 // recur every slice, and a timer read costs more than the slice's hand-over.
 __device__ __forceinline__ bool slice_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
@@ -127,8 +133,8 @@ __device__ __forceinline__ void store_row(TO* dst, const __nv_bfloat16* bias, in
 }
 
 // ----------------------------------------------------------------------------- many rows
-template <bool ROW_B, typename TO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+template <bool ROW_B, typename TO, int SPLITS>
+__global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThreads, 1)
     block_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                       const __grid_constant__ BlockArgs a) {
   constexpr uint32_t kIdesc = make_idesc<kKindF8>(256, 128);
@@ -144,13 +150,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const uint32_t rank = cluster_ctarank();
+  // a cluster is SPLITS (1 or 2) pairs, which share a tile's K: CTA `rank` of pair `part`
+  const uint32_t cta = cluster_ctarank(), rank = cta & 1, lead = SPLITS > 1 ? cta & ~1u : 0;
+  const uint16_t both = static_cast<uint16_t>(3u << lead);
+  const int part = SPLITS > 1 ? static_cast<int>(cta >> 1) : 0;
   const bool leader = rank == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int num_kb = a.num_kb;
+  const int first = (a.num_kb + SPLITS - 1) / SPLITS;  // slices of pair 0
+  const int kb0 = part * first, num_kb = part ? a.num_kb - first : first;
   const int tiles_m = (a.M + 255) / 256, tiles_n = (a.N + kPairN - 1) / kPairN;
   const int tiles = tiles_m * tiles_n;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int pair = blockIdx.x / (2 * SPLITS), pairs = gridDim.x / (2 * SPLITS);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 2);
@@ -181,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_b);
       }
-      const uint32_t full_leader = mapa_shared(smem_addr(full), 0);
+      const uint32_t full_leader = mapa_shared(smem_addr(full), lead);
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued = 0, parities = 0;  // bit s: stage s was filled, and with which parity last
@@ -196,9 +206,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const uint32_t bar = full_leader + static_cast<uint32_t>(stage * sizeof(uint64_t));
           if (elect_one()) {
             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
-            tma_load_2d_pair(st, &tm_a, bar, kb * kSlice, m0);
-            tma_load_2d_pair(st + kSlice * kSlice, &tm_b, bar, kb * kSlice, n0);
-            tma_load_2d_pair(st + kSlice * kSlice + 64 * kSlice, &tm_b, bar, kb * kSlice, n0 + 128);
+            tma_load_2d_pair(st, &tm_a, bar, (kb0 + kb) * kSlice, m0);
+            tma_load_2d_pair(st + kSlice * kSlice, &tm_b, bar, (kb0 + kb) * kSlice, n0);
+            tma_load_2d_pair(st + kSlice * kSlice + 64 * kSlice, &tm_b, bar, (kb0 + kb) * kSlice, n0 + 128);
           }
           __syncwarp();
           issued |= 1u << stage;
@@ -234,8 +244,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tc_mma_pair<kKindF8>(tmem + b * 256u + h * 128u, da + 2 * k, db + 2 * k, kIdesc, k > 0 ? 1u : 0u);
-            tc_commit_pair_mc(&pfull[2 * b + h], 0x3);
-            tc_commit_pair_mc(&empty[stage], 0x3);
+            tc_commit_pair_mc(&pfull[2 * b + h], both);
+            tc_commit_pair_mc(&empty[stage], both);
           }
           __syncwarp();
           if (++stage == kPairStages) stage = 0, phase ^= 1;
@@ -248,15 +258,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         mbar_wait(&drain[h], 0, &never, a.status, 0);
       }
     }
+    if constexpr (SPLITS > 1) {  // the promotion warps' two cluster barriers
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     regs_more<kPairManyRegs>();
     // ---------------- promotion: warp w reads TMEM lanes 32 (w % 4) .. (its row) and the 128 columns of
     // half h of each buffer, h its warpgroup
     const int quarter = warp & 3, h = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;
-    const uint32_t pempty_leader = mapa_shared(smem_addr(&pempty[h]), 0);
+    const uint32_t pempty_leader = mapa_shared(smem_addr(&pempty[h]), lead);
     const uint32_t t_base = tmem + static_cast<uint32_t>(h * 128) + (static_cast<uint32_t>(quarter * 32) << 16);
-    const float* my_ring = rings + (warp - 4) * kRing * kRingFloats;
+    float* my_ring = rings + (warp - 4) * kRing * kRingFloats;
     const uint32_t ring = smem_addr(my_ring);
     uint32_t it = 0;
     bool ok = true;
@@ -267,9 +282,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // the scales of slice kb come through this warp's ring of kRing slots in shared memory, copied
       // kRing - 1 slices ahead: lane l's row scale, and its column scales (the tile's one scale, or of
       // columns l, l + 32, l + 64, l + 96)
-      const float* pa = a.sa + (row_ok ? m : 0);
-      const float* pb = ROW_B ? a.sb : a.sb + static_cast<int64_t>(ng < a.N ? ng >> 7 : 0) * a.sb_n;
+      const float* pa = a.sa + static_cast<int64_t>(kb0) * a.M + (row_ok ? m : 0);
       const int64_t b_step = ROW_B ? static_cast<int64_t>(a.N) : a.sb_k;
+      const float* pb = a.sb + kb0 * b_step + (ROW_B ? 0 : static_cast<int64_t>(ng < a.N ? ng >> 7 : 0) * a.sb_n);
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -287,9 +302,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       };
       auto factor = [&](int kb) {
         copy_async_wait<kRing - 2>();
-        const float* v = my_ring + (kb % kRing) * kRingFloats;
-        if constexpr (ROW_B) __syncwarp();  // the other lanes' columns
-        return ROW_B ? fast_rcp(v[lane]) : fast_rcp(v[lane]) * fast_rcp(v[32 + lane]);
+        float* v = my_ring + (kb % kRing) * kRingFloats;
+        if constexpr (ROW_B) {  // the columns' reciprocals, once for the warp's 32 rows
+#pragma unroll
+          for (int e = 1; e < 5; ++e) v[32 * e + lane] = fast_rcp(v[32 * e + lane]);
+          __syncwarp();
+          return fast_rcp(v[lane]);
+        }
+        return fast_rcp(v[lane]) * fast_rcp(v[32 + lane]);
       };
 #pragma unroll
       for (int i = 0; i < kRing - 1; ++i) fetch(i);
@@ -309,10 +329,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 w = rb[i];
-              const float w4[4] = {w.x, w.y, w.z, w.w};
+              float w4[4];  // the two factors' products, two at a time
+              f32x2_split(fmul2(f32x2(w.x, w.y), f32x2(f, f)), w4[0], w4[1]);
+              f32x2_split(fmul2(f32x2(w.z, w.w), f32x2(f, f)), w4[2], w4[3]);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                acc[c * 32 + 4 * i + e] = fmaf(__uint_as_float(p[4 * i + e]), fast_rcp(w4[e]) * f, acc[c * 32 + 4 * i + e]);
+                acc[c * 32 + 4 * i + e] = fmaf(__uint_as_float(p[4 * i + e]), w4[e], acc[c * 32 + 4 * i + e]);
             }
           } else {
 #pragma unroll
@@ -333,8 +355,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         add(3, p1);
         fetch(kb + kRing - 1);
       }
-      if (ok && row_ok) {
-        TO* dst = static_cast<TO*>(a.out) + static_cast<int64_t>(m) * a.N;
+      TO* dst = static_cast<TO*>(a.out) + static_cast<int64_t>(m) * a.N;
+      if constexpr (SPLITS > 1) {
+        // The pairs' partial sums meet in the CTAs' stage rings, once both pairs are done with their own: pair q
+        // adds up half q of the tile's columns, [pair][column / 4][row][4], in pair order.  (A cluster that
+        // splits K has one tile.)
+        cluster_sync();
+        const uint32_t at = smem_addr(smem) + static_cast<uint32_t>(part * 65536 + row * 16);
+        const uint32_t owner = mapa_shared(at, static_cast<uint32_t>(2 * h) + rank);
+#pragma unroll
+        for (int j = 0; j < 128; j += 4)
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(owner + j * 512u), "f"(acc[j]), "f"(acc[j + 1]),
+                       "f"(acc[j + 2]), "f"(acc[j + 3])
+                       : "memory");
+        cluster_sync();
+        const float4* in = reinterpret_cast<const float4*>(smem) + row;
+#pragma unroll 1
+        for (int c = h * 64; c < h * 64 + 64; c += 32) {  // this warpgroup's half of the pair's columns
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 t = in[(c / 4 + i) * 128], w = in[4096 + (c / 4 + i) * 128];
+            v[4 * i] = t.x + w.x, v[4 * i + 1] = t.y + w.y, v[4 * i + 2] = t.z + w.z, v[4 * i + 3] = t.w + w.w;
+          }
+          const int n = (tile / tiles_m) * kPairN + part * 128 + c;
+          if (ok && row_ok && n < a.N) store_row<TO>(dst, a.bias, n, a.N, v);
+        }
+      } else if (ok && row_ok) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v[32];
@@ -745,18 +792,38 @@ bool code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, int64
   return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, stride, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool ROW_B, typename TO>
-cudaError_t run_pair(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream) {
+template <bool ROW_B, typename TO, int SPLITS>
+cudaError_t run_pair(const BlockGemm& p, const BlockArgs& a, int64_t tiles, cudaStream_t stream) {
   CUtensorMap ta, tb;
   if (!code_map(&ta, p.A, p.M, p.K, p.lda, 128) || !code_map(&tb, p.B, p.N, p.K, p.ldb, 64)) return cudaErrorInvalidValue;
-  auto kern = block_pair_kernel<ROW_B, TO>;
+  auto kern = block_pair_kernel<ROW_B, TO, SPLITS>;
   static Configured done;
   cudaError_t e = configure(kern, kPairSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + kPairN - 1) / kPairN);
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  const int pairs = static_cast<int>(tiles < num_sms() / 2 ? tiles : num_sms() / 2);
-  e = launch_pdl(kern, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, stream, ta, tb, a);
+  const int most = num_sms() / (2 * SPLITS);
+  const unsigned clusters = static_cast<unsigned>(tiles < most ? tiles : most);
+  e = launch_pdl(kern, dim3(2 * SPLITS * clusters), dim3(kPairThreads), kPairSmem, stream, ta, tb, a);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
+}
+
+// launch_pdl with clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster), attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_next_launch() ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -771,21 +838,8 @@ cudaError_t run_stream(const BlockGemm& p, const BlockArgs& a, int splits, cudaS
   static Configured done;
   cudaError_t e = configure(kern, Cfg::kSmem, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits), attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(splits, (p.N + 127) / 128, (p.M + NT - 1) / NT);
-  cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_next_launch() ? 2 : 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kern, ta, tb, a)) != cudaSuccess) return e;
-  count_launch();
-  return cudaGetLastError();
+  return launch_cluster(kern, dim3(splits, (p.N + 127) / 128, (p.M + NT - 1) / NT), splits, kStreamThreads, Cfg::kSmem, stream,
+                        ta, tb, a);
 }
 
 template <int CT, typename TO>
@@ -803,7 +857,10 @@ cudaError_t run_few(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
 // Which kernel.  Few rows: up to 16 rows of A the weights' bytes and the launch are the cost (1 x 6144 x 4096:
 // 6.7 us against 9.4 in the stream kernel, 1 x 1024 x 1024: 2.2 against 4.8; at 32 rows a CTA would read twice as
 // much of A as of B, 22 us against 15 at 32 x 12288 x 4096).  Many rows: the pair kernel once its tiles occupy
-// about half of the pairs (32 tiles: 512 x 4096 x 4096 23 us against 25; 16 tiles: 256 x 4096 x 4096 23 against 18).
+// about half of the pairs (32 tiles: 512 x 4096 x 4096 23 us against 25; 16 tiles: 256 x 4096 x 4096 23 against 18),
+// two pairs to a tile where all of them have a place and K is long (512 x 4096 x 14336: 37 us against 63, x 4096:
+// 17.2 against 22.8; 1000 x 1024 x 1024, 8 slices: 12.1 against 10.8; four pairs, clusters of 8, leave SMs idle: 50),
+// which pays from 16 tiles on if none of them is half empty (256 x 4096 x 14336: 37 us, in the stream kernel 43).
 // Between them the stream kernel, K split while two CTAs to an SM still hold every CTA of the launch (48 x 4096 x
 // 14336: 61, 35, 21, 18 us on 1, 2, 4, 8; 32 x 12288 x 4096, 96 tiles: 17.7, 15.0, 18.9 on 1, 2, 4).
 template <bool ROW_B, typename TO>
@@ -812,7 +869,10 @@ cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
     if (p.M <= 16 && a.num_kb <= kFewMaxSlices && p.lda == p.K && p.ldb == p.K)
       return p.M <= 8 ? run_few<1, TO>(p, a, stream) : run_few<2, TO>(p, a, stream);
   const int64_t pair_tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + kPairN - 1) / kPairN);
-  if (pair_tiles >= num_sms() / 5) return run_pair<ROW_B, TO>(p, a, stream);
+  if (pair_tiles > INT32_MAX) return cudaErrorInvalidValue;
+  const bool split = 4 * pair_tiles <= num_sms() && a.num_kb >= 16;
+  if (pair_tiles >= num_sms() / 5 || (split && p.M > 128 && pair_tiles >= num_sms() / 10))
+    return split ? run_pair<ROW_B, TO, 2>(p, a, pair_tiles, stream) : run_pair<ROW_B, TO, 1>(p, a, pair_tiles, stream);
   const int nt = p.M <= 32 ? 32 : 64;
   const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + nt - 1) / nt);
   int splits = 1;

@@ -46,6 +46,10 @@ struct Raw8<__nv_bfloat16> {
     v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
     v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
   }
+  __device__ __forceinline__ float at(int e) const {  // element e (a constant once unrolled)
+    const uint32_t w = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
+    return e & 1 ? bf16_hi(w) : bf16_lo(w);
+  }
 };
 template <>
 struct Raw8<float> {
@@ -56,6 +60,11 @@ struct Raw8<float> {
   }
   __device__ __forceinline__ void to_f32(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ float at(int e) const {
+    const float4& q = e < 4 ? a : b;
+    const int k = e & 3;
+    return k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
   }
 };
 

@@ -252,7 +252,7 @@ def sum_tol(a, b, slices):
 LINEAR_SHAPES = [(1, 8, 16), (1, 128, 128), (2, 136, 144), (4, 264, 1040), (5, 256, 128), (16, 120, 272), (17, 384, 2064),
                  (33, 136, 400), (64, 256, 4096), (65, 128, 528), (100, 520, 144), (128, 256, 256), (129, 264, 272),
                  (255, 8, 1024), (256, 256, 128), (300, 776, 656), (513, 1024, 384), (3, 24, 33024), (9, 8, 160),
-                 (12, 1040, 2000), (2100, 1288, 272)]
+                 (12, 1040, 2000), (2100, 1288, 272), (513, 2600, 2064), (300, 2056, 2176)]
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR_SHAPES)
@@ -311,7 +311,7 @@ def test_linear_extreme_scales():
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 8, 16), (16, 128, 128), (100, 136, 272), (129, 264, 400), (300, 776, 656),
-                                   (520, 128, 1040), (40, 600, 128)])
+                                   (520, 128, 1040), (40, 600, 128), (2100, 1288, 1360)])
 def test_linear_gradients(M, N, K):
     rng, x, w, _, _, wq, sw = linear_operands(M + N * 5 + K, M, N, K)
     ldm, ldn = (M + 15) // 16 * 16, (N + 15) // 16 * 16

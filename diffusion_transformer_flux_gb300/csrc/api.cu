@@ -2534,7 +2534,7 @@ mmdit_status mmdit_add_rmsnorm_fwd(int32_t act, int32_t res_f32, int32_t rows, i
   if (h && !residual) return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: h needs a residual (without one it is x)");
   if (!y && !y_q) return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: neither y nor y_q is given");
   if ((y_q == nullptr) != (s_y == nullptr)) return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: y_q and s_y go together");
-  if (y == x || y == residual || h == x || (h && h == y))
+  if ((y && (y == x || y == residual)) || (h && (h == x || h == y)) || (y_q && (y_q == x || y_q == residual || y_q == y || y_q == h)))
     return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm: only h may alias an input, and only the residual");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   pdl_begin_call();
@@ -2563,6 +2563,7 @@ mmdit_status mmdit_add_rmsnorm_bwd(int32_t act, int32_t res_f32, int32_t rows, i
     return fail(MMDIT_ERR_INVALID_ARG, "RMSNorm backward: dh_in, dx or dgain is not 16-byte aligned");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (rows == 0) {
+    MMDIT_CUDA(cudaMemsetAsync(workspace, 0, 4, st), "status clear");
     if (dgain) MMDIT_CUDA(cudaMemsetAsync(dgain, 0, static_cast<size_t>(dim) * sizeof(float), st), "dgain clear");
     return MMDIT_OK;
   }
@@ -2573,7 +2574,7 @@ mmdit_status mmdit_add_rmsnorm_bwd(int32_t act, int32_t res_f32, int32_t rows, i
   pdl_begin_call();
   ProfScope ps_("add_rmsnorm_bwd", st);
   MMDIT_CUDA(launch_add_rmsnorm_bwd(act, res_f32 ? 1 : 0, rows, dim, dy, h, gain, rstd, dh_in, dh, dx, dgain,
-                                    at<float>(workspace, kStatusBytes), st),
+                                    at<float>(workspace, kStatusBytes), status_word(workspace), st),
              "RMSNorm backward");
   return MMDIT_OK;
 }
@@ -2606,8 +2607,8 @@ static mmdit_status check_block_linear(int32_t M, int32_t N, int32_t K, const ch
   if (M < 0 || N < 1 || K < 1) return fail(MMDIT_ERR_INVALID_ARG, "%s: bad shape M=%d N=%d K=%d", what, M, N, K);
   if (N % 8 != 0 || K % 16 != 0)
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: N must be a multiple of 8 and K of 16 (N=%d, K=%d)", what, N, K);
-  if (M > (1 << 30) || N > (1 << 23) || K > (1 << 23))
-    return fail(MMDIT_ERR_UNSUPPORTED, "%s: M must be at most 2^30, N and K at most 2^23", what);
+  if (M > (1 << 30) || N > (1 << 22) || K > (1 << 22))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: M must be at most 2^30, N and K at most 2^22", what);
   return MMDIT_OK;
 }
 
@@ -2766,7 +2767,8 @@ mmdit_status rope_call(int32_t act, const mmdit_rope_cfg* cfg, int32_t batch, in
   if (cfg->rot_dim > head_dim)
     return fail(MMDIT_ERR_INVALID_ARG, "rope: rot_dim %d exceeds head_dim %d", cfg->rot_dim, head_dim);
   if (static_cast<int64_t>(heads_q) + heads_k > 65536) return fail(MMDIT_ERR_UNSUPPORTED, "rope: more than 65536 heads");
-  if (batch > 65535) return fail(MMDIT_ERR_UNSUPPORTED, "rope: batch must be at most 65535 (got %d)", batch);
+  if (batch > 65535 || seq > (1 << 30))
+    return fail(MMDIT_ERR_UNSUPPORTED, "rope: batch must be at most 65535 and seq at most 2^30 (got %d, %d)", batch, seq);
   if (static_cast<int64_t>(batch) * seq == 0) return MMDIT_OK;
   const bool tables = cos || sin;
   if (tables ? (!cos || !sin || positions) : !positions)
@@ -2787,6 +2789,8 @@ mmdit_status rope_call(int32_t act, const mmdit_rope_cfg* cfg, int32_t batch, in
     mmdit_status s = check_view(vi[i], unit, i ? "k" : "q");
     if (s != MMDIT_OK || (s = check_view(vo[i], unit, i ? "k_out" : "q_out")) != MMDIT_OK) return s;
     in[i] = *vi[i], out[i] = *vo[i];
+    if ((batch > 1 && out[i].stride_b == 0) || (seq > 1 && out[i].stride_s == 0) || (heads[i] > 1 && out[i].stride_h == 0))
+      return fail(MMDIT_ERR_INVALID_ARG, "rope: a stride of %s is zero: its elements would share an address", i ? "k_out" : "q_out");
     if (in[i].ptr == out[i].ptr && (in[i].stride_b != out[i].stride_b || in[i].stride_s != out[i].stride_s ||
                                     in[i].stride_h != out[i].stride_h))
       return fail(MMDIT_ERR_INVALID_ARG, "rope: in place needs the same strides");

@@ -221,14 +221,14 @@ struct BlockGemm {
 cudaError_t launch_gemm_block(const BlockGemm& p, uint32_t* status, int clear_status, cudaStream_t stream);
 // rmsnorm.cu: h = x + res, y = h g / sqrt(mean(h^2) + eps), and its backward (see the file's header).
 // T is the activation type, the residual's type is fp32 with res_f32 (or act 0), else T.  dim a
-// multiple of 8, at most 16384; part: add_rmsnorm_bwd_parts(rows, dim) * dim floats (with dgain).
+// multiple of 8, at most 16384; part: add_rmsnorm_bwd_parts(rows, dim) * dim floats (with dgain); the backward clears *status.
 int add_rmsnorm_bwd_parts(int rows, int dim);
 cudaError_t launch_add_rmsnorm_fwd(int act, int res_f32, int rows, int dim, float eps, const void* x, int64_t ldx,
                                    const void* res, const void* gain, void* h, void* y, uint8_t* yq, float* sy,
                                    float* rstd, cudaStream_t stream);
 cudaError_t launch_add_rmsnorm_bwd(int act, int res_f32, int rows, int dim, const void* dy, const void* h,
                                    const void* gain, const float* rstd, const void* dh_in, void* dh, void* dx,
-                                   float* dgain, float* part, cudaStream_t stream);
+                                   float* dgain, float* part, uint32_t* status, cudaStream_t stream);
 // rope_apply.cu: q and k (in[0], in[1]: [batch, seq, heads, head_dim] at the views' strides) rotated
 // into out; cos/sin tables [batch, seq, rot_dim / 2] or null (then positions pos[b * pos_bstride + s]).
 cudaError_t launch_rope_apply(int act, const mmdit_rope_cfg& cfg, int batch, int seq, int head_dim,

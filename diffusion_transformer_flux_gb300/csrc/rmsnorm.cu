@@ -128,6 +128,7 @@ struct NormBwdArgs {
   const void* dh_in;
   void *dh, *dx;
   float* part;  // [gridDim.x, dim], or null
+  uint32_t* status;  // cleared
   int rows, dim;
 };
 
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(MAX, MAX <= 320 ? 2 : 1) add_rmsnorm_bwd_kerne
   __shared__ float sums[NC == 1 ? 2048 : 1];
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0) *a.status = 0;
   const int chunks = a.dim >> 3;
   const float inv_dim = 1.f / static_cast<float>(a.dim);
   const int64_t groups = static_cast<int64_t>(gridDim.x) * blockDim.y, group = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -311,10 +313,10 @@ cudaError_t launch_add_rmsnorm_fwd(int act, int res_f32, int rows, int dim, floa
 
 cudaError_t launch_add_rmsnorm_bwd(int act, int res_f32, int rows, int dim, const void* dy, const void* h,
                                    const void* gain, const float* rstd, const void* dh_in, void* dh, void* dx,
-                                   float* dgain, float* part, cudaStream_t stream) {
+                                   float* dgain, float* part, uint32_t* status, cudaStream_t stream) {
   if (rows <= 0) return cudaSuccess;
   const BwdShape s = bwd_shape(rows, dim);
-  const NormBwdArgs a{dy, h, gain, rstd, dh_in, dh, dx, dgain ? part : nullptr, rows, dim};
+  const NormBwdArgs a{dy, h, gain, rstd, dh_in, dh, dx, dgain ? part : nullptr, status, rows, dim};
   cudaError_t e = act == 0 ? run_bwd<float, float>(a, s, stream)
                   : res_f32 ? run_bwd<__nv_bfloat16, float>(a, s, stream)
                             : run_bwd<__nv_bfloat16, __nv_bfloat16>(a, s, stream);

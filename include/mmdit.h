@@ -745,7 +745,8 @@ mmdit_status mmdit_fp8_block_cast(int32_t act, int32_t square, int32_t rows, int
  *   ceil(K/128)] (128 x 128 tiles); b [N] bf16 or NULL; y [M, N] bf16, or fp32 with y_f32 != 0.
  * Each slice is summed on the tensor cores in float32 and scaled into float32 sums in a fixed order:
  * the same bits from call to call.  1 / (s_x s_w) has to be finite in float32 (the amax of the two
- * tiles multiply to less than 6e43).  N a multiple of 8, K of 16; M == 0 is a no-op.
+ * tiles multiply to less than 6e43).  N a multiple of 8, K of 16, both at most 2^22; M at most 2^30, M == 0
+ * is a no-op.
  * workspace >= mmdit_fp8_block_linear_workspace_size(M, N, K) (the status word). */
 size_t mmdit_fp8_block_linear_workspace_size(int32_t M, int32_t N, int32_t K);
 mmdit_status mmdit_fp8_block_linear_fwd(int32_t M, int32_t N, int32_t K, const void *x, const float *s_x,
@@ -761,7 +762,8 @@ mmdit_status mmdit_fp8_block_linear_fwd(int32_t M, int32_t N, int32_t K, const v
  *   transposed codes and scales of x (square = 0, q_t, s_t);
  *   db = column sums of dy [N] fp32 (NULL: not computed), fixed order.
  * ldn, ldm: N, M rounded up to 16.  Written, not accumulated; deterministic.  N a multiple of 8, K of
- * 16; M == 0 zeroes dw and db.
+ * 16; M == 0 zeroes dw and db.  The casts of dy live in the workspace: calls that share one are ordered on
+ * one stream.
  * workspace >= mmdit_fp8_block_linear_bwd_workspace_size(M, N, K). */
 size_t mmdit_fp8_block_linear_bwd_workspace_size(int32_t M, int32_t N, int32_t K);
 mmdit_status mmdit_fp8_block_linear_bwd(int32_t M, int32_t N, int32_t K, const void *dy, const void *w_t,
@@ -801,11 +803,11 @@ mmdit_status mmdit_rope_config(mmdit_rope_cfg *cfg, int32_t rot_dim, int32_t int
  * [batch, seq, heads, head_dim] of type `act` at ptr + b stride_b + s stride_s + h stride_h + i
  * (strides in elements, multiples of 16 bytes, >= 0): token-major, head-major and packed q|k|v layouts
  * alike.  An output may be the input itself (same ptr and strides: in place) and must not overlap it
- * otherwise.  Angles come from positions [batch, seq] int64 (pos_bstride elements between samples, 0:
+ * otherwise; its strides may be zero only where the extent is one.  Angles come from positions [batch, seq] int64 (pos_bstride elements between samples, 0:
  * the same for all; any sign, exact far into a context) or from tables cos, sin [batch, seq,
  * rot_dim / 2] fp32, 16-byte aligned, as rope3d_freqs writes them: exactly one of the two.  cfg and the
  * views are host memory.  head_dim a multiple of 8, at most 512, >= cfg->rot_dim; float32 arithmetic.
- * batch at most 65535; batch * seq == 0 is a no-op.  No workspace. */
+ * batch at most 65535, seq at most 2^30; batch * seq == 0 is a no-op.  No workspace. */
 typedef struct mmdit_rope_view {
   void *ptr;
   int64_t stride_b, stride_s, stride_h;

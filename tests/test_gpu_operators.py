@@ -84,6 +84,25 @@ def test_norm(rows, dim, act, res):
         check(lm.decode(q.cpu().numpy()), v, np.maximum(np.abs(v) * 2.0 ** -4, 2.0 ** -10) + (stat + 8 * U) * np.abs(v), "codes")
 
 
+@pytest.mark.parametrize("res", [None, "bf16", "f32"])
+@pytest.mark.parametrize("outputs", ["y", "q", "yq", "h", "hq", "hyq"])
+def test_norm_output_sets(res, outputs):
+    """Every set of outputs that may be asked for gives what the full set gives."""
+    if res is None and "h" in outputs:
+        pytest.skip("h needs a residual")
+    rng = np.random.default_rng(8)
+    x, gain = make(rng, (5, 272)), make(rng, (272,))
+    r = None if res is None else make(rng, (5, 272), DT[res])
+    full = dict(h=None if r is None else nans(5, 272, dtype=r.dtype), y=nans(5, 272, dtype=torch.bfloat16), y_q=bytes_(5, 272),
+                s_y=nans(3, 5), rstd=nans(5))
+    L.mmdit_add_rmsnorm_fwd(x, gain, residual=r, **full)
+    names = ["y"] if outputs == "h" else []  # h beside y
+    names += [n for c, ns in (("h", ["h"]), ("y", ["y"]), ("q", ["y_q", "s_y"])) if c in outputs for n in ns]
+    some = {n: torch.full_like(full[n], 0xAA if n == "y_q" else float("nan")) for n in names}
+    L.mmdit_add_rmsnorm_fwd(x, gain, residual=r, **some)
+    assert all(torch.equal(some[n], full[n]) for n in names)
+
+
 def test_norm_strided_rows_in_place_residual():
     rng = np.random.default_rng(3)
     wide = make(rng, (9, 3 * 256))

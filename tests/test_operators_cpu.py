@@ -29,7 +29,7 @@ def _norm(lib, act=1, res_f32=0, rows=4, dim=256, eps=1e-6, x=A, ldx=None, res=B
     (INVALID, dict(eps=float("nan"))), (INVALID, dict(ldx=128)), (INVALID, dict(ldx=260)), (INVALID, dict(x=None)),
     (INVALID, dict(x=A + 8)), (INVALID, dict(gain=None)), (INVALID, dict(res=B_ + 4)), (INVALID, dict(h=D_ + 2)),
     (INVALID, dict(res=None)), (INVALID, dict(y=None)), (INVALID, dict(y_q=F_)), (INVALID, dict(s_y=F_)),
-    (INVALID, dict(y=A)), (INVALID, dict(y=B_)), (INVALID, dict(h=A)), (INVALID, dict(h=E_)),
+    (INVALID, dict(y=A)), (INVALID, dict(y=B_)), (INVALID, dict(y_q=A, s_y=F_)), (INVALID, dict(y_q=E_, s_y=F_)), (INVALID, dict(h=A)), (INVALID, dict(h=E_)),
 ])
 def test_norm_refusals(lib, status, kw):
     assert _norm(lib, **kw) == status and "RMSNorm" in L.last_error()
@@ -79,7 +79,7 @@ def _linear(lib, M=4, N=128, K=256, x=A, s_x=0x1004, w=B_, s_w=0x2004, b=None, y
 
 @pytest.mark.parametrize("status,kw", [
     (INVALID, dict(M=-1)), (INVALID, dict(N=0)), (INVALID, dict(K=0)), (UNSUPPORTED, dict(N=12)),
-    (UNSUPPORTED, dict(K=120)), (UNSUPPORTED, dict(M=(1 << 30) + 1)), (UNSUPPORTED, dict(N=(1 << 23) + 8)),
+    (UNSUPPORTED, dict(K=120)), (UNSUPPORTED, dict(M=(1 << 30) + 1)), (UNSUPPORTED, dict(N=(1 << 22) + 8)), (UNSUPPORTED, dict(K=(1 << 22) + 16)),
     (INVALID, dict(x=None)), (INVALID, dict(x=A + 8)), (INVALID, dict(w=None)), (INVALID, dict(y=C_ + 2)),
     (INVALID, dict(s_x=None)), (INVALID, dict(s_w=None)), (INVALID, dict(b=D_ + 2)), (WORKSPACE, dict(ws=None)),
     (WORKSPACE, dict(ws_bytes=255)), (WORKSPACE, dict(ws=F_ + 128)),
@@ -168,6 +168,8 @@ def _rope(lib, fn="mmdit_rope_fwd", act=1, cfg="ok", batch=1, seq=4, d=64, hq=2,
     (INVALID, dict(q=(A + 8, 512, 128, 64))), (INVALID, dict(q=(A, 512, 128, 60))), (INVALID, dict(qo=(B_, 512, -128, 64))),
     (INVALID, dict(qo=(A, 512, 64, 256))), (INVALID, dict(pos=None)), (INVALID, dict(cos=E_, sin=F_)),
     (INVALID, dict(pos=None, cos=E_)), (INVALID, dict(pb=-4)), (UNSUPPORTED, dict(hq=65536, hk=1)), (UNSUPPORTED, dict(batch=65536)),
+    (UNSUPPORTED, dict(seq=(1 << 30) + 1)), (INVALID, dict(qo=(B_, 512, 0, 64))), (INVALID, dict(batch=2, ko=(D_, 0, 64, 64))),
+    (INVALID, dict(qo=(B_, 512, 128, 0))),
     (INVALID, dict(pos=E_ + 4)), (INVALID, dict(pos=None, cos=E_ + 2, sin=F_)),
 ])
 def test_rope_refusals(lib, fn, status, kw):

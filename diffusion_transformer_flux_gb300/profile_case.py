@@ -9,6 +9,10 @@
     python -m diffusion_transformer_flux_gb300.profile_case modulation --jobs 4
     python -m diffusion_transformer_flux_gb300.profile_case blockwise_linear --m 4608 --n 12288 --k 3072
     python -m diffusion_transformer_flux_gb300.profile_case mxfp8_linear --m 4608 --n 12288 --k 3072
+    python -m diffusion_transformer_flux_gb300.profile_case block_linear --m 4608 --n 12288 --k 4096
+    python -m diffusion_transformer_flux_gb300.profile_case block_linear_bwd --m 4095 --n 4096 --k 4096
+    python -m diffusion_transformer_flux_gb300.profile_case add_rmsnorm --m 4608 --k 4096
+    python -m diffusion_transformer_flux_gb300.profile_case rope --batch 2 --seq 4608
 
 Inputs are drawn on the device (N(0,1) activations, N(0,0.02) weights); the case runs
 --iters times and exits 0 only if every kernel finished its waits.
@@ -37,7 +41,8 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["attention", "double_block", "single_block", "linear", "double_block_bwd",
                                      "fp8_attention", "head_loss", "modulation", "blockwise_linear",
-                                     "mxfp8_linear"])
+                                     "mxfp8_linear", "block_linear", "block_linear_bwd", "block_cast", "add_rmsnorm",
+                                     "add_rmsnorm_bwd", "rope"])
     ap.add_argument("--jobs", type=int, default=4)
     ap.add_argument("--batch", type=int, default=1)
     ap.add_argument("--seq", type=int, default=4608)
@@ -90,6 +95,43 @@ def main():
         x, w, b = _w(a.m, a.k, std=1.0), _w(a.n, a.k), _w(a.n)
         y = torch.empty(a.m, a.n, device="cuda", dtype=torch.bfloat16)
         run = lambda: wss.append(L.mmdit_fp8_mxfp8_linear_fwd(x, w, b, y))
+    elif a.case in ("block_linear", "block_linear_bwd", "block_cast"):
+        m, n, k = a.m, a.n, a.k
+        t = lambda v: (v + 127) // 128
+        e = lambda *s, dtype=torch.uint8: torch.empty(*s, dtype=dtype, device="cuda")
+        x, w = _w(m, k, std=1.0), _w(n, k)
+        xq, sx, xt, sxt = e(m, k), e(t(k), m, dtype=torch.float32), e(k, (m + 15) // 16 * 16), e(t(m), k, dtype=torch.float32)
+        wq, sw, wt = e(n, k), e(t(n), t(k), dtype=torch.float32), e(k, (n + 15) // 16 * 16)
+        cast = lambda: L.mmdit_fp8_block_cast(x, xq, sx, q_t=xt, s_t=sxt)
+        cast()
+        L.mmdit_fp8_block_cast(w, wq, sw, q_t=wt, square=True)
+        if a.case == "block_cast":
+            run = cast
+        elif a.case == "block_linear":
+            y, b = e(m, n, dtype=torch.bfloat16), _w(n)
+            run = lambda: wss.append(L.mmdit_fp8_block_linear_fwd(xq, sx, wq, sw, b, y))
+        else:
+            dy, dx = _w(m, n, std=1e-3), e(m, k, dtype=torch.bfloat16)
+            dw, db = e(n, k, dtype=torch.float32), e(n, dtype=torch.float32)
+            ws = L.workspace(L.mmdit_fp8_block_linear_bwd_workspace_size(m, n, k))
+            run = lambda: wss.append(L.mmdit_fp8_block_linear_bwd(dy, wt, sw, xt, sxt, dx=dx, dw=dw, db=db, ws=ws))
+    elif a.case in ("add_rmsnorm", "add_rmsnorm_bwd"):
+        x, res, gain = _w(a.m, a.k, std=1.0), _w(a.m, a.k, std=1.0).float(), _w(a.k, std=1.0)
+        h, rstd = torch.empty_like(res), torch.empty(a.m, device="cuda")
+        q, s = torch.empty(a.m, a.k, device="cuda", dtype=torch.uint8), torch.empty((a.k + 127) // 128, a.m, device="cuda")
+        fwd = lambda: L.mmdit_add_rmsnorm_fwd(x, gain, residual=res, h=h, y_q=q, s_y=s, rstd=rstd)
+        fwd()
+        dh, dg = torch.empty_like(x), torch.empty(a.k, device="cuda")
+        ws = L.workspace(L.mmdit_add_rmsnorm_bwd_workspace_size(a.m, a.k))
+        xb = x.clone()
+        run = fwd if a.case == "add_rmsnorm" else lambda: wss.append(
+            L.mmdit_add_rmsnorm_bwd(x, xb, gain, rstd, dh, dh_in=x, dgain=dg, ws=ws))
+    elif a.case == "rope":
+        q = _w(a.batch, a.seq, 32, 128, std=1.0)
+        k = _w(a.batch, a.seq, 8, 128, std=1.0)
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
+        cfg, pos = L.make_rope_cfg(128, scaling="linear", factor=4.0), torch.arange(a.seq, device="cuda")
+        run = lambda: L.mmdit_rope_fwd(cfg, q, qo, k=k, k_out=ko, positions=pos)
     else:
         B, Si, St, D, F = a.batch, a.seq_img, a.seq_txt, a.hidden, a.mlp
         S = Si + St

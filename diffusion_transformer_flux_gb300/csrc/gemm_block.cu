@@ -22,8 +22,8 @@
 // turned: 128 rows of B are the MMA's M side and 32 or 64 rows of A its N side, four slices' products in TMEM,
 // and the CTAs of a cluster split K, so that every SM streams its share of B through a ring of TMA stages.  The
 // partial sums meet in shared memory of the cluster (each CTA adds up its own columns, in rank order): no
-// workspace, no atomics, the same bits every time.  48 x 4096 x 14336: 17.7 us, 3.4 TB/s; its fixed part (start,
-// first bytes, two cluster barriers) is 4 us.
+// workspace, no atomics, the same bits every time.  48 x 4096 x 14336: 18.0 us, 3.3 TB/s (through the ring, behind a
+// cluster barrier of its own: 20.2); about 10 us of it are HBM time, the rest launch, first bytes and the join.
 //
 // block_few_kernel (up to 16 rows): B streams through rings of asynchronous copies that every warp keeps for
 // itself, straight into the register layout of mma.sync.  At these sizes the tensor cores' rate does not count
@@ -405,13 +405,13 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
 template <int NT>
 struct StreamCfg {
   static constexpr int kStageBytes = kSlice * kSlice + NT * kSlice;
-  static constexpr int kStages = 100 * 1024 / kStageBytes;      // two CTAs to an SM
+  static constexpr int kJoinBytes = NT * 128 * 4;               // the partial sums of this CTA's columns
+  static constexpr int kStages = (104 * 1024 - kJoinBytes) / kStageBytes;  // two CTAs to an SM
   static constexpr int kBufs = 4;                               // slices' products in TMEM
   static constexpr int kTmemCols = kBufs * NT;
   static constexpr int kFacSlices = 8;                          // slices whose factors are held at a time
-  static constexpr int kSmem = kStages * kStageBytes + 2 * kFacSlices * NT * 4 + 256 + 1024;
+  static constexpr int kSmem = kStages * kStageBytes + kJoinBytes + 2 * kFacSlices * NT * 4 + 256 + 1024;
   static_assert(NT == 32 || NT == 64, "columns of a tile");
-  static_assert(NT * 128 * 4 <= kStages * kStageBytes, "the partial sums reuse the stage ring");
 };
 constexpr int kStreamThreads = 64 + 128;
 
@@ -425,7 +425,8 @@ __global__ void __launch_bounds__(kStreamThreads)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* fac = reinterpret_cast<float*>(smem + Cfg::kStages * Cfg::kStageBytes);  // [2][kFac][NT]
+  uint8_t* join = smem + Cfg::kStages * Cfg::kStageBytes;
+  float* fac = reinterpret_cast<float*>(join + Cfg::kJoinBytes);  // [2][kFac][NT]
   uint64_t* full = reinterpret_cast<uint64_t*>(fac + 2 * kFac * NT);
   uint64_t* empty = full + Cfg::kStages;
   uint64_t* pfull = empty + Cfg::kStages;
@@ -457,6 +458,7 @@ __global__ void __launch_bounds__(kStreamThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (splits > 1) cluster_arrive();  // this CTA runs: its shared memory may be written
   pdl_wait();
   pdl_trigger();
   if (a.clear && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.status = 0;
@@ -606,14 +608,14 @@ __global__ void __launch_bounds__(kStreamThreads)
       for (int t = 0; t < NT; ++t) put(m0 + t, n0 + row, acc[t]);
     }
   } else {
-    // CTA q of the cluster adds up columns [q cols, (q + 1) cols) of every CTA's partial sums, which
-    // the others write into its stage ring once all of them are done with theirs: part [rank][cols / 4]
-    // [row][4], so that a warp's 16-byte stores and loads are contiguous
+    // CTA q of the cluster adds up columns [q cols, (q + 1) cols) of every CTA's partial sums, which the others
+    // write into its join buffer as soon as they have them: [rank][cols / 4][row][4], so that a warp's 16-byte
+    // stores and loads are contiguous
     const int shift = __ffs(NT / splits) - 1, cols = 1 << shift;
-    __syncthreads();
-    cluster_sync();
+    __syncwarp();
+    cluster_wait();  // every CTA of the cluster has started
     if (warp >= 2) {
-      const uint32_t base = smem_addr(smem) + static_cast<uint32_t>((rank << shift) * 512 + row * 16);
+      const uint32_t base = smem_addr(join) + static_cast<uint32_t>((rank << shift) * 512 + row * 16);
 #pragma unroll
       for (int t = 0; t < NT; t += 4) {
         const uint32_t dst = mapa_shared(base + static_cast<uint32_t>((t & (cols - 1)) * 512), static_cast<uint32_t>(t >> shift));
@@ -624,13 +626,16 @@ __global__ void __launch_bounds__(kStreamThreads)
     }
     cluster_sync();
     if (warp >= 2 && ok) {
-      const float4* part = reinterpret_cast<const float4*>(smem) + row;
+      const float4* part = reinterpret_cast<const float4*>(join) + row;
       for (int c = 0; c < cols; c += 4) {
-        float4 v = part[c * 32];
-        for (int r = 1; r < splits; ++r) {
-          const float4 w = part[((r << shift) + c) * 32];
-          v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-        }
+        float4 w[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < splits) w[r] = part[((r << shift) + c) * 32];
+        float4 v = w[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < splits) v.x += w[r].x, v.y += w[r].y, v.z += w[r].z, v.w += w[r].w;
         const int m = m0 + (rank << shift) + c;
         put(m, n0 + row, v.x), put(m + 1, n0 + row, v.y), put(m + 2, n0 + row, v.z), put(m + 3, n0 + row, v.w);
       }
@@ -854,24 +859,25 @@ cudaError_t run_few(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
   return cudaGetLastError();
 }
 
-// Which kernel.  Few rows: up to 16 rows of A the weights' bytes and the launch are the cost (1 x 6144 x 4096:
-// 6.7 us against 9.4 in the stream kernel, 1 x 1024 x 1024: 2.2 against 4.8; at 32 rows a CTA would read twice as
-// much of A as of B, 22 us against 15 at 32 x 12288 x 4096).  Many rows: the pair kernel once its tiles occupy
-// about half of the pairs (32 tiles: 512 x 4096 x 4096 23 us against 25; 16 tiles: 256 x 4096 x 4096 23 against 18),
-// two pairs to a tile where all of them have a place and K is long (512 x 4096 x 14336: 37 us against 63, x 4096:
-// 17.2 against 22.8; 1000 x 1024 x 1024, 8 slices: 12.1 against 10.8; four pairs, clusters of 8, leave SMs idle: 50),
-// which pays from 16 tiles on if none of them is half empty (256 x 4096 x 14336: 37 us, in the stream kernel 43).
-// Between them the stream kernel, K split while two CTAs to an SM still hold every CTA of the launch (48 x 4096 x
-// 14336: 61, 35, 21, 18 us on 1, 2, 4, 8; 32 x 12288 x 4096, 96 tiles: 17.7, 15.0, 18.9 on 1, 2, 4).
+// Which kernel.  Few rows: up to 8 rows of A, or 16 with K up to 8192, the weights' bytes and the launch are the
+// cost (1 x 6144 x 4096: 6.7 us against 9.4 in the stream kernel, 1 x 1024 x 1024: 2.2 against 4.4, 16 x 4096 x 4096:
+// 6.9 against 8.4, x 14336: 16.6 against 13.8).  Many rows: the pair kernel once its tiles occupy about half of the
+// pairs (32 tiles: 512 x 4096 x 4096 23 us against 25; 16 tiles: 256 x 4096 x 4096 23 against 18), but not for a
+// quarter of a tile's rows (64 x 12288 x 4096: 22.5 against 17.4); two pairs to a tile where all of them have a place
+// and K is long (512 x 4096 x 14336: 37 us against 63, x 4096: 17.2 against 22.8; 1000 x 1024 x 1024, 8 slices: 12.1
+// against 10.8; four pairs, clusters of 8, leave SMs idle: 50), which pays from 16 tiles on if none of them is half
+// empty (256 x 4096 x 14336: 37 us, in the stream kernel 43).  Between them the stream kernel, K split while two
+// CTAs to an SM still hold every CTA of the launch (64 x 4096 x 14336: 61, 34, 19, 16 us on 1, 2, 4, 8; 32 x 12288 x
+// 4096, 96 tiles: 17.5, 14.2, 16.8 on 1, 2, 4).
 template <bool ROW_B, typename TO>
 cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream) {
   if constexpr (!ROW_B)
-    if (p.M <= 16 && a.num_kb <= kFewMaxSlices && p.lda == p.K && p.ldb == p.K)
+    if (p.M <= 16 && a.num_kb <= (p.M <= 8 ? kFewMaxSlices : 64) && p.lda == p.K && p.ldb == p.K)
       return p.M <= 8 ? run_few<1, TO>(p, a, stream) : run_few<2, TO>(p, a, stream);
   const int64_t pair_tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + kPairN - 1) / kPairN);
   if (pair_tiles > INT32_MAX) return cudaErrorInvalidValue;
   const bool split = 4 * pair_tiles <= num_sms() && a.num_kb >= 16;
-  if (pair_tiles >= num_sms() / 5 || (split && p.M > 128 && pair_tiles >= num_sms() / 10))
+  if (p.M > 64 && (pair_tiles >= num_sms() / 5 || (split && p.M > 128 && pair_tiles >= num_sms() / 10)))
     return split ? run_pair<ROW_B, TO, 2>(p, a, pair_tiles, stream) : run_pair<ROW_B, TO, 1>(p, a, pair_tiles, stream);
   const int nt = p.M <= 32 ? 32 : 64;
   const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + nt - 1) / nt);

@@ -271,7 +271,8 @@ def sum_tol(a, b, slices):
 LINEAR_SHAPES = [(1, 8, 16), (1, 128, 128), (2, 136, 144), (4, 264, 1040), (5, 256, 128), (16, 120, 272), (17, 384, 2064),
                  (33, 136, 400), (64, 256, 4096), (65, 128, 528), (100, 520, 144), (128, 256, 256), (129, 264, 272),
                  (255, 8, 1024), (256, 256, 128), (300, 776, 656), (513, 1024, 384), (3, 24, 33024), (9, 8, 160),
-                 (12, 1040, 2000), (2100, 1288, 272), (513, 2600, 2064), (300, 2056, 2176)]
+                 (12, 1040, 2000), (2100, 1288, 272), (513, 2600, 2064), (300, 2056, 2176),
+                 (10, 136, 8208), (64, 7816, 272)]
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR_SHAPES)

@@ -311,6 +311,7 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
         }
         return fast_rcp(v[lane]) * fast_rcp(v[32 + lane]);
       };
+      __syncwarp();  // lanes without a row skip the stores: every lane has read the last tile's ring
 #pragma unroll
       for (int i = 0; i < kRing - 1; ++i) fetch(i);
       for (int kb = 0; kb < num_kb; ++kb, ++it) {

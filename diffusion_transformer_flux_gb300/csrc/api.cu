@@ -2789,12 +2789,16 @@ mmdit_status rope_call(int32_t act, const mmdit_rope_cfg* cfg, int32_t batch, in
     mmdit_status s = check_view(vi[i], unit, i ? "k" : "q");
     if (s != MMDIT_OK || (s = check_view(vo[i], unit, i ? "k_out" : "q_out")) != MMDIT_OK) return s;
     in[i] = *vi[i], out[i] = *vo[i];
-    if ((batch > 1 && out[i].stride_b == 0) || (seq > 1 && out[i].stride_s == 0) || (heads[i] > 1 && out[i].stride_h == 0))
-      return fail(MMDIT_ERR_INVALID_ARG, "rope: a stride of %s is zero: its elements would share an address", i ? "k_out" : "q_out");
+    // heads that start less than a head apart would overlap
+    if ((batch > 1 && out[i].stride_b < head_dim) || (seq > 1 && out[i].stride_s < head_dim) ||
+        (heads[i] > 1 && out[i].stride_h < head_dim))
+      return fail(MMDIT_ERR_INVALID_ARG, "rope: a stride of %s is below head_dim: its heads would overlap", i ? "k_out" : "q_out");
     if (in[i].ptr == out[i].ptr && (in[i].stride_b != out[i].stride_b || in[i].stride_s != out[i].stride_s ||
                                     in[i].stride_h != out[i].stride_h))
       return fail(MMDIT_ERR_INVALID_ARG, "rope: in place needs the same strides");
   }
+  if (heads[0] && heads[1] && (out[0].ptr == out[1].ptr || out[0].ptr == in[1].ptr || out[1].ptr == in[0].ptr))
+    return fail(MMDIT_ERR_INVALID_ARG, "rope: q_out and k_out must not be each other, nor the other's input");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   pdl_begin_call();
   ProfScope ps_(transposed ? "rope_bwd" : "rope", st);

@@ -802,11 +802,11 @@ mmdit_status mmdit_rope_config(mmdit_rope_cfg *cfg, int32_t rot_dim, int32_t int
 /* q and k rotated (k may be NULL: q alone).  A view is element (b, s, h, i) of a tensor
  * [batch, seq, heads, head_dim] of type `act` at ptr + b stride_b + s stride_s + h stride_h + i
  * (strides in elements, multiples of 16 bytes, >= 0): token-major, head-major and packed q|k|v layouts
- * alike.  An output may be the input itself (same ptr and strides: in place) and must not overlap it
- * otherwise; its strides may be zero only where the extent is one.  Angles come from positions [batch, seq] int64 (pos_bstride elements between samples, 0:
- * the same for all; any sign, exact far into a context) or from tables cos, sin [batch, seq,
- * rot_dim / 2] fp32, 16-byte aligned, as rope3d_freqs writes them: exactly one of the two.  cfg and the
- * views are host memory.  head_dim a multiple of 8, at most 512, >= cfg->rot_dim; float32 arithmetic.
+ * alike; an input's may be zero (broadcast).  An output may be its own input (same ptr and strides: in
+ * place) and must overlap no view otherwise; its strides are at least head_dim where the extent is above
+ * one.  Angles come from positions [batch, seq] int64 (pos_bstride elements between samples, 0: the same
+ * for all; any sign, exact far into a context) or from tables cos, sin [batch, seq, rot_dim / 2] fp32,
+ * 16-byte aligned, as rope3d_freqs writes them: exactly one of the two.  cfg and the views are host memory.  head_dim a multiple of 8, at most 512, >= cfg->rot_dim; float32 arithmetic.
  * batch at most 65535, seq at most 2^30; batch * seq == 0 is a no-op.  No workspace. */
 typedef struct mmdit_rope_view {
   void *ptr;

@@ -176,6 +176,15 @@ def test_rope_refusals(lib, fn, status, kw):
     assert _rope(lib, fn, **kw) == status and "rope" in L.last_error()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(qo=(B_, 512, 128, 56)), dict(qo=(B_, 512, 56, 64)), dict(batch=2, ko=(D_, 56, 64, 64)), dict(ko=(B_, 256, 64, 64)),
+    dict(qo=(C_, 512, 128, 64)), dict(ko=(A, 256, 64, 64)),
+])
+def test_rope_refuses_overlapping_outputs(lib, kw):
+    """Heads that start less than a head apart, q_out on k or k_out, k_out on q."""
+    assert _rope(lib, **kw) == INVALID and ("overlap" in L.last_error() or "each other" in L.last_error())
+
+
 def test_rope_empty(lib):
     assert _rope(lib, batch=0) == 0 and _rope(lib, seq=0) == 0
 

@@ -830,10 +830,15 @@ def _device(t):
     return t.device
 
 
-def _workspace_arg(ws, dev, nbytes):
-    """The caller's workspace, or a new one of nbytes(); its size and alignment are the library's to check."""
+def _workspace_arg(ws, dev, nbytes, stream):
+    """The caller's workspace, or a new one of nbytes(); its size and alignment are the library's to check.
+    A new one is zeroed, and given back, in the order of the call's stream."""
     if ws is None:
-        return workspace(nbytes(), dev)
+        if stream is None:
+            return workspace(nbytes(), dev)
+        raw = _stream(stream)
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw, dev) if raw else torch.cuda.default_stream(dev)):
+            return workspace(nbytes(), dev)
     if ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the call's tensors are on {dev}")
     return ws
@@ -871,7 +876,7 @@ def mmdit_add_rmsnorm_bwd(dy, h, gain, rstd, dh, dh_in=None, dx=None, dgain=None
     if hdt is not dt and hdt is not f32:
         raise TypeError(f"h has dtype {hdt}, expected {dt} or float32")
     R, D = dy.shape
-    ws = _workspace_arg(ws, dev, lambda: mmdit_add_rmsnorm_bwd_workspace_size(R, D))
+    ws = _workspace_arg(ws, dev, lambda: mmdit_add_rmsnorm_bwd_workspace_size(R, D), stream)
     _launch("mmdit_add_rmsnorm_bwd", dev, stream, act, int(hdt is f32), R, D, _arg("dy", dy, dev, dt, R, D),
             _arg("h", h, dev, hdt, R, D), _arg("gain", gain, dev, dt, D), _arg("rstd", rstd, dev, f32, R),
             _arg("dh_in", dh_in, dev, hdt, R, D), _arg("dh", dh, dev, hdt, R, D), _arg("dx", dx, dev, dt, R, D),
@@ -901,7 +906,7 @@ def mmdit_fp8_block_linear_fwd(x_q, s_x, w_q, s_w, b, y, ws=None, stream=None):
     dev, u8, f32 = _device(x_q), torch.uint8, torch.float32
     M, K = x_q.shape
     N = w_q.shape[0]
-    ws = _workspace_arg(ws, dev, lambda: mmdit_fp8_block_linear_workspace_size(M, N, K))
+    ws = _workspace_arg(ws, dev, lambda: mmdit_fp8_block_linear_workspace_size(M, N, K), stream)
     _launch("mmdit_fp8_block_linear_fwd", dev, stream, M, N, K, _arg("x_q", x_q, dev, u8, M, K),
             _arg("s_x", s_x, dev, f32, _tiles(K), M), _arg("w_q", w_q, dev, u8, N, K),
             _arg("s_w", s_w, dev, f32, _tiles(N), _tiles(K)), _arg("b", b, dev, torch.bfloat16, N),
@@ -922,7 +927,7 @@ def mmdit_fp8_block_linear_bwd(dy, w_t=None, s_w=None, x_t=None, s_xt=None, dx=N
     dev, u8, f32, b16 = _device(dy), torch.uint8, torch.float32, torch.bfloat16
     M, N = dy.shape
     K = next((t.shape[i] for t, i in ((w_t, 0), (x_t, 0), (dx, 1), (dw, 1)) if t is not None), 16)
-    ws = _workspace_arg(ws, dev, lambda: mmdit_fp8_block_linear_bwd_workspace_size(M, N, K))
+    ws = _workspace_arg(ws, dev, lambda: mmdit_fp8_block_linear_bwd_workspace_size(M, N, K), stream)
     _launch("mmdit_fp8_block_linear_bwd", dev, stream, M, N, K, _arg("dy", dy, dev, b16, M, N),
             _arg("w_t", w_t, dev, u8, K, _ld16(N)), _arg("s_w", s_w, dev, f32, _tiles(N), _tiles(K)),
             _arg("x_t", x_t, dev, u8, K, _ld16(M)), _arg("s_xt", s_xt, dev, f32, _tiles(M), K),

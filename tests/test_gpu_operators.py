@@ -478,6 +478,16 @@ def test_rope_special_values_pass():
         assert bad.sum() == 2 and bad[0, 1, 1].sum() == 2
 
 
+def test_rope_broadcast_input():
+    """An input whose heads share an address (one key rotated into every head's place)."""
+    one = make(np.random.default_rng(8), (2, 5, 1, 64))
+    out, alone = nans(2, 5, 4, 64, dtype=torch.bfloat16), nans(2, 5, 1, 64, dtype=torch.bfloat16)
+    cfg, pos = L.make_rope_cfg(64), torch.arange(5, device="cuda")
+    L.mmdit_rope_fwd(cfg, one.expand(2, 5, 4, 64), out, positions=pos)
+    L.mmdit_rope_fwd(cfg, one, alone, positions=pos)
+    assert torch.equal(out, alone.expand(2, 5, 4, 64))
+
+
 def test_rope_empty():
     e = torch.empty(1, 0, 2, 64, device="cuda")
     L.mmdit_rope_fwd(L.make_rope_cfg(64), e, e, positions=torch.empty(0, dtype=torch.int64, device="cuda"))
@@ -530,6 +540,20 @@ def test_other_stream_and_two_graphs_on_one_workspace():
     backward()
     assert all(torch.equal(a, b) for a, b in zip(r, (y, dx, dw)))
     assert L.mmdit_workspace_status(ws) == 0
+
+
+def test_workspace_of_a_call_on_another_stream():
+    """A workspace that the binding makes belongs to the call's stream: its zeros are written before the call,
+    not whenever the current stream comes to them."""
+    dy = make(np.random.default_rng(5), (200, 256))
+    side, db = torch.cuda.Stream(), nans(256)
+    for stream in (side, side.cuda_stream, 0):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        ws = L.mmdit_fp8_block_linear_bwd(dy, db=db, stream=stream)
+        torch.cuda.synchronize()
+        assert ws.count_nonzero() > 256  # the partial sums of db
+        check(f64(db), f64(dy).sum(0), 208 * U * np.abs(f64(dy)).sum(0), "db")
 
 
 def test_binding_refusals():

@@ -50,12 +50,6 @@ constexpr int kPairFewRegs = 40, kPairManyRegs = 232;
 static_assert(128 * kPairFewRegs + 256 * kPairManyRegs <= kPairThreads * 168, "register shares");
 constexpr int kPairN = 256;
 
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // mbar_wait that tries the barrier a few hundred times before it first reads the timer: the waits here
 // recur every slice, and a timer read costs more than the slice's hand-over.
 __device__ __forceinline__ bool slice_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
@@ -96,6 +90,20 @@ template <int R>
 __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
 __device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// 64 columns of 16 lanes of this warp's quarter: lane 4 g + q receives columns 8 i + 2 q, 8 i + 2 q + 1 of row g in
+// r[4 i], r[4 i + 1] and of row g + 8 in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
 
 struct BlockArgs {
   const float* sa;   // [num_kb, M]
@@ -300,14 +308,14 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
         }
         copy_async_commit();
       };
-      auto factor = [&](int kb) {
+      auto factor = [&](int kb) {  // of this lane's row and the tile (with row scales: the reciprocals stay in the ring)
         copy_async_wait<kRing - 2>();
         float* v = my_ring + (kb % kRing) * kRingFloats;
-        if constexpr (ROW_B) {  // the columns' reciprocals, once for the warp's 32 rows
+        if constexpr (ROW_B) {
 #pragma unroll
-          for (int e = 1; e < 5; ++e) v[32 * e + lane] = fast_rcp(v[32 * e + lane]);
+          for (int e = 0; e < 5; ++e) v[32 * e + lane] = fast_rcp(v[32 * e + lane]);
           __syncwarp();
-          return fast_rcp(v[lane]);
+          return 0.f;
         }
         return fast_rcp(v[lane]) * fast_rcp(v[32 + lane]);
       };
@@ -320,33 +328,49 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
         if (!ok) continue;
         tc_fence_after();
         const uint32_t t = t_base + b * 256u;
+        // the half buffer's columns in two loads of 64 (with row scales: of 16 lanes each, so that a thread holds
+        // two columns of four rows and reads a quarter of the column factors), the next pair of loads on their way
+        // while the first is added
+        auto load = [&](int k, uint32_t(&p)[32]) {
+          if constexpr (ROW_B)
+            tmem_ld16x64(t + static_cast<uint32_t>((k >> 1) * 64) + (static_cast<uint32_t>((k & 1) * 16) << 16), p);
+          else
+            tmem_ld32(t + static_cast<uint32_t>(k * 32), p);
+        };
         uint32_t p0[32], p1[32];
-        tmem_ld32(t, p0);
-        tmem_ld32(t + 32u, p1);
+        load(0, p0);
+        load(1, p1);
         const float f = factor(kb);  // while the loads are on their way
-        auto add = [&](int c, const uint32_t(&p)[32]) {
+        const float* fac = my_ring + (kb % kRing) * kRingFloats;
+        float2 cf[8];
+        auto columns = [&](int c) {  // the factors of the thread's columns of load pair c
           if constexpr (ROW_B) {
-            const float4* rb = reinterpret_cast<const float4*>(my_ring + (kb % kRing) * kRingFloats + 32 + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cf[i] = *reinterpret_cast<const float2*>(fac + 32 + c * 64 + 8 * i + 2 * (lane & 3));
+          }
+        };
+        auto add = [&](int k, const uint32_t(&p)[32]) {
+          if constexpr (ROW_B) {
+            const float lo = fac[(k & 1) * 16 + (lane >> 2)], hi = fac[(k & 1) * 16 + (lane >> 2) + 8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 w = rb[i];
-              float w4[4];  // the two factors' products, two at a time
-              f32x2_split(fmul2(f32x2(w.x, w.y), f32x2(f, f)), w4[0], w4[1]);
-              f32x2_split(fmul2(f32x2(w.z, w.w), f32x2(f, f)), w4[2], w4[3]);
+              const float w[4] = {cf[i].x * lo, cf[i].y * lo, cf[i].x * hi, cf[i].y * hi};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                acc[c * 32 + 4 * i + e] = fmaf(__uint_as_float(p[4 * i + e]), w4[e], acc[c * 32 + 4 * i + e]);
+                acc[k * 32 + 4 * i + e] = fmaf(__uint_as_float(p[4 * i + e]), w[e], acc[k * 32 + 4 * i + e]);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(p[i]), f, acc[c * 32 + i]);
+            for (int i = 0; i < 32; ++i) acc[k * 32 + i] = fmaf(__uint_as_float(p[i]), f, acc[k * 32 + i]);
           }
         };
+        columns(0);
         tmem_ld_deps64(p0, p1);
         add(0, p0);
-        tmem_ld32(t + 64u, p0);
+        load(2, p0);
         add(1, p1);
-        tmem_ld32(t + 96u, p1);
+        load(3, p1);
+        columns(1);
         tmem_ld_deps64(p0, p1);
         // this warp has read its part of the half buffer
         tc_fence_before();
@@ -359,29 +383,63 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
       TO* dst = static_cast<TO*>(a.out) + static_cast<int64_t>(m) * a.N;
       if constexpr (SPLITS > 1) {
         // The pairs' partial sums meet in the CTAs' stage rings, once both pairs are done with their own: pair q
-        // adds up half q of the tile's columns, [pair][column / 4][row][4], in pair order.  (A cluster that
-        // splits K has one tile.)
+        // adds up half q of the tile's columns, in pair order.  (A cluster that splits K has one tile.)  Layout
+        // [pair][column / 4][row][4], or with row scales, whose threads hold two columns of four rows,
+        // [pair][column / 2][row ^ 8 (column / 2 % 4)][2].
         cluster_sync();
-        const uint32_t at = smem_addr(smem) + static_cast<uint32_t>(part * 65536 + row * 16);
-        const uint32_t owner = mapa_shared(at, static_cast<uint32_t>(2 * h) + rank);
+        const uint32_t owner = mapa_shared(smem_addr(smem) + static_cast<uint32_t>(part * 65536), static_cast<uint32_t>(2 * h) + rank);
+        if constexpr (ROW_B) {
 #pragma unroll
-        for (int j = 0; j < 128; j += 4)
-          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(owner + j * 512u), "f"(acc[j]), "f"(acc[j + 1]),
-                       "f"(acc[j + 2]), "f"(acc[j + 3])
-                       : "memory");
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const int col2 = (k >> 1) * 32 + 4 * (j >> 2) + (lane & 3);
+              const int r = quarter * 32 + (k & 1) * 16 + (j & 2) * 4 + (lane >> 2);
+              asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(owner + col2 * 1024 + ((r ^ (8 * (lane & 3))) * 8)),
+                           "f"(acc[k * 32 + j]), "f"(acc[k * 32 + j + 1])
+                           : "memory");
+            }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 128; j += 4)
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(owner + row * 16 + j * 512u), "f"(acc[j]), "f"(acc[j + 1]),
+                         "f"(acc[j + 2]), "f"(acc[j + 3])
+                         : "memory");
+        }
         cluster_sync();
-        const float4* in = reinterpret_cast<const float4*>(smem) + row;
 #pragma unroll 1
         for (int c = h * 64; c < h * 64 + 64; c += 32) {  // this warpgroup's half of the pair's columns
           float v[32];
+          if constexpr (ROW_B) {
+            const float2* in = reinterpret_cast<const float2*>(smem);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 t = in[(c / 4 + i) * 128], w = in[4096 + (c / 4 + i) * 128];
-            v[4 * i] = t.x + w.x, v[4 * i + 1] = t.y + w.y, v[4 * i + 2] = t.z + w.z, v[4 * i + 3] = t.w + w.w;
+            for (int i = 0; i < 16; ++i) {
+              const int at = (c / 2 + i) * 128 + (row ^ (8 * (i & 3)));
+              const float2 t = in[at], w = in[8192 + at];
+              v[2 * i] = t.x + w.x, v[2 * i + 1] = t.y + w.y;
+            }
+          } else {
+            const float4* in = reinterpret_cast<const float4*>(smem) + row;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 t = in[(c / 4 + i) * 128], w = in[4096 + (c / 4 + i) * 128];
+              v[4 * i] = t.x + w.x, v[4 * i + 1] = t.y + w.y, v[4 * i + 2] = t.z + w.z, v[4 * i + 3] = t.w + w.w;
+            }
           }
           const int n = (tile / tiles_m) * kPairN + part * 128 + c;
           if (ok && row_ok && n < a.N) store_row<TO>(dst, a.bias, n, a.N, v);
         }
+      } else if constexpr (ROW_B) {
+        static_assert(sizeof(TO) == 4, "row scales have float32 outputs, and no bias");
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const int n = ng + (k >> 1) * 64 + 8 * (j >> 2), r = (k & 1) * 16 + (j & 2) * 4 + (lane >> 2);
+            if (ok && m - lane + r < a.M && n < a.N)  // N is a multiple of 8
+              *reinterpret_cast<float2*>(static_cast<float*>(a.out) + static_cast<int64_t>(m - lane + r) * a.N + n + 2 * (lane & 3)) =
+                  make_float2(acc[k * 32 + j], acc[k * 32 + j + 1]);
+          }
       } else if (ok && row_ok) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

@@ -14,9 +14,11 @@
 // warpgroup and barriers of their own; the arrivals carry no release at cluster scope, the waits read no
 // timer, a warp's scales come through a ring of asynchronous copies, and the issuers run on whole warps.
 // Each promotion thread holds a row's 128 float32 sums in registers (setmaxnreg moves them over from the
-// other warpgroup).  8192^3: 493 us, 2.23 PFLOP/s; 4608 x 12288 x 4096 with bias: 225 us, 2.06 PFLOP/s
-// (the same loop without the multiply-adds: 420 and 196 us, without reading TMEM either: 332 and 156 us;
-// with one N = 256 MMA and barrier per slice 558 and 256 us).
+// other warpgroup); the scales' ring runs on from tile to tile, and the outputs leave through shared memory by
+// TMA.  8192^3: 464 us, 2.37 PFLOP/s; 4608 x 12288 x 4096 with bias: 208 us, 2.23 PFLOP/s (a ring that starts anew
+// with each tile 492 and 227 us, with it but each thread storing its own row 472 and 218; at that first step the
+// loop without the multiply-adds took 420 and 196 us, without reading TMEM either 332 and 156, with one N = 256 MMA
+// and barrier per slice 558 and 256, with barriers for quarters of 64 columns 668 and 299).
 //
 // block_stream_kernel (tens of rows, or too few tiles for the pairs): B's bytes are the cost, so the roles are
 // turned: 128 rows of B are the MMA's M side and 32 or 64 rows of A its N side, four slices' products in TMEM,
@@ -40,11 +42,13 @@ namespace mmdit {
 namespace {
 
 constexpr int kSlice = 128;  // K of a scale block: 128 codes = one 128-byte swizzled row
-constexpr int kPairStages = 4;  // more only spread the pairs apart in L2: 8192^3 takes 493 us with 4, 507 with 5, 514 with 6, 522 with 3
+constexpr int kPairStages = 4;  // what the output boxes leave room for; more only spread the pairs apart in L2
+                                // (8192^3 before the boxes: 493 us with 4, 507 with 5, 514 with 6, 522 with 3)
 constexpr int kPairStageBytes = 2 * kSlice * kSlice;  // this CTA's 128 rows of A and of B
 constexpr int kPairThreads = 128 + 256;               // producer, two MMA issuers, an idle warp; 8 promotion warps
 constexpr int kRing = 4, kRingFloats = 32 + 128;      // per promotion warp: slices whose scales are held, floats of one
-constexpr int kPairSmem = kPairStages * kPairStageBytes + 8 * kRing * kRingFloats * 4 + 256 + 1024;
+constexpr int kBox = 32 * 128;                        // an output box: 32 rows of 128 bytes; two per promotion warp
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 8 * 2 * kBox + 8 * kRing * kRingFloats * 4 + 256 + 1024;
 // 384 threads start with 168 registers (64512); the promotion warpgroups take 232, the other one keeps 40
 constexpr int kPairFewRegs = 40, kPairManyRegs = 232;
 static_assert(128 * kPairFewRegs + 256 * kPairManyRegs <= kPairThreads * 168, "register shares");
@@ -90,6 +94,19 @@ template <int R>
 __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
 __device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// A box of shared memory stored to the tensor at column x, row y while the thread goes on; groups of stores are
+// awaited in order: until their shared memory is read, or until they are done.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* box, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tm), "r"(smem_addr(box)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
 
 // 64 columns of 16 lanes of this warp's quarter: lane 4 g + q receives columns 8 i + 2 q, 8 i + 2 q + 1 of row g in
 // r[4 i], r[4 i + 1] and of row g + 8 in r[4 i + 2], r[4 i + 3].
@@ -144,12 +161,13 @@ __device__ __forceinline__ void store_row(TO* dst, const __nv_bfloat16* bias, in
 template <bool ROW_B, typename TO, int SPLITS>
 __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThreads, 1)
     block_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                      const __grid_constant__ BlockArgs a) {
+                      const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ BlockArgs a) {
   constexpr uint32_t kIdesc = make_idesc<kKindF8>(256, 128);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* rings = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes);  // [8 warps][kRing][kRingFloats]
+  uint8_t* boxes = smem + kPairStages * kPairStageBytes;                     // [8 warps][2][kBox]
+  float* rings = reinterpret_cast<float*>(boxes + 8 * 2 * kBox);             // [8 warps][kRing][kRingFloats]
   uint64_t* full = reinterpret_cast<uint64_t*>(rings + 8 * kRing * kRingFloats);
   uint64_t* empty = full + kPairStages;
   uint64_t* pfull = empty + kPairStages;  // [buffer][half]
@@ -283,34 +301,48 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
     const uint32_t ring = smem_addr(my_ring);
     uint32_t it = 0;
     bool ok = true;
+    // The scales of a slice come through this warp's ring of kRing slots in shared memory, copied kRing - 1 slices
+    // ahead, over the end of a tile into the next: lane l's row scale, and its column scales (the tile's one scale,
+    // or of columns l, l + 32, l + 64, l + 96).
+    const int64_t b_step = ROW_B ? static_cast<int64_t>(a.N) : a.sb_k;
+    const float *pa, *pb;
+    int next_tile = pair, next_kb = 0, next_n;  // the slice that is copied next
+    auto aim = [&]() {
+      const int m = (next_tile % tiles_m) * 256 + static_cast<int>(rank) * 128 + row;
+      next_n = (next_tile / tiles_m) * kPairN + h * 128;
+      pa = a.sa + static_cast<int64_t>(kb0) * a.M + (m < a.M ? m : 0);
+      pb = a.sb + kb0 * b_step + (ROW_B ? 0 : static_cast<int64_t>(next_n < a.N ? next_n >> 7 : 0) * a.sb_n);
+    };
+    auto fetch = [&](uint32_t slot_of) {
+      if (next_tile < tiles) {
+        const uint32_t slot = ring + ((slot_of % kRing) * kRingFloats + static_cast<uint32_t>(lane)) * 4u;
+        copy_async4(slot, pa);
+#pragma unroll
+        for (int e = 0; e < (ROW_B ? 4 : 1); ++e) {
+          const int n = ROW_B ? next_n + 32 * e + lane : 0;
+          copy_async4(slot + 128u * (1 + e), pb + (n < a.N ? n : 0));
+        }
+        pa += a.M, pb += b_step;
+        if (++next_kb == num_kb) {
+          next_kb = 0, next_tile += pairs;
+          aim();
+        }
+      }
+      copy_async_commit();
+    };
+    aim();
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(i);
     for (int tile = pair; tile < tiles; tile += pairs) {
       const int m = (tile % tiles_m) * 256 + static_cast<int>(rank) * 128 + row;
       const int ng = (tile / tiles_m) * kPairN + h * 128;
       const bool row_ok = m < a.M;
-      // the scales of slice kb come through this warp's ring of kRing slots in shared memory, copied
-      // kRing - 1 slices ahead: lane l's row scale, and its column scales (the tile's one scale, or of
-      // columns l, l + 32, l + 64, l + 96)
-      const float* pa = a.sa + static_cast<int64_t>(kb0) * a.M + (row_ok ? m : 0);
-      const int64_t b_step = ROW_B ? static_cast<int64_t>(a.N) : a.sb_k;
-      const float* pb = a.sb + kb0 * b_step + (ROW_B ? 0 : static_cast<int64_t>(ng < a.N ? ng >> 7 : 0) * a.sb_n);
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      auto fetch = [&](int kb) {
-        if (kb < num_kb) {
-          const uint32_t slot = ring + static_cast<uint32_t>((kb % kRing) * kRingFloats + lane) * 4u;
-          copy_async4(slot, pa + static_cast<int64_t>(kb) * a.M);
-#pragma unroll
-          for (int e = 0; e < (ROW_B ? 4 : 1); ++e) {
-            const int n = ROW_B ? ng + 32 * e + lane : 0;
-            copy_async4(slot + 128u * (1 + e), pb + kb * b_step + (n < a.N ? n : 0));
-          }
-        }
-        copy_async_commit();
-      };
-      auto factor = [&](int kb) {  // of this lane's row and the tile (with row scales: the reciprocals stay in the ring)
+      auto factor = [&]() {  // of this lane's row and the tile (with row scales: the reciprocals stay in the ring)
         copy_async_wait<kRing - 2>();
-        float* v = my_ring + (kb % kRing) * kRingFloats;
+        float* v = my_ring + (it % kRing) * kRingFloats;
         if constexpr (ROW_B) {
 #pragma unroll
           for (int e = 0; e < 5; ++e) v[32 * e + lane] = fast_rcp(v[32 * e + lane]);
@@ -319,9 +351,6 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
         }
         return fast_rcp(v[lane]) * fast_rcp(v[32 + lane]);
       };
-      __syncwarp();  // lanes without a row skip the stores: every lane has read the last tile's ring
-#pragma unroll
-      for (int i = 0; i < kRing - 1; ++i) fetch(i);
       for (int kb = 0; kb < num_kb; ++kb, ++it) {
         const uint32_t b = it & 1;
         if (ok) ok = warp_wait(&pfull[2 * b + h], (it >> 1) & 1, abort_flag, a.status);
@@ -340,8 +369,8 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
         uint32_t p0[32], p1[32];
         load(0, p0);
         load(1, p1);
-        const float f = factor(kb);  // while the loads are on their way
-        const float* fac = my_ring + (kb % kRing) * kRingFloats;
+        const float f = factor();  // while the loads are on their way
+        const float* fac = my_ring + (it % kRing) * kRingFloats;
         float2 cf[8];
         auto columns = [&](int c) {  // the factors of the thread's columns of load pair c
           if constexpr (ROW_B) {
@@ -378,7 +407,7 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
         if (lane == 0) mbar_arrive_remote_relaxed(pempty_leader + b * 2 * static_cast<uint32_t>(sizeof(uint64_t)));
         add(2, p0);
         add(3, p1);
-        fetch(kb + kRing - 1);
+        fetch(it + kRing - 1);
       }
       TO* dst = static_cast<TO*>(a.out) + static_cast<int64_t>(m) * a.N;
       if constexpr (SPLITS > 1) {
@@ -429,27 +458,56 @@ __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kPairThread
           const int n = (tile / tiles_m) * kPairN + part * 128 + c;
           if (ok && row_ok && n < a.N) store_row<TO>(dst, a.bias, n, a.N, v);
         }
-      } else if constexpr (ROW_B) {
-        static_assert(sizeof(TO) == 4, "row scales have float32 outputs, and no bias");
+      } else if (ok) {
+        // the warp's 32 x 128 outputs leave through two boxes in shared memory, which TMA stores while the warp
+        // goes on (a thread's own 16-byte stores, a row each, take 2 us a tile)
+        constexpr int kCols = 128 / static_cast<int>(sizeof(TO));  // columns of a box
+        uint8_t* my_boxes = boxes + (warp - 4) * 2 * kBox;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int x = 0; x < 128 / kCols; ++x) {
+          uint8_t* box = my_boxes + (x & 1) * kBox;
+          if (lane == 0) store_wait_read<1>();  // the box's last contents are read
+          __syncwarp();
+          if constexpr (ROW_B) {
+            static_assert(sizeof(TO) == 4, "row scales have float32 outputs, and no bias");
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const int n = ng + (k >> 1) * 64 + 8 * (j >> 2), r = (k & 1) * 16 + (j & 2) * 4 + (lane >> 2);
-            if (ok && m - lane + r < a.M && n < a.N)  // N is a multiple of 8
-              *reinterpret_cast<float2*>(static_cast<float*>(a.out) + static_cast<int64_t>(m - lane + r) * a.N + n + 2 * (lane & 3)) =
+            for (int i = 0; i < 16; ++i) {  // (half of the lanes, row + 8, group of 8 columns)
+              const int k = (x >> 1) * 2 + (i >> 3), j = 16 * (x & 1) + 4 * (i & 3) + 2 * ((i >> 2) & 1);
+              const int r = (i >> 3) * 16 + ((i >> 2) & 1) * 8 + (lane >> 2), q = lane & 3;
+              *reinterpret_cast<float2*>(box + r * 128 + (((2 * (i & 3) + (q >> 1)) ^ (r & 7)) * 16) + (q & 1) * 8) =
                   make_float2(acc[k * 32 + j], acc[k * 32 + j + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kCols / 8; ++c) {
+              const int n = ng + x * kCols + c * 8;
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = acc[x * kCols + c * 8 + e];
+              if (a.bias && n < a.N) {  // N is a multiple of 8
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(a.bias + n));
+                v[0] += bf16_lo(u.x), v[1] += bf16_hi(u.x), v[2] += bf16_lo(u.y), v[3] += bf16_hi(u.y);
+                v[4] += bf16_lo(u.z), v[5] += bf16_hi(u.z), v[6] += bf16_lo(u.w), v[7] += bf16_hi(u.w);
+              }
+              if constexpr (sizeof(TO) == 2) {
+                *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) * 16)) =
+                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+              } else {
+                *reinterpret_cast<float4*>(box + lane * 128 + (((2 * c) ^ (lane & 7)) * 16)) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4*>(box + lane * 128 + (((2 * c + 1) ^ (lane & 7)) * 16)) = make_float4(v[4], v[5], v[6], v[7]);
+              }
+            }
           }
-      } else if (ok && row_ok) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = acc[c * 32 + i];
-          if (ng + c * 32 < a.N) store_row<TO>(dst, a.bias, ng + c * 32, a.N, v);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (m < a.M && ng + x * kCols < a.N) tma_store_2d(&tm_out, box, ng + x * kCols, m);  // TMA clips the edges
+            store_commit();
+          }
         }
       }
     }
+    if (SPLITS == 1 && lane == 0) store_wait<0>();
   }
 
   __syncthreads();
@@ -858,15 +916,21 @@ bool code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, int64
 
 template <bool ROW_B, typename TO, int SPLITS>
 cudaError_t run_pair(const BlockGemm& p, const BlockArgs& a, int64_t tiles, cudaStream_t stream) {
-  CUtensorMap ta, tb;
-  if (!code_map(&ta, p.A, p.M, p.K, p.lda, 128) || !code_map(&tb, p.B, p.N, p.K, p.ldb, 64)) return cudaErrorInvalidValue;
+  CUtensorMap ta, tb, to;
+  const uint64_t dims[2] = {static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M)}, stride[1] = {p.N * sizeof(TO)};
+  const uint32_t box[2] = {static_cast<uint32_t>(128 / sizeof(TO)), 32};
+  if (!code_map(&ta, p.A, p.M, p.K, p.lda, 128) || !code_map(&tb, p.B, p.N, p.K, p.ldb, 64) ||
+      !encode_tmap(&to, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.out, dims,
+                   stride, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   auto kern = block_pair_kernel<ROW_B, TO, SPLITS>;
   static Configured done;
   cudaError_t e = configure(kern, kPairSmem, done);
   if (e != cudaSuccess) return e;
   const int most = num_sms() / (2 * SPLITS);
+  if (SPLITS > 1 && tiles > most) return cudaErrorInvalidValue;  // a cluster that splits K joins once
   const unsigned clusters = static_cast<unsigned>(tiles < most ? tiles : most);
-  e = launch_pdl(kern, dim3(2 * SPLITS * clusters), dim3(kPairThreads), kPairSmem, stream, ta, tb, a);
+  e = launch_pdl(kern, dim3(2 * SPLITS * clusters), dim3(kPairThreads), kPairSmem, stream, ta, tb, to, a);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -921,11 +985,11 @@ cudaError_t run_few(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
 // Which kernel.  Few rows: up to 8 rows of A, or 16 with K up to 8192, the weights' bytes and the launch are the
 // cost (1 x 6144 x 4096: 6.7 us against 9.4 in the stream kernel, 1 x 1024 x 1024: 2.2 against 4.4, 16 x 4096 x 4096:
 // 6.9 against 8.4, x 14336: 16.6 against 13.8).  Many rows: the pair kernel once its tiles occupy about half of the
-// pairs (32 tiles: 512 x 4096 x 4096 23 us against 25; 16 tiles: 256 x 4096 x 4096 23 against 18), but not for a
-// quarter of a tile's rows (64 x 12288 x 4096: 22.5 against 17.4); two pairs to a tile where all of them have a place
-// and K is long (512 x 4096 x 14336: 37 us against 63, x 4096: 17.2 against 22.8; 1000 x 1024 x 1024, 8 slices: 12.1
-// against 10.8; four pairs, clusters of 8, leave SMs idle: 50), which pays from 16 tiles on if none of them is half
-// empty (256 x 4096 x 14336: 37 us, in the stream kernel 43).  Between them the stream kernel, K split while two
+// pairs (32 tiles: 512 x 4096 x 4096 21.8 us against 24.9; 16 tiles: 256 x 4096 x 4096 21.9 against 16.5), but not for a
+// quarter of a tile's rows (64 x 12288 x 4096: 22.7 against 17.2); two pairs to a tile where all of them have a place
+// and K is long (512 x 4096 x 14336: 36 us against 61, x 4096: 17.2 against 21.8; 1000 x 1024 x 1024, 8 slices: 10.0
+// against 9.6; four pairs, clusters of 8, leave SMs idle: 50), which pays from 16 tiles on if none of them is half
+// empty (256 x 4096 x 14336: 36 us, in the stream kernel 41.5).  Between them the stream kernel, K split while two
 // CTAs to an SM still hold every CTA of the launch (64 x 4096 x 14336: 61, 34, 19, 16 us on 1, 2, 4, 8; 32 x 12288 x
 // 4096, 96 tiles: 17.5, 14.2, 16.8 on 1, 2, 4).
 template <bool ROW_B, typename TO>

@@ -272,7 +272,8 @@ LINEAR_SHAPES = [(1, 8, 16), (1, 128, 128), (2, 136, 144), (4, 264, 1040), (5, 2
                  (33, 136, 400), (64, 256, 4096), (65, 128, 528), (100, 520, 144), (128, 256, 256), (129, 264, 272),
                  (255, 8, 1024), (256, 256, 128), (300, 776, 656), (513, 1024, 384), (3, 24, 33024), (9, 8, 160),
                  (12, 1040, 2000), (2100, 1288, 272), (513, 2600, 2064), (300, 2056, 2176),
-                 (10, 136, 8208), (64, 7816, 272)]
+                 (10, 136, 8208), (64, 7816, 272),
+                 (2100, 2568, 272), (5000, 1288, 16), (2100, 2568, 640)]  # more tiles than pairs, of 3, 1 and 5 slices
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR_SHAPES)
@@ -312,6 +313,20 @@ def test_linear_writes_its_rows_alone():
                                  torch.empty(0, 200, device="cuda", dtype=torch.bfloat16))
 
 
+def test_linear_tiles_write_inside_the_output():
+    """Tiles that reach over the last row and column leave what lies behind them."""
+    M, N, K = 2090, 2568, 272
+    _, _, _, xq, sx, wq, sw = linear_operands(6, M, N, K)
+    for dtype in (torch.bfloat16, torch.float32):
+        pad = torch.full((M + 30, N), 7.0, device="cuda", dtype=dtype)
+        L.mmdit_fp8_block_linear_fwd(xq, sx, wq, sw, None, pad[10:M + 10])
+        assert (pad[:10] == 7).all() and (pad[M + 10:] == 7).all()
+        row = nans(1, N, dtype=dtype)
+        L.mmdit_fp8_block_linear_fwd(xq[-1:], sx[:, -1:].contiguous(), wq, sw, None, row)
+        diff = (row[0].float() - pad[M + 9].float()).abs()
+        assert diff.max() <= 2.0 ** -7 * row.float().abs().max()
+
+
 def test_linear_extreme_scales():
     """Tiles at the scale's limit and near float32's top: the factor 1 / (s_x s_w) stays in range."""
     M, N, K = 20, 128, 256
@@ -331,7 +346,7 @@ def test_linear_extreme_scales():
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 8, 16), (16, 128, 128), (100, 136, 272), (129, 264, 400), (300, 776, 656),
-                                   (520, 128, 1040), (40, 600, 128), (2100, 1288, 1360)])
+                                   (520, 128, 1040), (40, 600, 128), (2100, 1288, 1360), (300, 2568, 2576), (16, 2568, 2576)])
 def test_linear_gradients(M, N, K):
     rng, x, w, _, _, wq, sw = linear_operands(M + N * 5 + K, M, N, K)
     ldm, ldn = (M + 15) // 16 * 16, (N + 15) // 16 * 16

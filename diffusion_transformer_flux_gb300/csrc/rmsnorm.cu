@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_fwd_kernel(const 
     const int c = threadIdx.x + i * blockDim.x;
     if (row_ok && c < chunks) {
       rx[i].load(x + 8 * c);
-      if (res) rr[i].load(res + 8 * c);
+      if (res) rr[i].load_rw(res + 8 * c);  // h may be the residual itself
     }
   }
   float ss = 0.f;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(MAX, MAX <= 320 ? 2 : 1) add_rmsnorm_bwd_kerne
       if (c < chunks) {
         x.dy[i].load(static_cast<const T*>(a.dy) + off + 8 * c);
         x.h[i].load(static_cast<const TR*>(a.h) + off + 8 * c);
-        if (a.dh_in) x.in[i].load(static_cast<const TR*>(a.dh_in) + off + 8 * c);
+        if (a.dh_in) x.in[i].load_rw(static_cast<const TR*>(a.dh_in) + off + 8 * c);  // dh may be dh_in itself
       }
     }
     x.r = __ldg(a.rstd + row);

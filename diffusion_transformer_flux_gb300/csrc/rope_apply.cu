@@ -78,7 +78,8 @@ __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
   }
 }
 
-// A piece as loaded: packed for the 16-byte ones, so that several fit a thread's registers.
+// A piece as loaded: packed for the 16-byte ones, so that several fit a thread's registers.  The loads are plain: the
+// heads may be rotated in place.
 template <typename T, int V>
 struct Piece {
   float v[V];
@@ -89,7 +90,9 @@ struct Piece {
   }
 };
 template <>
-struct Piece<__nv_bfloat16, 8> : Raw8<__nv_bfloat16> {};
+struct Piece<__nv_bfloat16, 8> : Raw8<__nv_bfloat16> {
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { load_rw(p); }
+};
 
 template <typename T, int V, bool INTER, int P>
 __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_apply_kernel(const RopeArgs a, const __grid_constant__ RopeTurns<P> turns) {

@@ -37,11 +37,13 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 }
 
 template <typename T>
-struct Raw8;  // 8 consecutive elements as loaded
+struct Raw8;  // 8 consecutive elements as loaded: load() through the read-only path, which is for memory that nothing
+              // writes during the kernel; load_rw() plainly, for an operand that the launch may update in place
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load_rw(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void to_f32(float (&v)[8]) const {
     v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
     v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
@@ -57,6 +59,10 @@ struct Raw8<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void load_rw(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void to_f32(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;

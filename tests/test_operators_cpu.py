@@ -216,3 +216,26 @@ def test_argument_checks():
         L._arg("t", t.t(), dev, torch.float32, 6, 4)
     with pytest.raises(ValueError, match="cpu"):
         L._arg("t", t, torch.device("meta"), torch.float32, 4, 6)
+
+
+def test_operands_updated_in_place_are_not_read_through_the_read_only_path():
+    """__ldg is for memory that nothing writes during the kernel.  The header lets h be the residual, dh be dh_in and
+    q and k be rotated in place: the kernels read these operands plainly."""
+    import os
+    import re
+
+    csrc = os.path.join(os.path.dirname(build_ext.__file__), "csrc")
+    read = lambda name: open(os.path.join(csrc, name)).read()  # noqa: E731
+    raw8 = re.findall(r"struct Raw8<\w+> \{.*?\n\};", read("rowwise.cuh"), re.S)
+    assert len(raw8) == 2
+    for body in raw8:
+        plain = re.search(r"void load_rw\(const \w+\* p\) \{(.*?)\}", body, re.S)
+        assert plain and "__ldg" not in plain.group(1)
+    norm = read("rmsnorm.cu")
+    assert re.findall(r"\brr\[i\]\.(\w+)\(res", norm) == ["load_rw"]
+    assert re.findall(r"\bin\[i\]\.(\w+)\(static_cast<const TR\*>\(a\.dh_in\)", norm) == ["load_rw"]
+    rope = read("rope_apply.cu")
+    assert re.search(r"struct Piece<__nv_bfloat16, 8> : Raw8<__nv_bfloat16> \{[^}]*void load\([^)]*\) \{ load_rw\(p\); \}", rope)
+    # the heads themselves are read through Piece and load_v alone, neither of which takes the read-only path
+    assert "__ldg" not in re.search(r"void load_v\(.*?\n\}", rope, re.S).group(0)
+    assert all(m.startswith(("a.cos", "a.sin", "a.pos")) for m in re.findall(r"__ldg\(([^)]*)", rope))

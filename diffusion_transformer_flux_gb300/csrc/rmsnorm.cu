@@ -277,7 +277,7 @@ BwdShape bwd_shape(int rows, int dim) {
   s.nc = chunks <= 256 ? 1 : chunks <= 2 * kNormMaxThreads ? 2 : 4;
   s.threads = norm_threads(chunks, s.nc);
   s.rows = norm_rows(s.threads);
-  const int ctas = (rows + s.rows - 1) / s.rows, most = (s.nc == 1 ? 4 : 2) * num_sms();
+  const int ctas = rows / s.rows + (rows % s.rows != 0), most = (s.nc == 1 ? 4 : 2) * num_sms();
   s.grid = ctas < most ? ctas : most;
   return s;
 }

@@ -239,3 +239,10 @@ def test_operands_updated_in_place_are_not_read_through_the_read_only_path():
     # the heads themselves are read through Piece and load_v alone, neither of which takes the read-only path
     assert "__ldg" not in re.search(r"void load_v\(.*?\n\}", rope, re.S).group(0)
     assert all(m.startswith(("a.cos", "a.sin", "a.pos")) for m in re.findall(r"__ldg\(([^)]*)", rope))
+
+
+def test_norm_gradient_workspace_of_the_most_rows(lib):
+    """The header sets no limit on the rows: the launch shape must not leave 32 bits on the way."""
+    most = L.mmdit_add_rmsnorm_bwd_workspace_size(1 << 20, 8)
+    for rows in ((1 << 31) - 1, (1 << 31) - 7, (1 << 31) - 8):
+        assert L.mmdit_add_rmsnorm_bwd_workspace_size(rows, 8) == most

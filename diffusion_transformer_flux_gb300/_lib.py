@@ -841,6 +841,8 @@ def _workspace_arg(ws, dev, nbytes, stream):
             return workspace(nbytes(), dev)
     if ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the call's tensors are on {dev}")
+    if not ws.is_contiguous():  # its elements are counted as the bytes behind its address
+        raise ValueError("ws must be contiguous")
     return ws
 
 

@@ -246,3 +246,13 @@ def test_norm_gradient_workspace_of_the_most_rows(lib):
     most = L.mmdit_add_rmsnorm_bwd_workspace_size(1 << 20, 8)
     for rows in ((1 << 31) - 1, (1 << 31) - 7, (1 << 31) - 8):
         assert L.mmdit_add_rmsnorm_bwd_workspace_size(rows, 8) == most
+
+
+def test_workspace_of_overlapping_elements_is_refused():
+    """An expanded tensor has fewer bytes than elements; the library would write behind it."""
+    dev = torch.device("cpu")
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(512, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            L._workspace_arg(ws, dev, lambda: 256, None)
+    ws = torch.zeros(512, dtype=torch.uint8)
+    assert L._workspace_arg(ws, dev, lambda: 256, None) is ws

@@ -964,6 +964,8 @@ def _rope_view(name, t, dev, dtype, shape):
 
 
 def _rope(name, cfg, q, q_out, k, k_out, positions, cos, sin, stream):
+    if q_out is None or (k is None) != (k_out is None):
+        raise ValueError("q_out is needed, and k and k_out go together")
     dev, dt = _device(q), q.dtype
     act = act_of(q)
     if q.dim() != 4:

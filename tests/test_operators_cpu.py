@@ -256,3 +256,14 @@ def test_workspace_of_overlapping_elements_is_refused():
             L._workspace_arg(ws, dev, lambda: 256, None)
     ws = torch.zeros(512, dtype=torch.uint8)
     assert L._workspace_arg(ws, dev, lambda: 256, None) is ws
+
+
+@pytest.mark.parametrize("fn", ["mmdit_rope_fwd", "mmdit_rope_bwd"])
+def test_rope_heads_without_their_other_half_are_refused(fn):
+    """k_out without k was taken for a call on q alone and left as it was."""
+    q = torch.zeros(1, 2, 1, 64)
+    for kw in (dict(k_out=q), dict(k=q)):
+        with pytest.raises(ValueError, match="go together"):
+            getattr(L, fn)(L.RopeCfg(), q, q, **kw)
+    with pytest.raises(ValueError, match="q_out"):
+        getattr(L, fn)(L.RopeCfg(), q, None)

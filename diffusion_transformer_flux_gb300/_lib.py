@@ -809,12 +809,20 @@ def _arg(name, t, dev, dtype, *shape):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _raw_stream_getter():
+    """A function from a device's index to the handle of its current stream: torch's own where this version has it
+    (it builds no Stream object), else by way of the public call."""
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+_raw_stream = _raw_stream_getter()
+
+
 def _launch(name, dev, stream, *args):
     """Calls entry point `name` with device `dev` current, on `stream` or on that device's current stream."""
     lib = _lib or load()
-    # the raw handle of the current stream, without the Stream object torch.cuda.current_stream would build
-    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
-    if torch._C._cuda_getDevice() == dev.index:
+    raw = _raw_stream(dev.index) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev.index:
         status = getattr(lib, name)(*args, raw)
     else:
         with torch.cuda.device(dev):

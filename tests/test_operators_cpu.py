@@ -267,3 +267,20 @@ def test_rope_heads_without_their_other_half_are_refused(fn):
             getattr(L, fn)(L.RopeCfg(), q, q, **kw)
     with pytest.raises(ValueError, match="q_out"):
         getattr(L, fn)(L.RopeCfg(), q, None)
+
+
+def test_launch_needs_no_private_name_of_torch(monkeypatch):
+    """On a torch without the private calls the current stream and device come from the public ones."""
+    import types
+
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    seen = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda i=None: types.SimpleNamespace(cuda_stream=70 + (i or 0)))
+    monkeypatch.setattr(L, "_lib", types.SimpleNamespace(f=lambda *a: seen.append(a) or 0))
+    if hasattr(L, "_raw_stream_getter"):
+        monkeypatch.setattr(L, "_raw_stream", L._raw_stream_getter())
+    L._launch("f", torch.device("cuda", 0), None, 1, 2)
+    L._launch("f", torch.device("cuda", 0), 5, 3)
+    assert seen == [(1, 2, 70), (3, 5)]

@@ -1,6 +1,7 @@
 // api.cu -- the C ABI of libmmdit.so (declared in include/mmdit.h): argument validation,
 // workspace planning and the launch sequences of each entry point.  No device memory is
 // allocated here; every buffer comes from the caller.
+#include <float.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -2718,8 +2719,9 @@ mmdit_status mmdit_rope_config(mmdit_rope_cfg* cfg, int32_t rot_dim, int32_t int
     return fail(MMDIT_ERR_UNSUPPORTED, "rope config: rot_dim must be even, 2 to 512 (got %d)", rot_dim);
   if (scaling < MMDIT_ROPE_SCALE_NONE || scaling > MMDIT_ROPE_SCALE_BY_PARTS)
     return fail(MMDIT_ERR_INVALID_ARG, "rope config: unknown scaling %d", scaling);
-  if (!(theta >= 1.0) || !std::isfinite(theta) || !std::isfinite(mscale))
-    return fail(MMDIT_ERR_INVALID_ARG, "rope config: theta must be at least 1, theta and mscale finite");
+  // mscale is held as a float: the double has to be within its range
+  if (!(theta >= 1.0) || !std::isfinite(theta) || !(std::fabs(mscale) <= FLT_MAX))
+    return fail(MMDIT_ERR_INVALID_ARG, "rope config: theta must be at least 1, theta and mscale finite (mscale in float32)");
   if (scaling != MMDIT_ROPE_SCALE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
     return fail(MMDIT_ERR_INVALID_ARG, "rope config: factor must be at least 1 and finite");
   if (scaling == MMDIT_ROPE_SCALE_BY_PARTS &&

@@ -782,7 +782,8 @@ mmdit_status mmdit_fp8_block_linear_bwd(int32_t M, int32_t N, int32_t K, const v
  *                              (high - low), 0, 1): pairs that turn more than `high` times within
  *                              orig_len keep their frequency, those below `low` are interpolated
  * turns[j] is f_j / 2 pi in units of 2^-64: the phase of an integer position is exact modulo a turn.
- * rot_dim even, 2 to 512; theta >= 1, factor >= 1, high > low, orig_len > 0 (BY_PARTS); mscale finite. */
+ * rot_dim even, 2 to 512; theta >= 1, factor >= 1, high > low, orig_len > 0 (BY_PARTS); mscale finite
+ * in float32. */
 typedef enum mmdit_rope_scaling {
   MMDIT_ROPE_SCALE_NONE = 0,
   MMDIT_ROPE_SCALE_LINEAR = 1,

@@ -284,3 +284,11 @@ def test_launch_needs_no_private_name_of_torch(monkeypatch):
     L._launch("f", torch.device("cuda", 0), None, 1, 2)
     L._launch("f", torch.device("cuda", 0), 5, 3)
     assert seen == [(1, 2, 70), (3, 5)]
+
+
+def test_rope_config_refuses_an_mscale_that_float32_cannot_hold(lib):
+    """The configuration keeps mscale as a float: a larger double became infinite."""
+    for m in (1e39, -1e39, 1e308, float("inf")):
+        assert _cfg(lib, mscale=m)[0] == INVALID
+    st, cfg = _cfg(lib, mscale=3e38)
+    assert st == 0 and cfg.mscale == pytest.approx(3e38)

@@ -7,9 +7,11 @@
 //
 // A position far into a context makes p f_j large, and a float32 angle would keep few bits of its
 // fraction of a turn.  The configuration therefore holds f_j / 2 pi as a 64-bit fixed-point fraction of
-// a turn, and the product with the integer position, taken modulo 2^64, is the exact fraction of the
-// angle (negative positions included); its upper 32 bits feed sincospi.  The frequencies' own rounding
-// (2^-53 relative, from the host's double) is then all that is left: 2^-36 of a turn at position 2^20.
+// a turn, and the product with the integer position, taken modulo 2^64, is the exact fraction of its
+// angle (negative positions included).  The fraction's upper 32 bits, as a float32 number of half turns, feed
+// sincospi: off by at most 2^-26 of a turn at every position.  The held frequency is itself rounded, by
+// 5 2^-53 of itself (four operations in double on the host) and the 64th bit, so position p adds
+// |p| (f 5 2^-53 / 2 pi + 2^-64) of a turn: 2^-33 at 2^20, as much as the rest from 2^27 on.
 //
 // Bound by memory: each element read and written once.  Thread (x, y, z) of a CTA takes piece x of heads y,
 // y + blockDim.y, ... of token z: interleaved pieces are 8 elements, half pieces a run of V first elements and the

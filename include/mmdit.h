@@ -781,7 +781,10 @@ mmdit_status mmdit_fp8_block_linear_bwd(int32_t M, int32_t N, int32_t K, const v
  *   MMDIT_ROPE_SCALE_BY_PARTS  f_j (g + (1 - g) / factor), g = clamp((orig_len f_j / 2 pi - low) /
  *                              (high - low), 0, 1): pairs that turn more than `high` times within
  *                              orig_len keep their frequency, those below `low` are interpolated
- * turns[j] is f_j / 2 pi in units of 2^-64: the phase of an integer position is exact modulo a turn.
+ * turns[j] is f_j / 2 pi in units of 2^-64 (from double arithmetic: off by at most 5 2^-53 of itself and one
+ * unit; BY_PARTS, whose ramp magnifies roundings, by factor (5 max(|low|, |high|) / (high - low) + 3) + 8 instead
+ * of 5).  The phase p turns[j] is formed in integers modulo a turn and then rounded to float32: 2^-26 of a
+ * turn at any p, beside p times the frequency's own rounding (2^-33 of a turn at 2^20, 2^-26 at 2^27).
  * rot_dim even, 2 to 512; theta >= 1, factor >= 1, high > low, orig_len > 0 (BY_PARTS); mscale finite
  * in float32. */
 typedef enum mmdit_rope_scaling {
@@ -806,7 +809,7 @@ mmdit_status mmdit_rope_config(mmdit_rope_cfg *cfg, int32_t rot_dim, int32_t int
  * alike; an input's may be zero (broadcast).  An output may be its own input (same ptr and strides: in
  * place) and must overlap no view otherwise; its strides are at least head_dim where the extent is above
  * one.  Angles come from positions [batch, seq] int64 (pos_bstride elements between samples, 0: the same
- * for all; any sign, exact far into a context) or from tables cos, sin [batch, seq, rot_dim / 2] fp32,
+ * for all; any sign; the angle's rounding is given above) or from tables cos, sin [batch, seq, rot_dim / 2] fp32,
  * 16-byte aligned, as rope3d_freqs writes them: exactly one of the two.  cfg and the views are host memory.  head_dim a multiple of 8, at most 512, >= cfg->rot_dim; float32 arithmetic.
  * batch at most 65535, seq at most 2^30; batch * seq == 0 is a no-op.  No workspace. */
 typedef struct mmdit_rope_view {

@@ -8,6 +8,7 @@ reproduced bit for bit; everything else is float64.
 from __future__ import annotations
 
 import math
+from decimal import Decimal, localcontext
 
 import numpy as np
 
@@ -138,6 +139,52 @@ def rope_cos_sin(positions, freqs):
         p = int(pos[idx])
         for j, t in enumerate(turns):
             ang[idx + (j,)] = ((p * t) % one) / one * two_pi
+    return np.cos(ang), np.sin(ang)
+
+
+def _two_pi(digits):
+    """2 pi as a Decimal of so many digits: 4 (4 arctan(1/5) - arctan(1/239)) 2, the series in whole numbers."""
+    one = 10 ** (digits + 10)
+
+    def arctan_inv(n):
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    with localcontext() as ctx:
+        ctx.prec = digits
+        return Decimal(8 * (4 * arctan_inv(5) - arctan_inv(239))) / one
+
+
+def rope_turns_exact(rot, theta=10000.0, scaling="none", factor=1.0, orig_len=0.0, low=1.0, high=4.0):
+    """f_j / 2 pi as Decimals of 80 digits: the frequencies without a double's rounding."""
+    with localcontext() as ctx:
+        ctx.prec = 80
+        theta, factor, orig, lo, hi = (Decimal(v) for v in (theta, factor, orig_len, low, high))
+        two_pi, out = _two_pi(80), []
+        for j in range(rot // 2):
+            f = theta ** (Decimal(-2 * j) / rot)
+            if scaling == "linear":
+                f = f / factor
+            elif scaling == "by_parts":
+                g = min(max((orig * f / two_pi - lo) / (hi - lo), Decimal(0)), Decimal(1))
+                f = f * g + f / factor * (1 - g)
+            out.append(f / two_pi)
+        return out
+
+
+def rope_cos_sin_exact(positions, turns):
+    """cos and sin [..., pairs] of position x exact frequency (rope_turns_exact), reduced in 80 digits."""
+    pos = np.asarray(positions)
+    ang = np.empty(pos.shape + (len(turns),))
+    with localcontext() as ctx:
+        ctx.prec = 80
+        for idx in np.ndindex(pos.shape):
+            for j, t in enumerate(turns):
+                ang[idx + (j,)] = float(int(pos[idx]) * t % 1) * 2.0 * math.pi
     return np.cos(ang), np.sin(ang)
 
 

@@ -654,3 +654,25 @@ def test_layer_of_a_text_model():
     assert torch.equal(h2, proj.float() + h)
     yo, _ = lm.rmsnorm(f64(h2), f64(gain), 1e-6)
     check(f64(y2), yo, (2.0 ** -8 + 300 * U) * np.abs(yo), "second norm")
+
+
+@pytest.mark.parametrize("scaling", ["none", "linear", "by_parts"])
+@pytest.mark.parametrize("start", [0, 1 << 20, (1 << 24) + 1, 1 << 31, (1 << 40) + 7, -(1 << 40) - 7])
+def test_rope_against_exact_frequencies(scaling, start):
+    """Far positions against angles without a double's rounding: the bound that the header states, in radians, on
+    top of the rotation's own."""
+    kw = dict(theta=500000.0, scaling=scaling, factor=16.0, orig_len=8192.0, low=1.0, high=32.0)
+    rot, S = 64, 5
+    pos = start + torch.arange(S)
+    x = make(np.random.default_rng(4), (1, S, 2, rot), torch.float32)
+    out = nans(1, S, 2, rot)
+    L.mmdit_rope_fwd(L.make_rope_cfg(rot, interleaved=False, **kw), x, out, positions=pos.cuda())
+    turns = lm.rope_turns_exact(rot, **kw)
+    cos, sin = lm.rope_cos_sin_exact(pos.numpy()[None], turns)
+    ref = lm.rope(f64(x), cos, sin, rot, False)
+    steps = 16.0 * (5 * 32 / 31 + 3) + 8 if scaling == "by_parts" else 5.0
+    f = np.array([float(t) for t in turns])
+    angle = 2 * np.pi * np.abs(pos.numpy())[:, None] * (f * steps * 2.0 ** -53 + 2.0 ** -64)
+    pair = np.abs(f64(x))[..., :rot // 2] + np.abs(f64(x))[..., rot // 2:]
+    tol = (16 * U + angle)[None, :, None, :] * pair
+    check(f64(out), ref, U * np.abs(ref) + np.concatenate([tol, tol], -1), "rotated")

@@ -676,3 +676,54 @@ def test_rope_against_exact_frequencies(scaling, start):
     pair = np.abs(f64(x))[..., :rot // 2] + np.abs(f64(x))[..., rot // 2:]
     tol = (16 * U + angle)[None, :, None, :] * pair
     check(f64(out), ref, U * np.abs(ref) + np.concatenate([tol, tol], -1), "rotated")
+
+
+@pytest.mark.parametrize("rows,dim", [(5003, 512), (5003, 264), (2500, 2048), (1300, 4096), (700, 5120), (700, 6152),
+                                      (701, 8192), (650, 8200)])
+@pytest.mark.parametrize("act,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_norm_gradients_over_many_rows(rows, dim, act, res):
+    """More rows than the launch has places: a CTA walks several (short ones in groups, the last group partly past the
+    end), with the next row's operands on their way, and in place."""
+    rng = np.random.default_rng(rows + dim)
+    dt, rt = DT[act], DT[res]
+    h, dy = make(rng, (rows, dim), rt, 3.0), make(rng, (rows, dim), dt)
+    gain, dh_in = (1 + 0.2 * make(rng, (dim,), torch.float32)).to(dt), make(rng, (rows, dim), rt)
+    h[1] = 0
+    r32 = (h.double().square().mean(1) + 1e-6).rsqrt().float()
+    dho, dgo = lm.rmsnorm_bwd(f64(dy), f64(h), f64(gain), 1e-6, f64(dh_in))
+    r = f64(r32)[:, None]
+    n, a = f64(h) * r, f64(dy) * f64(gain)
+    # r is half a step off; the row's sum dim u of its magnitudes; ten roundings beside, and the stored type's
+    big = r * (np.abs(a) + np.abs(n) * (np.abs(a * n)).mean(1, keepdims=True))
+    tol = (dim + 16) * U * big + (HALF[rt] + 2 * U) * np.abs(dho)
+    dh, dg, dx = nans(rows, dim, dtype=rt), nans(dim), nans(rows, dim, dtype=dt)
+    ws = L.mmdit_add_rmsnorm_bwd(dy, h, gain, r32, dh, dh_in=dh_in, dx=dx, dgain=dg)
+    check(f64(dh), dho, tol, "dh")
+    check(f64(dx), dho, tol + HALF[dt] * np.abs(dho), "dx")
+    check(f64(dg), dgo, (rows + 16) * U * np.abs(f64(dy) * n).sum(0) + U * np.abs(dgo), "dgain")
+    here, again = dh_in.clone(), nans(dim)
+    L.mmdit_add_rmsnorm_bwd(dy, h, gain, r32, here, dh_in=here, dgain=again, ws=ws)
+    assert torch.equal(here, dh) and torch.equal(again, dg)
+    assert L.mmdit_workspace_status(ws) == 0
+
+
+def test_norm_repeats_itself_and_codes_part_at_borders_alone():
+    """A prompt's norm gives the same bits again after other calls; a code is the nearest one of the float64 value, or
+    its neighbour where that value lies within the row sum's error of the border between them."""
+    rng = np.random.default_rng(12)
+    rows, dim = 4608, 4096
+    x, res, gain = make(rng, (rows, dim)), make(rng, (rows, dim), torch.float32, 3.0), (1 + 0.2 * make(rng, (dim,), torch.float32)).bfloat16()
+    first = None
+    for _ in range(4):
+        h, q, s, r = nans(rows, dim), bytes_(rows, dim), nans(tiles(dim), rows), nans(rows)
+        L.mmdit_add_rmsnorm_fwd(x, gain, residual=res, h=h, y_q=q, s_y=s, rstd=r)
+        L.mmdit_add_rmsnorm_fwd(x.flip(0), gain, residual=res, h=nans(rows, dim), y_q=bytes_(rows, dim), s_y=nans(tiles(dim), rows))
+        first = first or (h, q, s, r)
+        assert all(torch.equal(a, b) for a, b in zip(first, (h, q, s, r)))
+    some = slice(0, rows, 97)
+    yo, _ = lm.rmsnorm(f64(first[0][some]), f64(gain), 1e-6)
+    v = yo * np.repeat(f64(first[2][:, some]).T, 128, 1)
+    got, off = lm.decode(first[1][some].cpu().numpy()), (dim + 8 + 8) * U
+    assert (np.abs(got) >= np.abs(lm.decode(lm.encode(v * (1 - off))))).all()
+    assert (np.abs(got) <= np.abs(lm.decode(lm.encode(v * (1 + off))))).all()
+    assert (np.signbit(got) == np.signbit(v)).all()  # negative values below half a step become -0

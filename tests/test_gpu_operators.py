@@ -727,3 +727,84 @@ def test_norm_repeats_itself_and_codes_part_at_borders_alone():
     assert (np.abs(got) >= np.abs(lm.decode(lm.encode(v * (1 - off))))).all()
     assert (np.abs(got) <= np.abs(lm.decode(lm.encode(v * (1 + off))))).all()
     assert (np.signbit(got) == np.signbit(v)).all()  # negative values below half a step become -0
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (48, 136, 14336), (64, 264, 20496),                # 64 columns, K on eight CTAs: 14 and 21 slices each
+    (40, 5000, 4112), (64, 9800, 2576), (33, 19600, 1040),   # on four, two and one: 9, 11 and 9 slices
+    (24, 5000, 8208), (17, 9800, 5136), (20, 19600, 2064),   # the same with 32 columns
+    (7700, 8, 272), (7700, 24, 272), (7700, 56, 144), (7700, 40, 16),  # outputs narrower than a stored box
+    (7700, 24, 2064), (7940, 264, 2064), (2090, 2568, 1040),  # two pairs to a narrow tile; 9 slices to each of many tiles
+])
+def test_linear_walks_and_narrow_outputs(M, N, K):
+    """Shapes whose rings, product buffers and factor windows come round inside a tile, and outputs of fewer columns
+    than the kernel stores at once, with guard rows around them."""
+    rng, x, w, xq, sx, wq, sw = linear_operands(M + N * 3 + K, M, N, K)
+    b = make(rng, (N,))
+    xv = lm.values_rows(xq.cpu().numpy(), sx.cpu().numpy())
+    wv = lm.values_square(wq.cpu().numpy(), sw.cpu().numpy())
+    r = xv @ wv.T + f64(b)
+    t = sum_tol(xv, wv, tiles(K)) + 2 * U * np.abs(r)
+    ws = L.workspace(256)
+    for dtype in (torch.float32, torch.bfloat16):
+        pad = torch.full((M + 16, N), 7.0, device="cuda", dtype=dtype)
+        L.mmdit_fp8_block_linear_fwd(xq, sx, wq, sw, b, pad[8:M + 8], ws=ws)
+        check(f64(pad[8:M + 8]), r, t + (HALF[dtype] * np.abs(r) + 2.0 ** -8 * t if dtype is torch.bfloat16 else 0), str(dtype))
+        assert (pad[:8] == 7).all() and (pad[M + 8:] == 7).all()
+        again = torch.empty_like(pad)
+        L.mmdit_fp8_block_linear_fwd(xq, sx, wq, sw, b, again[8:M + 8], ws=ws)
+        assert torch.equal(again[8:M + 8], pad[8:M + 8])
+    assert L.mmdit_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(9000, 136, 128), (20000, 40, 144), (9000, 24, 272),  # dW on few tiles: 9 to 20 slices a CTA
+                                   (1000, 2568, 2576)])                                   # more tiles than pairs, of 8 slices
+def test_linear_gradients_of_many_rows(M, N, K):
+    rng, x, w, _, _, wq, sw = linear_operands(M + N * 5 + K, M, N, K)
+    ldm, ldn = (M + 15) // 16 * 16, (N + 15) // 16 * 16
+    dy = make(rng, (M, N), scale=1e-3)
+    wt, xt, sxt = bytes_(K, ldn), bytes_(K, ldm), nans(tiles(M), K)
+    L.mmdit_fp8_block_cast(w, s=sw, q_t=wt, square=True)
+    L.mmdit_fp8_block_cast(x, q_t=xt, s_t=sxt)
+    wqc, swc, xtc, sxtc = (t.cpu().numpy() for t in (wq, sw, xt, sxt))
+    g, gt = lm.values_rows(*lm.cast_rows(f64(dy))), lm.values_rows(*lm.cast_rows(f64(dy).T))
+    wv, xv = lm.values_square(wqc, swc), lm.values_rows(xtc[:, :M], sxtc)
+    dxo, dwo, dbo = g @ wv, gt @ xv.T, f64(dy).sum(0)
+    dx, dw, db = nans(M, K, dtype=torch.bfloat16), nans(N, K), nans(N)
+    ws = L.mmdit_fp8_block_linear_bwd(dy, wt, sw, xt, sxt, dx=dx, dw=dw, db=db)
+    check(f64(dx), dxo, sum_tol(g, wv.T, tiles(N)) * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(dxo), "dx")
+    check(f64(dw), dwo, sum_tol(gt, xv, tiles(M)), "dw")
+    check(f64(db), dbo, (M + 8) * U * np.abs(f64(dy)).sum(0), "db")
+    again = nans(N, K)
+    L.mmdit_fp8_block_linear_bwd(dy, x_t=xt, s_xt=sxt, dw=again, ws=ws)
+    assert torch.equal(again, dw)
+    assert L.mmdit_workspace_status(ws) == 0
+
+
+def test_linear_gradient_against_differences_within_the_casts_roundings():
+    """The slope of <y, dy> along directions in which it is large: the whole gradient's, and those of single quarters
+    of the rows, which a dW that leaves rows out would miss.  The casts' errors e are independent roundings, each at
+    most 2^-4 of its value (2^-10 of the code's unit below the normal range), that enter as
+    sum e_x (dy d) + sum e_dy (x d^T) + sum e_dy d e_x: sums of independent terms of bounds c stay below
+    6 sqrt(sum c^2) but for one time in 10^7."""
+    M, N, K = 256, 128, 128
+    rng, x, w, _, _, _, _ = linear_operands(9, M, N, K)
+    dy = make(rng, (M, N))
+    xt, sxt, dw = bytes_(K, M), nans(2, K), nans(N, K)
+    L.mmdit_fp8_block_cast(x, q_t=xt, s_t=sxt)
+    L.mmdit_fp8_block_linear_bwd(dy, x_t=xt, s_xt=sxt, dw=dw)
+    X, D, W, e = f64(x), f64(dy), f64(w), 1e-3
+
+    def error(v):  # of the codes of v's columns in tiles of 128 rows
+        amax = np.abs(v).reshape(2, 128, -1).max(1)
+        return np.maximum(2.0 ** -4 * np.abs(v), np.repeat(2.0 ** -10 * amax / 448, 128, 0))
+
+    ex, ed = error(X), error(D)
+    parts = [slice(0, M)] + [slice(64 * i, 64 * i + 64) for i in range(4)]
+    for p in parts:
+        d = D[p].T @ X[p] / 16 + 0.1 * rng.standard_normal((N, K))
+        loss = lambda t: float(((X @ (W + t * d).T) * D).sum())  # noqa: E731
+        slope = (loss(e) - loss(-e)) / (2 * e)
+        bar = 6 * np.sqrt((ex ** 2 * (D @ d) ** 2).sum() + (ed ** 2 * (X @ d.T) ** 2).sum() + ((ed ** 2 @ d ** 2) * ex ** 2).sum())
+        assert abs(slope) > 8 * bar
+        assert abs(float((f64(dw) * d).sum()) - slope) <= bar

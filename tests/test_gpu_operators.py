@@ -808,3 +808,97 @@ def test_linear_gradient_against_differences_within_the_casts_roundings():
         bar = 6 * np.sqrt((ex ** 2 * (D @ d) ** 2).sum() + (ed ** 2 * (X @ d.T) ** 2).sum() + ((ed ** 2 @ d ** 2) * ex ** 2).sum())
         assert abs(slope) > 8 * bar
         assert abs(float((f64(dw) * d).sum()) - slope) <= bar
+
+
+@pytest.mark.parametrize("B,S,Hq,Hk,d,rot,inter,act", [
+    (5, 1003, 2, 1, 64, 64, False, "bf16"),   # eight tokens to a CTA, the last one's partly behind the sequence
+    (5, 1003, 2, 1, 64, 64, True, "bf16"),
+    (3, 1537, 1, 1, 96, 20, True, "f32"),
+    (3, 1537, 1, 1, 96, 20, False, "f32"),
+    (2, 1001, 1, 1, 80, 38, False, "bf16"),
+    (1, 3, 70, 10, 256, 256, True, "bf16"),   # more heads than a CTA holds at a time
+    (1, 3, 70, 10, 256, 256, False, "bf16"),
+    (1, 2, 300, 30, 128, 64, True, "f32"),
+])
+def test_rope_of_token_groups_and_many_heads(B, S, Hq, Hk, d, rot, inter, act):
+    cfg, q, k, pos, (qo, ko), cos, sin = rope_case(B + S + d, B, S, Hq, Hk, d, rot, inter, act, start=3)
+    guard = torch.full((B * S * Hq * d + 64,), 7.0, device="cuda", dtype=DT[act])
+    qo = guard[:-64].view(B, S, Hq, d)
+    L.mmdit_rope_fwd(cfg, q, qo, k=k, k_out=ko, positions=pos)
+    rope_check(qo, q, cos, sin, rot, inter, 1.0, False, act)
+    rope_check(ko, k, cos, sin, rot, inter, 1.0, False, act)
+    assert (guard[-64:] == 7).all()
+
+
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("act,d,rot", [("bf16", 128, 128), ("bf16", 80, 20), ("f32", 96, 48), ("f32", 40, 38)])
+def test_rope_in_place_on_a_packed_projection(inter, act, d, rot):
+    """q and k rotated where they lie between each other and v, forward and by tables, then turned back."""
+    B, S, Hq, Hk = 2, 130, 6, 2
+    cfg, q, k, pos, (qo, ko), cos, sin = rope_case(d, B, S, Hq, Hk, d, rot, inter, act, start=70)
+    L.mmdit_rope_fwd(cfg, q, qo, k=k, k_out=ko, positions=pos)
+    packed = q._base if q._base is not None else q
+    packed = packed.view(B, S, (Hq + 2 * Hk) * d)
+    before = packed.clone()
+    L.mmdit_rope_fwd(cfg, q, q, k=k, k_out=k, positions=pos)
+    assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(packed[..., (Hq + Hk) * d:], before[..., (Hq + Hk) * d:])
+    packed.copy_(before)
+    c32, s32 = (torch.from_numpy(t.astype(np.float32)).cuda() for t in (cos, sin))
+    L.mmdit_rope_fwd(cfg, q, q, k=k, k_out=k, cos=c32, sin=s32)
+    x = before[..., :Hq * d].unflatten(-1, (Hq, d))
+    rope_check(q, x, f64(c32), f64(s32), rot, inter, 1.0, False, act)
+    turned, kt = q.clone(), k.clone()
+    L.mmdit_rope_bwd(cfg, q, q, k=k, k_out=k, cos=c32, sin=s32)
+    rope_check(q, turned, f64(c32), f64(s32), rot, inter, 1.0, True, act)
+    rope_check(k, kt, f64(c32), f64(s32), rot, inter, 1.0, True, act)
+
+
+def test_rope_of_k_alone():
+    cfg, q, k, pos, (_, ko), cos, sin = rope_case(3, 2, 9, 3, 2, 64, 64, True, "bf16")
+    none = q[:, :, :0]
+    L.mmdit_rope_fwd(cfg, none, none, k=k, k_out=ko, positions=pos)
+    rope_check(ko, k, cos, sin, 64, True, 1.0, False, "bf16")
+
+
+def test_two_streams_at_once():
+    """Every operator on two streams side by side, each with its own workspace and outputs: the bits of the calls one
+    after another."""
+    M, N, K = 2100, 2568, 1360
+    rng, x, w, xq, sx, wq, sw = linear_operands(31, M, N, K)
+    dy, gain = make(rng, (M, N), scale=1e-3), make(rng, (K,))
+    wt, xt, sxt = bytes_(K, (N + 15) // 16 * 16), bytes_(K, (M + 15) // 16 * 16), nans(tiles(M), K)
+    L.mmdit_fp8_block_cast(w, s=sw, q_t=wt, square=True)
+    L.mmdit_fp8_block_cast(x, q_t=xt, s_t=sxt)
+    heads, pos = x[:, :1344].reshape(1, M, 21, 64), torch.arange(M, device="cuda")
+    cfg, nbytes = L.make_rope_cfg(64), L.mmdit_fp8_block_linear_bwd_workspace_size(M, N, K)
+
+    def buffers():
+        b16 = lambda *s: nans(*s, dtype=torch.bfloat16)  # noqa: E731
+        return dict(y=b16(M, N), y48=b16(48, N), y1=b16(1, N), dx=b16(M, K), dw=nans(N, K), db=nans(N), n=b16(M, K), r=nans(M),
+                    dh=b16(M, K), dg=nans(K), q=bytes_(M, K), s=nans(tiles(K), M), turned=b16(1, M, 21, 64)), L.workspace(nbytes)
+
+    s48, s1 = sx[:, :48].contiguous(), sx[:, :1].contiguous()
+
+    def calls(o, ws):
+        L.mmdit_add_rmsnorm_fwd(x, gain, y=o["n"], rstd=o["r"])
+        L.mmdit_fp8_block_cast(x, o["q"], o["s"])
+        L.mmdit_fp8_block_linear_fwd(xq[:48], s48, wq, sw, None, o["y48"], ws=ws)
+        L.mmdit_fp8_block_linear_fwd(xq, sx, wq, sw, None, o["y"], ws=ws)
+        L.mmdit_fp8_block_linear_fwd(xq[:1], s1, wq, sw, None, o["y1"], ws=ws)
+        L.mmdit_rope_fwd(cfg, heads, o["turned"], positions=pos)
+        L.mmdit_fp8_block_linear_bwd(dy, wt, sw, xt, sxt, dx=o["dx"], dw=o["dw"], db=o["db"], ws=ws)
+        L.mmdit_add_rmsnorm_bwd(x, x, gain, o["r"], o["dh"], dgain=o["dg"], ws=ws)
+
+    want, ws = buffers()
+    calls(want, ws)
+    torch.cuda.synchronize()
+    sides = [(torch.cuda.Stream(), *buffers()) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for stream, o, w_ in sides:
+            with torch.cuda.stream(stream):
+                calls(o, w_)
+    torch.cuda.synchronize()
+    for _, o, w_ in sides:
+        assert all(torch.equal(o[n], want[n]) for n in want)
+        assert L.mmdit_workspace_status(w_) == 0

@@ -936,6 +936,31 @@ cudaError_t run_pair(const BlockGemm& p, const BlockArgs& a, int64_t tiles, cuda
   return cudaGetLastError();
 }
 
+// How many clusters of two pairs have a place at once on the current device.  Fewer than its SMs allow, because a
+// cluster lies within a group of SMs whose number need not be a multiple of four (36 of 38 on 152 SMs).  Asked once
+// per kernel and device.
+template <bool ROW_B, typename TO>
+cudaError_t two_pair_places(int* places) {
+  static std::atomic<int> known[64];  // places + 1
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int had = known[dev & 63].load(std::memory_order_relaxed);
+  if (had > 0) return *places = had - 1, cudaSuccess;
+  auto kern = block_pair_kernel<ROW_B, TO, 2>;
+  static Configured done;
+  if ((e = configure(kern, kPairSmem, done)) != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 4, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4), cfg.blockDim = dim3(kPairThreads), cfg.dynamicSmemBytes = kPairSmem;
+  cfg.attrs = attr, cfg.numAttrs = 1;
+  if ((e = cudaOccupancyMaxActiveClusters(places, kern, &cfg)) != cudaSuccess) return e;
+  known[dev & 63].store(*places + 1, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 // launch_pdl with clusters of `cluster` CTAs along x.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, int threads, int smem, cudaStream_t stream, Args... args) {
@@ -987,7 +1012,7 @@ cudaError_t run_few(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
 // 6.9 against 8.4, x 14336: 16.6 against 13.8).  Many rows: the pair kernel once its tiles occupy about half of the
 // pairs (32 tiles: 512 x 4096 x 4096 21.8 us against 24.9; 16 tiles: 256 x 4096 x 4096 21.9 against 16.5), but not for a
 // quarter of a tile's rows (64 x 12288 x 4096: 22.7 against 17.2); two pairs to a tile where all of them have a place
-// and K is long (512 x 4096 x 14336: 36 us against 61, x 4096: 17.2 against 21.8; 1000 x 1024 x 1024, 8 slices: 10.0
+// at once and K is long (37 tiles on 36 places, 256 x 9472 x 2048: 22.5 us against 13.8; 512 x 4096 x 14336: 36 us against 61, x 4096: 17.2 against 21.8; 1000 x 1024 x 1024, 8 slices: 10.0
 // against 9.6; four pairs, clusters of 8, leave SMs idle: 50), which pays from 16 tiles on if none of them is half
 // empty (256 x 4096 x 14336: 36 us, in the stream kernel 41.5).  Between them the stream kernel, K split while two
 // CTAs to an SM still hold every CTA of the launch (64 x 4096 x 14336: 61, 34, 19, 16 us on 1, 2, 4, 8; 32 x 12288 x
@@ -999,7 +1024,13 @@ cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
       return p.M <= 8 ? run_few<1, TO>(p, a, stream) : run_few<2, TO>(p, a, stream);
   const int64_t pair_tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + kPairN - 1) / kPairN);
   if (pair_tiles > INT32_MAX) return cudaErrorInvalidValue;
-  const bool split = 4 * pair_tiles <= num_sms() && a.num_kb >= 16;
+  bool split = 4 * pair_tiles <= num_sms() && a.num_kb >= 16;
+  if (split) {
+    int places = 0;
+    const cudaError_t e = two_pair_places<ROW_B, TO>(&places);
+    if (e != cudaSuccess) return e;
+    split = pair_tiles <= places;
+  }
   if (p.M > 64 && (pair_tiles >= num_sms() / 5 || (split && p.M > 128 && pair_tiles >= num_sms() / 10)))
     return split ? run_pair<ROW_B, TO, 2>(p, a, pair_tiles, stream) : run_pair<ROW_B, TO, 1>(p, a, pair_tiles, stream);
   const int nt = p.M <= 32 ? 32 : 64;

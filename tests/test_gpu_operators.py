@@ -902,3 +902,32 @@ def test_two_streams_at_once():
     for _, o, w_ in sides:
         assert all(torch.equal(o[n], want[n]) for n in want)
         assert L.mmdit_workspace_status(w_) == 0
+
+
+def test_two_pairs_to_a_tile_only_where_all_have_a_place():
+    """Past the clusters of two pairs that fit at once, a tile more would wait for a second turn of the whole launch
+    (1.8 times the time); one pair to a tile takes 1.1 times the time of the split tiles."""
+    M, K = 256, 2048
+    xq, sx = torch.randint(0, 120, (M, K), device="cuda", dtype=torch.uint8), torch.ones(tiles(K), M, device="cuda")
+
+    def time_of(N):
+        w, sw = torch.randint(0, 120, (N, K), device="cuda", dtype=torch.uint8), torch.ones(tiles(N), tiles(K), device="cuda")
+        y, ws = nans(M, N, dtype=torch.bfloat16), L.workspace(256)
+        call = lambda: L.mmdit_fp8_block_linear_fwd(xq, sx, w, sw, None, y, ws=ws)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        g, took = torch.cuda.CUDAGraph(), []
+        with torch.cuda.graph(g):
+            for _ in range(20):
+                call()
+        for _ in range(25):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.replay()
+            b.record()
+            b.synchronize()
+            took.append(a.elapsed_time(b))
+        return sorted(took)[12]
+
+    times = [time_of(256 * n) for n in range(32, 41)]
+    assert max(b / a for a, b in zip(times, times[1:])) < 1.5, times

@@ -936,11 +936,11 @@ cudaError_t run_pair(const BlockGemm& p, const BlockArgs& a, int64_t tiles, cuda
   return cudaGetLastError();
 }
 
-// How many clusters of two pairs have a place at once on the current device.  Fewer than its SMs allow, because a
-// cluster lies within a group of SMs whose number need not be a multiple of four (36 of 38 on 152 SMs).  Asked once
-// per kernel and device.
+// How many clusters of four SMs the current device has room for at once (two pairs of CTAs, an SM each).  Fewer than its
+// SMs make, because a cluster lies within a group of SMs whose number need not be a multiple of four (36 of 38 on
+// 152 SMs).  Asked once per kernel and device.
 template <bool ROW_B, typename TO>
-cudaError_t two_pair_places(int* places) {
+cudaError_t four_sm_places(int* places) {
   static std::atomic<int> known[64];  // places + 1
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1015,7 +1015,10 @@ cudaError_t run_few(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
 // at once and K is long (37 tiles on 36 places, 256 x 9472 x 2048: 22.5 us against 13.8; 512 x 4096 x 14336: 36 us against 61, x 4096: 17.2 against 21.8; 1000 x 1024 x 1024, 8 slices: 10.0
 // against 9.6; four pairs, clusters of 8, leave SMs idle: 50), which pays from 16 tiles on if none of them is half
 // empty (256 x 4096 x 14336: 36 us, in the stream kernel 41.5).  Between them the stream kernel, K split while two
-// CTAs to an SM still hold every CTA of the launch (64 x 4096 x 14336: 61, 34, 19, 16 us on 1, 2, 4, 8; 32 x 12288 x
+// CTAs to an SM still hold every CTA of the launch, clusters of eight only while each has a place (64 x 4736 x 2048, 37
+// tiles on 36 places: 11.2 us, on clusters of four 7.7; x 14336 27.6 and 25.7.  Clusters of four have 74 places: with 75
+// and 76 tiles they still take 13.2 us where two CTAs take 9.4, which nothing that can be asked of the device foretells)
+// (64 x 4096 x 14336: 61, 34, 19, 16 us on 1, 2, 4, 8; 32 x 12288 x
 // 4096, 96 tiles: 17.5, 14.2, 16.8 on 1, 2, 4).
 template <bool ROW_B, typename TO>
 cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream) {
@@ -1027,7 +1030,7 @@ cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
   bool split = 4 * pair_tiles <= num_sms() && a.num_kb >= 16;
   if (split) {
     int places = 0;
-    const cudaError_t e = two_pair_places<ROW_B, TO>(&places);
+    const cudaError_t e = four_sm_places<ROW_B, TO>(&places);
     if (e != cudaSuccess) return e;
     split = pair_tiles <= places;
   }
@@ -1037,6 +1040,12 @@ cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
   const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + nt - 1) / nt);
   int splits = 1;
   while (splits < 8 && 2 * splits <= a.num_kb && tiles * 2 * splits <= 2 * num_sms()) splits *= 2;
+  if (splits == 8) {  // eight CTAs, two to an SM
+    int places = 0;
+    const cudaError_t e = four_sm_places<ROW_B, TO>(&places);
+    if (e != cudaSuccess) return e;
+    if (tiles > places) splits = 4;
+  }
   return nt == 32 ? run_stream<32, ROW_B, TO>(p, a, splits, stream) : run_stream<64, ROW_B, TO>(p, a, splits, stream);
 }
 

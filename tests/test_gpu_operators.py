@@ -904,13 +904,12 @@ def test_two_streams_at_once():
         assert L.mmdit_workspace_status(w_) == 0
 
 
-def test_two_pairs_to_a_tile_only_where_all_have_a_place():
-    """Past the clusters of two pairs that fit at once, a tile more would wait for a second turn of the whole launch
-    (1.8 times the time); one pair to a tile takes 1.1 times the time of the split tiles."""
-    M, K = 256, 2048
+def linear_times(M, K, widths):
+    """GPU time of one call for each N: the shortest of 60 replays of 20 captured calls, so that nothing else on the
+    machine counts."""
     xq, sx = torch.randint(0, 120, (M, K), device="cuda", dtype=torch.uint8), torch.ones(tiles(K), M, device="cuda")
-
-    def time_of(N):
+    times = []
+    for N in widths:
         w, sw = torch.randint(0, 120, (N, K), device="cuda", dtype=torch.uint8), torch.ones(tiles(N), tiles(K), device="cuda")
         y, ws = nans(M, N, dtype=torch.bfloat16), L.workspace(256)
         call = lambda: L.mmdit_fp8_block_linear_fwd(xq, sx, w, sw, None, y, ws=ws)  # noqa: E731
@@ -920,14 +919,26 @@ def test_two_pairs_to_a_tile_only_where_all_have_a_place():
         with torch.cuda.graph(g):
             for _ in range(20):
                 call()
-        for _ in range(25):
+        for _ in range(60):
             a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             a.record()
             g.replay()
             b.record()
             b.synchronize()
-            took.append(a.elapsed_time(b))
-        return sorted(took)[12]
+            took.append(a.elapsed_time(b) / 20)
+        times.append(min(took))
+    return times
 
-    times = [time_of(256 * n) for n in range(32, 41)]
+
+def test_two_pairs_to_a_tile_only_where_all_have_a_place():
+    """Past the clusters of two pairs that fit at once, a tile more would wait for a second turn of the whole launch
+    (1.8 times the time); one pair to a tile takes 1.1 times the time of the split tiles."""
+    times = linear_times(256, 2048, range(256 * 32, 256 * 41, 256))
     assert max(b / a for a, b in zip(times, times[1:])) < 1.5, times
+
+
+def test_k_on_eight_ctas_only_where_all_clusters_have_a_place():
+    """Few rows: K goes to clusters of eight CTAs while all of them fit at once; one more would cost a second turn of
+    the launch (1.4 times the time), clusters of four take no longer."""
+    times = linear_times(64, 2048, range(128 * 32, 128 * 42, 128))
+    assert max(b / a for a, b in zip(times, times[1:])) < 1.2, times

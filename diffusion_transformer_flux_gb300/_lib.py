@@ -809,20 +809,22 @@ def _arg(name, t, dev, dtype, *shape):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _raw_stream_getter():
-    """A function from a device's index to the handle of its current stream: torch's own where this version has it
-    (it builds no Stream object), else by way of the public call."""
-    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+def _current_getters():
+    """(a function from a device's index to the handle of its current stream, one for the current device's index):
+    torch's inner ones where this version has them (0.08 us against 1.1, as no Stream object is built, and 0.09 against
+    0.22), else the public ones."""
+    return (getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream),
+            getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
 
 
-_raw_stream = _raw_stream_getter()
+_raw_stream, _current_device = _current_getters()
 
 
 def _launch(name, dev, stream, *args):
     """Calls entry point `name` with device `dev` current, on `stream` or on that device's current stream."""
     lib = _lib or load()
     raw = _raw_stream(dev.index) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         status = getattr(lib, name)(*args, raw)
     else:
         with torch.cuda.device(dev):

@@ -279,8 +279,9 @@ def test_launch_needs_no_private_name_of_torch(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda i=None: types.SimpleNamespace(cuda_stream=70 + (i or 0)))
     monkeypatch.setattr(L, "_lib", types.SimpleNamespace(f=lambda *a: seen.append(a) or 0))
-    if hasattr(L, "_raw_stream_getter"):
-        monkeypatch.setattr(L, "_raw_stream", L._raw_stream_getter())
+    if hasattr(L, "_current_getters"):
+        for name, get in zip(("_raw_stream", "_current_device"), L._current_getters()):
+            monkeypatch.setattr(L, name, get)
     L._launch("f", torch.device("cuda", 0), None, 1, 2)
     L._launch("f", torch.device("cuda", 0), 5, 3)
     assert seen == [(1, 2, 70), (3, 5)]

@@ -36,8 +36,9 @@ struct BlockCastArgs {
 };
 
 // A thread keeps its 32 elements as they were loaded (16 registers for bf16) and turns them into floats where it
-// needs them, so that three CTAs share an SM: 4095 x 4096 bf16 both ways in 16.4 us, 4.1 TB/s (256 threads with 64 elements
-// each: 17.5 us, as floats 23.3).
+// needs them, so that three CTAs share an SM: 4095 x 4096 bf16 both ways in 16.9 us, 4.0 TB/s, one way in 10.8 or 11.7, in
+// 128 x 128 tiles both ways 14.7 (256 threads with 64 elements each: 17.5 us, as floats 23.3).  40 registers are what
+// three CTAs leave; 20 to 24 bytes are spilled for them.
 constexpr int kCastThreads = 512, kRows = 4, kGroups = kTile / kRows;
 template <typename T, bool SQUARE>
 __global__ void __launch_bounds__(kCastThreads, sizeof(T) == 2 ? 3 : 2) block_cast_kernel(const BlockCastArgs a) {

@@ -15,10 +15,12 @@
 // timer, a warp's scales come through a ring of asynchronous copies, and the issuers run on whole warps.
 // Each promotion thread holds a row's 128 float32 sums in registers (setmaxnreg moves them over from the
 // other warpgroup); the scales' ring runs on from tile to tile, and the outputs leave through shared memory by
-// TMA.  8192^3: 464 us, 2.37 PFLOP/s; 4608 x 12288 x 4096 with bias: 208 us, 2.23 PFLOP/s (a ring that starts anew
-// with each tile 492 and 227 us, with it but each thread storing its own row 472 and 218; at that first step the
-// loop without the multiply-adds took 420 and 196 us, without reading TMEM either 332 and 156, with one N = 256 MMA
-// and barrier per slice 558 and 256, with barriers for quarters of 64 columns 668 and 299).
+// TMA.  From captured graphs 8192^3 takes 468 us, 2.35 PFLOP/s (480 to 489 back to back), and 4608 x 12288 x 4096 with
+// bias 210 us, 2.21 PFLOP/s (launched one by one 219).  When they took 464 and 208, a ring that started anew with each
+// tile took 492 and 227 us, with it but each thread storing its own row 472 and 218; at that first step the loop without
+// the multiply-adds took 420 and 196 us, without reading TMEM either 332 and 156, with one N = 256 MMA and barrier per
+// slice 558 and 256, with barriers for quarters of 64 columns 668 and 299.  The sums and loads fill the 232 registers:
+// 12 to 24 bytes of each form are spilled.
 //
 // block_stream_kernel (tens of rows, or too few tiles for the pairs): B's bytes are the cost, so the roles are
 // turned: 128 rows of B are the MMA's M side and 32 or 64 rows of A its N side, four slices' products in TMEM,
@@ -30,7 +32,7 @@
 // block_few_kernel (up to 16 rows): B streams through rings of asynchronous copies that every warp keeps for
 // itself, straight into the register layout of mma.sync.  At these sizes the tensor cores' rate does not count
 // and the latency does: no TMEM to allocate, no barrier and no cluster between the first copy and the sums.
-// 1 x 12288 x 4096: 11.2 us, 4.5 TB/s, of which 2 are the launch; 1 x 1024 x 1024: 2.2 us.
+// 1 x 12288 x 4096: 11.4 us, 4.4 TB/s, of which 2 are the launch; 1 x 1024 x 1024: 2.2 us.
 //
 // Every wait is bounded (common.cuh); after one gives up the remaining barriers are still met, so no
 // thread is left behind.
@@ -1007,19 +1009,28 @@ cudaError_t run_few(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream)
   return cudaGetLastError();
 }
 
-// Which kernel.  Few rows: up to 8 rows of A, or 16 with K up to 8192, the weights' bytes and the launch are the
-// cost (1 x 6144 x 4096: 6.7 us against 9.4 in the stream kernel, 1 x 1024 x 1024: 2.2 against 4.4, 16 x 4096 x 4096:
-// 6.9 against 8.4, x 14336: 16.6 against 13.8).  Many rows: the pair kernel once its tiles occupy about half of the
-// pairs (32 tiles: 512 x 4096 x 4096 21.8 us against 24.9; 16 tiles: 256 x 4096 x 4096 21.9 against 16.5), but not for a
-// quarter of a tile's rows (64 x 12288 x 4096: 22.7 against 17.2); two pairs to a tile where all of them have a place
-// at once and K is long (37 tiles on 36 places, 256 x 9472 x 2048: 22.5 us against 13.8; 512 x 4096 x 14336: 36 us against 61, x 4096: 17.2 against 21.8; 1000 x 1024 x 1024, 8 slices: 10.0
-// against 9.6; four pairs, clusters of 8, leave SMs idle: 50), which pays from 16 tiles on if none of them is half
-// empty (256 x 4096 x 14336: 36 us, in the stream kernel 41.5).  Between them the stream kernel, K split while two
-// CTAs to an SM still hold every CTA of the launch, clusters of eight only while each has a place (64 x 4736 x 2048, 37
-// tiles on 36 places: 11.2 us, on clusters of four 7.7; x 14336 27.6 and 25.7.  Clusters of four have 74 places: with 75
-// and 76 tiles they still take 13.2 us where two CTAs take 9.4, which nothing that can be asked of the device foretells)
-// (64 x 4096 x 14336: 61, 34, 19, 16 us on 1, 2, 4, 8; 32 x 12288 x
-// 4096, 96 tiles: 17.5, 14.2, 16.8 on 1, 2, 4).
+// Which kernel, with both sides of each rule (GPU times from captured graphs, M x N x K).
+// Up to 8 rows, or 16 with K up to 8192, the few-row kernel, as the weights' bytes and the launch are the cost: 1 x 6144
+// x 4096 5.7 us against 8.1 in the stream kernel, 1 x 1024 x 1024 2.2 against 4.3, 8 x 4096 x 14336 14.6 against 14.4, 16 x
+// 4096 x 4096 6.1 against 7.1, x 6144 8.0 against 7.9, x 8192 10.2 against 8.9, x 14336 18.2 against 14.4.  (With 9 to 16
+// rows and more columns the border lies lower than the rule has it: 16 x 8192 x 4096 10.5 against 9.2, x 8192 20.1
+// against 15.8.)
+// From 65 rows on the pair kernel once its tiles take 2 of 5 pairs: 32 tiles, 512 x 4096 x 4096 16.6 us against 26.2, x
+// 1024 9.9 against 10.4; tiles half empty, 128 x 7936 x 4096 16.9 against 18.3, 96 x 12288 x 4096 23.0 against 26.7; a
+// quarter full, 64 x 12288 x 4096 22.8 against 19.1; fewer tiles, 128 x 6144 x 4096 (24) 16.1 against 17.0, 128 x 4096 x
+// 4096 (16) 15.9 against 10.5.
+// Two pairs to a tile from 16 slices on where all of them have a place at once: 512 x 4096 x 14336 36.7 us against 61.3 on
+// one, x 2048 12.6 against 13.8, x 1536 (12 slices) 11.6 against 11.9, x 1024 10.6 against 9.9; 37 tiles on 36 places,
+// 256 x 9472 x 2048, 22.5 against 13.8; four pairs, clusters of eight, left SMs idle.  It pays from 16 tiles on if none of
+// them is half empty: 256 x 4096 x 14336 36.0 us against 43.6 in the stream kernel, x 4096 15.8 against 16.6; half empty,
+// 128 x 4096 x 14336 35.9 against 25.7.
+// With row scales (dW, times with the gradient's cast) the stream kernel comes nearer: 32 tiles of 2048 x 1024, 32 slices 29.5
+// us against 33.4, 16 19.0 against 18.7, 8 15.1 against 12.6; 16 tiles of 1024 x 1024, 32 slices 25.1 against 19.7.
+// Between them the stream kernel, K split while two CTAs to an SM still hold every CTA of the launch (64 x 4096 x 14336:
+// 68.5, 38.0, 22.2, 17.8 us on 1, 2, 4, 8; 32 x 12288 x 4096, 96 tiles: 18.3, 14.5, 17.1 on 1, 2, 4), clusters of eight only
+// while each has a place (64 x 4736 x 2048, 37 tiles on 36 places: 11.2 us, on clusters of four 7.7; x 14336 27.6 and
+// 25.7).  Clusters of four had 74 places: with 75 and 76 tiles they take 13.2 us where two CTAs take 9.4, which
+// nothing that can be asked of the device foretells.
 template <bool ROW_B, typename TO>
 cudaError_t run_any(const BlockGemm& p, const BlockArgs& a, cudaStream_t stream) {
   if constexpr (!ROW_B)

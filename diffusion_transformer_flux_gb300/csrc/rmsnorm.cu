@@ -5,12 +5,12 @@
 // the value that is normalised, so a backward pass that reads the stored h sees the same row),
 //   r = 1 / sqrt(mean(h^2) + eps),   y = h r g,
 // and y is written in the activation type, as E4M3 codes in 1 x 128 tiles with the scales of
-// fp8_block_scale (block_scale.cuh), or both; the codes are cast from the float32 y, not from its
+// block_scale (block_scale.cuh), or both; the codes are cast from the float32 y, not from its
 // bf16 rounding.
 // Backward, with n = h r and a = dy g:   dh = r (a - n mean(a n)) + dh_in,   dg = sum over rows of dy n.
 //
-// Both are bound by memory: one row per CTA, read once into registers in 16-byte pieces, every
-// statistic in float32.  A row of `dim` elements is dim / 8 chunks; thread t holds chunks t, t + T, ...
+// Both are bound by memory: a row to a CTA (of short rows several), read once into registers in 16-byte pieces,
+// every statistic in float32.  A row of `dim` elements is dim / 8 chunks; thread t holds chunks t, t + T, ...
 // (T threads, at most 4 chunks each), so a 128-wide tile's 16 chunks lie in 16 neighbouring lanes and
 // its amax is four shuffles.
 #include "block_scale.cuh"
@@ -135,7 +135,7 @@ struct NormBwdArgs {
 // A CTA holds blockDim.y groups of blockDim.x threads; group k of all groups takes rows k, k + groups, ... and
 // keeps its share of dg in registers.  A row's operands stay packed as they were loaded while the row's sum is
 // formed (12 registers per 8 bf16 elements instead of 24 float32 ones) and the next row's are already on
-// their way, so two CTAs to an SM keep the memory busy: 4095 x 5120 bf16 in 32.8 us, 5.1 TB/s, the sums of dg and
+// their way, so two CTAs to an SM keep the memory busy: 4095 x 5120 bf16 in 33.1 us, 5.1 TB/s, the sums of dg and
 // their second kernel included (floats kept across the sum, no prefetch: 60 us).
 template <typename T, typename TR, int NC, int MAX>
 __global__ void __launch_bounds__(MAX, MAX <= 320 ? 2 : 1) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
@@ -266,8 +266,13 @@ cudaError_t run_fwd(const NormFwdArgs& a, cudaStream_t stream) {
                     stream, a);
 }
 
-// The backward's launch: chunks per thread, threads of a row, rows of a CTA and CTAs: as many as stay resident
-// (four to an SM with one chunk per thread, two with two), each with its sums of dg.
+// The backward's launch: chunks per thread, threads of a row, rows of a CTA and CTAs, each with its sums of dg: four
+// CTAs to an SM with one chunk per thread, two otherwise.  By registers fewer stay resident: three with one chunk (72;
+// with a float32 stream two, 93 to 96), two of up to 320 threads with more, one of the 512-thread forms (111 to 128).
+// Where the launch has more than that, its last turn is partly empty: 20479 x 1024 bf16 42.6 us, 3.9 TB/s, 3411 x
+// 6144 38.6 us, 4.4 TB/s (5119 x 4096 and 4095 x 5120, whose CTAs all stay: 33 us, 5.1 TB/s).  320 threads is what
+// two CTAs of 96 registers have room for; for them the float32-stream forms spill 76 and 204 bytes (4095 x 5120 with
+// a float32 stream: 61.0 us, 4.8 TB/s; 5119 x 4096 50.3 us, 5.8 TB/s).
 struct BwdShape {
   int nc, threads, rows, grid;
 };

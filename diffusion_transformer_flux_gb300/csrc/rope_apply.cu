@@ -18,8 +18,10 @@
 // V second ones, V the largest of 8, 4, 2, 1 that divides rot_dim / 2; the pieces behind rot_dim pass.  The first
 // heads' loads are on their way while the CTA forms its tokens' cos and sin in shared memory, once for all
 // heads.  A CTA holds as many heads as it has threads for, and more tokens where a token has few: 2 x 4608
-// tokens of 32 + 8 heads of 128, interleaved, in 32.8 us, 5.7 TB/s (a CTA that walks four tokens in turn: 75 us,
-// one list of items with divided indices: 51, 64-bit divisions of the token alone: 41).  A piece is read before it is written by the same thread, so the rotation may be done
+// tokens of 32 + 8 heads of 128, interleaved, in 32.5 us, 5.8 TB/s (a CTA that walks four tokens in turn: 75 us,
+// one list of items with divided indices: 51, 64-bit divisions of the token alone: 41).  V of 2 and 1 load and store
+// single elements, behind rot_dim too: 2 x 4608 tokens of 40 heads of 80 with 20 rotated take 82.9 us in the half
+// layout, interleaved 24.7.  A piece is read before it is written by the same thread, so the rotation may be done
 // in place.
 #include <algorithm>
 

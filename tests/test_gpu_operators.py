@@ -942,3 +942,49 @@ def test_k_on_eight_ctas_only_where_all_clusters_have_a_place():
     the launch (1.4 times the time), clusters of four take no longer."""
     times = linear_times(64, 2048, range(128 * 32, 128 * 42, 128))
     assert max(b / a for a, b in zip(times, times[1:])) < 1.2, times
+
+
+FIRST_CALLS = """
+import torch
+from diffusion_transformer_flux_gb300 import _lib as L
+t = lambda n: (n + 127) // 128
+codes = lambda *s: torch.randint(0, 120, s, device="cuda", dtype=torch.uint8)
+ones, ws = lambda *s: torch.ones(*s, device="cuda"), L.workspace(64 << 20)
+todo = []
+for M, N, K in ((1, 1024, 1024), (48, 4096, 4096), (1024, 4096, 1024), (512, 4096, 4096)):
+    x, sx, w, sw, y = codes(M, K), ones(t(K), M), codes(N, K), ones(t(N), t(K)), torch.zeros(M, N, device="cuda")
+    todo.append((y, lambda x=x, sx=sx, w=w, sw=sw, y=y: L.mmdit_fp8_block_linear_fwd(x, sx, w, sw, None, y, ws=ws)))
+M, N, K = 1000, 1024, 2048
+dy, wt, sw, xt, sxt = torch.randn(M, N, device="cuda").bfloat16(), codes(K, N), ones(t(N), t(K)), codes(K, 1008), ones(t(M), K)
+dw, dx = torch.zeros(N, K, device="cuda"), torch.zeros(M, K, device="cuda", dtype=torch.bfloat16)
+todo.append((dw, lambda: L.mmdit_fp8_block_linear_bwd(dy, wt, sw, xt, sxt, dx=dx, dw=dw, ws=ws)))
+h, gain = torch.randn(100, 4096, device="cuda").bfloat16(), torch.ones(4096, device="cuda", dtype=torch.bfloat16)
+n, r, dh = torch.zeros_like(h), torch.ones(100, device="cuda"), torch.zeros_like(h)
+todo.append((n, lambda: L.mmdit_add_rmsnorm_fwd(h, gain, y=n)))
+todo.append((dh, lambda: L.mmdit_add_rmsnorm_bwd(h, h, gain, r, dh, ws=ws)))
+q, pos, cfg = torch.randn(2, 100, 4, 64, device="cuda"), torch.arange(100, device="cuda"), L.make_rope_cfg(64)
+o = torch.zeros_like(q)
+todo.append((o, lambda: L.mmdit_rope_fwd(cfg, q, o, positions=pos)))
+torch.cuda.synchronize()
+for i, (out, call) in enumerate(todo):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    graph.replay()
+    first = out.clone()
+    out.zero_()
+    call()
+    assert first.count_nonzero() and torch.equal(first, out), i
+assert L.mmdit_workspace_status(ws) == 0
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    """What a call asks of the device once (kernel sizes, places of clusters) may be asked while a graph is captured."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]

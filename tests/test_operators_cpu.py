@@ -293,3 +293,20 @@ def test_rope_config_refuses_an_mscale_that_float32_cannot_hold(lib):
         assert _cfg(lib, mscale=m)[0] == INVALID
     st, cfg = _cfg(lib, mscale=3e38)
     assert st == 0 and cfg.mscale == pytest.approx(3e38)
+
+
+def test_rope_config_holds_the_exact_frequencies_to_its_bound(lib):
+    """turns[j] against f_j / 2 pi without a double's rounding, at the bound that the header states."""
+    from decimal import Decimal
+
+    from oracle import lm
+
+    for rot, kw in ((128, dict()), (64, dict(theta=500000.0)), (96, dict(scaling="linear", factor=3.7)),
+                    (128, dict(theta=500000.0, scaling="by_parts", factor=16.0, orig_len=8192.0, low=1.0, high=32.0)),
+                    (128, dict(scaling="by_parts", factor=40.0, orig_len=4096.0, low=1.0, high=4.0))):
+        cfg = L.make_rope_cfg(rot, **kw)
+        steps = 5.0
+        if kw.get("scaling") == "by_parts":
+            steps = kw["factor"] * (5 * kw["high"] / (kw["high"] - kw["low"]) + 3) + 8
+        for j, t in enumerate(lm.rope_turns_exact(rot, **kw)):
+            assert abs(Decimal(cfg.turns[j]) - t * 2 ** 64) <= 1 + Decimal(steps) * t * 2 ** 11

@@ -137,22 +137,3 @@ def test_rope_exact_frequencies_and_angles():
     assert np.allclose(cos[[0, 2], 0], np.cos([3.0, -5.0]), atol=1e-15) and np.allclose(sin[[0, 2], 0], np.sin([3.0, -5.0]), atol=1e-15)
     # p 2^-12 at p = 2^40 + 7 is 2^28 + 7 2^-12: exact in a double, whose cosine math.cos reduces exactly
     assert abs(cos[1, 1] - math.cos(2.0 ** 28 + 7 * 2.0 ** -12)) < 1e-14 and abs(sin[1, 1] - math.sin(2.0 ** 28 + 7 * 2.0 ** -12)) < 1e-14
-
-
-def test_rope_config_holds_the_exact_frequencies_to_its_bound():
-    """turns[j] against f_j / 2 pi without a double's rounding, at the bound that the header states."""
-    from decimal import Decimal
-
-    from diffusion_transformer_flux_gb300 import _lib as L
-    from diffusion_transformer_flux_gb300 import build_ext
-
-    build_ext.build()
-    for rot, kw in ((128, dict()), (64, dict(theta=500000.0)), (96, dict(scaling="linear", factor=3.7)),
-                    (128, dict(theta=500000.0, scaling="by_parts", factor=16.0, orig_len=8192.0, low=1.0, high=32.0)),
-                    (128, dict(scaling="by_parts", factor=40.0, orig_len=4096.0, low=1.0, high=4.0))):
-        cfg = L.make_rope_cfg(rot, **kw)
-        steps = 5.0
-        if kw.get("scaling") == "by_parts":
-            steps = kw["factor"] * (5 * kw["high"] / (kw["high"] - kw["low"]) + 3) + 8
-        for j, t in enumerate(lm.rope_turns_exact(rot, **kw)):
-            assert abs(Decimal(cfg.turns[j]) - t * 2 ** 64) <= 1 + Decimal(steps) * t * 2 ** 11

@@ -47,6 +47,9 @@ EXPORTED = [
     "mmdit_fp8_block_cast", "mmdit_fp8_block_linear_workspace_size", "mmdit_fp8_block_linear_fwd",
     "mmdit_fp8_block_linear_bwd_workspace_size", "mmdit_fp8_block_linear_bwd",
     "mmdit_rope_config", "mmdit_rope_fwd", "mmdit_rope_bwd",
+    "mmdit_varlen_attention_workspace_size", "mmdit_varlen_attention_fwd",
+    "mmdit_varlen_attention_bwd_workspace_size", "mmdit_varlen_attention_bwd",
+    "mmdit_paged_attention_workspace_size", "mmdit_paged_attention_fwd", "mmdit_block_tables", "mmdit_kv_cache_write",
 ]
 
 
@@ -140,7 +143,16 @@ class RopeView(C.Structure):
     _fields_ = [("ptr", VP), ("stride_b", I64), ("stride_s", I64), ("stride_h", I64)]
 
 
+class HeadsView(C.Structure):
+    _fields_ = [("ptr", VP), ("stride_t", I64), ("stride_h", I64)]
+
+
+class PagesView(C.Structure):
+    _fields_ = [("ptr", VP), ("stride_page", I64), ("stride_t", I64), ("stride_h", I64)]
+
+
 ROPE_SCALINGS = ("none", "linear", "by_parts")  # mmdit_rope_scaling
+PHEADS, PPAGES = C.POINTER(HeadsView), C.POINTER(PagesView)
 PROPE, PVIEW, F64 = C.POINTER(RopeCfg), C.POINTER(RopeView), C.c_double
 PCOND, PFLUXC, PFLUXW = C.POINTER(CondW), C.POINTER(FluxConfig), C.POINTER(FluxW)
 
@@ -220,6 +232,17 @@ _SIGS = {
                                  VP]),
     "mmdit_rope_bwd": (C.c_int, [I32, PROPE, I32, I32, I32, I32, PVIEW, PVIEW, I32, PVIEW, PVIEW, VP, I64, VP, VP,
                                  VP]),
+    "mmdit_varlen_attention_workspace_size": (SZ, [I32, I32, I32]),
+    "mmdit_varlen_attention_fwd": (C.c_int, [I32, I32, I32, I32, I32, I32, I32, F32, PHEADS, PHEADS, PHEADS, VP, VP, PHEADS,
+                                             VP, VP, SZ, VP]),
+    "mmdit_varlen_attention_bwd_workspace_size": (SZ, [I32, I32, I32]),
+    "mmdit_varlen_attention_bwd": (C.c_int, [I32, I32, I32, I32, I32, I32, I32, F32, PHEADS, PHEADS, PHEADS, PHEADS, PHEADS, VP,
+                                             VP, VP, PHEADS, PHEADS, PHEADS, VP, SZ, VP]),
+    "mmdit_paged_attention_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+    "mmdit_paged_attention_fwd": (C.c_int, [I32, I32, I32, I32, I32, F32, PHEADS, PPAGES, PPAGES, I32, I32, VP, I32, VP, VP,
+                                            I32, I32, PHEADS, VP, VP, SZ, VP]),
+    "mmdit_block_tables": (C.c_int, [I32, I32, I32, I32, VP, VP, VP, VP, VP, VP, VP, I32, VP, VP, VP, VP]),
+    "mmdit_kv_cache_write": (C.c_int, [I32, I32, I32, PHEADS, PHEADS, PPAGES, PPAGES, I32, I32, VP, VP]),
 }
 
 _lib = None
@@ -1011,3 +1034,143 @@ def mmdit_rope_fwd(cfg: RopeCfg, q, q_out, k=None, k_out=None, positions=None, c
 def mmdit_rope_bwd(cfg: RopeCfg, dq, dq_out, k=None, k_out=None, positions=None, cos=None, sin=None, stream=None):
     """The gradient of mmdit_rope_fwd: dq (and k = dk) [B, S, H, d] of the rotated heads into those of q and k."""
     _rope("mmdit_rope_bwd", cfg, dq, dq_out, k, k_out, positions, cos, sin, stream)
+
+
+def _heads_view(name, t, dev, tokens=None, heads=None, d=None):
+    """The view of a tensor [T, H, d] bf16 with adjacent head elements; sizes that are given must be its own."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    if t.dim() != 3 or (tokens is not None and t.shape[0] != tokens) or (heads is not None and t.shape[1] != heads) or (
+            d is not None and t.shape[2] != d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens or 'T', heads or 'H', d or 'd')}")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a head must be adjacent")
+    return HeadsView(t.data_ptr(), st, sh)
+
+
+def _pages_view(name, t, dev, shape=None, heads=None, d=None):
+    """The view of a cache [pages, page size, H, d] bf16 with adjacent head elements."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    if t.dim() != 4 or (shape is not None and t.shape != shape) or (heads is not None and t.shape[2] != heads) or (
+            d is not None and t.shape[3] != d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{tuple(shape) if shape is not None else ('pages', 'page size', heads or 'H', d or 'd')}")
+    sp, st, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name}: the elements of a head must be adjacent")
+    return PagesView(t.data_ptr(), sp, st, sh)
+
+
+def mmdit_varlen_attention_workspace_size(tokens_q, heads_q, head_dim) -> int:
+    return load().mmdit_varlen_attention_workspace_size(tokens_q, heads_q, head_dim)
+
+
+def mmdit_varlen_attention_fwd(q, k, v, out, cu_q, cu_k=None, lse=None, causal=True, scale=None, ws=None, stream=None):
+    """Attention over packed sequences: q, out [Tq, Hq, d], k, v [Tk, Hk, d] bf16 (views with adjacent head elements);
+    sequence b's queries are rows cu_q[b] .. cu_q[b + 1] (int32 [B + 1]), its keys rows cu_k[b] .. (cu_q's without cu_k).
+    lse [Tq, Hq] fp32 for the backward; scale 1 / sqrt(d) by default."""
+    dev = _device(q)
+    vq = _heads_view("q", q, dev)
+    Tq, Hq, d = q.shape
+    vk = _heads_view("k", k, dev, d=d)
+    Tk, Hk = k.shape[0], k.shape[1]
+    B = cu_q.shape[0] - 1
+    ws = _workspace_arg(ws, dev, lambda: mmdit_varlen_attention_workspace_size(Tq, Hq, d), stream)
+    cq = _arg("cu_q", cu_q, dev, torch.int32, B + 1)
+    _launch("mmdit_varlen_attention_fwd", dev, stream, B, Tq, Tk, Hq, Hk, d, int(bool(causal)),
+            d ** -0.5 if scale is None else float(scale), vq, vk, _heads_view("v", v, dev, Tk, Hk, d), cq,
+            cq if cu_k is None else _arg("cu_k", cu_k, dev, torch.int32, B + 1), _heads_view("out", out, dev, Tq, Hq, d),
+            _arg("lse", lse, dev, torch.float32, Tq, Hq), ws.data_ptr(), ws.numel())
+    return ws
+
+
+def mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) -> int:
+    return load().mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim)
+
+
+def mmdit_varlen_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, cu_q, cu_k=None, causal=True, scale=None, ws=None,
+                               stream=None):
+    """Gradients of mmdit_varlen_attention_fwd: dq [Tq, Hq, d], dk, dv [Tk, Hk, d] bf16 (views) from dout and from the
+    forward's out and lse [Tq, Hq] fp32."""
+    dev = _device(q)
+    vq = _heads_view("q", q, dev)
+    Tq, Hq, d = q.shape
+    vk = _heads_view("k", k, dev, d=d)
+    Tk, Hk = k.shape[0], k.shape[1]
+    B = cu_q.shape[0] - 1
+    ws = _workspace_arg(ws, dev, lambda: mmdit_varlen_attention_bwd_workspace_size(Tq, Hq, d), stream)
+    cq = _arg("cu_q", cu_q, dev, torch.int32, B + 1)
+    _launch("mmdit_varlen_attention_bwd", dev, stream, B, Tq, Tk, Hq, Hk, d, int(bool(causal)),
+            d ** -0.5 if scale is None else float(scale), _heads_view("dout", dout, dev, Tq, Hq, d), vq, vk,
+            _heads_view("v", v, dev, Tk, Hk, d), _heads_view("out", out, dev, Tq, Hq, d),
+            _arg("lse", lse, dev, torch.float32, Tq, Hq), cq,
+            cq if cu_k is None else _arg("cu_k", cu_k, dev, torch.int32, B + 1), _heads_view("dq", dq, dev, Tq, Hq, d),
+            _heads_view("dk", dk, dev, Tk, Hk, d), _heads_view("dv", dv, dev, Tk, Hk, d), ws.data_ptr(), ws.numel())
+    return ws
+
+
+def mmdit_paged_attention_workspace_size(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv) -> int:
+    return load().mmdit_paged_attention_workspace_size(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv)
+
+
+def mmdit_paged_attention_fwd(q, k_cache, v_cache, out, tables, kv_lens, cu_q, lse=None, scale=None, max_q=None, max_kv=None,
+                              ws=None, stream=None):
+    """Causal attention of new tokens q [Tq, Hq, d] bf16 (sequence b's rows cu_q[b] .. cu_q[b + 1]) over the kv_lens[b] tokens
+    of their requests, which lie in pages tables[b] (int32 [B, width]) of k_cache, v_cache [pages, page size, Hk, d].
+    max_q and max_kv bound a request's new tokens and all its tokens (by default all of q's, and the tables' reach)."""
+    dev = _device(q)
+    vq = _heads_view("q", q, dev)
+    Tq, Hq, d = q.shape
+    vk = _pages_view("k_cache", k_cache, dev, d=d)
+    n_pages, page, Hk, _ = k_cache.shape
+    if tables.dim() != 2:
+        raise ValueError("tables must be [B, width]")
+    B, width = tables.shape
+    max_q = Tq if max_q is None else int(max_q)
+    max_kv = width * page if max_kv is None else int(max_kv)
+    ws = _workspace_arg(ws, dev, lambda: mmdit_paged_attention_workspace_size(Tq, B, Hq, Hk, d, max_q, min(max_kv, width * page)),
+                        stream)
+    _launch("mmdit_paged_attention_fwd", dev, stream, B, Tq, Hq, Hk, d, d ** -0.5 if scale is None else float(scale), vq, vk,
+            _pages_view("v_cache", v_cache, dev, k_cache.shape), n_pages, page,
+            _arg("tables", tables, dev, torch.int32, B, width), width, _arg("kv_lens", kv_lens, dev, torch.int32, B),
+            _arg("cu_q", cu_q, dev, torch.int32, B + 1), max_q, max_kv, _heads_view("out", out, dev, Tq, Hq, d),
+            _arg("lse", lse, dev, torch.float32, Tq, Hq), ws.data_ptr(), ws.numel())
+    return ws
+
+
+def mmdit_block_tables(before, after, tables, free_pages, n_free, page_size, n_free_out, cu, positions, slots, missing,
+                       stream=None):
+    """Block tables and slot maps of a paged cache, on the GPU: requests go from before[b] to after[b] tokens (int32 [B]);
+    pages move between tables [B, width] and the stack free_pages [pages] (int32, n_free [1] high; n_free_out [1], which
+    may be n_free, takes its new height); cu [B + 1] int32 are prefix sums of the new tokens, positions and slots
+    [capacity] int64 (or None) their places; missing [2] int32 counts pages that were not free and tokens left out."""
+    dev, i32 = _device(before), torch.int32
+    B = before.shape[0]
+    if tables.dim() != 2:
+        raise ValueError("tables must be [B, width]")
+    width, n_pages = tables.shape[1], free_pages.shape[0]
+    cap = next((t.shape[0] for t in (positions, slots) if t is not None), 0)
+    _launch("mmdit_block_tables", dev, stream, B, page_size, width, n_pages, _arg("before", before, dev, i32, B),
+            _arg("after", after, dev, i32, B), _arg("tables", tables, dev, i32, B, width),
+            _arg("free_pages", free_pages, dev, i32, n_pages), _arg("n_free", n_free, dev, i32, 1),
+            _arg("n_free_out", n_free_out, dev, i32, 1), _arg("cu", cu, dev, i32, B + 1), cap,
+            _arg("positions", positions, dev, torch.int64, cap), _arg("slots", slots, dev, torch.int64, cap),
+            _arg("missing", missing, dev, i32, 2))
+
+
+def mmdit_kv_cache_write(k, v, k_cache, v_cache, slots, stream=None):
+    """New keys and values k, v [T, H, d] bf16 (views with adjacent head elements) into slots[t] (int64 [T]; those outside
+    the cache are skipped) of k_cache, v_cache [pages, page size, H, d]."""
+    dev = _device(k)
+    vk = _heads_view("k", k, dev)
+    T, H, d = k.shape
+    vkc = _pages_view("k_cache", k_cache, dev, heads=H, d=d)
+    _launch("mmdit_kv_cache_write", dev, stream, T, H, d, vk, _heads_view("v", v, dev, T, H, d), vkc,
+            _pages_view("v_cache", v_cache, dev, k_cache.shape), k_cache.shape[0], k_cache.shape[1],
+            _arg("slots", slots, dev, torch.int64, T))

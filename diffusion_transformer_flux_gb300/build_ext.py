@@ -24,7 +24,8 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxe
          "-Xptxas", "-warn-spills"]
 SOURCES = ["gemm_bf16.cu", "gemm_tf32.cu", "gemm_fp8.cu", "gemm_blockwise.cu", "fp8.cu", "attention.cu",
            "attention_bwd.cu", "attention_fp8.cu", "elementwise.cu", "backward.cu", "api.cu", "noalloc.cu",
-           "mxfp8.cu", "rmsnorm.cu", "block_cast.cu", "gemm_block.cu", "rope_apply.cu"]
+           "mxfp8.cu", "rmsnorm.cu", "block_cast.cu", "gemm_block.cu", "rope_apply.cu",
+           "attention_varlen.cu", "attention_varlen_bwd.cu", "paged_attention.cu", "kv_cache.cu"]
 
 
 def _nvcc() -> str:

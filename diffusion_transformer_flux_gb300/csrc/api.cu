@@ -12,6 +12,7 @@
 #include <array>
 #include <cmath>
 #include <initializer_list>
+#include <utility>
 #include <vector>
 
 #include "../../include/mmdit.h"
@@ -2827,6 +2828,356 @@ mmdit_status mmdit_rope_bwd(int32_t act, const mmdit_rope_cfg* cfg, int32_t batc
                             int64_t pos_bstride, const float* cos, const float* sin, void* stream) {
   return rope_call(act, cfg, batch, seq, head_dim, heads_q, q, q_out, heads_k, k, k_out, positions, pos_bstride, cos,
                    sin, 1, stream);
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------- attention of a text model
+namespace {
+constexpr int64_t kMostStride = int64_t{1} << 36;
+
+// A view whose extents (its dimensions but the head's elements) are `n[i]` with strides `st[i]`; written ones must not
+// overlap themselves: sorted by stride, each holds what lies below it.
+mmdit_status check_strides(const char* what, const char* name, std::initializer_list<int64_t> extents,
+                           std::initializer_list<int64_t> strides, int head_dim, bool written) {
+  std::array<std::pair<int64_t, int64_t>, 3> d{};
+  int n = 0;
+  auto st = strides.begin();
+  for (int64_t e : extents) {
+    const int64_t s = *st++;
+    if (e <= 1) continue;
+    if (s % 8 != 0 || s < head_dim || s > kMostStride)
+      return fail(MMDIT_ERR_INVALID_ARG, "%s: %s's strides must be multiples of 8 elements, head_dim to 2^36", what, name);
+    d[n++] = {s, e};
+  }
+  if (!written) return MMDIT_OK;
+  std::sort(d.begin(), d.begin() + n);
+  int64_t below = head_dim;
+  for (int i = 0; i < n; ++i) {
+    if (d[i].first < below) return fail(MMDIT_ERR_INVALID_ARG, "%s: rows of %s overlap", what, name);
+    below += d[i].first * (d[i].second - 1);
+  }
+  return MMDIT_OK;
+}
+mmdit_status check_heads(const char* what, const char* name, const mmdit_heads_view* v, int64_t tokens, int heads, int head_dim,
+                         bool written) {
+  if (!v || !v->ptr) return fail(MMDIT_ERR_INVALID_ARG, "%s: %s is NULL", what, name);
+  if (!aligned16(v->ptr)) return fail(MMDIT_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", what, name);
+  return check_strides(what, name, {tokens, heads}, {v->stride_t, v->stride_h}, head_dim, written);
+}
+mmdit_status check_pages(const char* what, const char* name, const mmdit_pages_view* v, int64_t pages, int64_t page_size,
+                         int heads, int head_dim, bool written) {
+  if (!v || !v->ptr) return fail(MMDIT_ERR_INVALID_ARG, "%s: %s is NULL", what, name);
+  if (!aligned16(v->ptr)) return fail(MMDIT_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", what, name);
+  return check_strides(what, name, {pages, page_size, heads}, {v->stride_page, v->stride_t, v->stride_h}, head_dim, written);
+}
+mmdit_status check_page_size(const char* what, int32_t page_size, int32_t n_pages) {
+  if (page_size < 1 || n_pages < 0) return fail(MMDIT_ERR_INVALID_ARG, "%s: bad page_size %d or n_pages %d", what, page_size, n_pages);
+  if (page_size < 8 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0)
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: page_size must be a power of two from 8 to 2^20 (got %d)", what, page_size);
+  if (n_pages > (1 << 30)) return fail(MMDIT_ERR_UNSUPPORTED, "%s: n_pages must be at most 2^30", what);
+  return MMDIT_OK;
+}
+int log2_of(int32_t power) {
+  int s = 0;
+  while ((1 << s) < power) ++s;
+  return s;
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+HeadsView heads_view(const mmdit_heads_view* v) { return {v->ptr, v->stride_t, v->stride_h}; }
+PagesView pages_view(const mmdit_pages_view* v) { return {v->ptr, v->stride_page, v->stride_t, v->stride_h}; }
+
+mmdit_status check_attention(const char* what, int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q,
+                             int32_t heads_k, int32_t head_dim, float scale) {
+  if (batch < 0 || tokens_q < 0 || tokens_k < 0 || heads_q < 1 || heads_k < 1 || head_dim < 1)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: bad shape (batch %d, tokens %d and %d, heads %d and %d of %d)", what, batch, tokens_q,
+                tokens_k, heads_q, heads_k, head_dim);
+  if (heads_q % heads_k != 0)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: heads_q (%d) must be a multiple of heads_k (%d)", what, heads_q, heads_k);
+  if (head_dim % 8 != 0 || head_dim > 128)
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: head_dim must be a multiple of 8, at most 128 (got %d)", what, head_dim);
+  if (heads_q / heads_k > 128 || heads_q > 65535)
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: at most 128 query heads to a key head and 65535 in all (got %d, %d)", what,
+                heads_q / heads_k, heads_q);
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MMDIT_ERR_INVALID_ARG, "%s: scale must be positive and finite", what);
+  if (tokens_q > (1 << 30) || tokens_k > (1 << 30) || batch > (1 << 20))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: at most 2^30 tokens and 2^20 sequences", what);
+  // the CTAs: one for two tiles of 128 / group tokens and each key head
+  const int64_t pairs = tokens_q / (2 * (128 / (heads_q / heads_k))) + static_cast<int64_t>(batch);
+  if (pairs * heads_k > INT32_MAX) return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
+  return MMDIT_OK;
+}
+
+SeqAttnArgs attention_args(int32_t batch, int32_t tokens_q, int32_t heads_q, int32_t heads_k, int32_t head_dim, float scale) {
+  SeqAttnArgs a = {};
+  a.batch = batch, a.tokens_q = tokens_q, a.hq = heads_q, a.hk = heads_k, a.group = heads_q / heads_k, a.head_dim = head_dim;
+  a.scale = scale, a.scale_log2 = scale * 1.4426950408889634f;
+  a.tile_tokens = seq_tile_tokens(a.group);
+  return a;
+}
+
+// How a call over a paged cache splits its work.  Keys of a sequence go to several CTAs where the sequences and key heads
+// alone are too few for the GPU's 152 SMs.
+struct PagedPlan {
+  int few, tiles;  // whether paged_few_kernel and the tile kernel run
+  int few_keys, few_splits, split_keys, splits;
+  size_t few_part, few_lse, part, lse, total;
+};
+PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, int head_dim, int64_t max_q, int64_t max_kv) {
+  PagedPlan p = {};
+  const int group = heads_q / heads_k, d = head_dim <= 64 ? 64 : 128;
+  const int64_t sms = 152;
+  p.tiles = max_q * group > kFewRows;
+  p.few = !p.tiles || batch > 1;
+  p.few_splits = p.splits = 1;
+  max_kv = std::max<int64_t>(max_kv, 1);
+  if (p.few) {
+    const int64_t want = std::max<int64_t>(1, 4 * sms / std::max<int64_t>(1, batch * heads_k));
+    const int64_t keys = std::max<int64_t>(256, round_up((max_kv + want - 1) / want, 64));
+    p.few_splits = static_cast<int>((max_kv + keys - 1) / keys);
+    p.few_keys = static_cast<int>(keys);
+  }
+  if (p.tiles) {
+    const int64_t items = (tokens_q / (2 * (128 / group)) + batch) * heads_k;
+    const int64_t want = items >= sms ? 1 : std::max<int64_t>(1, std::min(sms / items, max_kv / 512));
+    const int64_t keys = round_up((max_kv + want - 1) / want, 128);
+    p.splits = static_cast<int>((max_kv + keys - 1) / keys);
+    p.split_keys = p.splits > 1 ? static_cast<int>(keys) : 0;
+  }
+  Carver c;
+  if (p.few_splits > 1) {
+    const size_t rows = static_cast<size_t>(p.few_splits) * batch * heads_k * kFewRows;
+    p.few_part = c.take(rows * d * 4), p.few_lse = c.take(rows * 4);
+  }
+  if (p.splits > 1) {
+    const size_t rows = static_cast<size_t>(p.splits) * tokens_q * heads_q;
+    p.part = c.take(rows * d * 4), p.lse = c.take(rows * 4);
+  }
+  p.total = c.off;
+  return p;
+}
+}  // namespace
+
+extern "C" {
+
+size_t mmdit_varlen_attention_workspace_size(int32_t, int32_t, int32_t) { return kStatusBytes; }
+
+mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,
+                                        int32_t head_dim, int32_t causal, float scale, const mmdit_heads_view* q,
+                                        const mmdit_heads_view* k, const mmdit_heads_view* v, const int32_t* cu_q,
+                                        const int32_t* cu_k, const mmdit_heads_view* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  const char* what = "varlen attention";
+  mmdit_status s = check_attention(what, batch, tokens_q, tokens_k, heads_q, heads_k, head_dim, scale);
+  if (s != MMDIT_OK) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, kStatusBytes)) != MMDIT_OK) return s;
+  if (batch == 0 || tokens_q == 0) return MMDIT_OK;
+  if ((s = check_heads(what, "q", q, tokens_q, heads_q, head_dim, false)) != MMDIT_OK) return s;
+  if (tokens_k > 0 && (s = check_heads(what, "k", k, tokens_k, heads_k, head_dim, false)) != MMDIT_OK) return s;
+  if (tokens_k > 0 && (s = check_heads(what, "v", v, tokens_k, heads_k, head_dim, false)) != MMDIT_OK) return s;
+  if ((s = check_heads(what, "out", out, tokens_q, heads_q, head_dim, true)) != MMDIT_OK) return s;
+  if (out->ptr == q->ptr || (tokens_k > 0 && (out->ptr == k->ptr || out->ptr == v->ptr)))
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: out must not be an input", what);
+  if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse))
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: cu_q or cu_k is NULL, or one of them or lse not 4-byte aligned", what);
+  SeqAttnArgs a = attention_args(batch, tokens_q, heads_q, heads_k, head_dim, scale);
+  a.tokens_k = tokens_k, a.causal = causal != 0, a.cu_q = cu_q, a.cu_k = cu_k;
+  a.q = heads_view(q), a.out = heads_view(out), a.lse = lse;
+  a.status = status_word(workspace), a.clear = 1;
+  // without keys nothing is loaded through the maps of k and v
+  const HeadsView vk = tokens_k > 0 ? heads_view(k) : a.q, vv = tokens_k > 0 ? heads_view(v) : a.q;
+  SeqAttnMaps m;
+  if (!encode_heads_map(&m.q, a.q, head_dim, heads_q, tokens_q, a.group, a.tile_tokens) ||
+      !encode_heads_map(&m.k, vk, head_dim, tokens_k > 0 ? heads_k : 1, std::max(tokens_k, 1), 1, 128) ||
+      !encode_heads_map(&m.v, vv, head_dim, tokens_k > 0 ? heads_k : 1, std::max(tokens_k, 1), 1, 128))
+    return fail(MMDIT_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", what);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  pdl_begin_call();
+  ProfScope ps_("varlen_attention", st);
+  MMDIT_CUDA(launch_seq_attention(a, m, 0, 1, st), what);
+  return MMDIT_OK;
+}
+
+size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t) {
+  if (tokens_q < 1 || heads_q < 1) return kStatusBytes;
+  Carver c;
+  c.take(static_cast<size_t>(tokens_q) * heads_q * sizeof(float2));
+  return c.off;
+}
+
+mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,
+                                        int32_t head_dim, int32_t causal, float scale, const mmdit_heads_view* dout,
+                                        const mmdit_heads_view* q, const mmdit_heads_view* k, const mmdit_heads_view* v,
+                                        const mmdit_heads_view* out, const float* lse, const int32_t* cu_q,
+                                        const int32_t* cu_k, const mmdit_heads_view* dq, const mmdit_heads_view* dk,
+                                        const mmdit_heads_view* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* what = "varlen attention backward";
+  mmdit_status s = check_attention(what, batch, tokens_q, tokens_k, heads_q, heads_k, head_dim, scale);
+  if (s != MMDIT_OK) return s;
+  const int64_t tiles = std::max(tokens_k / 128, tokens_q / (128 / (heads_q / heads_k))) + static_cast<int64_t>(batch);
+  if (tiles * heads_k > INT32_MAX || static_cast<int64_t>(tokens_q) * heads_q > (int64_t{1} << 34))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
+  if ((s = check_workspace(workspace, workspace_bytes, mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim))) !=
+      MMDIT_OK)
+    return s;
+  if (batch == 0 || (tokens_q == 0 && tokens_k == 0)) return MMDIT_OK;
+  const mmdit_heads_view *vq[] = {dout, q, out, dq}, *vk[] = {k, v, dk, dv};
+  const char *nq[] = {"dout", "q", "out", "dq"}, *nk[] = {"k", "v", "dk", "dv"};
+  for (int i = 0; i < 4; ++i) {
+    if (tokens_q > 0 && (s = check_heads(what, nq[i], vq[i], tokens_q, heads_q, head_dim, i == 3)) != MMDIT_OK) return s;
+    if (tokens_k > 0 && (s = check_heads(what, nk[i], vk[i], tokens_k, heads_k, head_dim, i >= 2)) != MMDIT_OK) return s;
+  }
+  for (int i = 0; i < 4; ++i)  // no gradient is an input or another gradient
+    for (int j = 0; j < 4; ++j) {
+      const bool both = tokens_q > 0 && tokens_k > 0;
+      if ((tokens_q > 0 && i < 3 && dq->ptr == vq[i]->ptr) || (both && dq->ptr == vk[j]->ptr) ||
+          (both && j >= 2 && vk[j]->ptr == vq[i]->ptr) || (tokens_k > 0 && j >= 2 && i < j && vk[j]->ptr == vk[i]->ptr))
+        return fail(MMDIT_ERR_INVALID_ARG, "%s: a gradient must not be an input or another gradient", what);
+    }
+  if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k) || (tokens_q > 0 && !lse) || !aligned4(lse))
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: cu_q, cu_k or lse is NULL or not 4-byte aligned", what);
+  SeqAttnBwdArgs a = {};
+  a.batch = batch, a.tokens_q = tokens_q, a.tokens_k = tokens_k, a.hq = heads_q, a.hk = heads_k, a.group = heads_q / heads_k;
+  a.head_dim = head_dim, a.causal = causal != 0, a.tile_tokens = seq_tile_tokens(a.group);
+  a.scale = scale, a.scale_log2 = scale * 1.4426950408889634f;
+  a.cu_q = cu_q, a.cu_k = cu_k, a.lse = lse, a.sums = at<float2>(workspace, kStatusBytes);
+  if (tokens_q > 0) a.dout = heads_view(dout), a.out = heads_view(out), a.dq = heads_view(dq);
+  if (tokens_k > 0) a.dk = heads_view(dk), a.dv = heads_view(dv);
+  a.status = status_word(workspace), a.clear = 1;
+  // where a side has no rows nothing is loaded through its maps
+  const HeadsView mq = tokens_q > 0 ? heads_view(q) : heads_view(k), md = tokens_q > 0 ? a.dout : mq;
+  const HeadsView mk = tokens_k > 0 ? heads_view(k) : mq, mv = tokens_k > 0 ? heads_view(v) : mq;
+  SeqAttnBwdMaps m;
+  if (!encode_heads_map(&m.q, mq, head_dim, tokens_q > 0 ? heads_q : 1, std::max(tokens_q, 1), a.group, a.tile_tokens) ||
+      !encode_heads_map(&m.dout, md, head_dim, tokens_q > 0 ? heads_q : 1, std::max(tokens_q, 1), a.group, a.tile_tokens) ||
+      !encode_heads_map(&m.k, mk, head_dim, tokens_k > 0 ? heads_k : 1, std::max(tokens_k, 1), 1, 128) ||
+      !encode_heads_map(&m.v, mv, head_dim, tokens_k > 0 ? heads_k : 1, std::max(tokens_k, 1), 1, 128))
+    return fail(MMDIT_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", what);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  pdl_begin_call();
+  ProfScope ps_("varlen_attention_bwd", st);
+  MMDIT_CUDA(launch_seq_attention_bwd(a, m, st), what);
+  return MMDIT_OK;
+}
+
+size_t mmdit_paged_attention_workspace_size(int32_t tokens_q, int32_t batch, int32_t heads_q, int32_t heads_k, int32_t head_dim,
+                                            int32_t max_q, int32_t max_kv) {
+  if (tokens_q < 1 || batch < 1 || heads_k < 1 || heads_q < heads_k || heads_q / heads_k > 128 || max_q < 0 || max_kv < 0)
+    return kStatusBytes;
+  return plan_paged(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv).total;
+}
+
+mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t heads_q, int32_t heads_k, int32_t head_dim,
+                                       float scale, const mmdit_heads_view* q, const mmdit_pages_view* k,
+                                       const mmdit_pages_view* v, int32_t n_pages, int32_t page_size, const int32_t* tables,
+                                       int32_t table_width, const int32_t* kv_lens, const int32_t* cu_q, int32_t max_q,
+                                       int32_t max_kv, const mmdit_heads_view* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  const char* what = "paged attention";
+  mmdit_status s = check_attention(what, batch, tokens_q, 0, heads_q, heads_k, head_dim, scale);
+  if (s != MMDIT_OK || (s = check_page_size(what, page_size, n_pages)) != MMDIT_OK) return s;
+  if (table_width < 1 || max_q < 0 || max_kv < 0)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: bad table_width %d, max_q %d or max_kv %d", what, table_width, max_q, max_kv);
+  if (n_pages < 1) return fail(MMDIT_ERR_INVALID_ARG, "%s: a cache has at least one page", what);
+  const int64_t reach = static_cast<int64_t>(table_width) * page_size;
+  if (reach > (1 << 30)) return fail(MMDIT_ERR_UNSUPPORTED, "%s: table_width page_size must be at most 2^30", what);
+  const int most = static_cast<int>(max_kv > 0 ? std::min<int64_t>(max_kv, reach) : reach);
+  const PagedPlan p = plan_paged(std::max(tokens_q, 1), std::max(batch, 1), heads_q, heads_k, head_dim, max_q, most);
+  if (tokens_q > 0 && batch > 0 && (p.few_splits > 65535 || p.splits > 65535))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many parts", what);
+  if ((s = check_workspace(workspace, workspace_bytes, batch == 0 || tokens_q == 0 ? kStatusBytes : p.total)) != MMDIT_OK) return s;
+  if (batch == 0 || tokens_q == 0 || max_q == 0) return MMDIT_OK;
+  if ((s = check_heads(what, "q", q, tokens_q, heads_q, head_dim, false)) != MMDIT_OK) return s;
+  if ((s = check_pages(what, "k", k, n_pages, page_size, heads_k, head_dim, false)) != MMDIT_OK) return s;
+  if ((s = check_pages(what, "v", v, n_pages, page_size, heads_k, head_dim, false)) != MMDIT_OK) return s;
+  if ((s = check_heads(what, "out", out, tokens_q, heads_q, head_dim, true)) != MMDIT_OK) return s;
+  if (out->ptr == q->ptr || out->ptr == k->ptr || out->ptr == v->ptr)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: out must not be an input", what);
+  if (!cu_q || !tables || !kv_lens || !aligned4(cu_q) || !aligned4(tables) || !aligned4(kv_lens) || !aligned4(lse))
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: cu_q, tables or kv_lens is NULL, or one of them or lse not 4-byte aligned", what);
+  SeqAttnArgs a = attention_args(batch, tokens_q, heads_q, heads_k, head_dim, scale);
+  a.causal = 1, a.cu_q = cu_q, a.q = heads_view(q), a.out = heads_view(out), a.lse = lse;
+  a.k_pages = pages_view(k), a.v_pages = pages_view(v);
+  a.tables = tables, a.kv_lens = kv_lens, a.table_width = table_width, a.n_pages = n_pages, a.max_keys = most;
+  a.page_shift = log2_of(page_size), a.page_rows = std::min(page_size, 128);
+  a.few_rows = p.few ? kFewRows : 0, a.few_keys = p.few_keys, a.split_keys = p.split_keys;
+  if (p.few_splits > 1) a.few_part = at<float>(workspace, p.few_part), a.few_lse = at<float>(workspace, p.few_lse);
+  if (p.splits > 1) a.part = at<float>(workspace, p.part), a.part_lse = at<float>(workspace, p.lse);
+  a.status = status_word(workspace), a.clear = 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SeqAttnMaps m;
+  if (p.tiles && (!encode_heads_map(&m.q, a.q, head_dim, heads_q, tokens_q, a.group, a.tile_tokens) ||
+                  !encode_pages_map(&m.k, a.k_pages, head_dim, heads_k, n_pages, page_size, a.page_rows) ||
+                  !encode_pages_map(&m.v, a.v_pages, head_dim, heads_k, n_pages, page_size, a.page_rows)))
+    return fail(MMDIT_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", what);
+  pdl_begin_call();
+  ProfScope ps_("paged_attention", st);
+  if (p.tiles) {
+    MMDIT_CUDA(launch_seq_attention(a, m, 1, p.splits, st), what);
+    a.clear = 0;
+  }
+  if (p.few) MMDIT_CUDA(launch_paged_few(a, p.few_splits, st), "paged attention of few rows");
+  if (p.few_splits > 1 || p.splits > 1) MMDIT_CUDA(launch_paged_combine(a, st), "paged attention's join");
+  return MMDIT_OK;
+}
+
+mmdit_status mmdit_block_tables(int32_t batch, int32_t page_size, int32_t table_width, int32_t n_pages, const int32_t* before,
+                                const int32_t* after, int32_t* tables, int32_t* free_pages, const int32_t* n_free,
+                                int32_t* n_free_out, int32_t* cu, int32_t capacity, int64_t* positions, int64_t* slots,
+                                int32_t* missing, void* stream) {
+  const char* what = "block tables";
+  mmdit_status s = check_page_size(what, page_size, n_pages);
+  if (s != MMDIT_OK) return s;
+  if (batch < 0 || table_width < 1 || capacity < 0)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: bad batch %d, table_width %d or capacity %d", what, batch, table_width, capacity);
+  if (static_cast<int64_t>(batch) * table_width > (1 << 30) || static_cast<int64_t>(table_width) * page_size > (1 << 30))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: batch table_width and table_width page_size must be at most 2^30", what);
+  if (!n_free || !n_free_out || !cu || !missing || (batch > 0 && (!before || !after || !tables)) || (n_pages > 0 && !free_pages))
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: NULL argument", what);
+  for (const void* ptr : {static_cast<const void*>(before), static_cast<const void*>(after), static_cast<const void*>(tables),
+                          static_cast<const void*>(free_pages), static_cast<const void*>(n_free),
+                          static_cast<const void*>(n_free_out), static_cast<const void*>(cu), static_cast<const void*>(missing)})
+    if (!aligned4(ptr)) return fail(MMDIT_ERR_INVALID_ARG, "%s: an argument is not 4-byte aligned", what);
+  if ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0 || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: positions or slots is not 8-byte aligned", what);
+  BlockTableArgs a = {};
+  a.batch = batch, a.width = table_width, a.n_pages = n_pages, a.page_shift = log2_of(page_size), a.capacity = capacity;
+  a.before = before, a.after = after, a.tables = tables, a.free_pages = free_pages, a.n_free = n_free, a.n_free_out = n_free_out;
+  a.cu = cu, a.missing = missing, a.positions = positions, a.slots = slots;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  pdl_begin_call();
+  ProfScope ps_("block_tables", st);
+  MMDIT_CUDA(launch_block_tables(a, st), what);
+  return MMDIT_OK;
+}
+
+mmdit_status mmdit_kv_cache_write(int32_t tokens, int32_t heads, int32_t head_dim, const mmdit_heads_view* k,
+                                  const mmdit_heads_view* v, const mmdit_pages_view* k_cache, const mmdit_pages_view* v_cache,
+                                  int32_t n_pages, int32_t page_size, const int64_t* slots, void* stream) {
+  const char* what = "cache write";
+  mmdit_status s = check_page_size(what, page_size, n_pages);
+  if (s != MMDIT_OK) return s;
+  if (tokens < 0 || heads < 1 || head_dim < 1)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: bad shape (%d tokens, %d heads of %d)", what, tokens, heads, head_dim);
+  if (head_dim % 8 != 0 || head_dim > 512 || heads > 65535 || tokens > (1 << 30))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: head_dim must be a multiple of 8 up to 512, heads at most 65535, tokens 2^30", what);
+  if (tokens == 0 || n_pages == 0) return MMDIT_OK;
+  if ((s = check_heads(what, "k", k, tokens, heads, head_dim, false)) != MMDIT_OK) return s;
+  if ((s = check_heads(what, "v", v, tokens, heads, head_dim, false)) != MMDIT_OK) return s;
+  if ((s = check_pages(what, "k_cache", k_cache, n_pages, page_size, heads, head_dim, true)) != MMDIT_OK) return s;
+  if ((s = check_pages(what, "v_cache", v_cache, n_pages, page_size, heads, head_dim, true)) != MMDIT_OK) return s;
+  if (k_cache->ptr == v_cache->ptr || k_cache->ptr == k->ptr || v_cache->ptr == v->ptr || k_cache->ptr == v->ptr || v_cache->ptr == k->ptr)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: the caches must not be each other or an input", what);
+  if (!slots || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+    return fail(MMDIT_ERR_INVALID_ARG, "%s: slots is NULL or not 8-byte aligned", what);
+  CacheWriteArgs a = {};
+  a.tokens = tokens, a.heads = heads, a.head_dim = head_dim, a.n_pages = n_pages, a.page_shift = log2_of(page_size);
+  a.k = heads_view(k), a.v = heads_view(v), a.k_pages = pages_view(k_cache), a.v_pages = pages_view(v_cache), a.slots = slots;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  pdl_begin_call();
+  ProfScope ps_("kv_cache_write", st);
+  MMDIT_CUDA(launch_kv_write(a, st), what);
+  return MMDIT_OK;
 }
 
 }  // extern "C"

@@ -450,4 +450,84 @@ cudaError_t launch_flow_match(int dtype, const void* z0, const void* z1, const f
                               int64_t n_per_sample, void* z_t, const void* pred, float* loss,
                               float* partials, int n_partials, cudaStream_t stream);
 
+// attention_varlen.cu, attention_varlen_bwd.cu, paged_attention.cu: attention over packed sequences and paged caches.
+// Element (token, head, i) of a packed tensor at ptr + token stride_t + head stride_h + i (elements); of a paged cache
+// (page, slot, head, i) at ptr + page stride_page + slot stride_t + head stride_h + i.
+struct HeadsView {
+  void* ptr;
+  int64_t stride_t, stride_h;
+};
+struct PagesView {
+  void* ptr;
+  int64_t stride_page, stride_t, stride_h;
+};
+struct SeqAttnArgs {
+  int batch, tokens_q, tokens_k;
+  int hq, hk, group, head_dim, causal;
+  int tile_tokens;  // tokens of a query tile, 128 / group (set by the launcher)
+  float scale, scale_log2;
+  const int *cu_q, *cu_k;
+  HeadsView q, out;
+  float* lse;  // [tokens_q, hq] or null
+  // paged cache
+  PagesView k_pages, v_pages;
+  const int *tables, *kv_lens;
+  int table_width, n_pages, page_shift, page_rows, max_keys;  // page_rows: rows of a copied piece, at most 128
+  int few_rows;  // sequences of at most that many rows (tokens by the group's heads) are paged_few_kernel's: kFewRows or 0
+  int few_keys, split_keys;  // keys of one CTA of paged_few_kernel, of the tile kernel (0: all)
+  // normalised parts and their log2-sums: [splits, tokens_q, hq(, D)] of the tile kernel, [splits, batch, hk, kFewRows(, D)]
+  // of paged_few_kernel
+  float *part, *part_lse, *few_part, *few_lse;
+  uint32_t* status;
+  int clear;           // this kernel is the call's first and clears the status word
+};
+constexpr int kFewRows = 16;
+struct SeqAttnMaps {
+  CUtensorMap q, k, v;
+};
+int seq_tile_tokens(int group);
+bool encode_heads_map(CUtensorMap* map, const HeadsView& v, int head_dim, int heads, int64_t tokens, int box_heads, int box_tokens);
+bool encode_pages_map(CUtensorMap* map, const PagesView& v, int head_dim, int heads, int n_pages, int page_size, int rows);
+cudaError_t launch_seq_attention(SeqAttnArgs a, const SeqAttnMaps& m, int paged, int splits, cudaStream_t stream);
+// few rows to a sequence: `splits` CTAs of few_keys keys each; then the join of the parts of either kernel
+cudaError_t launch_paged_few(const SeqAttnArgs& a, int splits, cudaStream_t stream);
+cudaError_t launch_paged_combine(const SeqAttnArgs& a, cudaStream_t stream);
+
+// gradients of the attention over packed sequences
+struct SeqAttnBwdArgs {
+  int batch, tokens_q, tokens_k;
+  int hq, hk, group, head_dim, causal, tile_tokens;
+  float scale, scale_log2;
+  const int *cu_q, *cu_k;
+  HeadsView dout, out, dq, dk, dv;
+  const float* lse;  // [tokens_q, hq]
+  float2* sums;      // [tokens_q, hq]: lse log2(e), dout . out
+  uint32_t* status;
+  int clear;
+};
+struct SeqAttnBwdMaps {
+  CUtensorMap q, dout, k, v;
+};
+cudaError_t launch_seq_attention_bwd(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaStream_t stream);
+
+// kv_cache.cu: block tables and slot maps of a paged cache, and the write of new keys and values into it
+struct BlockTableArgs {
+  int batch, width, n_pages, page_shift;
+  int64_t capacity;  // entries of positions and slots
+  const int *before, *after;
+  int *tables, *free_pages;
+  const int* n_free;
+  int *n_free_out, *cu, *missing;
+  int64_t *positions, *slots;
+};
+struct CacheWriteArgs {
+  int64_t tokens;
+  int heads, head_dim, n_pages, page_shift;
+  HeadsView k, v;
+  PagesView k_pages, v_pages;
+  const int64_t* slots;
+};
+cudaError_t launch_block_tables(const BlockTableArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_write(const CacheWriteArgs& a, cudaStream_t stream);
+
 }  // namespace mmdit

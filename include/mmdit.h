@@ -829,6 +829,109 @@ mmdit_status mmdit_rope_bwd(int32_t act, const mmdit_rope_cfg *cfg, int32_t batc
                             const mmdit_rope_view *k_out, const int64_t *positions, int64_t pos_bstride,
                             const float *cos, const float *sin, void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Attention of a text model: causal or not, fewer key than query heads, sequences of different lengths packed one behind
+ * the other, and a cache of earlier tokens in pages.  [ARCH] §Implementation details, Attention implementation, is the
+ * blocks' attention (mmdit_attention_fwd: no mask, equal heads of 128, dense batches); this is its form for text.
+ *
+ * Packed sequences: sequence b's queries are rows cu_q[b] .. cu_q[b + 1] of q, its keys rows cu_k[b] .. cu_k[b + 1] of k and
+ * v; cu_q, cu_k [batch + 1] int32 on the device, not falling, at most tokens_q, tokens_k (entries beyond are taken as the
+ * nearest of those: no row outside the tensors is touched, whatever they hold).  Rows of no sequence are left as they
+ * were.  Query i of a sequence of n queries and m keys stands at position m - n + i; with causal != 0 it sees the keys up to
+ * its own position, else all:
+ *   z_ij = scale q_i . k_j,   lse_i = log sum_j exp(z_ij),   out_i = sum_j exp(z_ij - lse_i) v_j   over the keys it sees;
+ * a row that sees none gives zeros and lse -inf.  Query head h reads key head h / (heads_q / heads_k).  Nothing of a key
+ * that a row does not see reaches it; a non-finite element of a v that it sees, within 128 keys of the first that it does not,
+ * makes that column NaN.
+ *
+ * bf16 tensors, products on the tensor cores with float32 sums; the weights exp(z - max) enter the second product rounded to
+ * bf16.  A view is element (token, head, i) at ptr + token stride_t + head stride_h + i (elements; multiples of 8, at most
+ * 2^36, not below head_dim where the extent is above one; ptr 16-byte aligned); a view that is written must not overlap
+ * itself or another view of the call.  The views are host memory.  head_dim a multiple of 8, at most 128; heads_q a
+ * multiple of heads_k, at most 128 times it and at most 65535; scale positive and finite; tokens at most 2^30, batch at
+ * most 2^20. */
+typedef struct mmdit_heads_view {
+  void *ptr;
+  int64_t stride_t, stride_h;
+} mmdit_heads_view;
+
+/* out [tokens_q, heads_q, head_dim]; lse NULL, or [tokens_q, heads_q] fp32 (for the backward).
+ * workspace >= mmdit_varlen_attention_workspace_size(tokens_q, heads_q, head_dim) (the status word).
+ * The same bits from call to call. */
+size_t mmdit_varlen_attention_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim);
+mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,
+                                        int32_t head_dim, int32_t causal, float scale, const mmdit_heads_view *q,
+                                        const mmdit_heads_view *k, const mmdit_heads_view *v, const int32_t *cu_q,
+                                        const int32_t *cu_k, const mmdit_heads_view *out, float *lse, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/* Its gradients, from the forward's out and lse: with p_ij = exp(z_ij - lse_i) and dz_ij = p_ij (dout_i . v_j - dout_i . out_i)
+ *   dq_i = scale sum_j dz_ij k_j,   dk_j = scale sum_i dz_ij q_i,   dv_j = sum_i p_ij dout_i,
+ * dk and dv summed over the query heads of their group.  All rows of the sequences are written, rows of none left as they
+ * were.  Sums in float32 in a fixed order: the same bits from call to call.  p and dz enter the products rounded to bf16.  A
+ * query row whose q or dout is not finite, within 128 rows (tokens by the group's heads) of one that sees fewer keys, makes
+ * the gradients of the keys it sees NaN; a key row likewise those of the queries that see it.
+ * workspace >= mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) (two floats for each row: calls that
+ * share one are ordered on one stream). */
+size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim);
+mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,
+                                        int32_t head_dim, int32_t causal, float scale, const mmdit_heads_view *dout,
+                                        const mmdit_heads_view *q, const mmdit_heads_view *k, const mmdit_heads_view *v,
+                                        const mmdit_heads_view *out, const float *lse, const int32_t *cu_q,
+                                        const int32_t *cu_k, const mmdit_heads_view *dq, const mmdit_heads_view *dk,
+                                        const mmdit_heads_view *dv, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Paged cache: key j of sequence b is slot j % page_size of page tables[b, j / page_size], element (page, slot, head, i) of
+ * k and v at ptr + page stride_page + slot stride_t + head stride_h + i (strides as above; page_size a power of two from 8
+ * to 2^20, n_pages at most 2^30).  tables [batch, table_width] int32, kv_lens [batch] int32 (tokens of the sequence, the new ones
+ * among them; at most table_width page_size, more are taken as that) on the device.  A table entry outside [0, n_pages) is
+ * a page without keys: what lies on it is seen by no row.  Slots behind a sequence's last token may hold anything.
+ *
+ * The queries are the last tokens of their sequences (a chunk of a prompt, or one token each), so the mask is causal.
+ * max_q: no sequence has more queries (one that has is not computed where max_q heads_q / heads_k <= 16); max_kv: no
+ * sequence has more keys (0: table_width page_size; more keys than that are not seen).  They and the shapes alone decide how the
+ * work is split; the device's lengths may change between launches of a captured graph.
+ * out [tokens_q, heads_q, head_dim]; lse NULL or [tokens_q, heads_q] fp32.  The same bits from call to call.
+ * workspace >= mmdit_paged_attention_workspace_size(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv), with
+ * max_kv as the call takes it (parts of split sequences: calls that share one are ordered on one stream). */
+typedef struct mmdit_pages_view {
+  void *ptr;
+  int64_t stride_page, stride_t, stride_h;
+} mmdit_pages_view;
+size_t mmdit_paged_attention_workspace_size(int32_t tokens_q, int32_t batch, int32_t heads_q, int32_t heads_k,
+                                            int32_t head_dim, int32_t max_q, int32_t max_kv);
+mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t heads_q, int32_t heads_k, int32_t head_dim,
+                                       float scale, const mmdit_heads_view *q, const mmdit_pages_view *k,
+                                       const mmdit_pages_view *v, int32_t n_pages, int32_t page_size,
+                                       const int32_t *tables, int32_t table_width, const int32_t *kv_lens,
+                                       const int32_t *cu_q, int32_t max_q, int32_t max_kv, const mmdit_heads_view *out,
+                                       float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Block tables and slot maps of such a cache.  Request b goes from before[b] to after[b] tokens [batch] int32 (negative ones
+ * are taken as 0, more than table_width page_size as that), so from ceil(before / page_size) to ceil(after / page_size) pages:
+ * first the pages of all requests that shrink (0: done) go onto the stack free_pages [n_pages] int32, whose height is
+ * n_free, then the others' new pages come from its top, both in the order of requests and of their pages.
+ *   tables [batch, table_width] int32: the new entries are written (-1 where no page was free), the others left;
+ *   n_free_out: the stack's height after the call (may be n_free);
+ *   cu [batch + 1] int32: prefix sums of the new tokens max(after - before, 0), at most capacity;
+ *   positions, slots [capacity] int64 (either may be NULL): of each new token in the order of requests, its position in its
+ *   request and page page_size + slot (-1 without a page); entries behind the last new token are 0 and -1;
+ *   missing [2] int32: pages wanted that were not free, and new tokens left out (beyond capacity or the tables' width).
+ * All of them on the device.  Called again with the same before, after and n_free (and n_free_out elsewhere) it gives the
+ * same result.  batch table_width and batch at most 2^30, table_width page_size at most 2^30.  No workspace. */
+mmdit_status mmdit_block_tables(int32_t batch, int32_t page_size, int32_t table_width, int32_t n_pages,
+                                const int32_t *before, const int32_t *after, int32_t *tables, int32_t *free_pages,
+                                const int32_t *n_free, int32_t *n_free_out, int32_t *cu, int32_t capacity,
+                                int64_t *positions, int64_t *slots, int32_t *missing, void *stream);
+
+/* New keys and values into a paged cache: token t's heads [tokens, heads, head_dim] go to slot slots[t] of k_cache and v_cache
+ * (page slots[t] / page_size); tokens whose slot lies outside [0, n_pages page_size) are skipped, and no slot is given
+ * twice.  bf16, views and limits as above (up to 512 elements to a head); the cache's heads must not overlap.  No workspace. */
+mmdit_status mmdit_kv_cache_write(int32_t tokens, int32_t heads, int32_t head_dim, const mmdit_heads_view *k,
+                                  const mmdit_heads_view *v, const mmdit_pages_view *k_cache,
+                                  const mmdit_pages_view *v_cache, int32_t n_pages, int32_t page_size,
+                                  const int64_t *slots, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

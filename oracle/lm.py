@@ -200,3 +200,93 @@ def rope(x, cos, sin, rot, interleaved, mscale=1.0, transposed=False):
         a, b = x[..., :rot // 2], x[..., rot // 2:rot]
         y[..., :rot // 2], y[..., rot // 2:rot] = a * c - b * s, a * s + b * c
     return y
+
+
+# ------------------------------------------------------------------------------------- attention
+def seen(n, m, causal):
+    """Whether query i of n, at position m - n + i, sees key j of m: [n, m]."""
+    return np.arange(m)[None, :] <= (m - n + np.arange(n)[:, None]) if causal else np.ones((n, m), bool)
+
+
+def attention(q, k, v, scale, causal):
+    """One sequence: q [n, Hq, d], k and v [m, Hk, d]; (out [n, Hq, d], lse [n, Hq]).  Sums run over the seen keys alone, so
+    nothing of the others enters; a row that sees none has out 0 and lse -inf."""
+    q, k, v = _f64(q), _f64(k), _f64(v)
+    n, heads, _ = q.shape
+    group = heads // k.shape[1]
+    out, lse = np.zeros(q.shape), np.full((n, heads), -np.inf)
+    see = seen(n, k.shape[0], causal)
+    for i in range(n):
+        at = np.flatnonzero(see[i])
+        if not len(at):
+            continue
+        for h in range(heads):
+            z = scale * (k[at, h // group] @ q[i, h])
+            top = z.max()
+            w = np.exp(z - top)
+            out[i, h] = w @ v[at, h // group] / w.sum()
+            lse[i, h] = top + np.log(w.sum())
+    return out, lse
+
+
+def attention_bwd(dout, q, k, v, out, lse, scale, causal):
+    """(dq, dk, dv) of one sequence by the chain rule from the forward's out and lse: with p_ij = exp(z_ij - lse_i),
+    dv_j = sum_i p_ij dout_i, dz_ij = p_ij (dout_i . v_j - dout_i . out_i); a key head sums over its group's query heads."""
+    dout, q, k, v, out, lse = (_f64(x) for x in (dout, q, k, v, out, lse))
+    n, heads, _ = q.shape
+    group = heads // k.shape[1]
+    dq, dk, dv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    see = seen(n, k.shape[0], causal)
+    for i in range(n):
+        at = np.flatnonzero(see[i])
+        if not len(at):
+            continue
+        for h in range(heads):
+            g = h // group
+            p = np.exp(scale * (k[at, g] @ q[i, h]) - lse[i, h])
+            dz = p * (v[at, g] @ dout[i, h] - out[i, h] @ dout[i, h])
+            dq[i, h] = scale * (dz @ k[at, g])
+            dk[at, g] += scale * np.outer(dz, q[i, h])
+            dv[at, g] += np.outer(p, dout[i, h])
+    return dq, dk, dv
+
+
+# ------------------------------------------------------------------------------------- paged cache
+def block_tables(before, after, tables, free_pages, n_free, page_size, capacity):
+    """One request after the other: requests that shrink push their pages onto the stack of free ones, then the others pop
+    theirs.  (tables, free_pages, n_free, cu, positions, slots, missing) after the step."""
+    tables, stack = np.array(tables), np.array(free_pages)
+    n_pages, width = len(stack), tables.shape[1]
+    most = width * page_size
+    clip = [(min(max(int(b), 0), most), min(max(int(a), 0), most)) for b, a in zip(before, after)]
+    pages = [(-(-b // page_size), -(-a // page_size)) for b, a in clip]
+    top = min(max(int(n_free), 0), n_pages)
+    for r, (held, need) in enumerate(pages):
+        for p in range(need, held):
+            if 0 <= tables[r, p] < n_pages:
+                if top < n_pages:
+                    stack[top] = tables[r, p]
+                top += 1
+    top = min(top, n_pages)
+    short = 0
+    for r, (held, need) in enumerate(pages):
+        for p in range(held, need):
+            if top > 0:
+                top -= 1
+                tables[r, p] = stack[top]
+            else:
+                tables[r, p] = -1
+                short += 1
+    cu, positions, slots, left = [0], np.zeros(capacity, np.int64), np.full(capacity, -1, np.int64), 0
+    total = 0
+    for r, (b, a) in enumerate(clip):
+        left += max(max(int(after[r]) - max(int(before[r]), 0), 0) - max(a - b, 0), 0)
+        for p in range(b, a):
+            if total < capacity:
+                positions[total] = p
+                page = tables[r, p // page_size]
+                if 0 <= page < n_pages:
+                    slots[total] = int(page) * page_size + p % page_size
+            total += 1
+        cu.append(min(total, capacity))
+    return tables, stack, top, np.array(cu), positions, slots, (short, left + max(total - capacity, 0))

@@ -53,7 +53,8 @@ struct Barriers {
   uint64_t v_full[Cfg<D>::kStages];
   uint64_t v_clean[Cfg<D>::kStages];
   uint64_t v_issued[Cfg<D>::kStages];  // tiles to clean: their copies are on the way (so v_full's phase is this tile's)
-  uint64_t kv_empty[Cfg<D>::kStages];
+  uint64_t k_empty[Cfg<D>::kStages];
+  uint64_t v_empty[Cfg<D>::kStages];
   uint64_t s_full[2];
   uint64_t p_full[2];
   uint64_t o_full[2];
@@ -61,14 +62,15 @@ struct Barriers {
   uint32_t tmem_slot;
   int abort_flag;
   int any_bad;
-  uint32_t lost_pages[Cfg<D>::kStages];  // paged: pieces of the stage's tile whose page does not exist
+  // paged: pieces of tile j whose page does not exist; two rounds of the ring, as a K tile is free before all rows read this
+  uint32_t lost_pages[2 * Cfg<D>::kStages];
   int worst[D];
 };
 static_assert(sizeof(Barriers<128>) <= 1024 && sizeof(Barriers<64>) <= 1024, "barriers");
 
 template <int D, bool PAGED>
 __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tmem, const SeqAttnArgs& a, const Segment& seg,
-                                             int hk, int t0, int cnt, int js, int split, int n_splits) {
+                                             int hk, int t0, int cnt, int js, int split, int n_splits, bool last) {
   volatile int* abort_flag = &sb->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;
@@ -90,14 +92,29 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
       w = mbar_wait(&sb->k_full[st], static_cast<uint32_t>(j / Cfg<D>::kStages) & 1u, abort_flag, a.status, kErrAttnWait);
     if (!__all_sync(0xffffffffu, w)) return;
     tc_fence_after();
+    // the products are done in their order: with the last tile's scores of K_j, V_(j-1) is read as well
+    if (last && (threadIdx.x & 127) == 0) {
+      mbar_arrive(&sb->k_empty[st]);
+      if (j > 0) mbar_arrive(&sb->v_empty[(j - 1) % Cfg<D>::kStages]);
+    }
     const int rel = lim - (js + j) * kSeqTile;  // keys of this tile that the row sees
-    // the 128 scores of this row: one TMEM round trip (four loads, one wait)
+    // the 128 scores of this row
     uint32_t r0[32], r1[32], r2[32], r3[32];
-    tmem_ld32(s_cols, r0);
-    tmem_ld32(s_cols + 32, r1);
-    tmem_ld64_wait(s_cols + 64, r2, r3);
-    tmem_ld_deps64(r0, r1);
-    if (__any_sync(0xffffffffu, rel < kSeqTile)) {
+    tmem_ld64_wait(s_cols, r0, r1);
+    tmem_ld32(s_cols + 64, r2);
+    tmem_ld32(s_cols + 96, r3);
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+    const bool part = __any_sync(0xffffffffu, rel < kSeqTile);
+    if (!part) {  // while the second half is on its way
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        mx0 = fmax3(mx0, __uint_as_float(r0[i]), __uint_as_float(r0[i + 1]));
+        mx1 = fmax3(mx1, __uint_as_float(r1[i]), __uint_as_float(r1[i + 1]));
+      }
+    }
+    tmem_ld_deps64(r2, r3);
+    bool whole = !part;
+    if (part) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         if (i >= rel) r0[i] = __float_as_uint(-INFINITY);
@@ -107,8 +124,9 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
       }
     }
     if (PAGED) {
-      const uint32_t lost = *reinterpret_cast<volatile uint32_t*>(&sb->lost_pages[st]);
+      const uint32_t lost = *reinterpret_cast<volatile uint32_t*>(&sb->lost_pages[j % (2 * Cfg<D>::kStages)]);
       if (lost) {  // pieces of at least 8 keys
+        whole = false;
         uint32_t eights = 0;
         for (int e = 0; e < 16; ++e) eights |= (lost >> (e * 8 / a.page_rows) & 1u) << e;
 #pragma unroll
@@ -120,13 +138,22 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
         }
       }
     }
-    float mx0 = -INFINITY, mx1 = -INFINITY;
+    if (!whole) {
+      mx0 = mx1 = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      mx0 = fmax3(mx0, fmax3(__uint_as_float(r0[i]), __uint_as_float(r1[i]), __uint_as_float(r2[i])),
-                  __uint_as_float(r3[i]));
-      mx1 = fmax3(mx1, fmax3(__uint_as_float(r0[i + 1]), __uint_as_float(r1[i + 1]), __uint_as_float(r2[i + 1])),
-                  __uint_as_float(r3[i + 1]));
+      for (int i = 0; i < 32; i += 2) {
+        mx0 = fmax3(mx0, __uint_as_float(r0[i]), __uint_as_float(r0[i + 1]));
+        mx1 = fmax3(mx1, __uint_as_float(r1[i]), __uint_as_float(r1[i + 1]));
+      }
+    }
+    {
+      float mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        mx2 = fmax3(mx2, __uint_as_float(r2[i]), __uint_as_float(r2[i + 1]));
+        mx3 = fmax3(mx3, __uint_as_float(r3[i]), __uint_as_float(r3[i + 1]));
+      }
+      mx0 = fmaxf(mx0, mx2), mx1 = fmaxf(mx1, mx3);
     }
     const float mx = fmaxf(mx0, mx1) * c;
     float alpha = 1.f;
@@ -137,6 +164,17 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
       alpha = fast_exp2(m_run - mx);
       m_run = mx;
       rescale = true;
+    }
+    // O holds sum_{t<j} P_t V_t (PV(j-1) was issued before S(j), whose completion we saw)
+    if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+      for (int e = 0; e < D / 16; ++e) {
+        uint32_t r[16];
+        tmem_ld16_wait(o_cols + e * 16, r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+        tmem_st16(o_cols + e * 16, r);
+      }
     }
     // a row that has seen no key yet: exp2(-inf - 0) = 0
     const float m_use = m_run == -INFINITY ? 0.f : m_run;
@@ -169,21 +207,10 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
       f32x2_split(sum_b, b0, b1);
       sum = (a0 + a1) + (b0 + b1);
     }
-    // O holds sum_{t<j} P_t V_t (PV(j-1) was issued before S(j), whose completion we saw)
-    if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-      for (int e = 0; e < D / 16; ++e) {
-        uint32_t r[16];
-        tmem_ld16_wait(o_cols + e * 16, r);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-        tmem_st16(o_cols + e * 16, r);
-      }
-    }
     tmem_st_wait();
-    l_run = l_run * alpha + sum;
     tc_fence_before();
     mbar_arrive(&sb->p_full[X]);
+    l_run = l_run * alpha + sum;
   }
   if (cnt > 0) {
     const bool w = mbar_wait(&sb->o_full[X], 0, abort_flag, a.status, kErrAttnWait);
@@ -287,7 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sb->v_full[s], 1);
       mbar_init(&sb->v_clean[s], 64);
       mbar_init(&sb->v_issued[s], 1);
-      mbar_init(&sb->kv_empty[s], 1);
+      mbar_init(&sb->k_empty[s], 1);
+      mbar_init(&sb->v_empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sb->s_full[x], 1);
@@ -333,56 +361,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p = a.tables[static_cast<int64_t>(b) * a.table_width + (key >> a.page_shift)];
         return p >= 0 && p < a.n_pages ? p : -2;
       };
-      int page = PAGED ? page_of(0) : 0;
-      for (int j = 0; j < n_kv; ++j) {
-        const int st = j % C::kStages;
-        const bool w = mbar_wait(&sb->kv_empty[st], (static_cast<uint32_t>(j / C::kStages) & 1u) ^ 1u, abort_flag, a.status,
-                                 kErrAttnWait);
-        if (!__all_sync(0xffffffffu, w)) break;
+      // K runs ahead of V by a tile: it is free once its scores are formed, V when they have been multiplied
+      auto empty = [&](uint64_t* bar, int j) {
+        const bool w = mbar_wait(bar, (static_cast<uint32_t>(j / C::kStages) & 1u) ^ 1u, abort_flag, a.status, kErrAttnWait);
+        return __all_sync(0xffffffffu, w) != 0;
+      };
+      auto load = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, int j, int page) {
         if constexpr (PAGED) {
-          const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
-          if (lane == 0) {
-            *reinterpret_cast<volatile uint32_t*>(&sb->lost_pages[st]) = lost;
-            mbar_arrive_expect_tx(&sb->k_full[st], C::kTileBytes);
-            mbar_arrive_expect_tx(&sb->v_full[st], C::kTileBytes);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
           __syncwarp();
-          const int next = j + 1 < n_kv ? page_of(j + 1) : -1;
           if (lane < pieces) {
             const int z = page < 0 ? a.n_pages : page;  // behind the last page: the box reads zeros
             const int y = ((js + j) * kSeqTile + lane * a.page_rows) & ((1 << a.page_shift) - 1);
             for (int h = 0; h < D / 64; ++h)
-              tma_load_4d(k_tile(st) + h * kSeqBlock + lane * a.page_rows * 128, &tm_k, &sb->k_full[st], h * 64, y, hk, z);
-            for (int h = 0; h < D / 64; ++h)
-              tma_load_4d(v_tile(st) + h * kSeqBlock + lane * a.page_rows * 128, &tm_v, &sb->v_full[st], h * 64, y, hk, z);
+              tma_load_4d(tile + h * kSeqBlock + lane * a.page_rows * 128, map, bar, h * 64, y, hk, z);
           }
-          page = next;
         } else if (lane == 0) {
-          const int key = seg.k0 + (js + j) * kSeqTile;
-          mbar_arrive_expect_tx(&sb->k_full[st], C::kTileBytes);
-          for (int h = 0; h < D / 64; ++h) tma_load_3d(k_tile(st) + h * kSeqBlock, &tm_k, &sb->k_full[st], h * 64, hk, key);
-          mbar_arrive_expect_tx(&sb->v_full[st], C::kTileBytes);
-          for (int h = 0; h < D / 64; ++h) tma_load_3d(v_tile(st) + h * kSeqBlock, &tm_v, &sb->v_full[st], h * 64, hk, key);
+          mbar_arrive_expect_tx(bar, C::kTileBytes);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(tile + h * kSeqBlock, map, bar, h * 64, hk, seg.k0 + (js + j) * kSeqTile);
         }
+      };
+      int page = PAGED ? page_of(0) : 0, next = PAGED && n_kv > 1 ? page_of(1) : 0;
+      int k_issued = 0;
+      auto load_k = [&](int j, int p) {
+        const int st = j % C::kStages;
+        if (!empty(&sb->k_empty[st], j)) return false;
+        if constexpr (PAGED) {
+          const uint32_t lost = __ballot_sync(0xffffffffu, p == -2);
+          if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&sb->lost_pages[j % (2 * C::kStages)]) = lost;
+        }
+        load(k_tile(st), &tm_k, &sb->k_full[st], j, p);
+        k_issued = j + 1;
+        return true;
+      };
+      bool ok = load_k(0, page);
+      for (int j = 0; ok && j < n_kv; ++j) {
+        const int st = j % C::kStages;
+        if (j + 1 < n_kv) ok = load_k(j + 1, next);
+        if (!ok || !empty(&sb->v_empty[st], j)) break;
+        load(v_tile(st), &tm_v, &sb->v_full[st], j, page);
         if (lane == 0 && to_scrub(j)) mbar_arrive(&sb->v_issued[st]);
         issued = j + 1;
+        page = next;
+        if (PAGED && j + 2 < n_kv) next = page_of(j + 2);
       }
       if (*abort_flag) {
         // give the copies already issued a bounded chance to land before the CTA exits
         int never = 0;
         mbar_wait(&sb->q_full, 0, &never, a.status, 0);
-        for (int t = max(issued - C::kStages, 0); t < issued; ++t) {
+        for (int t = max(k_issued - C::kStages, 0); t < k_issued; ++t)
           mbar_wait(&sb->k_full[t % C::kStages], static_cast<uint32_t>(t / C::kStages) & 1u, &never, a.status, 0);
+        for (int t = max(issued - C::kStages, 0); t < issued; ++t)
           mbar_wait(&sb->v_full[t % C::kStages], static_cast<uint32_t>(t / C::kStages) & 1u, &never, a.status, 0);
-        }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && n_kv > 0) {
-      // ---------------- MMA issuer
+    if (n_kv > 0) {
+      // ---------------- MMA issuer: the tensor core's queue is short, so whatever this warp waits for leaves it idle.  The
+      // warp's lanes test the barriers of a step side by side, one lane issues.
       // K-step k of a K-major operand tile: 16 elements into its 128-byte swizzle atoms
       auto koff = [](int k) -> uint64_t { return static_cast<uint64_t>(((k >> 2) * kSeqBlock + (k & 3) * 32) >> 4); };
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
+      };
       auto mma_s = [&](int x, int j) {  // S_x(j) = Q_x K_j^T into columns [128x, 128x + 128)
         const uint64_t q_desc = sdesc_kmajor_sw128(smem_addr(q_tile(x)));
         const uint64_t k_desc = sdesc_kmajor_sw128(smem_addr(k_tile(j % C::kStages)));
@@ -400,45 +442,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_mma_ts_f16(d_o, p_cols + static_cast<uint32_t>(k * 8), v_desc + static_cast<uint64_t>((k * 2048) >> 4), C::kIdescPV,
                         (j > 0 || k > 0) ? 1u : 0u);
       };
-      auto k_ready = [&](int j) { return wait(&sb->k_full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1u); };
       uint32_t cleaned = 0;  // per stage: the parity of its next cleaned tile
-      auto v_ready = [&](int j) {
-        const int st = j % C::kStages;
-        if (!wait(&sb->v_full[st], static_cast<uint32_t>(j / C::kStages) & 1u)) return false;
-        if (to_scrub(j)) {
-          if (!wait(&sb->v_clean[st], cleaned >> st & 1u)) return false;
-          cleaned ^= 1u << st;
-        }
-        return true;
-      };
-      auto p_ready = [&](int x, int j) {
-        if (!wait(&sb->p_full[x], static_cast<uint32_t>(j) & 1u)) return false;
-        tc_fence_after();
-        return true;
-      };
-      bool ok = wait(&sb->q_full, 0) && k_ready(0);
-      if (ok)
+      bool ok = wait(lane == 0 ? &sb->q_full : &sb->k_full[0], 0);
+      if (ok && lane == 0)
         for (int x = 0; x < 2; ++x)
           if (cnt[x] > 0) mma_s(x, 0);
+      __syncwarp();
       for (int j = 0; ok && j < n_kv; ++j) {
-        if (!v_ready(j)) break;
-        bool next_k = false;
+        const int st = j % C::kStages;
+        bool first = true;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (!ok || j >= cnt[x]) continue;
-          ok = p_ready(x, j);
-          if (!ok) continue;
-          mma_pv(x, j);
-          // K_j and V_j are fully consumed once their last product lands
-          if (x == 1 || j >= cnt[1]) tc_commit(&sb->kv_empty[j % C::kStages]);
-          if (j + 1 == cnt[x]) tc_commit(&sb->o_full[x]);
-          if (j + 1 < cnt[x]) {
-            if (!next_k) ok = k_ready(j + 1), next_k = true;
-            if (ok) mma_s(x, j + 1);
+          uint64_t* bar = &sb->p_full[x];
+          uint32_t parity = static_cast<uint32_t>(j) & 1u;
+          if (first) {  // and what both tiles' products of this step read
+            if (lane == 1) bar = &sb->v_full[st], parity = static_cast<uint32_t>(j / C::kStages) & 1u;
+            if (lane == 2 && j + 1 < n_kv)
+              bar = &sb->k_full[(j + 1) % C::kStages], parity = static_cast<uint32_t>((j + 1) / C::kStages) & 1u;
+            if (to_scrub(j)) {
+              if (lane == 3) bar = &sb->v_clean[st], parity = cleaned >> st & 1u;
+              cleaned ^= 1u << st;
+            }
+            first = false;
           }
+          ok = wait(bar, parity);
+          if (ok && lane == 0) {
+            tc_fence_after();
+            mma_pv(x, j);
+            if (j + 1 == cnt[x]) tc_commit(&sb->o_full[x]);
+            if (j + 1 < cnt[x]) mma_s(x, j + 1);
+          }
+          __syncwarp();
         }
       }
-      if (*abort_flag) {
+      if (*abort_flag && lane == 0) {
         // wait (bounded) for every MMA issued so far before TMEM is released
         int never = 0;
         tc_commit(&sb->drain);
@@ -460,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&sb->v_clean[st]);
     }
   } else {
-    softmax_role<D, PAGED>(sb, (warp - 4) >> 2, tmem, a, seg, hk, t0, cnt[(warp - 4) >> 2], js, split, n_splits);
+    softmax_role<D, PAGED>(sb, (warp - 4) >> 2, tmem, a, seg, hk, t0, cnt[(warp - 4) >> 2], js, split, n_splits,
+                           (warp - 4) >> 2 == (cnt[1] > 0 ? 1 : 0));
   }
 
   __syncthreads();

@@ -100,6 +100,14 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&v)[32
     }
 }
 
+// One lane of a converged warp.  What is computed before it stays uniform, so that the operands of the instructions behind
+// it need no moves out of a lane's registers.
+__device__ __forceinline__ bool one_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // A box of a 4D tensor.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y, int32_t z,
                                             int32_t w) {

@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       uint32_t cleaned = 0;  // per stage: the parity of its next cleaned tile
       bool ok = wait(lane == 0 ? &sb->q_full : &sb->k_full[0], 0);
-      if (ok && lane == 0)
+      if (ok && one_lane())
         for (int x = 0; x < 2; ++x)
           if (cnt[x] > 0) mma_s(x, 0);
       __syncwarp();
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             first = false;
           }
           ok = wait(bar, parity);
-          if (ok && lane == 0) {
+          if (ok && one_lane()) {
             tc_fence_after();
             mma_pv(x, j);
             if (j + 1 == cnt[x]) tc_commit(&sb->o_full[x]);
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
-      if (*abort_flag && lane == 0) {
+      if (!ok && one_lane()) {
         // wait (bounded) for every MMA issued so far before TMEM is released
         int never = 0;
         tc_commit(&sb->drain);

@@ -56,7 +56,7 @@ struct Barriers {
   uint64_t k_empty[Cfg<D>::kStages];
   uint64_t v_empty[Cfg<D>::kStages];
   uint64_t s_full[2];
-  uint64_t p_full[2];
+  uint64_t p_full[2][2];  // per tile: the weights of its first 64 keys, of its last
   uint64_t o_full[2];
   uint64_t drain;
   uint32_t tmem_slot;
@@ -198,6 +198,10 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
     };
     emit(r0, 0);   // keys [0, 32)   -> columns [0, 16)
     emit(r1, 16);  // keys [32, 64)  -> columns [16, 32)
+    // the product of these keys may run while the others' weights are formed
+    tmem_st_wait();
+    tc_fence_before();
+    mbar_arrive(&sb->p_full[X][0]);
     emit(r2, 32);  // keys [64, 96)  -> columns [32, 48)
     emit(r3, 48);  // keys [96, 128) -> columns [48, 64)
     float sum;
@@ -209,7 +213,7 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
     }
     tmem_st_wait();
     tc_fence_before();
-    mbar_arrive(&sb->p_full[X]);
+    mbar_arrive(&sb->p_full[X][1]);
     l_run = l_run * alpha + sum;
   }
   if (cnt > 0) {
@@ -319,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sb->s_full[x], 1);
-      mbar_init(&sb->p_full[x], 128);
+      mbar_init(&sb->p_full[x][0], 128);
+      mbar_init(&sb->p_full[x][1], 128);
       mbar_init(&sb->o_full[x], 1);
     }
     mbar_init(&sb->drain, 1);
@@ -433,12 +438,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < D / 16; ++k) tc_mma<kKindF16>(d_s, q_desc + koff(k), k_desc + koff(k), C::kIdescS, k > 0 ? 1u : 0u);
         tc_commit(&sb->s_full[x]);
       };
-      auto mma_pv = [&](int x, int j) {  // O_x += P_x(j) V_j, P read from TMEM over S_x
+      auto mma_pv = [&](int x, int j, int half) {  // O_x += P_x(j) V_j over half of the keys, P read from TMEM over S_x
         const uint64_t v_desc = sdesc_mnmajor_sw128(smem_addr(v_tile(j % C::kStages)), kSeqBlock);
         const uint32_t p_cols = tmem + static_cast<uint32_t>(x * 128);  // 16 keys per 8 columns
         const uint32_t d_o = tmem + 256u + static_cast<uint32_t>(x * 128);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
           tc_mma_ts_f16(d_o, p_cols + static_cast<uint32_t>(k * 8), v_desc + static_cast<uint64_t>((k * 2048) >> 4), C::kIdescPV,
                         (j > 0 || k > 0) ? 1u : 0u);
       };
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (!ok || j >= cnt[x]) continue;
-          uint64_t* bar = &sb->p_full[x];
+          uint64_t* bar = &sb->p_full[x][0];
           uint32_t parity = static_cast<uint32_t>(j) & 1u;
           if (first) {  // and what both tiles' products of this step read
             if (lane == 1) bar = &sb->v_full[st], parity = static_cast<uint32_t>(j / C::kStages) & 1u;
@@ -469,7 +474,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(bar, parity);
           if (ok && one_lane()) {
             tc_fence_after();
-            mma_pv(x, j);
+            mma_pv(x, j, 0);
+          }
+          __syncwarp();
+          ok = ok && wait(&sb->p_full[x][1], static_cast<uint32_t>(j) & 1u);
+          if (ok && one_lane()) {
+            tc_fence_after();
+            mma_pv(x, j, 1);
             if (j + 1 == cnt[x]) tc_commit(&sb->o_full[x]);
             if (j + 1 < cnt[x]) mma_s(x, j + 1);
           }

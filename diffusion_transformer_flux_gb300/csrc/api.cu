@@ -2994,7 +2994,7 @@ mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   pdl_begin_call();
   ProfScope ps_("varlen_attention", st);
-  MMDIT_CUDA(launch_seq_attention(a, m, 0, 1, st), what);
+  MMDIT_CUDA(launch_seq_attention(a, m, 0, 1, status_word(workspace) + 32, st), what);
   return MMDIT_OK;
 }
 
@@ -3113,7 +3113,7 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
   pdl_begin_call();
   ProfScope ps_("paged_attention", st);
   if (p.tiles) {
-    MMDIT_CUDA(launch_seq_attention(a, m, 1, p.splits, st), what);
+    MMDIT_CUDA(launch_seq_attention(a, m, 1, p.splits, status_word(workspace) + 32, st), what);
     a.clear = 0;
   }
   if (p.few) MMDIT_CUDA(launch_paged_few(a, p.few_splits, st), "paged attention of few rows");

@@ -45,59 +45,101 @@ __device__ __forceinline__ int keys_seen(const Segment& s, int i, int causal) {
   return causal ? min(max(s.m - s.n + i + 1, 0), s.m) : s.m;
 }
 
-// Rows [r0, 128) of a [128][D] bf16 tile (128-byte swizzle, 64-column blocks `block` bytes apart) that not every
-// row of the other operand's tile may see.  A product multiplies them by weights of zero, and zero times an infinity or a
-// NaN is NaN; so rows from `end` on (of no token of this sequence) become zeros, and non-finite elements of the others
-// become zeros that are remembered: worst[c] takes the smallest (SMALLEST) or largest number first + r of such a row r in
-// column c.  A row that does see it writes NaN there in the end.
-template <int D, bool SMALLEST>
-__device__ __forceinline__ void scrub_rows(uint8_t* tile, int block, int r0, int end, int first, int* worst,
-                                           volatile int* any, int tid, int threads) {
-  constexpr int kChunks = D / 8;
-  for (int i = r0 * kChunks + tid; i < kSeqTile * kChunks; i += threads) {
-    const int r = i / kChunks, c = i % kChunks;
-    uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * block + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-    if (r >= end) {
-      *p = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    uint4 v = *p;
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool found = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t mask = 0x7F80u << (16 * (e & 1));
-      if ((w[e >> 1] & mask) == mask) {
-        w[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-        if (SMALLEST)
-          atomicMin(worst + c * 8 + e, first + r);
-        else
-          atomicMax(worst + c * 8 + e, first + r);
-        found = true;
-      }
-    }
-    if (found) {
-      *p = make_uint4(w[0], w[1], w[2], w[3]);
-      *any = 1;
-    }
+// The same for the tiles of a packed batch: x is a number of tiles of `span` rows, of which sequence b's are number
+// cu[b] / span + b and the following, that sequence's first row and rows in cu, and those in `other` as well.  Up to 31 sequences
+// take one round of loads.
+struct Located {
+  int b, first, count, other_first, other_count;
+};
+__device__ __forceinline__ Located locate(const int* cu, int total, const int* other, int other_total, int batch, int span, int x) {
+  Located r;
+  if (batch < 32) {
+    const int lane = threadIdx.x & 31, i = min(lane, batch);
+    const int v = min(max(cu[i], 0), total), w = other ? min(max(other[i], 0), other_total) : 0;
+    const unsigned below = __ballot_sync(0xffffffffu, lane < batch && v / span + lane <= x);
+    r.b = 31 - __clz(below | 1u);
+    r.first = __shfl_sync(0xffffffffu, v, r.b);
+    r.count = max(__shfl_sync(0xffffffffu, v, r.b + 1) - r.first, 0);
+    r.other_first = __shfl_sync(0xffffffffu, w, r.b);
+    r.other_count = max(__shfl_sync(0xffffffffu, w, r.b + 1) - r.other_first, 0);
+    return r;
   }
+  r.b = find_segment(batch, x, [&](int i) { return min(max(cu[i], 0), total) / span + i; });
+  clip_segment(cu, r.b, total, r.first, r.count);
+  r.other_first = r.other_count = 0;
+  if (other) clip_segment(other, r.b, other_total, r.other_first, r.other_count);
+  return r;
+}
+
+// Whether one of eight bf16 values is not finite: its exponent is all ones, and adding one to that carries into the sign's place.
+__device__ __forceinline__ uint32_t not_finite(const uint4& v) {
+  constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
+  return (((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne)) & 0x80008000u;
+}
+
+// Rows [r0, 128) of a [128][D] bf16 tile (128-byte swizzle, 64-column blocks) that not every row of the other operand's
+// tile may see.  A product multiplies them by weights of zero, and zero times an infinity or a NaN is NaN; so rows from `end` on
+// (of no token of this sequence) become zeros, and non-finite elements of the others become zeros that are remembered:
+// worst[c] takes the smallest number first + r of such a row r in column c.  A row that does see it writes NaN there in the
+// end.  Called by 64 threads; eight pieces are in flight in each.
+template <int D>
+__device__ __forceinline__ void scrub_rows(uint8_t* tile, int r0, int end, int first, int* worst, volatile int* any, int tid) {
+  constexpr int kChunks = D / 8;
+  auto at = [&](int i) {
+    const int r = i / kChunks, c = i % kChunks;
+    return reinterpret_cast<uint4*>(tile + (c >> 3) * kSeqBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+  };
+  const int stop = min(max(end, r0), kSeqTile) * kChunks;
+  for (int i0 = r0 * kChunks + tid; i0 < stop; i0 += 8 * 64) {
+    uint4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = i0 + 64 * u < stop ? *at(i0 + 64 * u) : make_uint4(0, 0, 0, 0);
+    uint32_t bad = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) bad |= (not_finite(v[u]) ? 1u : 0u) << u;
+    if (bad == 0) continue;
+    for (int u = 0; u < 8; ++u)
+      if (bad >> u & 1u) {
+        const int i = i0 + 64 * u, c = i % kChunks;
+        uint16_t* e = reinterpret_cast<uint16_t*>(at(i));
+        for (int k = 0; k < 8; ++k)
+          if ((e[k] & 0x7F80u) == 0x7F80u) {
+            e[k] = 0;
+            atomicMin(worst + c * 8 + k, first + i / kChunks);
+          }
+        *any = 1;
+      }
+  }
+  for (int i = stop + tid; i < kSeqTile * kChunks; i += 64) *at(i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
 }
 
-// `n` (a multiple of 8, up to 32) bf16 values of one row.
-__device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&v)[32], int n) {
-  if (n >= 32) {
-    store32(p, v);
-    return;
+// 32 rows of D bf16 values out of a warp's 32 x D / 8 16-byte pieces in shared memory (piece c of a row at c ^ (row & 7)), whole rows
+// at a time: lane l holds the address `row` of row l (null: not written).  A thread that stored its own row would touch 32
+// lines with each store (5000 cycles for a CTA's two tiles against 1000).
+template <int D>
+__device__ __forceinline__ void store_rows(const uint8_t* pieces, const __nv_bfloat16* row, int head_dim) {
+  constexpr int kChunks = D / 8, kRows = 32 / kChunks;
+  const int lane = threadIdx.x & 31, c = lane % kChunks, r0 = lane / kChunks;
+#pragma unroll 4
+  for (int i = 0; i < 32 / kRows; ++i) {
+    const int r = i * kRows + r0;
+    const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(row), r);
+    const uint4 v = *reinterpret_cast<const uint4*>(pieces + r * (2 * D) + ((c ^ (r & 7)) << 4));
+    if (p && c * 8 < head_dim) reinterpret_cast<uint4*>(p)[c] = v;
   }
+}
+// The pieces of 32 columns (from 32 e) of this lane's row.
+template <int D>
+__device__ __forceinline__ void put_pieces(uint8_t* pieces, int e, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (8 * i < n) {
-      uint4 u;
-      u.x = pack_bf16x2(v[8 * i + 0], v[8 * i + 1]), u.y = pack_bf16x2(v[8 * i + 2], v[8 * i + 3]);
-      u.z = pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), u.w = pack_bf16x2(v[8 * i + 6], v[8 * i + 7]);
-      reinterpret_cast<uint4*>(p)[i] = u;
-    }
+  for (int i = 0; i < 4; ++i) {
+    uint4 u;
+    u.x = pack_bf16x2(v[8 * i + 0], v[8 * i + 1]), u.y = pack_bf16x2(v[8 * i + 2], v[8 * i + 3]);
+    u.z = pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), u.w = pack_bf16x2(v[8 * i + 6], v[8 * i + 7]);
+    *reinterpret_cast<uint4*>(pieces + lane * (2 * D) + (((4 * e + i) ^ (lane & 7)) << 4)) = u;
+  }
 }
 
 // One lane of a converged warp.  What is computed before it stays uniform, so that the operands of the instructions behind
@@ -107,6 +149,15 @@ __device__ __forceinline__ bool one_lane() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+
+// Moves registers between the warpgroups of a CTA: the sum of the shares is what the launch gave.
+template <int R>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+// 384 threads are launched with 168 each: 128 x 72 + 256 x 216.
+constexpr int kLaunchRegisters = 168, kServiceRegisters = 72, kSoftmaxRegisters = 216;
+static_assert(128 * kServiceRegisters + 256 * kSoftmaxRegisters <= 384 * kLaunchRegisters, "shares of the launch's registers");
 
 // A box of a 4D tensor.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y, int32_t z,

@@ -63,30 +63,31 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Rows [lo, hi) of a tile that hold a non-finite element become zeros and are noted, rows [hi, 128) become zeros.
+// Rows [lo, hi) of a tile that hold a non-finite element become zeros and are noted, rows [zero_from, 128) become zeros.
+// Called by 64 threads; eight pieces are in flight in each.
 template <int D, bool KEYS>
 __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int zero_from, int first, int* worst, int tid) {
   constexpr int kChunks = D / 8;
-  for (int i = tid; i < kSeqTile * kChunks; i += 64) {
+  auto at = [&](int i) {
     const int r = i / kChunks, c = i % kChunks;
-    uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * kSeqBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-    if (r >= zero_from) {
-      *p = make_uint4(0, 0, 0, 0);
-    } else if (r >= lo && r < hi) {
-      const uint4 v = *p;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      bool bad = false;
+    return reinterpret_cast<uint4*>(tile + (c >> 3) * kSeqBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+  };
+  const int stop = min(hi, kSeqTile) * kChunks;
+  for (int i0 = lo * kChunks + tid; i0 < stop; i0 += 8 * 64) {
+    uint4 v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) bad |= (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
-      if (bad) {
-        *p = make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < 8; ++u) v[u] = i0 + 64 * u < stop ? *at(i0 + 64 * u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (not_finite(v[u])) {
+        *at(i0 + 64 * u) = make_uint4(0, 0, 0, 0);
         if (KEYS)
-          atomicMax(worst, first + r);
+          atomicMax(worst, first + (i0 + 64 * u) / kChunks);
         else
-          atomicMin(worst, first + r);
+          atomicMin(worst, first + (i0 + 64 * u) / kChunks);
       }
-    }
   }
+  for (int i = max(zero_from, 0) * kChunks + tid; i < kSeqTile * kChunks; i += 64) *at(i) = make_uint4(0, 0, 0, 0);
 }
 
 template <int D, bool KEYS>
@@ -391,32 +392,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (__all_sync(0xffffffffu, w)) {
       tc_fence_after();
       const int worst = *reinterpret_cast<volatile int*>(&sb->worst);
-      if constexpr (KEYS) {  // half 0 writes dV, half 1 dK
-        const HeadsView& out = h ? a.dk : a.dv;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.ptr) +
-                             (static_cast<int64_t>(seg.k0) + first + row) * out.stride_t + hk * out.stride_h;
-        const float f = worst >= from && valid ? __int_as_float(0x7FC00000) : h ? a.scale : 1.f;
+      // through the resident tiles' memory, whose products are done
+      uint8_t* pieces = smem + (warp - 4) * 32 * 2 * D;
+      if (KEYS || D == 128 || h == 0) {
+        // keys: half 0 writes dV, half 1 dK; queries: each half 64 columns of dQ
+        const HeadsView& out = !KEYS ? a.dq : h ? a.dk : a.dv;
+        const int64_t at = KEYS ? (static_cast<int64_t>(seg.k0) + first + row) * out.stride_t + hk * out.stride_h
+                                : (static_cast<int64_t>(seg.q0) + tok) * out.stride_t + (hk * G + row % G) * out.stride_h;
+        __nv_bfloat16* dst = valid ? static_cast<__nv_bfloat16*>(out.ptr) + at : nullptr;
+        const bool bad = valid && (KEYS ? worst >= from : worst < lim);
+        const float f = bad ? __int_as_float(0x7FC00000) : KEYS && h == 0 ? 1.f : a.scale;
+        const int blocks = KEYS ? D / 64 : 1, block0 = KEYS ? 0 : h;  // of 64 columns
 #pragma unroll 1
-        for (int e = 0; e < D / 32; ++e) {
-          float v[32];
-          uint32_t r[32];
-          if (count > 0) tmem_ld32_wait(tmem + kTmAcc + h * D + e * 32 + lane_off, r);
+        for (int k = block0; k < block0 + blocks; ++k) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(r[k]) * f : 0.f;
-          if (valid && e * 32 < a.head_dim) store_cols(dst + e * 32, v, a.head_dim - e * 32);
-        }
-      } else {  // each half writes half of dQ's columns
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq.ptr) + (static_cast<int64_t>(seg.q0) + tok) * a.dq.stride_t +
-                             (hk * G + row % G) * a.dq.stride_h;
-        const float f = worst < lim ? __int_as_float(0x7FC00000) : a.scale;
-#pragma unroll 1
-        for (int e = h * D / 64; e < (h + 1) * D / 64; ++e) {
-          float v[32];
-          uint32_t r[32];
-          if (count > 0) tmem_ld32_wait(tmem + kTmAcc + e * 32 + lane_off, r);
+          for (int e = 0; e < 2; ++e) {
+            float v[32];
+            uint32_t r[32];
+            if (count > 0) tmem_ld32_wait(tmem + kTmAcc + (KEYS ? h * D : 0) + k * 64 + e * 32 + lane_off, r);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(r[k]) * f : 0.f;
-          if (valid && e * 32 < a.head_dim) store_cols(dst + e * 32, v, a.head_dim - e * 32);
+            for (int i = 0; i < 32; ++i) v[i] = count > 0 ? __uint_as_float(r[i]) * f : 0.f;
+            put_pieces<64>(pieces, e, v);
+          }
+          __syncwarp();
+          store_rows<64>(pieces, dst ? dst + k * 64 : nullptr, a.head_dim - k * 64);
+          __syncwarp();
         }
       }
     }

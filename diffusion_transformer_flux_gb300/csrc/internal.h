@@ -480,6 +480,11 @@ struct SeqAttnArgs {
   float *part, *part_lse, *few_part, *few_lse;
   uint32_t* status;
   int clear;           // this kernel is the call's first and clears the status word
+  // set by the launcher: tile pairs of the queries, parts of their keys, and where there are more items than CTAs a counter of
+  // those handed out beside the first `first_next`
+  int pairs, splits;
+  uint32_t* next;
+  int first_next;
 };
 constexpr int kFewRows = 16;
 struct SeqAttnMaps {
@@ -488,7 +493,7 @@ struct SeqAttnMaps {
 int seq_tile_tokens(int group);
 bool encode_heads_map(CUtensorMap* map, const HeadsView& v, int head_dim, int heads, int64_t tokens, int box_heads, int box_tokens);
 bool encode_pages_map(CUtensorMap* map, const PagesView& v, int head_dim, int heads, int n_pages, int page_size, int rows);
-cudaError_t launch_seq_attention(SeqAttnArgs a, const SeqAttnMaps& m, int paged, int splits, cudaStream_t stream);
+cudaError_t launch_seq_attention(SeqAttnArgs a, const SeqAttnMaps& m, int paged, int splits, uint32_t* counter, cudaStream_t stream);
 // few rows to a sequence: `splits` CTAs of few_keys keys each; then the join of the parts of either kernel
 cudaError_t launch_paged_few(const SeqAttnArgs& a, int splits, cudaStream_t stream);
 cudaError_t launch_paged_combine(const SeqAttnArgs& a, cudaStream_t stream);

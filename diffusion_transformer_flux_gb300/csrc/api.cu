@@ -3043,7 +3043,7 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
   a.cu_q = cu_q, a.cu_k = cu_k, a.lse = lse, a.sums = at<float2>(workspace, kStatusBytes);
   if (tokens_q > 0) a.dout = heads_view(dout), a.out = heads_view(out), a.dq = heads_view(dq);
   if (tokens_k > 0) a.dk = heads_view(dk), a.dv = heads_view(dv);
-  a.status = status_word(workspace), a.clear = 1;
+  a.status = status_word(workspace), a.counters = a.status + 32;
   // where a side has no rows nothing is loaded through its maps
   const HeadsView mq = tokens_q > 0 ? heads_view(q) : heads_view(k), md = tokens_q > 0 ? a.dout : mq;
   const HeadsView mk = tokens_k > 0 ? heads_view(k) : mq, mv = tokens_k > 0 ? heads_view(v) : mq;

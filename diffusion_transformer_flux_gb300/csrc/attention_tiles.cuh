@@ -142,6 +142,28 @@ __device__ __forceinline__ void put_pieces(uint8_t* pieces, int e, const float (
   }
 }
 
+// The same for 32 columns at a time, from 2 KB: piece c of row r at c ^ (r / 2 & 3) of its 64 bytes.
+__device__ __forceinline__ void put_pieces32(uint8_t* pieces, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 u;
+    u.x = pack_bf16x2(v[8 * i + 0], v[8 * i + 1]), u.y = pack_bf16x2(v[8 * i + 2], v[8 * i + 3]);
+    u.z = pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), u.w = pack_bf16x2(v[8 * i + 6], v[8 * i + 7]);
+    *reinterpret_cast<uint4*>(pieces + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) = u;
+  }
+}
+__device__ __forceinline__ void store_rows32(const uint8_t* pieces, const __nv_bfloat16* row, int columns) {
+  const int lane = threadIdx.x & 31, c = lane & 3, r0 = lane >> 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + r0;
+    const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(row), r);
+    const uint4 v = *reinterpret_cast<const uint4*>(pieces + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+    if (p && c * 8 < columns) reinterpret_cast<uint4*>(p)[c] = v;
+  }
+}
+
 // One lane of a converged warp.  What is computed before it stays uniform, so that the operands of the instructions behind
 // it need no moves out of a lane's registers.
 __device__ __forceinline__ bool one_lane() {

@@ -7,18 +7,22 @@
 // memory from every key tile, in an order that changes the bits, through float32 traffic of several times the tensors' size.
 // Here every sum stays in tensor memory and is written once, in bf16.
 //
-// Both passes are one kernel, with a resident tile pair F (of 128 rows) and moving tile pairs M:
+// Both passes are one kernel, whose work items have a resident tile pair F (of 128 rows) and moving tile pairs M:
 //   keys:    F = K, V;     M = Q, dO;   S = K Q^T, dP = V dO^T;   dV += P dO,  dK += dS Q     (rows of S are keys)
 //   queries: F = Q, dO;    M = K, V;    S = Q K^T, dP = dO V^T;   dQ += dS K                  (rows of S are queries)
 // A tile of queries is 128 / group tokens by the group's heads, as in the forward, so the sum over the group's heads is the sum
 // over a moving tile's rows.  A moving tile is worked on in halves of 64 rows, so that one half's products run while the
-// other half's P and dS are formed.  Twelve warps:
-//   warp 0       TMA: F once, then M tiles into two stages
+// other half's P and dS are formed.  With N = 64 a product of two tiles in shared memory reads 6 KB for 32 cycles of
+// multiplication (48 cycles); where tensor memory has room for F (queries, and keys with D = 64), F is copied there.  Items are
+// found and handed out as in the forward.  Twelve warps:
+//   warp 0       items and TMA: F, then M tiles into two stages
 //   warp 1       MMA issuer: S, dP of half h of tile i + 1 follow the accumulating products of half h of tile i
 //   warps 2, 3   keys: -lse and -delta of the tile's rows; both: rows that part of the tile must not see (scrub_pair)
 //   warps 4..7   half 0: one row of S and dP per thread, P = exp2(c S - L) and dS = P (dP - delta) back into tensor memory as
-//                bf16 pairs (the operands of the accumulating products, each off by at most 2^-9 of itself); warps 8..11 half 1
-// TMEM columns: S [0,128), dP [128,256), then dV and dK, or dQ, D each.
+//                bf16 pairs (the operands of the accumulating products, each off by at most 2^-8 of itself); warps 8..11 half 1
+// TMEM columns: S [0,128), dP [128,256), then dV and dK, or dQ, D each, and F from 384 where it fits.
+#include <algorithm>
+
 #include "attention_tiles.cuh"
 
 namespace mmdit {
@@ -26,22 +30,34 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmP = 0, kTmD = 128, kTmAcc = 256;
+constexpr uint32_t kTmP = 0, kTmD = 128, kTmAcc = 256, kTmF = 384;
 constexpr int kStages = 2;
 
-template <int D>
+template <int D, bool KEYS>
 struct Cfg {
+  static constexpr bool kFInTmem = !KEYS || D == 64;
   static constexpr int kTileBytes = (D / 64) * kSeqBlock;
-  static constexpr int kData = (2 + 2 * kStages) * kTileBytes;
-  static constexpr int kSums = kData;                              // keys: per stage -L, then -delta, of 128 rows
+  static constexpr int kPieces = (2 + 2 * kStages) * kTileBytes;  // rows on their way out, 64 columns of 16 rows for each warp
+  static constexpr int kSums = kPieces + 8 * 16 * 128;            // keys: per stage -L, then -delta, of 128 rows
   static constexpr int kBar = kSums + kStages * 2 * kSeqTile * 4;
-  static constexpr int kSmem = kBar + 512 + 1024;
+  static constexpr int kSmem = kBar + 1024 + 1024;
   static constexpr uint32_t kIdescS = make_idesc<kKindF16>(128, 64);
   static constexpr uint32_t kIdescAcc = make_idesc<kKindF16>(128, D) | kIdescBMnMajor;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct Work {
+  int live;   // 0: no more items
+  int hk;
+  int first, count;  // first row of F in its sequence (a key, or a token), moving tiles
+  int m_first;       // keys: the first token that sees a key of the tile
+  int all_see;       // queries: keys that every row sees
+  Segment seg;
 };
 
 struct Barriers {
-  uint64_t f_full;
+  uint64_t work_full[2], work_empty[2];
+  uint64_t f_full, f_ready, f_empty;
   uint64_t st_full[kStages];
   uint64_t st_clean[kStages];
   uint64_t st_empty[kStages];
@@ -49,13 +65,14 @@ struct Barriers {
   uint64_t st_issued[kStages];  // queries: the copies of a tile to clean are on the way (so st_full's phase is this tile's)
   uint64_t sp_full[2];
   uint64_t pd_full[2];
-  uint64_t done;
+  uint64_t done, acc_free;
   uint64_t drain;
   uint32_t tmem_slot;
   int abort_flag;
-  int worst;  // the row of M that is not finite and that most rows of F see (keys: the last query row, queries: the first key)
+  int worst[2];  // per item: the row of M that is not finite and that most rows of F see (keys: the last query row, queries: the first key)
+  Work work[2];
 };
-static_assert(sizeof(Barriers) <= 512, "barriers");
+static_assert(sizeof(Barriers) <= 1024, "barriers");
 
 __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   uint64_t r;
@@ -90,269 +107,115 @@ __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int ze
   for (int i = max(zero_from, 0) * kChunks + tid; i < kSeqTile * kChunks; i += 64) *at(i) = make_uint4(0, 0, 0, 0);
 }
 
-template <int D, bool KEYS>
-__global__ void __launch_bounds__(kThreads, 1)
-    seq_attention_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                             const __grid_constant__ SeqAttnBwdArgs a) {
-  using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Barriers* sb = reinterpret_cast<Barriers*>(smem + C::kBar);
-  volatile int* abort_flag = &sb->abort_flag;
-  auto f_tile = [&](int x) { return smem + x * C::kTileBytes; };
-  auto m_tile = [&](int st, int x) { return smem + (2 + 2 * st + x) * C::kTileBytes; };
-  auto sums = [&](int st) { return reinterpret_cast<float*>(smem + C::kSums) + st * 2 * kSeqTile; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  pdl_wait();
-  // ---------------- this CTA's tile
-  const int hk = blockIdx.x % a.hk, G = a.group, T = a.tile_tokens;
-  Segment seg;
-  int first, count;  // first row of F (a key, or a token), moving tiles
-  int m_first = 0;   // keys: the first token that sees a key of the tile
+// Rows of moving tile i: [0, zero_from) are of this sequence, those of [lo, hi) not seen by every row of F.  Whether there
+// is something to clean.
+template <bool KEYS>
+__device__ __forceinline__ bool rows_of(const SeqAttnBwdArgs& a, const Work& w, int i, int& lo, int& hi, int& zero_from) {
   if constexpr (KEYS) {
-    const int idx = blockIdx.x / a.hk;  // the first keys have the most queries
-    const int b = find_segment(a.batch, idx, [&](int i) { return min(max(a.cu_k[i], 0), a.tokens_k) / kSeqTile + i; });
-    clip_segment(a.cu_k, b, a.tokens_k, seg.k0, seg.m);
-    clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
-    first = (idx - (seg.k0 / kSeqTile + b)) * kSeqTile;
-    if (first < 0 || first >= seg.m) return;
-    m_first = a.causal ? max(first - seg.m + seg.n, 0) : 0;
-    count = seg.n > m_first ? (seg.n - m_first + T - 1) / T : 0;
+    const int t = w.m_first + i * a.tile_tokens, last_key = min(w.first + kSeqTile, w.seg.m) - 1;
+    zero_from = a.group * min(a.tile_tokens, w.seg.n - t);
+    lo = 0;
+    hi = a.causal ? min(a.group * min(max(last_key - (w.seg.m - w.seg.n) - t, 0), a.tile_tokens), zero_from) : 0;
+    return zero_from < a.group * a.tile_tokens || hi > 0;
   } else {
-    const int idx = (gridDim.x - 1 - blockIdx.x) / a.hk;  // the last queries see the most keys
-    const int b = find_segment(a.batch, idx, [&](int i) { return min(max(a.cu_q[i], 0), a.tokens_q) / T + i; });
-    clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
-    clip_segment(a.cu_k, b, a.tokens_k, seg.k0, seg.m);
-    first = (idx - (seg.q0 / T + b)) * T;
-    if (first < 0 || first >= seg.n) return;
-    count = (keys_seen(seg, min(first + T, seg.n) - 1, a.causal) + kSeqTile - 1) / kSeqTile;
+    zero_from = min(w.seg.m - i * kSeqTile, kSeqTile);
+    lo = max(w.all_see - i * kSeqTile, 0), hi = zero_from;
+    return (i + 1) * kSeqTile > w.all_see;
   }
-  const int lag = seg.m - seg.n;  // query i stands at lag + i
-  const int all_see = KEYS ? 0 : keys_seen(seg, first, a.causal);
-  // rows of moving tile i: [0, zero_from) are of this sequence, those of [lo, hi) not seen by every row of F
-  auto rows_of = [&](int i, int& lo, int& hi, int& zero_from) {
-    if constexpr (KEYS) {
-      const int t = m_first + i * T, last_key = min(first + kSeqTile, seg.m) - 1;
-      zero_from = G * min(T, seg.n - t);
-      lo = 0, hi = a.causal ? min(G * min(max(last_key - lag - t, 0), T), zero_from) : 0;
-      return zero_from < G * T || hi > 0;
-    } else {
-      zero_from = min(seg.m - i * kSeqTile, kSeqTile);
-      lo = max(all_see - i * kSeqTile, 0), hi = zero_from;
-      return (i + 1) * kSeqTile > all_see;
-    }
+}
+
+// The next item of the counter, by all lanes of a warp.
+__device__ __forceinline__ int take_next(uint32_t* counter, int first_next) {
+  uint32_t v = 0;
+  if ((threadIdx.x & 31) == 0) v = atomicAdd(counter, 1u);
+  return first_next + static_cast<int>(__shfl_sync(0xffffffffu, v, 0));
+}
+
+template <int D, bool KEYS>
+__device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t tmem, const SeqAttnBwdArgs& a) {
+  using C = Cfg<D, KEYS>;
+  volatile int* abort_flag = &sb->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+  const int G = a.group, T = a.tile_tokens;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t t_p = tmem + kTmP + 64 * h + lane_off, t_d = tmem + kTmD + 64 * h + lane_off;
+  const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+  const int row_tok = row / G, row_head = row % G;
+  uint8_t* pieces = smem + C::kPieces + (warp - 4) * 16 * 128;
+  const float* sums_base = reinterpret_cast<const float*>(smem + C::kSums);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
   };
-
-  if (threadIdx.x == 0) {
-    mbar_init(&sb->f_full, 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sb->st_full[s], 1);
-      mbar_init(&sb->st_clean[s], 64);
-      mbar_init(&sb->st_empty[s], 1);
-      mbar_init(&sb->sums_full[s], 64);
-      mbar_init(&sb->st_issued[s], 1);
-    }
-    for (int h = 0; h < 2; ++h) mbar_init(&sb->sp_full[h], 1), mbar_init(&sb->pd_full[h], 128);
-    mbar_init(&sb->done, 1);
-    mbar_init(&sb->drain, 1);
-    sb->abort_flag = 0;
-    sb->worst = KEYS ? -1 : INT32_MAX;
-    fence_mbar_init();
-  }
-  if (KEYS && G * T < kSeqTile) {
-    // rows that no box fills: the products that sum over a moving tile's rows read them
-    const int rows = kSeqTile - G * T;
-    for (int i = threadIdx.x; i < kStages * 2 * (D / 64) * rows * 8; i += kThreads) {
-      const int c = i % 8, r = G * T + (i / 8) % rows, blk = i / (8 * rows);
-      *reinterpret_cast<uint4*>(smem + 2 * C::kTileBytes + blk * kSeqBlock + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
-  }
-  if (warp == 1) {
-    tmem_alloc(&sb->tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sb->tmem_slot;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait); };
-
-  if (warp == 0) {
-    if (lane == 0 && count > 0) {
-      // ---------------- TMA producer
-      const CUtensorMap *f0 = KEYS ? &tm_k : &tm_q, *f1 = KEYS ? &tm_v : &tm_do;
-      const CUtensorMap *m0 = KEYS ? &tm_q : &tm_k, *m1 = KEYS ? &tm_do : &tm_v;
-      tma_prefetch_desc(f0), tma_prefetch_desc(f1), tma_prefetch_desc(m0), tma_prefetch_desc(m1);
-      const int bytes_q = (D / 64) * G * T * 128;  // a box of queries
-      const int f_head = KEYS ? hk : hk * G, m_head = KEYS ? hk * G : hk;
-      const int f_row = KEYS ? seg.k0 + first : seg.q0 + first;
-      mbar_arrive_expect_tx(&sb->f_full, 2 * (KEYS ? C::kTileBytes : bytes_q));
-      for (int h = 0; h < D / 64; ++h) {
-        tma_load_3d(f_tile(0) + h * kSeqBlock, f0, &sb->f_full, h * 64, f_head, f_row);
-        tma_load_3d(f_tile(1) + h * kSeqBlock, f1, &sb->f_full, h * 64, f_head, f_row);
-      }
-      int issued = 0;
-      for (int i = 0; i < count; ++i) {
-        const int st = i % kStages;
-        if (!wait(&sb->st_empty[st], (static_cast<uint32_t>(i / kStages) & 1u) ^ 1u)) break;
-        const int row = KEYS ? seg.q0 + m_first + i * T : seg.k0 + i * kSeqTile;
-        mbar_arrive_expect_tx(&sb->st_full[st], 2 * (KEYS ? bytes_q : C::kTileBytes));
-        for (int h = 0; h < D / 64; ++h) {
-          tma_load_3d(m_tile(st, 0) + h * kSeqBlock, m0, &sb->st_full[st], h * 64, m_head, row);
-          tma_load_3d(m_tile(st, 1) + h * kSeqBlock, m1, &sb->st_full[st], h * 64, m_head, row);
-        }
-        int lo, hi, zero_from;
-        if (!KEYS && rows_of(i, lo, hi, zero_from)) mbar_arrive(&sb->st_issued[st]);
-        issued = i + 1;
-      }
-      if (*abort_flag) {
-        int never = 0;
-        mbar_wait(&sb->f_full, 0, &never, a.status, 0);
-        for (int t = max(issued - kStages, 0); t < issued; ++t)
-          mbar_wait(&sb->st_full[t % kStages], static_cast<uint32_t>(t / kStages) & 1u, &never, a.status, 0);
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && count > 0) {
-      // ---------------- MMA issuer
-      auto koff = [](int k) -> uint64_t { return static_cast<uint64_t>(((k >> 2) * kSeqBlock + (k & 3) * 32) >> 4); };
-      const uint64_t df0 = sdesc_kmajor_sw128(smem_addr(f_tile(0))), df1 = sdesc_kmajor_sw128(smem_addr(f_tile(1)));
-      uint32_t cleaned = 0;
-      auto scores = [&](int i, int h) -> bool {  // S and dP of half h of tile i
-        const int st = i % kStages;
-        if (h == 0) {
-          if (!wait(&sb->st_full[st], static_cast<uint32_t>(i / kStages) & 1u)) return false;
-          int lo, hi, zero_from;
-          if (rows_of(i, lo, hi, zero_from)) {
-            if (!wait(&sb->st_clean[st], cleaned >> st & 1u)) return false;
-            cleaned ^= 1u << st;
-          }
-          tc_fence_after();
-        }
-        const uint64_t dm0 = sdesc_kmajor_sw128(smem_addr(m_tile(st, 0)) + h * 64 * 128);
-        const uint64_t dm1 = sdesc_kmajor_sw128(smem_addr(m_tile(st, 1)) + h * 64 * 128);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma<kKindF16>(tmem + kTmP + 64 * h, df0 + koff(k), dm0 + koff(k), C::kIdescS, k > 0 ? 1u : 0u);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma<kKindF16>(tmem + kTmD + 64 * h, df1 + koff(k), dm1 + koff(k), C::kIdescS, k > 0 ? 1u : 0u);
-        tc_commit(&sb->sp_full[h]);
-        return true;
-      };
-      bool ok = wait(&sb->f_full, 0) && scores(0, 0) && scores(0, 1);
-      for (int i = 0; ok && i < count; ++i) {
-        const int st = i % kStages;
-        for (int h = 0; ok && h < 2; ++h) {
-          ok = wait(&sb->pd_full[h], static_cast<uint32_t>(i) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dm0 = sdesc_mnmajor_sw128(smem_addr(m_tile(st, 0)) + h * 64 * 128, kSeqBlock);
-          const uint64_t dm1 = sdesc_mnmajor_sw128(smem_addr(m_tile(st, 1)) + h * 64 * 128, kSeqBlock);
-          const uint32_t more = i > 0 || h > 0 ? 1u : 0u;
-          if constexpr (KEYS) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // dV
-              tc_mma_ts_f16(tmem + kTmAcc, tmem + kTmP + 64 * h + 8 * k, dm1 + static_cast<uint64_t>((k * 2048) >> 4), C::kIdescAcc,
-                            k > 0 ? 1u : more);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // dK
-              tc_mma_ts_f16(tmem + kTmAcc + D, tmem + kTmD + 64 * h + 8 * k, dm0 + static_cast<uint64_t>((k * 2048) >> 4),
-                            C::kIdescAcc, k > 0 ? 1u : more);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // dQ
-              tc_mma_ts_f16(tmem + kTmAcc, tmem + kTmP + 64 * h + 8 * k, dm0 + static_cast<uint64_t>((k * 2048) >> 4), C::kIdescAcc,
-                            k > 0 ? 1u : more);
-          }
-          if (h == 1) tc_commit(&sb->st_empty[st]);
-          if (i + 1 < count) ok = scores(i + 1, h);
-        }
-      }
-      if (ok) tc_commit(&sb->done);
-      if (*abort_flag) {
-        int never = 0;
-        tc_commit(&sb->drain);
-        mbar_wait(&sb->drain, 0, &never, a.status, 0);
-      }
-    }
-  } else if (warp < 4) {
-    // ---------------- sums of the moving rows, and rows that part of F must not see
-    const int tid = static_cast<int>(threadIdx.x) - 64;
-    uint32_t cleaned = 0;  // per stage: the parity of its next tile to clean
-    for (int i = 0; i < count; ++i) {
-      const int st = i % kStages;
-      bool w = true;
-      if constexpr (KEYS) {
-        w = wait(&sb->st_empty[st], (static_cast<uint32_t>(i / kStages) & 1u) ^ 1u);
-        if (!__all_sync(0xffffffffu, w)) break;
-        const int t = m_first + i * T, rows = G * min(T, seg.n - t);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = tid + 64 * e;
-          float2 s = make_float2(0.f, 0.f);
-          if (r < rows) s = a.sums[(static_cast<size_t>(seg.q0) + t + r / G) * a.hq + hk * G + r % G];
-          sums(st)[r] = -s.x, sums(st)[kSeqTile + r] = -s.y;
-        }
-        mbar_arrive(&sb->sums_full[st]);
-      }
-      int lo, hi, zero_from;
-      if (!rows_of(i, lo, hi, zero_from)) continue;
-      // (keys: st_empty has told that the stage's previous tile is done)
-      if (!KEYS) w = wait(&sb->st_issued[st], cleaned >> st & 1u), cleaned ^= 1u << st;
-      if (w) w = wait(&sb->st_full[st], static_cast<uint32_t>(i / kStages) & 1u);
-      if (!__all_sync(0xffffffffu, w)) break;
-      const int at = KEYS ? G * (m_first + i * T) : i * kSeqTile;
-      scrub_pair<D, KEYS>(m_tile(st, 0), lo, hi, zero_from, at, &sb->worst, tid);
-      if (KEYS) scrub_pair<D, KEYS>(m_tile(st, 1), lo, hi, zero_from, at, &sb->worst, tid);
-      fence_proxy_async_smem();
-      mbar_arrive(&sb->st_clean[st]);
-    }
-  } else {
-    // ---------------- P and dS of half h; then the sums
-    const int h = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_p = tmem + kTmP + 64 * h + lane_off, t_d = tmem + kTmD + 64 * h + lane_off;
-    const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
+  uint32_t f_turn = 0, sp_turn = 0, done_turn = 0, sums_turn = 0;  // parities of the next phases (sums: a bit for each stage)
+  for (uint32_t it = 0;; ++it) {
+    const int slot = it & 1;
+    if (!wait(&sb->work_full[slot], it >> 1 & 1u)) return;
+    const Work w = sb->work[slot];
+    if (!w.live) return;
+    const int lag = w.seg.m - w.seg.n;  // query i stands at lag + i
     // queries: this row's sums and the keys it sees; keys: the first query row (tokens by group) that sees it
-    const int tok = first + row / G;
-    const bool valid = KEYS ? first + row < seg.m : row < G * T && tok < seg.n;
-    const int lim = KEYS || !valid ? 0 : keys_seen(seg, tok, a.causal);
-    const int from = !KEYS ? 0 : !valid ? INT32_MAX : a.causal ? G * max(first + row - lag, 0) : 0;
+    const int tok = w.first + row_tok;
+    const bool valid = KEYS ? w.first + row < w.seg.m : row < G * T && tok < w.seg.n;
+    const int lim = KEYS || !valid ? 0 : keys_seen(w.seg, tok, a.causal);
+    const int from = !KEYS ? 0 : !valid ? INT32_MAX : a.causal ? G * max(w.first + row - lag, 0) : 0;
     uint64_t neg_l = 0, neg_d = 0;
     if constexpr (!KEYS) {
       float2 s = make_float2(0.f, 0.f);
-      if (valid) s = a.sums[(static_cast<size_t>(seg.q0) + tok) * a.hq + hk * G + row % G];
+      if (valid) s = a.sums[(static_cast<size_t>(w.seg.q0) + tok) * a.hq + w.hk * G + row_head];
       neg_l = f32x2(-s.x, -s.x), neg_d = f32x2(-s.y, -s.y);
     }
-    bool live = true;
-    for (int i = 0; i < count; ++i) {
-      const int st = i % kStages;
-      bool w = wait(&sb->sp_full[h], static_cast<uint32_t>(i) & 1u);
-      if (KEYS && w) w = wait(&sb->sums_full[st], static_cast<uint32_t>(i / kStages) & 1u);
-      if (!__all_sync(0xffffffffu, w)) { live = false; break; }
+    if (C::kFInTmem && w.count > 0) {
+      // F into tensor memory, half 0 its first tile, half 1 its second; the last item's scores are formed (sp_full)
+      if (!wait(&sb->f_full, f_turn)) return;
+      f_turn ^= 1u;
+      const uint8_t* tile = smem + h * C::kTileBytes + row * 128;
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        uint32_t r[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(tile + b * kSeqBlock + ((c ^ (row & 7)) << 4));
+          r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
+        }
+        tmem_st32(tmem + kTmF + h * (D / 2) + b * 32 + lane_off, r);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sb->f_empty);
+      mbar_arrive(&sb->f_ready);
+    }
+    int st = 0;
+    for (int i = 0; i < w.count; ++i) {
+      if (!wait(&sb->sp_full[h], sp_turn)) return;
+      sp_turn ^= 1u;
+      if constexpr (KEYS) {
+        if (!wait(&sb->sums_full[st], sums_turn >> st & 1u)) return;
+        sums_turn ^= 1u << st;
+      }
       tc_fence_after();
       // columns [lo, hi) of the tile are seen by this row
       int lo, hi;
       if constexpr (KEYS) {
-        const int t = m_first + i * T;
-        hi = G * min(T, seg.n - t), lo = from == INT32_MAX ? kSeqTile : max(from - G * t, 0);
+        const int t = w.m_first + i * T;
+        hi = G * min(T, w.seg.n - t), lo = from == INT32_MAX ? kSeqTile : max(from - G * t, 0);
       } else {
         lo = 0, hi = lim - i * kSeqTile;
       }
       const bool part = __any_sync(0xffffffffu, lo > 64 * h || hi < 64 * h + 64);
+      const float* sums = sums_base + st * 2 * kSeqTile + 64 * h;
+      uint32_t s[2][32], d[2][32];
+      tmem_ld32(t_p, s[0]);
+      tmem_ld32(t_d, d[0]);
+      tmem_ld_deps64(s[0], d[0]);
+      tmem_ld32(t_p + 32, s[1]);
+      tmem_ld32(t_d + 32, d[1]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint32_t s[32], d[32];
-        tmem_ld32(t_p + 32 * c, s);
-        tmem_ld32(t_d + 32 * c, d);
-        tmem_ld_deps64(s, d);
+        if (c == 1) tmem_ld_deps64(s[1], d[1]);
         uint32_t pk[16], dk[16];
-        const float4* l4 = reinterpret_cast<const float4*>(sums(st) + 64 * h + 32 * c);
-        const float4* d4 = reinterpret_cast<const float4*>(sums(st) + kSeqTile + 64 * h + 32 * c);
+        const float4* l4 = reinterpret_cast<const float4*>(sums + 32 * c);
+        const float4* d4 = reinterpret_cast<const float4*>(sums + kSeqTile + 32 * c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           uint64_t nl[2] = {neg_l, neg_l}, nd[2] = {neg_d, neg_d};
@@ -364,9 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 0; g < 2; ++g) {
             const int k = 4 * e + 2 * g;
             float p0, p1, z0, z1;
-            f32x2_split(ffma2(f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, nl[g]), p0, p1);
+            f32x2_split(ffma2(f32x2(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), scale2, nl[g]), p0, p1);
             p0 = fast_exp2(p0), p1 = fast_exp2(p1);
-            f32x2_split(fmul2(f32x2(p0, p1), fadd2(f32x2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), nd[g])), z0, z1);
+            f32x2_split(fmul2(f32x2(p0, p1), fadd2(f32x2(__uint_as_float(d[c][k]), __uint_as_float(d[c][k + 1])), nd[g])), z0, z1);
             if (part) {
               const int col = 64 * h + 32 * c + k;
               if (col < lo || col >= hi) p0 = z0 = 0.f;
@@ -386,39 +249,336 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&sb->pd_full[h]);
+      st ^= 1;
     }
-    bool w = live;
-    if (w && count > 0) w = wait(&sb->done, 0);
-    if (__all_sync(0xffffffffu, w)) {
+    if (w.count > 0) {
+      if (!wait(&sb->done, done_turn)) return;
+      done_turn ^= 1u;
       tc_fence_after();
-      const int worst = *reinterpret_cast<volatile int*>(&sb->worst);
-      // through the resident tiles' memory, whose products are done
-      uint8_t* pieces = smem + (warp - 4) * 32 * 2 * D;
-      if (KEYS || D == 128 || h == 0) {
-        // keys: half 0 writes dV, half 1 dK; queries: each half 64 columns of dQ
-        const HeadsView& out = !KEYS ? a.dq : h ? a.dk : a.dv;
-        const int64_t at = KEYS ? (static_cast<int64_t>(seg.k0) + first + row) * out.stride_t + hk * out.stride_h
-                                : (static_cast<int64_t>(seg.q0) + tok) * out.stride_t + (hk * G + row % G) * out.stride_h;
-        __nv_bfloat16* dst = valid ? static_cast<__nv_bfloat16*>(out.ptr) + at : nullptr;
-        const bool bad = valid && (KEYS ? worst >= from : worst < lim);
-        const float f = bad ? __int_as_float(0x7FC00000) : KEYS && h == 0 ? 1.f : a.scale;
-        const int blocks = KEYS ? D / 64 : 1, block0 = KEYS ? 0 : h;  // of 64 columns
+    }
+    const int worst = *reinterpret_cast<volatile int*>(&sb->worst[slot]);
+    if (KEYS || D == 128 || h == 0) {
+      // keys: half 0 writes dV, half 1 dK; queries: each half 64 columns of dQ
+      const HeadsView& out = !KEYS ? a.dq : h ? a.dk : a.dv;
+      const int64_t at = KEYS ? (static_cast<int64_t>(w.seg.k0) + w.first + row) * out.stride_t + w.hk * out.stride_h
+                              : (static_cast<int64_t>(w.seg.q0) + tok) * out.stride_t + (w.hk * G + row_head) * out.stride_h;
+      __nv_bfloat16* dst = valid ? static_cast<__nv_bfloat16*>(out.ptr) + at : nullptr;
+      const bool bad = valid && (KEYS ? worst >= from : worst < lim);
+      const float f = bad ? __int_as_float(0x7FC00000) : KEYS && h == 0 ? 1.f : a.scale;
+      const int blocks = KEYS ? D / 32 : 2, block0 = KEYS ? 0 : 2 * h;  // of 32 columns
 #pragma unroll 1
-        for (int k = block0; k < block0 + blocks; ++k) {
+      for (int k = block0; k < block0 + blocks; ++k) {
+        float v[32];
+        uint32_t r[32];
+        if (w.count > 0) tmem_ld32_wait(tmem + kTmAcc + (KEYS ? h * D : 0) + k * 32 + lane_off, r);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v[32];
-            uint32_t r[32];
-            if (count > 0) tmem_ld32_wait(tmem + kTmAcc + (KEYS ? h * D : 0) + k * 64 + e * 32 + lane_off, r);
+        for (int i = 0; i < 32; ++i) v[i] = w.count > 0 ? __uint_as_float(r[i]) * f : 0.f;
+        put_pieces32(pieces, v);
+        __syncwarp();
+        store_rows32(pieces, dst ? dst + k * 32 : nullptr, a.head_dim - k * 32);
+        __syncwarp();
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (w.count > 0) mbar_arrive(&sb->acc_free);  // the sums have been read
+      mbar_arrive(&sb->work_empty[slot]);
+    }
+  }
+}
+
+template <int D, bool KEYS>
+__global__ void __launch_bounds__(kThreads, 1)
+    seq_attention_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                             const __grid_constant__ SeqAttnBwdArgs a, int items, int first_next) {
+  using C = Cfg<D, KEYS>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Barriers* sb = reinterpret_cast<Barriers*>(smem + C::kBar);
+  volatile int* abort_flag = &sb->abort_flag;
+  auto f_tile = [&](int x) { return smem + x * C::kTileBytes; };
+  auto m_tile = [&](int st, int x) { return smem + (2 + 2 * st + x) * C::kTileBytes; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.group, T = a.tile_tokens;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sb->work_full[s], 1);
+      mbar_init(&sb->work_empty[s], 1 + 2 + 8);  // warps 1, 2, 3 and the warps of rows
+      mbar_init(&sb->sp_full[s], 1);
+      mbar_init(&sb->pd_full[s], 128);
+    }
+    mbar_init(&sb->f_full, 1);
+    mbar_init(&sb->f_ready, 256);
+    mbar_init(&sb->f_empty, C::kFInTmem ? 256 : 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sb->st_full[s], 1);
+      mbar_init(&sb->st_clean[s], 64);
+      mbar_init(&sb->st_empty[s], 1);
+      mbar_init(&sb->sums_full[s], 64);
+      mbar_init(&sb->st_issued[s], 1);
+    }
+    mbar_init(&sb->done, 1);
+    mbar_init(&sb->acc_free, 8);
+    mbar_init(&sb->drain, 1);
+    sb->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (KEYS && G * T < kSeqTile) {
+    // rows that no box fills: the products that sum over a moving tile's rows read them
+    const int rows = kSeqTile - G * T;
+    for (int i = threadIdx.x; i < kStages * 2 * (D / 64) * rows * 8; i += kThreads) {
+      const int c = i % 8, r = G * T + (i / 8) % rows, blk = i / (8 * rows);
+      *reinterpret_cast<uint4*>(smem + 2 * C::kTileBytes + blk * kSeqBlock + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sb->tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sb->tmem_slot;
+  pdl_wait();
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
+  };
+
+  if (warp >= 4) {
+    more_registers<kSoftmaxRegisters>();
+    rows_role<D, KEYS>(sb, smem, tmem, a);
+  } else if (fewer_registers<kServiceRegisters>(), warp == 0) {
+    // ---------------- items and TMA
+    const CUtensorMap *f0 = KEYS ? &tm_k : &tm_q, *f1 = KEYS ? &tm_v : &tm_do;
+    const CUtensorMap *m0 = KEYS ? &tm_q : &tm_k, *m1 = KEYS ? &tm_do : &tm_v;
+    if (lane == 0) tma_prefetch_desc(f0), tma_prefetch_desc(f1), tma_prefetch_desc(m0), tma_prefetch_desc(m1);
+    uint32_t* counter = a.counters + (KEYS ? 0 : 1);
+    const int bytes_q = (D / 64) * G * T * 128;  // a box of queries
+    uint32_t f_turn = 0, st_turn = 0, st_used = 0;
+    bool ok = true, f_used = false;
+    int item = blockIdx.x;
+    for (uint32_t it = 0; ok; ++it) {
+      Work w;
+      w.live = 0;
+      for (; item < items; item = items > first_next ? take_next(counter, first_next) : items) {
+        w.hk = item % a.hk;
+        if constexpr (KEYS) {
+          const int idx = item / a.hk;  // the first keys have the most queries
+          const Located at = locate(a.cu_k, a.tokens_k, a.cu_q, a.tokens_q, a.batch, kSeqTile, idx);
+          w.seg = {at.other_first, at.other_count, at.first, at.count};
+          w.first = (idx - (w.seg.k0 / kSeqTile + at.b)) * kSeqTile;
+          if (w.first < 0 || w.first >= w.seg.m) continue;
+          w.m_first = a.causal ? max(w.first - w.seg.m + w.seg.n, 0) : 0;
+          w.count = w.seg.n > w.m_first ? (w.seg.n - w.m_first + T - 1) / T : 0;
+          w.all_see = 0;
+        } else {
+          const int idx = (items - 1 - item) / a.hk;  // the last queries see the most keys
+          const Located at = locate(a.cu_q, a.tokens_q, a.cu_k, a.tokens_k, a.batch, T, idx);
+          w.seg = {at.first, at.count, at.other_first, at.other_count};
+          w.first = (idx - (w.seg.q0 / T + at.b)) * T;
+          if (w.first < 0 || w.first >= w.seg.n) continue;
+          w.count = (keys_seen(w.seg, min(w.first + T, w.seg.n) - 1, a.causal) + kSeqTile - 1) / kSeqTile;
+          w.m_first = 0;
+          w.all_see = keys_seen(w.seg, w.first, a.causal);
+        }
+        w.live = 1;
+        break;
+      }
+      const int slot = it & 1;
+      ok = wait(&sb->work_empty[slot], (it >> 1 & 1u) ^ 1u);
+      if (!ok) break;
+      if (lane == 0) {
+        sb->work[slot] = w;
+        *reinterpret_cast<volatile int*>(&sb->worst[slot]) = KEYS ? -1 : INT32_MAX;
+        mbar_arrive(&sb->work_full[slot]);
+      }
+      __syncwarp();
+      if (!w.live) break;
+      const int next_item = items > first_next ? take_next(counter, first_next) : items;
+      if (w.count > 0) {
+        ok = wait(&sb->f_empty, f_turn ^ 1u);
+        if (!ok) break;
+        f_turn ^= 1u, f_used = true;
+        if (lane == 0) {
+          const int f_head = KEYS ? w.hk : w.hk * G, f_row = KEYS ? w.seg.k0 + w.first : w.seg.q0 + w.first;
+          mbar_arrive_expect_tx(&sb->f_full, 2 * (KEYS ? C::kTileBytes : bytes_q));
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = count > 0 ? __uint_as_float(r[i]) * f : 0.f;
-            put_pieces<64>(pieces, e, v);
+          for (int b = 0; b < D / 64; ++b) {
+            tma_load_3d(f_tile(0) + b * kSeqBlock, f0, &sb->f_full, b * 64, f_head, f_row);
+            tma_load_3d(f_tile(1) + b * kSeqBlock, f1, &sb->f_full, b * 64, f_head, f_row);
           }
-          __syncwarp();
-          store_rows<64>(pieces, dst ? dst + k * 64 : nullptr, a.head_dim - k * 64);
-          __syncwarp();
         }
       }
+      int st = 0;
+      for (int i = 0; i < w.count; ++i, st ^= 1) {
+        ok = wait(&sb->st_empty[st], (st_turn >> st & 1u) ^ 1u);
+        if (!ok) break;
+        st_turn ^= 1u << st, st_used |= 1u << st;
+        if (lane == 0) {
+          const int m_head = KEYS ? w.hk * G : w.hk, row = KEYS ? w.seg.q0 + w.m_first + i * T : w.seg.k0 + i * kSeqTile;
+          mbar_arrive_expect_tx(&sb->st_full[st], 2 * (KEYS ? bytes_q : C::kTileBytes));
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b) {
+            tma_load_3d(m_tile(st, 0) + b * kSeqBlock, m0, &sb->st_full[st], b * 64, m_head, row);
+            tma_load_3d(m_tile(st, 1) + b * kSeqBlock, m1, &sb->st_full[st], b * 64, m_head, row);
+          }
+          int lo, hi, zero_from;
+          if (!KEYS && rows_of<KEYS>(a, w, i, lo, hi, zero_from)) mbar_arrive(&sb->st_issued[st]);
+        }
+        __syncwarp();
+      }
+      item = next_item;
+    }
+    if (!ok) {
+      // give the copies already issued a bounded chance to land before the CTA exits
+      int never = 0;
+      if (f_used) mbar_wait(&sb->f_full, f_turn ^ 1u, &never, a.status, 0);
+      for (int s = 0; s < kStages; ++s)
+        if (st_used >> s & 1u) mbar_wait(&sb->st_full[s], (st_turn >> s & 1u) ^ 1u, &never, a.status, 0);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer: the warp's lanes test the barriers of a step side by side, one lane issues; of a descriptor
+    // only the address in its lower half changes (see attention_varlen.cu)
+    auto koff = [](int k) -> uint32_t { return static_cast<uint32_t>(((k >> 2) * kSeqBlock + (k & 3) * 32) >> 4); };
+    auto desc = [](uint64_t base, uint32_t lo) { return (base & 0xFFFFFFFF00000000ull) | lo; };
+    const uint64_t k_base = sdesc_kmajor_sw128(smem_addr(f_tile(0))), n_base = sdesc_mnmajor_sw128(smem_addr(m_tile(0, 0)), kSeqBlock);
+    uint32_t f_lo = static_cast<uint32_t>(k_base), m_lo = static_cast<uint32_t>(sdesc_kmajor_sw128(smem_addr(m_tile(0, 0)))),
+             n_lo = static_cast<uint32_t>(n_base);
+    constexpr uint32_t kStep = static_cast<uint32_t>(C::kTileBytes) >> 4, kHalf = (64 * 128) >> 4;
+    auto scores = [&](int st, int h) {  // S and dP of half h of the tile in stage st
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t to = tmem + (x ? kTmD : kTmP) + 64 * h;
+          const uint64_t m = desc(k_base, m_lo + (2 * st + x) * kStep + h * kHalf + koff(k));
+          if constexpr (C::kFInTmem)
+            tc_mma_ts_f16(to, tmem + kTmF + x * (D / 2) + k * 8, m, C::kIdescS, k > 0 ? 1u : 0u);
+          else
+            tc_mma<kKindF16>(to, desc(k_base, f_lo + x * kStep + koff(k)), m, C::kIdescS, k > 0 ? 1u : 0u);
+        }
+      tc_commit(&sb->sp_full[h]);
+    };
+    auto products = [&](int st, int h, uint32_t more) {
+#pragma unroll
+      for (int x = KEYS ? 0 : 1; x < 2; ++x)  // dV += P dO and dK += dS Q, or dQ += dS K
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_ts_f16(tmem + kTmAcc + (KEYS ? x * D : 0), tmem + (KEYS && x ? kTmD : kTmP) + 64 * h + 8 * k,
+                        desc(n_base, n_lo + (2 * st + (x ? 0 : 1)) * kStep + h * kHalf + ((k * 2048) >> 4)), C::kIdescAcc,
+                        k > 0 ? 1u : more);
+    };
+    uint32_t f_turn = 0, st_turn = 0, clean_turn = 0, pd_turn = 0, acc_turn = 1;  // parities (st: a bit for each stage)
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
+      const int slot = it & 1;
+      ok = wait(&sb->work_full[slot], it >> 1 & 1u);
+      if (!ok) break;
+      const Work w = sb->work[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb->work_empty[slot]);
+      if (!w.live) break;
+      if (w.count == 0) continue;
+      int lo, hi, zero_from;
+      if (rows_of<KEYS>(a, w, 0, lo, hi, zero_from)) {
+        ok = wait(&sb->st_clean[0], clean_turn & 1u);
+        clean_turn ^= 1u;
+      }
+      ok = ok && wait(lane == 0 ? (C::kFInTmem ? &sb->f_ready : &sb->f_full) : &sb->st_full[0], lane == 0 ? f_turn : st_turn & 1u);
+      f_turn ^= 1u, st_turn ^= 1u;
+      if (ok && one_lane()) {
+        tc_fence_after();
+        scores(0, 0);
+        scores(0, 1);
+        if (!C::kFInTmem && w.count == 1) tc_commit(&sb->f_empty);
+      }
+      __syncwarp();
+      for (int i0 = 0; ok && i0 < w.count; i0 += kStages) {
+#pragma unroll
+        for (int st = 0; st < kStages; ++st) {
+          const int i = i0 + st;
+          if (!ok || i >= w.count) break;
+          const bool next = i + 1 < w.count;
+          if (next && rows_of<KEYS>(a, w, i + 1, lo, hi, zero_from)) {
+            ok = wait(&sb->st_clean[st ^ 1], clean_turn >> (st ^ 1) & 1u);
+            clean_turn ^= 1u << (st ^ 1);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            asm volatile("" : "+r"(f_lo), "+r"(m_lo), "+r"(n_lo));  // the sums below are formed here, not kept in registers
+            const bool st_too = h == 0 && next && lane == 1, acc_too = h == 0 && i == 0 && lane == 2;
+            ok = ok && wait(st_too ? &sb->st_full[st ^ 1] : acc_too ? &sb->acc_free : &sb->pd_full[h],
+                            st_too ? st_turn >> (st ^ 1) & 1u : acc_too ? acc_turn : pd_turn);
+            if (ok && one_lane()) {
+              tc_fence_after();
+              products(st, h, i > 0 || h > 0 ? 1u : 0u);
+              if (h == 1) tc_commit(&sb->st_empty[st]);
+              if (next)
+                scores(st ^ 1, h);
+              else if (h == 1)
+                tc_commit(&sb->done);
+              if (!C::kFInTmem && h == 1 && i + 2 == w.count) tc_commit(&sb->f_empty);
+            }
+            __syncwarp();
+          }
+          pd_turn ^= 1u;
+          if (next) st_turn ^= 1u << (st ^ 1);
+        }
+      }
+      acc_turn ^= 1u;
+    }
+    if (!ok && one_lane()) {
+      int never = 0;
+      tc_commit(&sb->drain);
+      mbar_wait(&sb->drain, 0, &never, a.status, 0);
+    }
+  } else {
+    // ---------------- sums of the moving rows, and rows that part of F must not see
+    const int tid = static_cast<int>(threadIdx.x) - 64;
+    uint32_t st_turn = 0, clean_turn = 0;  // a bit for each stage: the tile's turn, that of the next tile to clean
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
+      const int slot = it & 1;
+      ok = wait(&sb->work_full[slot], it >> 1 & 1u);
+      if (!ok) break;
+      const Work w = sb->work[slot];
+      int st = 0;
+      for (int i = 0; w.live && ok && i < w.count; ++i, st ^= 1) {
+        const uint32_t parity = st_turn >> st & 1u;
+        st_turn ^= 1u << st;
+        if constexpr (KEYS) {
+          ok = wait(&sb->st_empty[st], parity ^ 1u);
+          if (!ok) break;
+          float* sums = reinterpret_cast<float*>(smem + C::kSums) + st * 2 * kSeqTile;
+          const int t = w.m_first + i * T, rows = G * min(T, w.seg.n - t);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = tid + 64 * e;
+            float2 s = make_float2(0.f, 0.f);
+            if (r < rows) s = a.sums[(static_cast<size_t>(w.seg.q0) + t + r / G) * a.hq + w.hk * G + r % G];
+            sums[r] = -s.x, sums[kSeqTile + r] = -s.y;
+          }
+          mbar_arrive(&sb->sums_full[st]);
+        }
+        int lo, hi, zero_from;
+        if (!rows_of<KEYS>(a, w, i, lo, hi, zero_from)) continue;
+        // (keys: st_empty has told that the stage's previous tile is done)
+        if (!KEYS) ok = wait(&sb->st_issued[st], clean_turn >> st & 1u), clean_turn ^= 1u << st;
+        ok = ok && wait(&sb->st_full[st], parity);
+        if (!ok) break;
+        const int at = KEYS ? G * (w.m_first + i * T) : i * kSeqTile;
+        scrub_pair<D, KEYS>(m_tile(st, 0), lo, hi, zero_from, at, &sb->worst[slot], tid);
+        if (KEYS) scrub_pair<D, KEYS>(m_tile(st, 1), lo, hi, zero_from, at, &sb->worst[slot], tid);
+        fence_proxy_async_smem();
+        mbar_arrive(&sb->st_clean[st]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb->work_empty[slot]);
+      if (!w.live) break;
     }
   }
 
@@ -432,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (lse log2(e), dout . out) of every row, float32: 16 lanes to a row.  Rows of no sequence are read and not used.
 __global__ void __launch_bounds__(256) seq_sums_kernel(const __grid_constant__ SeqAttnBwdArgs a) {
   pdl_wait();
-  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0, a.counters[0] = 0, a.counters[1] = 0;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
   const int c = (threadIdx.x & 15) * 8;
   if (row >= static_cast<int64_t>(a.tokens_q) * a.hq) return;
@@ -454,13 +614,14 @@ __global__ void __launch_bounds__(256) seq_sums_kernel(const __grid_constant__ S
 
 template <int D, bool KEYS>
 cudaError_t launch_pass(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaStream_t stream) {
-  const int64_t tiles = (KEYS ? a.tokens_k / kSeqTile : a.tokens_q / a.tile_tokens) + static_cast<int64_t>(a.batch);
-  if (tiles * a.hk > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(seq_attention_bwd_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<D>::kSmem);
+  const int64_t items = ((KEYS ? a.tokens_k / kSeqTile : a.tokens_q / a.tile_tokens) + static_cast<int64_t>(a.batch)) * a.hk;
+  if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
+  using C = Cfg<D, KEYS>;
+  cudaError_t e = cudaFuncSetAttribute(seq_attention_bwd_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(seq_attention_bwd_kernel<D, KEYS>, dim3(static_cast<unsigned>(tiles * a.hk)), dim3(kThreads), Cfg<D>::kSmem,
-                 stream, m.q, m.dout, m.k, m.v, a);
+  const int grid = static_cast<int>(std::min<int64_t>(items, num_sms()));
+  e = launch_pdl(seq_attention_bwd_kernel<D, KEYS>, dim3(grid), dim3(kThreads), C::kSmem, stream, m.q, m.dout, m.k, m.v, a,
+                 static_cast<int>(items), grid);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -469,13 +630,12 @@ cudaError_t launch_pass(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaSt
 }  // namespace
 
 cudaError_t launch_seq_attention_bwd(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaStream_t stream) {
-  cudaError_t e;
-  if (a.tokens_q > 0) {
-    const int64_t rows = static_cast<int64_t>(a.tokens_q) * a.hq;
-    e = launch_pdl(seq_sums_kernel, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, stream, a);
-    if (e != cudaSuccess) return e;
-    count_launch();
-  }
+  // the first kernel also clears the status word and the counters
+  const int64_t rows = static_cast<int64_t>(a.tokens_q) * a.hq;
+  cudaError_t e = launch_pdl(seq_sums_kernel, dim3(static_cast<unsigned>(std::max<int64_t>((rows + 15) / 16, 1))), dim3(256), 0,
+                             stream, a);
+  if (e != cudaSuccess) return e;
+  count_launch();
   if (a.tokens_k > 0) {
     e = a.head_dim <= 64 ? launch_pass<64, true>(a, m, stream) : launch_pass<128, true>(a, m, stream);
     if (e != cudaSuccess) return e;

@@ -508,7 +508,7 @@ struct SeqAttnBwdArgs {
   const float* lse;  // [tokens_q, hq]
   float2* sums;      // [tokens_q, hq]: lse log2(e), dout . out
   uint32_t* status;
-  int clear;
+  uint32_t* counters;  // of the items handed out in each pass
 };
 struct SeqAttnBwdMaps {
   CUtensorMap q, dout, k, v;

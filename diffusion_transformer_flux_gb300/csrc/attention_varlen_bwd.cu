@@ -22,6 +22,7 @@
 //                bf16 pairs (the operands of the accumulating products, each off by at most 2^-8 of itself); warps 8..11 half 1
 // TMEM columns: S [0,128), dP [128,256), then dV and dK, or dQ, D each, and F from 384 where it fits.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_tiles.cuh"
 
@@ -210,9 +211,8 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       tmem_ld_deps64(s[0], d[0]);
       tmem_ld32(t_p + 32, s[1]);
       tmem_ld32(t_d + 32, d[1]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (c == 1) tmem_ld_deps64(s[1], d[1]);
+      // 32 columns; a tile that is seen in part has a loop of its own, a branch for each pair would hold every chain up
+      auto columns = [&](auto in_part, const uint32_t (&sc)[32], const uint32_t (&dc)[32], int c) {
         uint32_t pk[16], dk[16];
         const float4* l4 = reinterpret_cast<const float4*>(sums + 32 * c);
         const float4* d4 = reinterpret_cast<const float4*>(sums + kSeqTile + 32 * c);
@@ -227,10 +227,10 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
           for (int g = 0; g < 2; ++g) {
             const int k = 4 * e + 2 * g;
             float p0, p1, z0, z1;
-            f32x2_split(ffma2(f32x2(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), scale2, nl[g]), p0, p1);
+            f32x2_split(ffma2(f32x2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), scale2, nl[g]), p0, p1);
             p0 = fast_exp2(p0), p1 = fast_exp2(p1);
-            f32x2_split(fmul2(f32x2(p0, p1), fadd2(f32x2(__uint_as_float(d[c][k]), __uint_as_float(d[c][k + 1])), nd[g])), z0, z1);
-            if (part) {
+            f32x2_split(fmul2(f32x2(p0, p1), fadd2(f32x2(__uint_as_float(dc[k]), __uint_as_float(dc[k + 1])), nd[g])), z0, z1);
+            if constexpr (decltype(in_part)::value) {
               const int col = 64 * h + 32 * c + k;
               if (col < lo || col >= hi) p0 = z0 = 0.f;
               if (col + 1 < lo || col + 1 >= hi) p1 = z1 = 0.f;
@@ -245,6 +245,15 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
         } else {
           tmem_st16(t_p + 16 * c, dk);
         }
+      };
+      if (part) {
+        columns(std::true_type{}, s[0], d[0], 0);
+        tmem_ld_deps64(s[1], d[1]);
+        columns(std::true_type{}, s[1], d[1], 1);
+      } else {
+        columns(std::false_type{}, s[0], d[0], 0);
+        tmem_ld_deps64(s[1], d[1]);
+        columns(std::false_type{}, s[1], d[1], 1);
       }
       tmem_st_wait();
       tc_fence_before();

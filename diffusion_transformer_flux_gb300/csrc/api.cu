@@ -3014,6 +3014,8 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
   const char* what = "varlen attention backward";
   mmdit_status s = check_attention(what, batch, tokens_q, tokens_k, heads_q, heads_k, head_dim, scale);
   if (s != MMDIT_OK) return s;
+  if (heads_q / heads_k > kBwdMaxGroup)
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: at most 64 query heads to a key head (got %d)", what, heads_q / heads_k);
   const int64_t tiles = std::max(tokens_k / 128, tokens_q / (128 / (heads_q / heads_k))) + static_cast<int64_t>(batch);
   if (tiles * heads_k > INT32_MAX || static_cast<int64_t>(tokens_q) * heads_q > (int64_t{1} << 34))
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
@@ -3038,7 +3040,8 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
     return fail(MMDIT_ERR_INVALID_ARG, "%s: cu_q, cu_k or lse is NULL or not 4-byte aligned", what);
   SeqAttnBwdArgs a = {};
   a.batch = batch, a.tokens_q = tokens_q, a.tokens_k = tokens_k, a.hq = heads_q, a.hk = heads_k, a.group = heads_q / heads_k;
-  a.head_dim = head_dim, a.causal = causal != 0, a.tile_tokens = seq_tile_tokens(a.group);
+  a.head_dim = head_dim, a.causal = causal != 0;
+  a.tile_tokens = seq_tile_tokens(a.group), a.unit_tokens = 64 / a.group;
   a.scale = scale, a.scale_log2 = scale * 1.4426950408889634f;
   a.cu_q = cu_q, a.cu_k = cu_k, a.lse = lse, a.sums = at<float2>(workspace, kStatusBytes);
   if (tokens_q > 0) a.dout = heads_view(dout), a.out = heads_view(out), a.dq = heads_view(dq);
@@ -3048,10 +3051,13 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
   const HeadsView mq = tokens_q > 0 ? heads_view(q) : heads_view(k), md = tokens_q > 0 ? a.dout : mq;
   const HeadsView mk = tokens_k > 0 ? heads_view(k) : mq, mv = tokens_k > 0 ? heads_view(v) : mq;
   SeqAttnBwdMaps m;
-  if (!encode_heads_map(&m.q, mq, head_dim, tokens_q > 0 ? heads_q : 1, std::max(tokens_q, 1), a.group, a.tile_tokens) ||
-      !encode_heads_map(&m.dout, md, head_dim, tokens_q > 0 ? heads_q : 1, std::max(tokens_q, 1), a.group, a.tile_tokens) ||
-      !encode_heads_map(&m.k, mk, head_dim, tokens_k > 0 ? heads_k : 1, std::max(tokens_k, 1), 1, 128) ||
-      !encode_heads_map(&m.v, mv, head_dim, tokens_k > 0 ? heads_k : 1, std::max(tokens_k, 1), 1, 128))
+  const int hq = tokens_q > 0 ? heads_q : 1, hk = tokens_k > 0 ? heads_k : 1, tq = std::max(tokens_q, 1), tk = std::max(tokens_k, 1);
+  if (!encode_heads_map(&m.f_q, mq, head_dim, hq, tq, a.group, a.tile_tokens) ||
+      !encode_heads_map(&m.f_dout, md, head_dim, hq, tq, a.group, a.tile_tokens) ||
+      !encode_heads_map(&m.f_k, mk, head_dim, hk, tk, 1, 128) || !encode_heads_map(&m.f_v, mv, head_dim, hk, tk, 1, 128) ||
+      !encode_heads_map(&m.m_q, mq, head_dim, hq, tq, a.group, a.unit_tokens) ||
+      !encode_heads_map(&m.m_dout, md, head_dim, hq, tq, a.group, a.unit_tokens) ||
+      !encode_heads_map(&m.m_k, mk, head_dim, hk, tk, 1, 64) || !encode_heads_map(&m.m_v, mv, head_dim, hk, tk, 1, 64))
     return fail(MMDIT_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", what);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   pdl_begin_call();

@@ -45,31 +45,98 @@ __device__ __forceinline__ int keys_seen(const Segment& s, int i, int causal) {
   return causal ? min(max(s.m - s.n + i + 1, 0), s.m) : s.m;
 }
 
-// The same for the tiles of a packed batch: x is a number of tiles of `span` rows, of which sequence b's are number
-// cu[b] / span + b and the following, that sequence's first row and rows in cu, and those in `other` as well.  Up to 31 sequences
-// take one round of loads.
-struct Located {
-  int b, first, count, other_first, other_count;
-};
-__device__ __forceinline__ Located locate(const int* cu, int total, const int* other, int other_total, int batch, int span, int x) {
-  Located r;
-  if (batch < 32) {
-    const int lane = threadIdx.x & 31, i = min(lane, batch);
-    const int v = min(max(cu[i], 0), total), w = other ? min(max(other[i], 0), other_total) : 0;
-    const unsigned below = __ballot_sync(0xffffffffu, lane < batch && v / span + lane <= x);
-    r.b = 31 - __clz(below | 1u);
-    r.first = __shfl_sync(0xffffffffu, v, r.b);
-    r.count = max(__shfl_sync(0xffffffffu, v, r.b + 1) - r.first, 0);
-    r.other_first = __shfl_sync(0xffffffffu, w, r.b);
-    r.other_count = max(__shfl_sync(0xffffffffu, w, r.b + 1) - r.other_first, 0);
-    return r;
+// The tiles of a packed batch (of `span` rows of the sequences in cu; `other` is the other side's prefix sums, or null) in the
+// order in which they are handed out, held by the lanes of a warp.  Dear ones go first, so that the GPU's SMs end together.
+//   Up to 32 sequences: a lane holds one each, sorted by the other side's length.  Where a tile's cost falls with its number
+//   (causal) the tiles of all sequences come level by level, else sequence by sequence; number x is found by counting.
+//   More: sequence b's tiles are number cu[b] / span + b and the following, which leaves each at least as many numbers as
+//   it needs without a prefix sum; those left over are of no tile, and the sequences come in their order.
+// `from_end`: a sequence's last tile is its dearest.
+struct TileOrder {
+  const int *cu, *other;
+  int total, other_total, batch, span, causal, from_end;
+  int n;                                                // numbers
+  int seq, first, count, other_first, other_count;      // this lane's sequence
+  int tiles;
+  int level, base;                                      // where the last search ended
+
+  __device__ __forceinline__ void init(const int* cu_, int total_, const int* other_, int other_total_, int batch_, int span_,
+                                       int causal_, int from_end_) {
+    cu = cu_, total = total_, other = other_, other_total = other_total_, batch = batch_, span = span_;
+    causal = causal_, from_end = from_end_, level = 0, base = 0;
+    if (batch > 32) {
+      n = total / span + batch;
+      return;
+    }
+    const int lane = threadIdx.x & 31, i = min(lane, batch - 1);
+    seq = lane;
+    clip_segment(cu, i, total, first, count);
+    other_first = 0, other_count = 0;
+    if (other) clip_segment(other, i, other_total, other_first, other_count);
+    const int length = other ? other_count : count;
+    int rank = lane < batch ? 0 : lane, from = lane;
+    for (int j = 0; j < batch; ++j) {
+      const int l = __shfl_sync(0xffffffffu, length, j);
+      rank += lane < batch && (l > length || (l == length && j < lane));
+    }
+    for (int j = 0; j < batch; ++j)
+      if (__shfl_sync(0xffffffffu, rank, j) == lane) from = j;
+    seq = __shfl_sync(0xffffffffu, seq, from), first = __shfl_sync(0xffffffffu, first, from);
+    count = __shfl_sync(0xffffffffu, count, from), other_first = __shfl_sync(0xffffffffu, other_first, from);
+    other_count = __shfl_sync(0xffffffffu, other_count, from);
+    tiles = lane < batch ? (count + span - 1) / span : 0;
+    n = tiles;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   }
-  r.b = find_segment(batch, x, [&](int i) { return min(max(cu[i], 0), total) / span + i; });
-  clip_segment(cu, r.b, total, r.first, r.count);
-  r.other_first = r.other_count = 0;
-  if (other) clip_segment(other, r.b, other_total, r.other_first, r.other_count);
-  return r;
-}
+
+  struct Found {
+    int b, first, count, other_first, other_count;
+    int start;  // the tile's first row in its sequence
+  };
+  // Number x < n; false where it is of no tile.
+  __device__ __forceinline__ bool find(int x, Found& f) {
+    int tile;
+    if (batch > 32) {
+      const int y = from_end ? n - 1 - x : x;
+      f.b = find_segment(batch, y, [&](int i) { return min(max(cu[i], 0), total) / span + i; });
+      clip_segment(cu, f.b, total, f.first, f.count);
+      f.other_first = f.other_count = 0;
+      if (other) clip_segment(other, f.b, other_total, f.other_first, f.other_count);
+      tile = y - (f.first / span + f.b);
+    } else {
+      int lane;
+      if (causal) {
+        if (x < base) level = 0, base = 0;
+        unsigned have = __ballot_sync(0xffffffffu, tiles > level);
+        while (x >= base + __popc(have) && have) {
+          base += __popc(have), ++level;
+          have = __ballot_sync(0xffffffffu, tiles > level);
+        }
+        const unsigned mine = 1u << (threadIdx.x & 31);
+        lane = __ffs(__ballot_sync(0xffffffffu, (have & mine) && __popc(have & (mine - 1)) == x - base)) - 1;
+        lane = max(lane, 0);
+        tile = level;
+      } else {
+        int sum = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, sum, o);
+          if ((threadIdx.x & 31) >= o) sum += y;
+        }
+        const unsigned after = __ballot_sync(0xffffffffu, sum > x);
+        lane = after ? __ffs(after) - 1 : 0;
+        tile = x - __shfl_sync(0xffffffffu, sum - tiles, lane);
+      }
+      f.b = __shfl_sync(0xffffffffu, seq, lane), f.first = __shfl_sync(0xffffffffu, first, lane);
+      f.count = __shfl_sync(0xffffffffu, count, lane), f.other_first = __shfl_sync(0xffffffffu, other_first, lane);
+      f.other_count = __shfl_sync(0xffffffffu, other_count, lane);
+      if (from_end) tile = __shfl_sync(0xffffffffu, tiles, lane) - 1 - tile;
+    }
+    f.start = tile * span;
+    return tile >= 0 && f.start < f.count;
+  }
+};
 
 // Whether one of eight bf16 values is not finite: its exponent is all ones, and adding one to that carries into the sign's place.
 __device__ __forceinline__ uint32_t not_finite(const uint4& v) {

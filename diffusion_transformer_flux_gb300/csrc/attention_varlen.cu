@@ -7,11 +7,10 @@
 // The query heads of a group read the same keys, so a tile's 128 rows are 128 / group tokens by the group's heads (row
 // r is token r / group, head r % group): a key tile is loaded once for all of them, and a short chunk of new tokens
 // fills a tile `group` times as well.  A work item is two such tiles (A and B, consecutive tokens) of one key head, which walk
-// the keys in tiles of 128 with an online softmax.  Items are found by a search in cu_q: sequence b's first tile pair is
-// number cu_q[b] / (2 tokens) + b, which leaves each at least as many numbers as it needs without a prefix sum; numbers
-// that are left over are skipped.  Items with the most keys come first; one CTA to an SM takes its first by its number and further
-// ones from a counter, loads the next one's tiles while it ends the last, and forms the next one's first scores while its
-// softmax warps write the last one's rows (a CTA for each item: 20500 cycles beside 2800 a key tile).
+// the keys in tiles of 128 with an online softmax.  Items with the most keys come first (TileOrder); one CTA to an SM takes its
+// first by its number and further ones from a counter, loads the next one's tiles while it ends the last, and forms the next
+// one's first scores while its softmax warps write the last one's rows (a CTA for each item: 20500 cycles beside 2800 a key
+// tile).
 //
 // Twelve warps:
 //   warp 0       items and TMA: both Q tiles, then K and V tiles into rings (in a paged cache a lane for each page of a tile)
@@ -362,7 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
     if (a.clear && blockIdx.x == 0 && lane == 0) *a.status = 0;
     const int pieces = PAGED ? kSeqTile / a.page_rows : 1;
-    const int span = 2 * a.tile_tokens, per_split = a.pairs * a.hk, items = per_split * a.splits;
+    TileOrder order;
+    order.init(a.cu_q, a.tokens_q, PAGED ? nullptr : a.cu_k, a.tokens_k, a.batch, 2 * a.tile_tokens, a.causal, 1);
+    const int per_split = order.n * a.hk, items = per_split * a.splits;
     uint32_t q_turn = 0, k_turn = 0, v_turn = 0;  // the next phases' parities; k, v: a bit for each stage
     uint32_t k_used = 0, v_used = 0;
     bool ok = true, q_used = false;
@@ -371,12 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Work w;
       w.live = 0;
       for (; item < items; item = a.next ? take_next(a) : items) {
-        const int rest = item % per_split, pair = a.pairs - 1 - rest / a.hk;
-        const Located at = locate(a.cu_q, a.tokens_q, PAGED ? nullptr : a.cu_k, a.tokens_k, a.batch, span, pair);
-        w.b = at.b, w.hk = rest % a.hk, w.split = item / per_split;
+        const int rest = item % per_split;
+        TileOrder::Found at;
+        if (!order.find(rest / a.hk, at)) continue;
+        w.b = at.b, w.hk = rest % a.hk, w.split = item / per_split, w.t0 = at.start;
         w.seg = {at.first, at.count, at.other_first, at.other_count};
-        w.t0 = (pair - (w.seg.q0 / span + w.b)) * span;
-        if (w.t0 < 0 || w.t0 >= w.seg.n) continue;
         int split_tiles = INT32_MAX;
         w.n_splits = 1, w.js = 0;
         if constexpr (PAGED) {
@@ -666,7 +666,7 @@ cudaError_t launch_seq_attention(SeqAttnArgs a, const SeqAttnMaps& m, int paged,
   const int64_t pairs = a.tokens_q / (2 * a.tile_tokens) + static_cast<int64_t>(a.batch);
   const int64_t items = pairs * a.hk * splits;
   if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
-  a.pairs = static_cast<int>(pairs), a.splits = splits;
+  a.splits = splits;
   const int grid = static_cast<int>(std::min<int64_t>(items, num_sms()));
   cudaError_t e;
   if (items > grid) {  // further items are handed out by a counter (status word and counter share the workspace's first line)

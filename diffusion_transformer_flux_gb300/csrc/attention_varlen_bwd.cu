@@ -11,15 +11,17 @@
 //   keys:    F = K, V;     M = Q, dO;   S = K Q^T, dP = V dO^T;   dV += P dO,  dK += dS Q     (rows of S are keys)
 //   queries: F = Q, dO;    M = K, V;    S = Q K^T, dP = dO V^T;   dQ += dS K                  (rows of S are queries)
 // A tile of queries is 128 / group tokens by the group's heads, as in the forward, so the sum over the group's heads is the sum
-// over a moving tile's rows.  A moving tile is worked on in halves of 64 rows, so that one half's products run while the
-// other half's P and dS are formed.  With N = 64 a product of two tiles in shared memory reads 6 KB for 32 cycles of
+// over a moving tile's rows.  Moving tiles have up to 64 rows and take turns in two buffers of S and dP, so that the products
+// of one run while P and dS of the other are formed; their ring in shared memory holds four to eight (the load of one takes
+// as long as the work on two).  With N = 64 a product of two tiles in shared memory reads 6 KB for 32 cycles of
 // multiplication (48 cycles); where tensor memory has room for F (queries, and keys with D = 64), F is copied there.  Items are
 // found and handed out as in the forward.  Twelve warps:
-//   warp 0       items and TMA: F, then M tiles into two stages
-//   warp 1       MMA issuer: S, dP of half h of tile i + 1 follow the accumulating products of half h of tile i
+//   warp 0       items and TMA: F, then M tiles
+//   warp 1       MMA issuer: S, dP of tile u + 2 follow the accumulating products of tile u
 //   warps 2, 3   keys: -lse and -delta of the tile's rows; both: rows that part of the tile must not see (scrub_pair)
-//   warps 4..7   half 0: one row of S and dP per thread, P = exp2(c S - L) and dS = P (dP - delta) back into tensor memory as
-//                bf16 pairs (the operands of the accumulating products, each off by at most 2^-8 of itself); warps 8..11 half 1
+//   warps 4..7   tiles of even number: one row of S and dP per thread, P = exp2(c S - L) and dS = P (dP - delta) back into tensor
+//                memory as bf16 pairs (the operands of the accumulating products, each off by at most 2^-8 of itself);
+//                warps 8..11 those of odd number
 // TMEM columns: S [0,128), dP [128,256), then dV and dK, or dQ, D each, and F from 384 where it fits.
 #include <algorithm>
 #include <type_traits>
@@ -32,17 +34,23 @@ namespace {
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmP = 0, kTmD = 128, kTmAcc = 256, kTmF = 384;
-constexpr int kStages = 2;
+constexpr int kUnit = 64;  // rows of a moving tile
 
 template <int D, bool KEYS>
 struct Cfg {
   static constexpr bool kFInTmem = !KEYS || D == 64;
-  static constexpr int kTileBytes = (D / 64) * kSeqBlock;
-  static constexpr int kPieces = (2 + 2 * kStages) * kTileBytes;  // rows on their way out, 64 columns of 16 rows for each warp
-  static constexpr int kSums = kPieces + 8 * 16 * 128;            // keys: per stage -L, then -delta, of 128 rows
-  static constexpr int kBar = kSums + kStages * 2 * kSeqTile * 4;
+  static constexpr bool kFInRing = !KEYS;  // F passes through two slots of the ring (a pair of 128 rows has their size)
+  static constexpr int kTileBytes = (D / 64) * kSeqBlock;  // of F
+  static constexpr int kUnitBlock = kUnit * 128;           // 64 rows of 64 columns
+  static constexpr int kHalfSlot = (D / 64) * kUnitBlock;
+  static constexpr int kSlotBytes = 2 * kHalfSlot;         // the moving pair
+  static constexpr int kSlots = D == 64 ? 8 : KEYS ? 4 : 6;
+  static constexpr int kRing = kFInRing ? 0 : 2 * kTileBytes;
+  static constexpr int kPieces = kRing + kSlots * kSlotBytes;  // rows on their way out, 32 columns of 32 rows for each warp
+  static constexpr int kSums = kPieces + 8 * 32 * 64;          // keys: per slot -L, then -delta, of 64 rows
+  static constexpr int kBar = kSums + (KEYS ? kSlots * 2 * kUnit * 4 : 0);
   static constexpr int kSmem = kBar + 1024 + 1024;
-  static constexpr uint32_t kIdescS = make_idesc<kKindF16>(128, 64);
+  static constexpr uint32_t kIdescS = make_idesc<kKindF16>(128, kUnit);
   static constexpr uint32_t kIdescAcc = make_idesc<kKindF16>(128, D) | kIdescBMnMajor;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -58,12 +66,9 @@ struct Work {
 
 struct Barriers {
   uint64_t work_full[2], work_empty[2];
-  uint64_t f_full, f_ready, f_empty;
-  uint64_t st_full[kStages];
-  uint64_t st_clean[kStages];
-  uint64_t st_empty[kStages];
-  uint64_t sums_full[kStages];
-  uint64_t st_issued[kStages];  // queries: the copies of a tile to clean are on the way (so st_full's phase is this tile's)
+  uint64_t f_full, f_copied, f_empty;
+  uint64_t st_full[8], st_clean[8], st_empty[8], sums_full[8];
+  uint64_t st_issued[8];  // queries: the copies of a tile to clean are on the way (so st_full's phase is this tile's)
   uint64_t sp_full[2];
   uint64_t pd_full[2];
   uint64_t done, acc_free;
@@ -81,16 +86,16 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Rows [lo, hi) of a tile that hold a non-finite element become zeros and are noted, rows [zero_from, 128) become zeros.
+// Rows [lo, hi) of a moving tile that hold a non-finite element have it zeroed and are noted, rows [zero_from, 64) become zeros.
 // Called by 64 threads; eight pieces are in flight in each.
 template <int D, bool KEYS>
 __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int zero_from, int first, int* worst, int tid) {
   constexpr int kChunks = D / 8;
   auto at = [&](int i) {
     const int r = i / kChunks, c = i % kChunks;
-    return reinterpret_cast<uint4*>(tile + (c >> 3) * kSeqBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    return reinterpret_cast<uint4*>(tile + (c >> 3) * kUnit * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
   };
-  const int stop = min(hi, kSeqTile) * kChunks;
+  const int stop = min(hi, kUnit) * kChunks;
   for (int i0 = lo * kChunks + tid; i0 < stop; i0 += 8 * 64) {
     uint4 v[8];
 #pragma unroll
@@ -105,23 +110,23 @@ __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int ze
           atomicMin(worst, first + (i0 + 64 * u) / kChunks);
       }
   }
-  for (int i = max(zero_from, 0) * kChunks + tid; i < kSeqTile * kChunks; i += 64) *at(i) = make_uint4(0, 0, 0, 0);
+  for (int i = max(zero_from, 0) * kChunks + tid; i < kUnit * kChunks; i += 64) *at(i) = make_uint4(0, 0, 0, 0);
 }
 
-// Rows of moving tile i: [0, zero_from) are of this sequence, those of [lo, hi) not seen by every row of F.  Whether there
+// Rows of moving tile u: [0, zero_from) are of this sequence, those of [lo, hi) not seen by every row of F.  Whether there
 // is something to clean.
 template <bool KEYS>
-__device__ __forceinline__ bool rows_of(const SeqAttnBwdArgs& a, const Work& w, int i, int& lo, int& hi, int& zero_from) {
+__device__ __forceinline__ bool rows_of(const SeqAttnBwdArgs& a, const Work& w, int u, int& lo, int& hi, int& zero_from) {
   if constexpr (KEYS) {
-    const int t = w.m_first + i * a.tile_tokens, last_key = min(w.first + kSeqTile, w.seg.m) - 1;
-    zero_from = a.group * min(a.tile_tokens, w.seg.n - t);
+    const int T = a.unit_tokens, t = w.m_first + u * T, last_key = min(w.first + kSeqTile, w.seg.m) - 1;
+    zero_from = a.group * min(T, w.seg.n - t);
     lo = 0;
-    hi = a.causal ? min(a.group * min(max(last_key - (w.seg.m - w.seg.n) - t, 0), a.tile_tokens), zero_from) : 0;
-    return zero_from < a.group * a.tile_tokens || hi > 0;
+    hi = a.causal ? min(a.group * min(max(last_key - (w.seg.m - w.seg.n) - t, 0), T), zero_from) : 0;
+    return zero_from < a.group * T || hi > 0;
   } else {
-    zero_from = min(w.seg.m - i * kSeqTile, kSeqTile);
-    lo = max(w.all_see - i * kSeqTile, 0), hi = zero_from;
-    return (i + 1) * kSeqTile > w.all_see;
+    zero_from = min(w.seg.m - u * kUnit, kUnit);
+    lo = max(w.all_see - u * kUnit, 0), hi = zero_from;
+    return (u + 1) * kUnit > w.all_see;
   }
 }
 
@@ -143,12 +148,17 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
   const uint32_t t_p = tmem + kTmP + 64 * h + lane_off, t_d = tmem + kTmD + 64 * h + lane_off;
   const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
   const int row_tok = row / G, row_head = row % G;
-  uint8_t* pieces = smem + C::kPieces + (warp - 4) * 16 * 128;
+  uint8_t* pieces = smem + C::kPieces + (warp - 4) * 32 * 64;
   const float* sums_base = reinterpret_cast<const float*>(smem + C::kSums);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
   };
-  uint32_t f_turn = 0, sp_turn = 0, done_turn = 0, sums_turn = 0;  // parities of the next phases (sums: a bit for each stage)
+  uint32_t f_turn = 0, sp_turn = 0, done_turn = 0, st_turn = 0;  // parities of the next phases (st: a bit for each slot)
+  int slot_u = 0;                                                // the next slot of the ring
+  auto next_slot = [&]() {
+    st_turn ^= 1u << slot_u;
+    slot_u = slot_u + 1 == C::kSlots ? 0 : slot_u + 1;
+  };
   for (uint32_t it = 0;; ++it) {
     const int slot = it & 1;
     if (!wait(&sb->work_full[slot], it >> 1 & 1u)) return;
@@ -167,10 +177,19 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       neg_l = f32x2(-s.x, -s.x), neg_d = f32x2(-s.y, -s.y);
     }
     if (C::kFInTmem && w.count > 0) {
-      // F into tensor memory, half 0 its first tile, half 1 its second; the last item's scores are formed (sp_full)
-      if (!wait(&sb->f_full, f_turn)) return;
-      f_turn ^= 1u;
-      const uint8_t* tile = smem + h * C::kTileBytes + row * 128;
+      // F into tensor memory, these warps its first tile, the others its second; the last item's scores are formed
+      const uint8_t* tile;
+      if constexpr (C::kFInRing) {
+        if (h) next_slot();
+        if (!wait(&sb->st_full[slot_u], st_turn >> slot_u & 1u)) return;
+        tile = smem + slot_u * C::kSlotBytes + row * 128;
+        next_slot();
+        if (!h) next_slot();
+      } else {
+        if (!wait(&sb->f_full, f_turn)) return;
+        f_turn ^= 1u;
+        tile = smem + h * C::kTileBytes + row * 128;
+      }
 #pragma unroll
       for (int b = 0; b < D / 64; ++b) {
         uint32_t r[32];
@@ -183,28 +202,24 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sb->f_empty);
-      mbar_arrive(&sb->f_ready);
+      mbar_arrive(&sb->f_copied);
     }
-    int st = 0;
-    for (int i = 0; i < w.count; ++i) {
+    for (int u = 0; u < w.count; ++u, next_slot()) {
+      if ((u & 1) != h) continue;
       if (!wait(&sb->sp_full[h], sp_turn)) return;
       sp_turn ^= 1u;
-      if constexpr (KEYS) {
-        if (!wait(&sb->sums_full[st], sums_turn >> st & 1u)) return;
-        sums_turn ^= 1u << st;
-      }
+      if (KEYS && !wait(&sb->sums_full[slot_u], st_turn >> slot_u & 1u)) return;
       tc_fence_after();
       // columns [lo, hi) of the tile are seen by this row
       int lo, hi;
       if constexpr (KEYS) {
-        const int t = w.m_first + i * T;
-        hi = G * min(T, w.seg.n - t), lo = from == INT32_MAX ? kSeqTile : max(from - G * t, 0);
+        const int t = w.m_first + u * a.unit_tokens;
+        hi = G * min(a.unit_tokens, w.seg.n - t), lo = from == INT32_MAX ? kUnit : max(from - G * t, 0);
       } else {
-        lo = 0, hi = lim - i * kSeqTile;
+        lo = 0, hi = lim - u * kUnit;
       }
-      const bool part = __any_sync(0xffffffffu, lo > 64 * h || hi < 64 * h + 64);
-      const float* sums = sums_base + st * 2 * kSeqTile + 64 * h;
+      const bool part = __any_sync(0xffffffffu, lo > 0 || hi < kUnit);
+      const float* sums = sums_base + slot_u * 2 * kUnit;
       uint32_t s[2][32], d[2][32];
       tmem_ld32(t_p, s[0]);
       tmem_ld32(t_d, d[0]);
@@ -214,13 +229,12 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       // 32 columns; a tile that is seen in part has a loop of its own, a branch for each pair would hold every chain up
       auto columns = [&](auto in_part, const uint32_t (&sc)[32], const uint32_t (&dc)[32], int c) {
         uint32_t pk[16], dk[16];
-        const float4* l4 = reinterpret_cast<const float4*>(sums + 32 * c);
-        const float4* d4 = reinterpret_cast<const float4*>(sums + kSeqTile + 32 * c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           uint64_t nl[2] = {neg_l, neg_l}, nd[2] = {neg_d, neg_d};
           if constexpr (KEYS) {
-            const float4 x = l4[e], y = d4[e];
+            const float4 x = reinterpret_cast<const float4*>(sums + 32 * c)[e];
+            const float4 y = reinterpret_cast<const float4*>(sums + kUnit + 32 * c)[e];
             nl[0] = f32x2(x.x, x.y), nl[1] = f32x2(x.z, x.w), nd[0] = f32x2(y.x, y.y), nd[1] = f32x2(y.z, y.w);
           }
 #pragma unroll
@@ -231,7 +245,7 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
             p0 = fast_exp2(p0), p1 = fast_exp2(p1);
             f32x2_split(fmul2(f32x2(p0, p1), fadd2(f32x2(__uint_as_float(dc[k]), __uint_as_float(dc[k + 1])), nd[g])), z0, z1);
             if constexpr (decltype(in_part)::value) {
-              const int col = 64 * h + 32 * c + k;
+              const int col = 32 * c + k;
               if (col < lo || col >= hi) p0 = z0 = 0.f;
               if (col + 1 < lo || col + 1 >= hi) p1 = z1 = 0.f;
             }
@@ -258,7 +272,6 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&sb->pd_full[h]);
-      st ^= 1;
     }
     if (w.count > 0) {
       if (!wait(&sb->done, done_turn)) return;
@@ -299,18 +312,18 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
 
 template <int D, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
-    seq_attention_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                             const __grid_constant__ SeqAttnBwdArgs a, int items, int first_next) {
+    seq_attention_bwd_kernel(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ CUtensorMap tm_f1,
+                             const __grid_constant__ CUtensorMap tm_m0, const __grid_constant__ CUtensorMap tm_m1,
+                             const __grid_constant__ SeqAttnBwdArgs a, int first_next) {
   using C = Cfg<D, KEYS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Barriers* sb = reinterpret_cast<Barriers*>(smem + C::kBar);
   volatile int* abort_flag = &sb->abort_flag;
   auto f_tile = [&](int x) { return smem + x * C::kTileBytes; };
-  auto m_tile = [&](int st, int x) { return smem + (2 + 2 * st + x) * C::kTileBytes; };
+  auto m_tile = [&](int sl, int x) { return smem + C::kRing + sl * C::kSlotBytes + x * C::kHalfSlot; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.group, T = a.tile_tokens;
+  const int G = a.group, T = a.tile_tokens, U = a.unit_tokens;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -320,9 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sb->pd_full[s], 128);
     }
     mbar_init(&sb->f_full, 1);
-    mbar_init(&sb->f_ready, 256);
-    mbar_init(&sb->f_empty, C::kFInTmem ? 256 : 1);
-    for (int s = 0; s < kStages; ++s) {
+    mbar_init(&sb->f_copied, 256);
+    mbar_init(&sb->f_empty, 1);
+    for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&sb->st_full[s], 1);
       mbar_init(&sb->st_clean[s], 64);
       mbar_init(&sb->st_empty[s], 1);
@@ -335,12 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     sb->abort_flag = 0;
     fence_mbar_init();
   }
-  if (KEYS && G * T < kSeqTile) {
+  if (KEYS && G * U < kUnit) {
     // rows that no box fills: the products that sum over a moving tile's rows read them
-    const int rows = kSeqTile - G * T;
-    for (int i = threadIdx.x; i < kStages * 2 * (D / 64) * rows * 8; i += kThreads) {
-      const int c = i % 8, r = G * T + (i / 8) % rows, blk = i / (8 * rows);
-      *reinterpret_cast<uint4*>(smem + 2 * C::kTileBytes + blk * kSeqBlock + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    const int rows = kUnit - G * U;
+    for (int i = threadIdx.x; i < C::kSlots * 2 * (D / 64) * rows * 8; i += kThreads) {
+      const int c = i % 8, r = G * U + (i / 8) % rows, blk = i / (8 * rows);
+      *reinterpret_cast<uint4*>(smem + C::kRing + blk * C::kUnitBlock + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
   }
@@ -362,35 +375,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     rows_role<D, KEYS>(sb, smem, tmem, a);
   } else if (fewer_registers<kServiceRegisters>(), warp == 0) {
     // ---------------- items and TMA
-    const CUtensorMap *f0 = KEYS ? &tm_k : &tm_q, *f1 = KEYS ? &tm_v : &tm_do;
-    const CUtensorMap *m0 = KEYS ? &tm_q : &tm_k, *m1 = KEYS ? &tm_do : &tm_v;
-    if (lane == 0) tma_prefetch_desc(f0), tma_prefetch_desc(f1), tma_prefetch_desc(m0), tma_prefetch_desc(m1);
+    if (lane == 0) tma_prefetch_desc(&tm_f0), tma_prefetch_desc(&tm_f1), tma_prefetch_desc(&tm_m0), tma_prefetch_desc(&tm_m1);
     uint32_t* counter = a.counters + (KEYS ? 0 : 1);
-    const int bytes_q = (D / 64) * G * T * 128;  // a box of queries
+    const int bytes_f = KEYS ? C::kTileBytes : (D / 64) * G * T * 128, bytes_m = KEYS ? (D / 64) * G * U * 128 : C::kHalfSlot;
+    TileOrder order;
+    if constexpr (KEYS)
+      order.init(a.cu_k, a.tokens_k, a.cu_q, a.tokens_q, a.batch, kSeqTile, a.causal, 0);  // the first keys have the most queries
+    else
+      order.init(a.cu_q, a.tokens_q, a.cu_k, a.tokens_k, a.batch, T, a.causal, 1);  // the last queries see the most keys
+    const int items = order.n * a.hk;
     uint32_t f_turn = 0, st_turn = 0, st_used = 0;
+    int sl = 0;
     bool ok = true, f_used = false;
+    auto take_slot = [&]() {  // the next slot of the ring, once it is empty
+      ok = wait(&sb->st_empty[sl], (st_turn >> sl & 1u) ^ 1u);
+      st_turn ^= 1u << sl;
+      if (ok) st_used |= 1u << sl;
+      return ok;
+    };
+    auto next_slot = [&]() { sl = sl + 1 == C::kSlots ? 0 : sl + 1; };
     int item = blockIdx.x;
     for (uint32_t it = 0; ok; ++it) {
       Work w;
       w.live = 0;
       for (; item < items; item = items > first_next ? take_next(counter, first_next) : items) {
-        w.hk = item % a.hk;
+        TileOrder::Found at;
+        if (!order.find(item / a.hk, at)) continue;
+        w.hk = item % a.hk, w.first = at.start;
         if constexpr (KEYS) {
-          const int idx = item / a.hk;  // the first keys have the most queries
-          const Located at = locate(a.cu_k, a.tokens_k, a.cu_q, a.tokens_q, a.batch, kSeqTile, idx);
           w.seg = {at.other_first, at.other_count, at.first, at.count};
-          w.first = (idx - (w.seg.k0 / kSeqTile + at.b)) * kSeqTile;
-          if (w.first < 0 || w.first >= w.seg.m) continue;
           w.m_first = a.causal ? max(w.first - w.seg.m + w.seg.n, 0) : 0;
-          w.count = w.seg.n > w.m_first ? (w.seg.n - w.m_first + T - 1) / T : 0;
+          w.count = w.seg.n > w.m_first ? (w.seg.n - w.m_first + U - 1) / U : 0;
           w.all_see = 0;
         } else {
-          const int idx = (items - 1 - item) / a.hk;  // the last queries see the most keys
-          const Located at = locate(a.cu_q, a.tokens_q, a.cu_k, a.tokens_k, a.batch, T, idx);
           w.seg = {at.first, at.count, at.other_first, at.other_count};
-          w.first = (idx - (w.seg.q0 / T + at.b)) * T;
-          if (w.first < 0 || w.first >= w.seg.n) continue;
-          w.count = (keys_seen(w.seg, min(w.first + T, w.seg.n) - 1, a.causal) + kSeqTile - 1) / kSeqTile;
+          w.count = (keys_seen(w.seg, min(w.first + T, w.seg.n) - 1, a.causal) + kUnit - 1) / kUnit;
           w.m_first = 0;
           w.all_see = keys_seen(w.seg, w.first, a.causal);
         }
@@ -409,36 +428,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!w.live) break;
       const int next_item = items > first_next ? take_next(counter, first_next) : items;
       if (w.count > 0) {
-        ok = wait(&sb->f_empty, f_turn ^ 1u);
-        if (!ok) break;
-        f_turn ^= 1u, f_used = true;
-        if (lane == 0) {
-          const int f_head = KEYS ? w.hk : w.hk * G, f_row = KEYS ? w.seg.k0 + w.first : w.seg.q0 + w.first;
-          mbar_arrive_expect_tx(&sb->f_full, 2 * (KEYS ? C::kTileBytes : bytes_q));
+        const int f_head = KEYS ? w.hk : w.hk * G, f_row = KEYS ? w.seg.k0 + w.first : w.seg.q0 + w.first;
+        if constexpr (C::kFInRing) {
 #pragma unroll
-          for (int b = 0; b < D / 64; ++b) {
-            tma_load_3d(f_tile(0) + b * kSeqBlock, f0, &sb->f_full, b * 64, f_head, f_row);
-            tma_load_3d(f_tile(1) + b * kSeqBlock, f1, &sb->f_full, b * 64, f_head, f_row);
+          for (int x = 0; x < 2; ++x) {
+            if (!take_slot()) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sb->st_full[sl], bytes_f);
+#pragma unroll
+              for (int b = 0; b < D / 64; ++b)
+                tma_load_3d(m_tile(sl, 0) + b * kSeqBlock, x ? &tm_f1 : &tm_f0, &sb->st_full[sl], b * 64, f_head, f_row);
+            }
+            __syncwarp();
+            next_slot();
           }
+        } else {
+          ok = wait(&sb->f_empty, f_turn ^ 1u);
+          f_turn ^= 1u;
+          if (ok) f_used = true;
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&sb->f_full, 2 * bytes_f);
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) {
+              tma_load_3d(f_tile(0) + b * kSeqBlock, &tm_f0, &sb->f_full, b * 64, f_head, f_row);
+              tma_load_3d(f_tile(1) + b * kSeqBlock, &tm_f1, &sb->f_full, b * 64, f_head, f_row);
+            }
+          }
+          __syncwarp();
         }
       }
-      int st = 0;
-      for (int i = 0; i < w.count; ++i, st ^= 1) {
-        ok = wait(&sb->st_empty[st], (st_turn >> st & 1u) ^ 1u);
-        if (!ok) break;
-        st_turn ^= 1u << st, st_used |= 1u << st;
+      for (int u = 0; ok && u < w.count; ++u) {
+        if (!take_slot()) break;
         if (lane == 0) {
-          const int m_head = KEYS ? w.hk * G : w.hk, row = KEYS ? w.seg.q0 + w.m_first + i * T : w.seg.k0 + i * kSeqTile;
-          mbar_arrive_expect_tx(&sb->st_full[st], 2 * (KEYS ? bytes_q : C::kTileBytes));
+          const int m_head = KEYS ? w.hk * G : w.hk, row = KEYS ? w.seg.q0 + w.m_first + u * U : w.seg.k0 + u * kUnit;
+          mbar_arrive_expect_tx(&sb->st_full[sl], 2 * bytes_m);
 #pragma unroll
           for (int b = 0; b < D / 64; ++b) {
-            tma_load_3d(m_tile(st, 0) + b * kSeqBlock, m0, &sb->st_full[st], b * 64, m_head, row);
-            tma_load_3d(m_tile(st, 1) + b * kSeqBlock, m1, &sb->st_full[st], b * 64, m_head, row);
+            tma_load_3d(m_tile(sl, 0) + b * C::kUnitBlock, &tm_m0, &sb->st_full[sl], b * 64, m_head, row);
+            tma_load_3d(m_tile(sl, 1) + b * C::kUnitBlock, &tm_m1, &sb->st_full[sl], b * 64, m_head, row);
           }
           int lo, hi, zero_from;
-          if (!KEYS && rows_of<KEYS>(a, w, i, lo, hi, zero_from)) mbar_arrive(&sb->st_issued[st]);
+          if (!KEYS && rows_of<KEYS>(a, w, u, lo, hi, zero_from)) mbar_arrive(&sb->st_issued[sl]);
         }
         __syncwarp();
+        next_slot();
       }
       item = next_item;
     }
@@ -446,42 +479,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       // give the copies already issued a bounded chance to land before the CTA exits
       int never = 0;
       if (f_used) mbar_wait(&sb->f_full, f_turn ^ 1u, &never, a.status, 0);
-      for (int s = 0; s < kStages; ++s)
+      for (int s = 0; s < C::kSlots; ++s)
         if (st_used >> s & 1u) mbar_wait(&sb->st_full[s], (st_turn >> s & 1u) ^ 1u, &never, a.status, 0);
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer: the warp's lanes test the barriers of a step side by side, one lane issues; of a descriptor
-    // only the address in its lower half changes (see attention_varlen.cu)
-    auto koff = [](int k) -> uint32_t { return static_cast<uint32_t>(((k >> 2) * kSeqBlock + (k & 3) * 32) >> 4); };
+    // ---------------- MMA issuer: one lane issues, the warp stays converged; of a descriptor only the address in its lower half
+    // changes (see attention_varlen.cu)
+    auto koff = [](int k, int block) -> uint32_t { return static_cast<uint32_t>(((k >> 2) * block + (k & 3) * 32) >> 4); };
     auto desc = [](uint64_t base, uint32_t lo) { return (base & 0xFFFFFFFF00000000ull) | lo; };
-    const uint64_t k_base = sdesc_kmajor_sw128(smem_addr(f_tile(0))), n_base = sdesc_mnmajor_sw128(smem_addr(m_tile(0, 0)), kSeqBlock);
-    uint32_t f_lo = static_cast<uint32_t>(k_base), m_lo = static_cast<uint32_t>(sdesc_kmajor_sw128(smem_addr(m_tile(0, 0)))),
+    const uint64_t k_base = sdesc_kmajor_sw128(smem_addr(m_tile(0, 0))), n_base = sdesc_mnmajor_sw128(smem_addr(m_tile(0, 0)), C::kUnitBlock);
+    uint32_t f_lo = static_cast<uint32_t>(sdesc_kmajor_sw128(smem_addr(f_tile(0)))), k_lo = static_cast<uint32_t>(k_base),
              n_lo = static_cast<uint32_t>(n_base);
-    constexpr uint32_t kStep = static_cast<uint32_t>(C::kTileBytes) >> 4, kHalf = (64 * 128) >> 4;
-    auto scores = [&](int st, int h) {  // S and dP of half h of the tile in stage st
+    constexpr uint32_t kSlot = static_cast<uint32_t>(C::kSlotBytes) >> 4, kHalf = static_cast<uint32_t>(C::kHalfSlot) >> 4,
+                       kF = static_cast<uint32_t>(C::kTileBytes) >> 4;
+    auto scores = [&](int sl, int h) {  // S and dP of the tile in slot sl into buffer h
+      const uint32_t m_lo = k_lo + sl * kSlot;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t to = tmem + (x ? kTmD : kTmP) + 64 * h;
-          const uint64_t m = desc(k_base, m_lo + (2 * st + x) * kStep + h * kHalf + koff(k));
+          const uint64_t m = desc(k_base, m_lo + x * kHalf + koff(k, C::kUnitBlock));
           if constexpr (C::kFInTmem)
             tc_mma_ts_f16(to, tmem + kTmF + x * (D / 2) + k * 8, m, C::kIdescS, k > 0 ? 1u : 0u);
           else
-            tc_mma<kKindF16>(to, desc(k_base, f_lo + x * kStep + koff(k)), m, C::kIdescS, k > 0 ? 1u : 0u);
+            tc_mma<kKindF16>(to, desc(k_base, f_lo + x * kF + koff(k, kSeqBlock)), m, C::kIdescS, k > 0 ? 1u : 0u);
         }
       tc_commit(&sb->sp_full[h]);
     };
-    auto products = [&](int st, int h, uint32_t more) {
+    auto products = [&](int sl, int h, uint32_t more) {
+      const uint32_t m_lo = n_lo + sl * kSlot;
 #pragma unroll
       for (int x = KEYS ? 0 : 1; x < 2; ++x)  // dV += P dO and dK += dS Q, or dQ += dS K
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           tc_mma_ts_f16(tmem + kTmAcc + (KEYS ? x * D : 0), tmem + (KEYS && x ? kTmD : kTmP) + 64 * h + 8 * k,
-                        desc(n_base, n_lo + (2 * st + (x ? 0 : 1)) * kStep + h * kHalf + ((k * 2048) >> 4)), C::kIdescAcc,
-                        k > 0 ? 1u : more);
+                        desc(n_base, m_lo + (x ? 0 : kHalf) + ((k * 2048) >> 4)), C::kIdescAcc, k > 0 ? 1u : more);
     };
-    uint32_t f_turn = 0, st_turn = 0, clean_turn = 0, pd_turn = 0, acc_turn = 1;  // parities (st: a bit for each stage)
+    uint32_t f_turn = 0, st_turn = 0, clean_turn = 0, pd_turn = 0, acc_turn = 1;  // parities (st, clean: a bit for each slot, pd: for each buffer)
+    int done_slot = 0, sl = 0;  // the ring's slots: of the products, of the scores (two tiles ahead)
+    auto next = [&](int s) { return s + 1 == C::kSlots ? 0 : s + 1; };
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int slot = it & 1;
@@ -492,50 +529,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&sb->work_empty[slot]);
       if (!w.live) break;
       if (w.count == 0) continue;
-      int lo, hi, zero_from;
-      if (rows_of<KEYS>(a, w, 0, lo, hi, zero_from)) {
-        ok = wait(&sb->st_clean[0], clean_turn & 1u);
-        clean_turn ^= 1u;
+      ok = wait(C::kFInTmem ? &sb->f_copied : &sb->f_full, f_turn);
+      f_turn ^= 1u;
+      if (ok && C::kFInTmem) {
+        if (C::kFInRing) {  // the two slots F came through
+          if (lane < 2) mbar_arrive(&sb->st_empty[lane ? next(sl) : sl]);
+          st_turn ^= (1u << sl) | (1u << next(sl));
+          sl = next(next(sl)), done_slot = sl;
+        } else if (lane == 0) {
+          mbar_arrive(&sb->f_empty);
+        }
+        __syncwarp();
       }
-      ok = ok && wait(lane == 0 ? (C::kFInTmem ? &sb->f_ready : &sb->f_full) : &sb->st_full[0], lane == 0 ? f_turn : st_turn & 1u);
-      f_turn ^= 1u, st_turn ^= 1u;
-      if (ok && one_lane()) {
-        tc_fence_after();
-        scores(0, 0);
-        scores(0, 1);
-        if (!C::kFInTmem && w.count == 1) tc_commit(&sb->f_empty);
-      }
-      __syncwarp();
-      for (int i0 = 0; ok && i0 < w.count; i0 += kStages) {
+      auto tile_ready = [&](int u) {
+        ok = ok && wait(&sb->st_full[sl], st_turn >> sl & 1u);
+        st_turn ^= 1u << sl;
+        int lo, hi, zero_from;
+        if (ok && rows_of<KEYS>(a, w, u, lo, hi, zero_from)) {
+          ok = wait(&sb->st_clean[sl], clean_turn >> sl & 1u);
+          clean_turn ^= 1u << sl;
+        }
+        return ok;
+      };
 #pragma unroll
-        for (int st = 0; st < kStages; ++st) {
-          const int i = i0 + st;
-          if (!ok || i >= w.count) break;
-          const bool next = i + 1 < w.count;
-          if (next && rows_of<KEYS>(a, w, i + 1, lo, hi, zero_from)) {
-            ok = wait(&sb->st_clean[st ^ 1], clean_turn >> (st ^ 1) & 1u);
-            clean_turn ^= 1u << (st ^ 1);
+      for (int h = 0; h < 2; ++h)
+        if (ok && h < w.count && tile_ready(h)) {
+          if (one_lane()) {
+            tc_fence_after();
+            scores(sl, h);
+            if (!C::kFInTmem && h + 1 == w.count) tc_commit(&sb->f_empty);
           }
+          __syncwarp();
+          sl = next(sl);
+        }
+      for (int u0 = 0; ok && u0 < w.count; u0 += 2) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            asm volatile("" : "+r"(f_lo), "+r"(m_lo), "+r"(n_lo));  // the sums below are formed here, not kept in registers
-            const bool st_too = h == 0 && next && lane == 1, acc_too = h == 0 && i == 0 && lane == 2;
-            ok = ok && wait(st_too ? &sb->st_full[st ^ 1] : acc_too ? &sb->acc_free : &sb->pd_full[h],
-                            st_too ? st_turn >> (st ^ 1) & 1u : acc_too ? acc_turn : pd_turn);
-            if (ok && one_lane()) {
+        for (int h = 0; h < 2; ++h) {
+          const int u = u0 + h;
+          if (!ok || u >= w.count) break;
+          asm volatile("" : "+r"(f_lo), "+r"(k_lo), "+r"(n_lo));  // the sums below are formed here, not kept in registers
+          const bool acc_too = u == 0 && lane == 1;
+          ok = wait(acc_too ? &sb->acc_free : &sb->pd_full[h], acc_too ? acc_turn : pd_turn >> h & 1u);
+          pd_turn ^= 1u << h;
+          if (ok && one_lane()) {
+            tc_fence_after();
+            products(done_slot, h, u > 0 ? 1u : 0u);
+            tc_commit(&sb->st_empty[done_slot]);
+            if (u + 1 == w.count) tc_commit(&sb->done);
+          }
+          __syncwarp();
+          done_slot = next(done_slot);
+          if (u + 2 < w.count && tile_ready(u + 2)) {
+            if (one_lane()) {
               tc_fence_after();
-              products(st, h, i > 0 || h > 0 ? 1u : 0u);
-              if (h == 1) tc_commit(&sb->st_empty[st]);
-              if (next)
-                scores(st ^ 1, h);
-              else if (h == 1)
-                tc_commit(&sb->done);
-              if (!C::kFInTmem && h == 1 && i + 2 == w.count) tc_commit(&sb->f_empty);
+              scores(sl, h);
+              if (!C::kFInTmem && u + 3 == w.count) tc_commit(&sb->f_empty);
             }
             __syncwarp();
+            sl = next(sl);
           }
-          pd_turn ^= 1u;
-          if (next) st_turn ^= 1u << (st ^ 1);
         }
       }
       acc_turn ^= 1u;
@@ -548,42 +600,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- sums of the moving rows, and rows that part of F must not see
     const int tid = static_cast<int>(threadIdx.x) - 64;
-    uint32_t st_turn = 0, clean_turn = 0;  // a bit for each stage: the tile's turn, that of the next tile to clean
+    uint32_t st_turn = 0, clean_turn = 0;  // a bit for each slot: the tile's turn, that of the next tile to clean
+    int sl = 0;
+    auto next_slot = [&]() {
+      st_turn ^= 1u << sl;
+      sl = sl + 1 == C::kSlots ? 0 : sl + 1;
+    };
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int slot = it & 1;
       ok = wait(&sb->work_full[slot], it >> 1 & 1u);
       if (!ok) break;
       const Work w = sb->work[slot];
-      int st = 0;
-      for (int i = 0; w.live && ok && i < w.count; ++i, st ^= 1) {
-        const uint32_t parity = st_turn >> st & 1u;
-        st_turn ^= 1u << st;
+      if (C::kFInRing && w.live && w.count > 0) next_slot(), next_slot();
+      for (int u = 0; w.live && ok && u < w.count; ++u, next_slot()) {
+        const uint32_t parity = st_turn >> sl & 1u;
         if constexpr (KEYS) {
-          ok = wait(&sb->st_empty[st], parity ^ 1u);
+          ok = wait(&sb->st_empty[sl], parity ^ 1u);
           if (!ok) break;
-          float* sums = reinterpret_cast<float*>(smem + C::kSums) + st * 2 * kSeqTile;
-          const int t = w.m_first + i * T, rows = G * min(T, w.seg.n - t);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = tid + 64 * e;
-            float2 s = make_float2(0.f, 0.f);
-            if (r < rows) s = a.sums[(static_cast<size_t>(w.seg.q0) + t + r / G) * a.hq + w.hk * G + r % G];
-            sums[r] = -s.x, sums[kSeqTile + r] = -s.y;
-          }
-          mbar_arrive(&sb->sums_full[st]);
+          float* sums = reinterpret_cast<float*>(smem + C::kSums) + sl * 2 * kUnit;
+          const int t = w.m_first + u * U, rows = G * min(U, w.seg.n - t);
+          float2 s = make_float2(0.f, 0.f);
+          if (tid < rows) s = a.sums[(static_cast<size_t>(w.seg.q0) + t + tid / G) * a.hq + w.hk * G + tid % G];
+          sums[tid] = -s.x, sums[kUnit + tid] = -s.y;
+          mbar_arrive(&sb->sums_full[sl]);
         }
         int lo, hi, zero_from;
-        if (!rows_of<KEYS>(a, w, i, lo, hi, zero_from)) continue;
-        // (keys: st_empty has told that the stage's previous tile is done)
-        if (!KEYS) ok = wait(&sb->st_issued[st], clean_turn >> st & 1u), clean_turn ^= 1u << st;
-        ok = ok && wait(&sb->st_full[st], parity);
+        if (!rows_of<KEYS>(a, w, u, lo, hi, zero_from)) continue;
+        // (keys: st_empty has told that the slot's previous tile is done)
+        if (!KEYS) ok = wait(&sb->st_issued[sl], clean_turn >> sl & 1u), clean_turn ^= 1u << sl;
+        ok = ok && wait(&sb->st_full[sl], parity);
         if (!ok) break;
-        const int at = KEYS ? G * (w.m_first + i * T) : i * kSeqTile;
-        scrub_pair<D, KEYS>(m_tile(st, 0), lo, hi, zero_from, at, &sb->worst[slot], tid);
-        if (KEYS) scrub_pair<D, KEYS>(m_tile(st, 1), lo, hi, zero_from, at, &sb->worst[slot], tid);
+        const int at = KEYS ? G * (w.m_first + u * U) : u * kUnit;
+        scrub_pair<D, KEYS>(m_tile(sl, 0), lo, hi, zero_from, at, &sb->worst[slot], tid);
+        if (KEYS) scrub_pair<D, KEYS>(m_tile(sl, 1), lo, hi, zero_from, at, &sb->worst[slot], tid);
         fence_proxy_async_smem();
-        mbar_arrive(&sb->st_clean[st]);
+        mbar_arrive(&sb->st_clean[sl]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sb->work_empty[slot]);
@@ -629,8 +681,8 @@ cudaError_t launch_pass(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaSt
   cudaError_t e = cudaFuncSetAttribute(seq_attention_bwd_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = static_cast<int>(std::min<int64_t>(items, num_sms()));
-  e = launch_pdl(seq_attention_bwd_kernel<D, KEYS>, dim3(grid), dim3(kThreads), C::kSmem, stream, m.q, m.dout, m.k, m.v, a,
-                 static_cast<int>(items), grid);
+  e = launch_pdl(seq_attention_bwd_kernel<D, KEYS>, dim3(grid), dim3(kThreads), C::kSmem, stream, KEYS ? m.f_k : m.f_q,
+                 KEYS ? m.f_v : m.f_dout, KEYS ? m.m_q : m.m_k, KEYS ? m.m_dout : m.m_v, a, grid);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();

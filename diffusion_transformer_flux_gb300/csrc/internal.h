@@ -480,9 +480,9 @@ struct SeqAttnArgs {
   float *part, *part_lse, *few_part, *few_lse;
   uint32_t* status;
   int clear;           // this kernel is the call's first and clears the status word
-  // set by the launcher: tile pairs of the queries, parts of their keys, and where there are more items than CTAs a counter of
-  // those handed out beside the first `first_next`
-  int pairs, splits;
+  // set by the launcher: parts of the keys, and where there may be more items than CTAs a counter of those handed out beside
+  // the first `first_next`
+  int splits;
   uint32_t* next;
   int first_next;
 };
@@ -501,7 +501,8 @@ cudaError_t launch_paged_combine(const SeqAttnArgs& a, cudaStream_t stream);
 // gradients of the attention over packed sequences
 struct SeqAttnBwdArgs {
   int batch, tokens_q, tokens_k;
-  int hq, hk, group, head_dim, causal, tile_tokens;
+  int hq, hk, group, head_dim, causal;
+  int tile_tokens, unit_tokens;  // tokens of a resident query tile (128 / group), of a moving one (64 / group)
   float scale, scale_log2;
   const int *cu_q, *cu_k;
   HeadsView dout, out, dq, dk, dv;
@@ -511,8 +512,9 @@ struct SeqAttnBwdArgs {
   uint32_t* counters;  // of the items handed out in each pass
 };
 struct SeqAttnBwdMaps {
-  CUtensorMap q, dout, k, v;
+  CUtensorMap f_q, f_dout, f_k, f_v, m_q, m_dout, m_k, m_v;  // boxes of resident and of moving tiles
 };
+constexpr int kBwdMaxGroup = 64;
 cudaError_t launch_seq_attention_bwd(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaStream_t stream);
 
 // kv_cache.cu: block tables and slot maps of a paged cache, and the write of new keys and values into it

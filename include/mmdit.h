@@ -869,8 +869,9 @@ mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t
  *   dq_i = scale sum_j dz_ij k_j,   dk_j = scale sum_i dz_ij q_i,   dv_j = sum_i p_ij dout_i,
  * dk and dv summed over the query heads of their group.  All rows of the sequences are written, rows of none left as they
  * were.  Sums in float32 in a fixed order: the same bits from call to call.  p and dz enter the products rounded to bf16.  A
- * query row whose q or dout is not finite, within 128 rows (tokens by the group's heads) of one that sees fewer keys, makes
- * the gradients of the keys it sees NaN; a key row likewise those of the queries that see it.
+ * query row whose q or dout is not finite, within 64 rows (tokens by the group's heads) of one that sees fewer keys, makes
+ * the gradients of the keys it sees NaN; a key row likewise those of the queries that see it.  heads_q at most 64 times
+ * heads_k.
  * workspace >= mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) (two floats for each row: calls that
  * share one are ordered on one stream). */
 size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim);

@@ -276,7 +276,7 @@ def test_gradients(lengths, causal, hq, hk, d):
     compare_gradients(*packed(rng, nq, nk, hq, hk, d, pad=3), causal)
 
 
-@pytest.mark.parametrize("hq,hk", [(1, 1), (6, 3), (7, 1), (16, 1), (48, 1), (128, 1), (14, 2)])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (6, 3), (7, 1), (16, 1), (48, 1), (64, 1), (14, 2)])
 def test_gradients_groups(hq, hk):
     rng = np.random.default_rng(hq + 1)
     compare_gradients(*packed(rng, [9, 37], [40, 37], hq, hk, 64, pad=1), True)

@@ -3044,7 +3044,7 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
   a.tile_tokens = seq_tile_tokens(a.group), a.unit_tokens = 64 / a.group;
   a.scale = scale, a.scale_log2 = scale * 1.4426950408889634f;
   a.cu_q = cu_q, a.cu_k = cu_k, a.lse = lse, a.sums = at<float2>(workspace, kStatusBytes);
-  if (tokens_q > 0) a.dout = heads_view(dout), a.out = heads_view(out), a.dq = heads_view(dq);
+  if (tokens_q > 0) a.q = heads_view(q), a.dout = heads_view(dout), a.out = heads_view(out), a.dq = heads_view(dq);
   if (tokens_k > 0) a.dk = heads_view(dk), a.dv = heads_view(dv);
   a.status = status_word(workspace), a.counters = a.status + 32;
   // where a side has no rows nothing is loaded through its maps

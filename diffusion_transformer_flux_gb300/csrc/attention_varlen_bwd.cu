@@ -18,7 +18,7 @@
 // found and handed out as in the forward.  Twelve warps:
 //   warp 0       items and TMA: F, then M tiles
 //   warp 1       MMA issuer: S, dP of tile u + 2 follow the accumulating products of tile u
-//   warps 2, 3   keys: -lse and -delta of the tile's rows; both: rows that part of the tile must not see (scrub_pair)
+//   warps 2, 3   keys: -lse and -delta of the moving rows; both: rows that part of F must not see (scrub_pair)
 //   warps 4..7   tiles of even number: one row of S and dP per thread, P = exp2(c S - L) and dS = P (dP - delta) back into tensor
 //                memory as bf16 pairs (the operands of the accumulating products, each off by at most 2^-8 of itself);
 //                warps 8..11 those of odd number
@@ -68,7 +68,7 @@ struct Barriers {
   uint64_t work_full[2], work_empty[2];
   uint64_t f_full, f_copied, f_empty;
   uint64_t st_full[8], st_clean[8], st_empty[8], sums_full[8];
-  uint64_t st_issued[8];  // queries: the copies of a tile to clean are on the way (so st_full's phase is this tile's)
+  uint64_t st_issued[8];  // the copies of a tile to clean are on the way (so st_full's phase is this tile's)
   uint64_t sp_full[2];
   uint64_t pd_full[2];
   uint64_t done, acc_free;
@@ -80,6 +80,17 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers) <= 1024, "barriers");
 
+// The wait for earlier loads of tensor memory, their registers threaded through it.
+__device__ __forceinline__ void tmem_ld32_deps(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -87,8 +98,8 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
 }
 
 // Rows [lo, hi) of a moving tile that hold a non-finite element have it zeroed and are noted, rows [zero_from, 64) become zeros.
-// Called by 64 threads; eight pieces are in flight in each.
-template <int D, bool KEYS>
+// Called by THREADS threads; eight pieces are in flight in each.
+template <int D, bool KEYS, int THREADS>
 __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int zero_from, int first, int* worst, int tid) {
   constexpr int kChunks = D / 8;
   auto at = [&](int i) {
@@ -96,21 +107,23 @@ __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int ze
     return reinterpret_cast<uint4*>(tile + (c >> 3) * kUnit * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
   };
   const int stop = min(hi, kUnit) * kChunks;
-  for (int i0 = lo * kChunks + tid; i0 < stop; i0 += 8 * 64) {
+  for (int i0 = lo * kChunks + tid; i0 < stop; i0 += 8 * THREADS) {
     uint4 v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = i0 + 64 * u < stop ? *at(i0 + 64 * u) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < 8; ++u) v[u] = i0 + THREADS * u < stop ? *at(i0 + THREADS * u) : make_uint4(0, 0, 0, 0);
+    uint32_t bad = 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (not_finite(v[u])) {
-        *at(i0 + 64 * u) = make_uint4(0, 0, 0, 0);
-        if (KEYS)
-          atomicMax(worst, first + (i0 + 64 * u) / kChunks);
-        else
-          atomicMin(worst, first + (i0 + 64 * u) / kChunks);
-      }
+    for (int u = 0; u < 8; ++u) bad |= (not_finite(v[u]) ? 1u : 0u) << u;
+    for (; bad; bad &= bad - 1) {
+      const int i = i0 + THREADS * (__ffs(bad) - 1);
+      *at(i) = make_uint4(0, 0, 0, 0);
+      if (KEYS)
+        atomicMax(worst, first + i / kChunks);
+      else
+        atomicMin(worst, first + i / kChunks);
+    }
   }
-  for (int i = max(zero_from, 0) * kChunks + tid; i < kUnit * kChunks; i += 64) *at(i) = make_uint4(0, 0, 0, 0);
+  for (int i = max(zero_from, 0) * kChunks + tid; i < kUnit * kChunks; i += THREADS) *at(i) = make_uint4(0, 0, 0, 0);
 }
 
 // Rows of moving tile u: [0, zero_from) are of this sequence, those of [lo, hi) not seen by every row of F.  Whether there
@@ -206,9 +219,19 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
     }
     for (int u = 0; u < w.count; ++u, next_slot()) {
       if ((u & 1) != h) continue;
+      // keys: -L of the columns, and -delta of the first 32, before the scores are there: beside the products, which read shared
+      // memory at its full rate, these loads take longer than the arithmetic (behind the scores: 1300 against 500 cycles)
+      float4 nl[16], nd[8];
+      const float4* sums = reinterpret_cast<const float4*>(sums_base + slot_u * 2 * kUnit);
+      if constexpr (KEYS) {
+        if (!wait(&sb->sums_full[slot_u], st_turn >> slot_u & 1u)) return;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) nl[e] = sums[e];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) nd[e] = sums[16 + e];
+      }
       if (!wait(&sb->sp_full[h], sp_turn)) return;
       sp_turn ^= 1u;
-      if (KEYS && !wait(&sb->sums_full[slot_u], st_turn >> slot_u & 1u)) return;
       tc_fence_after();
       // columns [lo, hi) of the tile are seen by this row
       int lo, hi;
@@ -219,38 +242,33 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
         lo = 0, hi = lim - u * kUnit;
       }
       const bool part = __any_sync(0xffffffffu, lo > 0 || hi < kUnit);
-      const float* sums = sums_base + slot_u * 2 * kUnit;
-      uint32_t s[2][32], d[2][32];
-      tmem_ld32(t_p, s[0]);
-      tmem_ld32(t_d, d[0]);
-      tmem_ld_deps64(s[0], d[0]);
-      tmem_ld32(t_p + 32, s[1]);
-      tmem_ld32(t_d + 32, d[1]);
-      // 32 columns; a tile that is seen in part has a loop of its own, a branch for each pair would hold every chain up
-      auto columns = [&](auto in_part, const uint32_t (&sc)[32], const uint32_t (&dc)[32], int c) {
+      uint32_t s[2][32], d[32];
+      tmem_ld64_wait(t_p, s[0], s[1]);
+      tmem_ld32(t_d, d);
+      // P over the scores' registers
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        uint32_t* x = s[e >> 3] + (e & 7) * 4;
+        float p0, p1, p2, p3;
+        f32x2_split(ffma2(f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, KEYS ? f32x2(nl[e].x, nl[e].y) : neg_l), p0, p1);
+        f32x2_split(ffma2(f32x2(__uint_as_float(x[2]), __uint_as_float(x[3])), scale2, KEYS ? f32x2(nl[e].z, nl[e].w) : neg_l), p2, p3);
+        x[0] = __float_as_uint(fast_exp2(p0)), x[1] = __float_as_uint(fast_exp2(p1));
+        x[2] = __float_as_uint(fast_exp2(p2)), x[3] = __float_as_uint(fast_exp2(p3));
+      }
+      // dS of 32 columns; a tile that is seen in part has a loop of its own, a branch for each pair would hold every chain up
+      auto columns = [&](auto in_part, int c) {
         uint32_t pk[16], dk[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint64_t nl[2] = {neg_l, neg_l}, nd[2] = {neg_d, neg_d};
-          if constexpr (KEYS) {
-            const float4 x = reinterpret_cast<const float4*>(sums + 32 * c)[e];
-            const float4 y = reinterpret_cast<const float4*>(sums + kUnit + 32 * c)[e];
-            nl[0] = f32x2(x.x, x.y), nl[1] = f32x2(x.z, x.w), nd[0] = f32x2(y.x, y.y), nd[1] = f32x2(y.z, y.w);
+        for (int k = 0; k < 32; k += 2) {
+          float p0 = __uint_as_float(s[c][k]), p1 = __uint_as_float(s[c][k + 1]), z0, z1;
+          const uint64_t minus = !KEYS ? neg_d : k & 2 ? f32x2(nd[k / 4].z, nd[k / 4].w) : f32x2(nd[k / 4].x, nd[k / 4].y);
+          f32x2_split(fmul2(f32x2(p0, p1), fadd2(f32x2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), minus)), z0, z1);
+          if constexpr (decltype(in_part)::value) {
+            const int col = 32 * c + k;
+            if (col < lo || col >= hi) p0 = z0 = 0.f;
+            if (col + 1 < lo || col + 1 >= hi) p1 = z1 = 0.f;
           }
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const int k = 4 * e + 2 * g;
-            float p0, p1, z0, z1;
-            f32x2_split(ffma2(f32x2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), scale2, nl[g]), p0, p1);
-            p0 = fast_exp2(p0), p1 = fast_exp2(p1);
-            f32x2_split(fmul2(f32x2(p0, p1), fadd2(f32x2(__uint_as_float(dc[k]), __uint_as_float(dc[k + 1])), nd[g])), z0, z1);
-            if constexpr (decltype(in_part)::value) {
-              const int col = 32 * c + k;
-              if (col < lo || col >= hi) p0 = z0 = 0.f;
-              if (col + 1 < lo || col + 1 >= hi) p1 = z1 = 0.f;
-            }
-            pk[k / 2] = pack_bf16x2(p0, p1), dk[k / 2] = pack_bf16x2(z0, z1);
-          }
+          pk[k / 2] = pack_bf16x2(p0, p1), dk[k / 2] = pack_bf16x2(z0, z1);
         }
         // over columns that were read: packed pairs take half as many
         if constexpr (KEYS) {
@@ -260,15 +278,20 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
           tmem_st16(t_p + 16 * c, dk);
         }
       };
-      if (part) {
-        columns(std::true_type{}, s[0], d[0], 0);
-        tmem_ld_deps64(s[1], d[1]);
-        columns(std::true_type{}, s[1], d[1], 1);
-      } else {
-        columns(std::false_type{}, s[0], d[0], 0);
-        tmem_ld_deps64(s[1], d[1]);
-        columns(std::false_type{}, s[1], d[1], 1);
+      tmem_ld32_deps(d);
+      if (part)
+        columns(std::true_type{}, 0);
+      else
+        columns(std::false_type{}, 0);
+      if constexpr (KEYS) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) nd[e] = sums[24 + e];
       }
+      tmem_ld32_wait(t_d + 32, d);
+      if (part)
+        columns(std::true_type{}, 1);
+      else
+        columns(std::false_type{}, 1);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&sb->pd_full[h]);
@@ -337,9 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sb->f_empty, 1);
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&sb->st_full[s], 1);
-      mbar_init(&sb->st_clean[s], 64);
+      mbar_init(&sb->st_clean[s], KEYS ? 32 : 64);
       mbar_init(&sb->st_empty[s], 1);
-      mbar_init(&sb->sums_full[s], 64);
+      mbar_init(&sb->sums_full[s], 32);
       mbar_init(&sb->st_issued[s], 1);
     }
     mbar_init(&sb->done, 1);
@@ -468,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(m_tile(sl, 1) + b * C::kUnitBlock, &tm_m1, &sb->st_full[sl], b * 64, m_head, row);
           }
           int lo, hi, zero_from;
-          if (!KEYS && rows_of<KEYS>(a, w, u, lo, hi, zero_from)) mbar_arrive(&sb->st_issued[sl]);
+          if (rows_of<KEYS>(a, w, u, lo, hi, zero_from)) mbar_arrive(&sb->st_issued[sl]);
         }
         __syncwarp();
         next_slot();
@@ -598,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&sb->drain, 0, &never, a.status, 0);
     }
   } else {
-    // ---------------- sums of the moving rows, and rows that part of F must not see
-    const int tid = static_cast<int>(threadIdx.x) - 64;
+    // ---------------- keys: warp 2 the sums of the moving rows, warp 3 rows that part of F must not see; queries: both warps those
+    const int tid = KEYS ? lane : static_cast<int>(threadIdx.x) - 64;
     uint32_t st_turn = 0, clean_turn = 0;  // a bit for each slot: the tile's turn, that of the next tile to clean
     int sl = 0;
     auto next_slot = [&]() {
@@ -613,29 +636,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const Work w = sb->work[slot];
       if (C::kFInRing && w.live && w.count > 0) next_slot(), next_slot();
-      for (int u = 0; w.live && ok && u < w.count; ++u, next_slot()) {
-        const uint32_t parity = st_turn >> sl & 1u;
-        if constexpr (KEYS) {
-          ok = wait(&sb->st_empty[sl], parity ^ 1u);
+      const int count = w.live ? w.count : 0;
+      if (KEYS && warp == 2) {
+        for (int u = 0; ok && u < count; ++u, next_slot()) {
+          const int t = w.m_first + u * U, rows = G * min(U, w.seg.n - t);
+          float2 s[2];  // on their way while the slot empties
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = lane + 32 * e;
+            s[e] = make_float2(0.f, 0.f);
+            if (r < rows) s[e] = a.sums[(static_cast<size_t>(w.seg.q0) + t + r / G) * a.hq + w.hk * G + r % G];
+          }
+          ok = wait(&sb->st_empty[sl], (st_turn >> sl & 1u) ^ 1u);
           if (!ok) break;
           float* sums = reinterpret_cast<float*>(smem + C::kSums) + sl * 2 * kUnit;
-          const int t = w.m_first + u * U, rows = G * min(U, w.seg.n - t);
-          float2 s = make_float2(0.f, 0.f);
-          if (tid < rows) s = a.sums[(static_cast<size_t>(w.seg.q0) + t + tid / G) * a.hq + w.hk * G + tid % G];
-          sums[tid] = -s.x, sums[kUnit + tid] = -s.y;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) sums[lane + 32 * e] = -s[e].x, sums[kUnit + lane + 32 * e] = -s[e].y;
           mbar_arrive(&sb->sums_full[sl]);
         }
-        int lo, hi, zero_from;
-        if (!rows_of<KEYS>(a, w, u, lo, hi, zero_from)) continue;
-        // (keys: st_empty has told that the slot's previous tile is done)
-        if (!KEYS) ok = wait(&sb->st_issued[sl], clean_turn >> sl & 1u), clean_turn ^= 1u << sl;
-        ok = ok && wait(&sb->st_full[sl], parity);
-        if (!ok) break;
-        const int at = KEYS ? G * (w.m_first + u * U) : u * kUnit;
-        scrub_pair<D, KEYS>(m_tile(sl, 0), lo, hi, zero_from, at, &sb->worst[slot], tid);
-        if (KEYS) scrub_pair<D, KEYS>(m_tile(sl, 1), lo, hi, zero_from, at, &sb->worst[slot], tid);
-        fence_proxy_async_smem();
-        mbar_arrive(&sb->st_clean[sl]);
+      } else {
+        for (int u = 0; ok && u < count; ++u, next_slot()) {
+          int lo, hi, zero_from;
+          if (!rows_of<KEYS>(a, w, u, lo, hi, zero_from)) continue;
+          if constexpr (KEYS) {  // rows to clean are noted in their sums
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = lane + 32 * e;
+              if (r < hi) bad |= isnan(a.sums[(static_cast<size_t>(w.seg.q0) + w.m_first + u * U + r / G) * a.hq + w.hk * G + r % G].x);
+            }
+            if (!__any_sync(0xffffffffu, bad)) hi = 0;
+          }
+          ok = wait(&sb->st_issued[sl], clean_turn >> sl & 1u) && wait(&sb->st_full[sl], st_turn >> sl & 1u);
+          clean_turn ^= 1u << sl;
+          if (!ok) break;
+          const int at = KEYS ? G * (w.m_first + u * U) : u * kUnit;
+          scrub_pair<D, KEYS, KEYS ? 32 : 64>(m_tile(sl, 0), lo, hi, zero_from, at, &sb->worst[slot], tid);
+          if (KEYS) scrub_pair<D, KEYS, 32>(m_tile(sl, 1), lo, hi, zero_from, at, &sb->worst[slot], tid);
+          fence_proxy_async_smem();
+          mbar_arrive(&sb->st_clean[sl]);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sb->work_empty[slot]);
@@ -650,27 +690,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// (lse log2(e), dout . out) of every row, float32: 16 lanes to a row.  Rows of no sequence are read and not used.
+// (lse log2(e), dout . out) of every row, float32: 16 lanes to a row, four rows in flight.  A row whose q or dout is not finite
+// has NaN for the first, which tells the pass over keys to look at its tile.  Rows of no sequence are read and not used.
+constexpr int kSumsRows = 4;
 __global__ void __launch_bounds__(256) seq_sums_kernel(const __grid_constant__ SeqAttnBwdArgs a) {
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0, a.counters[0] = 0, a.counters[1] = 0;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
   const int c = (threadIdx.x & 15) * 8;
-  if (row >= static_cast<int64_t>(a.tokens_q) * a.hq) return;
-  const int64_t t = row / a.hq, h = row % a.hq;
-  float s = 0.f;
-  if (c < a.head_dim) {
-    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout.ptr) + t * a.dout.stride_t +
-                                                    h * a.dout.stride_h + c);
-    const uint4 y =
-        *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out.ptr) + t * a.out.stride_t + h * a.out.stride_h + c);
-    s = bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) + bf16_hi(x.y) * bf16_hi(y.y) +
-        bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) + bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+  const int64_t rows = static_cast<int64_t>(a.tokens_q) * a.hq;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 16 * kSumsRows + (threadIdx.x >> 4);
+  const bool there = c < a.head_dim;
+  uint4 x[kSumsRows], y[kSumsRows], z[kSumsRows];
+#pragma unroll
+  for (int e = 0; e < kSumsRows; ++e) {
+    const int64_t row = row0 + 16 * e;
+    x[e] = y[e] = z[e] = make_uint4(0, 0, 0, 0);
+    if (row < rows && there) {
+      const int64_t t = row / a.hq, h = row - t * a.hq;
+      auto at = [&](const HeadsView& v) {
+        return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(v.ptr) + t * v.stride_t + h * v.stride_h + c);
+      };
+      x[e] = at(a.dout), y[e] = at(a.out), z[e] = at(a.q);
+    }
   }
   const unsigned half = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
-  for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(half, s, o);
-  if ((threadIdx.x & 15) == 0) a.sums[row] = make_float2(a.lse[row] * kLog2e, s);
+  for (int e = 0; e < kSumsRows; ++e) {
+    const int64_t row = row0 + 16 * e;
+    float s = bf16_lo(x[e].x) * bf16_lo(y[e].x) + bf16_hi(x[e].x) * bf16_hi(y[e].x) + bf16_lo(x[e].y) * bf16_lo(y[e].y) +
+              bf16_hi(x[e].y) * bf16_hi(y[e].y) + bf16_lo(x[e].z) * bf16_lo(y[e].z) + bf16_hi(x[e].z) * bf16_hi(y[e].z) +
+              bf16_lo(x[e].w) * bf16_lo(y[e].w) + bf16_hi(x[e].w) * bf16_hi(y[e].w);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const bool bad = (__ballot_sync(0xffffffffu, not_finite(x[e]) || not_finite(z[e])) & half) != 0;
+    if ((threadIdx.x & 15) == 0 && row < rows)
+      a.sums[row] = make_float2(bad ? __int_as_float(0x7FC00000) : a.lse[row] * kLog2e, s);
+  }
 }
 
 template <int D, bool KEYS>
@@ -693,7 +748,7 @@ cudaError_t launch_pass(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaSt
 cudaError_t launch_seq_attention_bwd(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaStream_t stream) {
   // the first kernel also clears the status word and the counters
   const int64_t rows = static_cast<int64_t>(a.tokens_q) * a.hq;
-  cudaError_t e = launch_pdl(seq_sums_kernel, dim3(static_cast<unsigned>(std::max<int64_t>((rows + 15) / 16, 1))), dim3(256), 0,
+  cudaError_t e = launch_pdl(seq_sums_kernel, dim3(static_cast<unsigned>(std::max<int64_t>((rows + 16 * kSumsRows - 1) / (16 * kSumsRows), 1))), dim3(256), 0,
                              stream, a);
   if (e != cudaSuccess) return e;
   count_launch();

@@ -505,9 +505,9 @@ struct SeqAttnBwdArgs {
   int tile_tokens, unit_tokens;  // tokens of a resident query tile (128 / group), of a moving one (64 / group)
   float scale, scale_log2;
   const int *cu_q, *cu_k;
-  HeadsView dout, out, dq, dk, dv;
+  HeadsView q, dout, out, dq, dk, dv;
   const float* lse;  // [tokens_q, hq]
-  float2* sums;      // [tokens_q, hq]: lse log2(e), dout . out
+  float2* sums;      // [tokens_q, hq]: lse log2(e) (NaN where q or dout is not finite), dout . out
   uint32_t* status;
   uint32_t* counters;  // of the items handed out in each pass
 };

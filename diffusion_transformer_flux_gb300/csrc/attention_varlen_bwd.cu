@@ -217,6 +217,7 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       tc_fence_before();
       mbar_arrive(&sb->f_copied);
     }
+    int held = -1;  // the slot of these warps' last tile
     for (int u = 0; u < w.count; ++u, next_slot()) {
       if ((u & 1) != h) continue;
       // keys: -L of the columns, and -delta of the first 32, before the scores are there: beside the products, which read shared
@@ -233,6 +234,12 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       if (!wait(&sb->sp_full[h], sp_turn)) return;
       sp_turn ^= 1u;
       tc_fence_after();
+      // the products are done in their order: with these scores the tile before the last has been used up, with the last ones F
+      if ((threadIdx.x & 127) == 0) {
+        if (held >= 0) mbar_arrive(&sb->st_empty[held]);
+        if (!C::kFInTmem && u + 1 == w.count) mbar_arrive(&sb->f_empty);
+      }
+      held = slot_u;
       // columns [lo, hi) of the tile are seen by this row
       int lo, hi;
       if constexpr (KEYS) {
@@ -300,6 +307,7 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       if (!wait(&sb->done, done_turn)) return;
       done_turn ^= 1u;
       tc_fence_after();
+      if (held >= 0 && (threadIdx.x & 127) == 0) mbar_arrive(&sb->st_empty[held]);
     }
     const int worst = *reinterpret_cast<volatile int*>(&sb->worst[slot]);
     if (KEYS || D == 128 || h == 0) {
@@ -564,9 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      auto tile_ready = [&](int u) {
-        ok = ok && wait(&sb->st_full[sl], st_turn >> sl & 1u);
-        st_turn ^= 1u << sl;
+      // whether the copies of tile u have been cleaned
+      auto cleaned = [&](int u) {
         int lo, hi, zero_from;
         if (ok && rows_of<KEYS>(a, w, u, lo, hi, zero_from)) {
           ok = wait(&sb->st_clean[sl], clean_turn >> sl & 1u);
@@ -576,41 +583,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (ok && h < w.count && tile_ready(h)) {
-          if (one_lane()) {
+        if (ok && h < w.count) {
+          ok = wait(&sb->st_full[sl], st_turn >> sl & 1u);
+          st_turn ^= 1u << sl;
+          if (cleaned(h) && one_lane()) {
             tc_fence_after();
             scores(sl, h);
-            if (!C::kFInTmem && h + 1 == w.count) tc_commit(&sb->f_empty);
           }
           __syncwarp();
           sl = next(sl);
         }
+      // a step: the products of tile u, the scores of tile u + 2 into the same buffer, and one commit, which stands for both
       for (int u0 = 0; ok && u0 < w.count; u0 += 2) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int u = u0 + h;
           if (!ok || u >= w.count) break;
           asm volatile("" : "+r"(f_lo), "+r"(k_lo), "+r"(n_lo));  // the sums below are formed here, not kept in registers
-          const bool acc_too = u == 0 && lane == 1;
-          ok = wait(acc_too ? &sb->acc_free : &sb->pd_full[h], acc_too ? acc_turn : pd_turn >> h & 1u);
+          const bool ahead = u + 2 < w.count;
+          if (ahead && !cleaned(u + 2)) break;
+          const bool acc_too = u == 0 && lane == 1, st_too = ahead && lane == 2;
+          ok = wait(acc_too ? &sb->acc_free : st_too ? &sb->st_full[sl] : &sb->pd_full[h],
+                    (acc_too ? acc_turn : st_too ? st_turn >> sl : pd_turn >> h) & 1u);
           pd_turn ^= 1u << h;
           if (ok && one_lane()) {
             tc_fence_after();
             products(done_slot, h, u > 0 ? 1u : 0u);
-            tc_commit(&sb->st_empty[done_slot]);
+            if (ahead) scores(sl, h);
             if (u + 1 == w.count) tc_commit(&sb->done);
           }
           __syncwarp();
           done_slot = next(done_slot);
-          if (u + 2 < w.count && tile_ready(u + 2)) {
-            if (one_lane()) {
-              tc_fence_after();
-              scores(sl, h);
-              if (!C::kFInTmem && u + 3 == w.count) tc_commit(&sb->f_empty);
-            }
-            __syncwarp();
-            sl = next(sl);
-          }
+          if (ahead) st_turn ^= 1u << sl, sl = next(sl);
         }
       }
       acc_turn ^= 1u;

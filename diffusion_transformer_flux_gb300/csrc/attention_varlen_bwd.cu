@@ -61,6 +61,7 @@ struct Work {
   int first, count;  // first row of F in its sequence (a key, or a token), moving tiles
   int m_first;       // keys: the first token that sees a key of the tile
   int all_see;       // queries: keys that every row sees
+  int clean_to, clean_from;  // tiles [0, clean_to) and [clean_from, count) have rows to clean
   Segment seg;
 };
 
@@ -126,22 +127,31 @@ __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int ze
   for (int i = max(zero_from, 0) * kChunks + tid; i < kUnit * kChunks; i += THREADS) *at(i) = make_uint4(0, 0, 0, 0);
 }
 
-// Rows of moving tile u: [0, zero_from) are of this sequence, those of [lo, hi) not seen by every row of F.  Whether there
-// is something to clean.
+// Rows of moving tile u: [0, zero_from) are of this sequence, those of [lo, hi) not seen by every row of F.
 template <bool KEYS>
-__device__ __forceinline__ bool rows_of(const SeqAttnBwdArgs& a, const Work& w, int u, int& lo, int& hi, int& zero_from) {
+__device__ __forceinline__ void rows_of(const SeqAttnBwdArgs& a, const Work& w, int u, int& lo, int& hi, int& zero_from) {
   if constexpr (KEYS) {
     const int T = a.unit_tokens, t = w.m_first + u * T, last_key = min(w.first + kSeqTile, w.seg.m) - 1;
     zero_from = a.group * min(T, w.seg.n - t);
     lo = 0;
     hi = a.causal ? min(a.group * min(max(last_key - (w.seg.m - w.seg.n) - t, 0), T), zero_from) : 0;
-    return zero_from < a.group * T || hi > 0;
   } else {
     zero_from = min(w.seg.m - u * kUnit, kUnit);
     lo = max(w.all_see - u * kUnit, 0), hi = zero_from;
-    return (u + 1) * kUnit > w.all_see;
   }
 }
+// Whether tile u has such rows: once for each item, as the MMA warp has no time for it at each tile.
+template <bool KEYS>
+__device__ __forceinline__ void set_cleaning(const SeqAttnBwdArgs& a, Work& w) {
+  if constexpr (KEYS) {
+    const int T = a.unit_tokens, before = min(w.first + kSeqTile, w.seg.m) - 1 - (w.seg.m - w.seg.n) - w.m_first;
+    w.clean_to = a.causal ? (max(before, 0) + T - 1) / T : 0;
+    w.clean_from = (w.seg.n - w.m_first) / T;  // a last tile of fewer tokens
+  } else {
+    w.clean_to = 0, w.clean_from = w.all_see / kUnit;
+  }
+}
+__device__ __forceinline__ bool to_clean(const Work& w, int u) { return u < w.clean_to || u >= w.clean_from; }
 
 // The next item of the counter, by all lanes of a warp.
 __device__ __forceinline__ int take_next(uint32_t* counter, int first_next) {
@@ -444,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.m_first = 0;
           w.all_see = keys_seen(w.seg, w.first, a.causal);
         }
+        set_cleaning<KEYS>(a, w);
         w.live = 1;
         break;
       }
@@ -498,8 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(m_tile(sl, 0) + b * C::kUnitBlock, &tm_m0, &sb->st_full[sl], b * 64, m_head, row);
             tma_load_3d(m_tile(sl, 1) + b * C::kUnitBlock, &tm_m1, &sb->st_full[sl], b * 64, m_head, row);
           }
-          int lo, hi, zero_from;
-          if (rows_of<KEYS>(a, w, u, lo, hi, zero_from)) mbar_arrive(&sb->st_issued[sl]);
+          if (to_clean(w, u)) mbar_arrive(&sb->st_issued[sl]);
         }
         __syncwarp();
         next_slot();
@@ -574,8 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // whether the copies of tile u have been cleaned
       auto cleaned = [&](int u) {
-        int lo, hi, zero_from;
-        if (ok && rows_of<KEYS>(a, w, u, lo, hi, zero_from)) {
+        if (ok && to_clean(w, u)) {
           ok = wait(&sb->st_clean[sl], clean_turn >> sl & 1u);
           clean_turn ^= 1u << sl;
         }
@@ -660,8 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         for (int u = 0; ok && u < count; ++u, next_slot()) {
+          if (!to_clean(w, u)) continue;
           int lo, hi, zero_from;
-          if (!rows_of<KEYS>(a, w, u, lo, hi, zero_from)) continue;
+          rows_of<KEYS>(a, w, u, lo, hi, zero_from);
           if constexpr (KEYS) {  // rows to clean are noted in their sums
             bool bad = false;
 #pragma unroll

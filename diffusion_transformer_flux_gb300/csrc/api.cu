@@ -3042,7 +3042,7 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
   a.batch = batch, a.tokens_q = tokens_q, a.tokens_k = tokens_k, a.hq = heads_q, a.hk = heads_k, a.group = heads_q / heads_k;
   a.head_dim = head_dim, a.causal = causal != 0;
   a.tile_tokens = seq_tile_tokens(a.group), a.unit_tokens = 64 / a.group;
-  a.scale = scale, a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale = scale, a.scale_log2 = scale * 1.4426950408889634f, a.minus_inv_scale = -1.f / a.scale_log2;
   a.cu_q = cu_q, a.cu_k = cu_k, a.lse = lse, a.sums = at<float2>(workspace, kStatusBytes);
   if (tokens_q > 0) a.q = heads_view(q), a.dout = heads_view(dout), a.out = heads_view(out), a.dq = heads_view(dq);
   if (tokens_k > 0) a.dk = heads_view(dk), a.dv = heads_view(dv);

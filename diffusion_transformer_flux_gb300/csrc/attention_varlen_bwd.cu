@@ -15,10 +15,15 @@
 // of one run while P and dS of the other are formed; their ring in shared memory holds four to eight (the load of one takes
 // as long as the work on two).  With N = 64 a product of two tiles in shared memory reads 6 KB for 32 cycles of
 // multiplication (48 cycles); where tensor memory has room for F (queries, and keys with D = 64), F is copied there.  Items are
-// found and handed out as in the forward.  Twelve warps:
+// found and handed out as in the forward.
+// In the pass over keys L and delta belong to the columns of S and dP.  The products subtract them: a last step of 16 columns
+// has ones in three columns of its F side and -L / c (or -delta), cut into three bf16 numbers, in those columns of its M
+// side, so that the accumulators hold S - L / c and dP - delta.  (Read from shared memory by each row they took longer than
+// the arithmetic, beside products that read shared memory at its full rate: 1330 against 770 cycles a tile with D = 64.)
+// Twelve warps:
 //   warp 0       items and TMA: F, then M tiles
 //   warp 1       MMA issuer: S, dP of tile u + 2 follow the accumulating products of tile u
-//   warps 2, 3   keys: -lse and -delta of the moving rows; both: rows that part of F must not see (scrub_pair)
+//   warps 2, 3   keys: the last step's M side; both: rows that part of F must not see (scrub_pair)
 //   warps 4..7   tiles of even number: one row of S and dP per thread, P = exp2(c S - L) and dS = P (dP - delta) back into tensor
 //                memory as bf16 pairs (the operands of the accumulating products, each off by at most 2^-8 of itself);
 //                warps 8..11 those of odd number
@@ -33,8 +38,10 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmP = 0, kTmD = 128, kTmAcc = 256, kTmF = 384;
+constexpr uint32_t kTmP = 0, kTmD = 128, kTmAcc = 256, kTmF = 384, kTmExt = 448;
 constexpr int kUnit = 64;  // rows of a moving tile
+constexpr int kBwdService = 152, kBwdRows = 176;  // registers of the warps that issue, of the warps of rows
+static_assert(128 * kBwdService + 256 * kBwdRows <= 384 * kLaunchRegisters, "shares of the launch's registers");
 
 template <int D, bool KEYS>
 struct Cfg {
@@ -47,8 +54,9 @@ struct Cfg {
   static constexpr int kSlots = D == 64 ? 8 : KEYS ? 4 : 6;
   static constexpr int kRing = kFInRing ? 0 : 2 * kTileBytes;
   static constexpr int kPieces = kRing + kSlots * kSlotBytes;  // rows on their way out, 32 columns of 32 rows for each warp
-  static constexpr int kSums = kPieces + 8 * 32 * 64;          // keys: per slot -L, then -delta, of 64 rows
-  static constexpr int kBar = kSums + (KEYS ? kSlots * 2 * kUnit * 4 : 0);
+  static constexpr int kExt = kPieces + 8 * 32 * 64;           // keys: the last step, 32 bytes a row: M's per slot, then F's two
+  static constexpr int kExtM = kUnit * 32, kExtF = kSeqTile * 32;
+  static constexpr int kBar = kExt + (KEYS ? kSlots * kExtM + 2 * kExtF : 0);
   static constexpr int kSmem = kBar + 1024 + 1024;
   static constexpr uint32_t kIdescS = make_idesc<kKindF16>(128, kUnit);
   static constexpr uint32_t kIdescAcc = make_idesc<kKindF16>(128, D) | kIdescBMnMajor;
@@ -68,7 +76,7 @@ struct Work {
 struct Barriers {
   uint64_t work_full[2], work_empty[2];
   uint64_t f_full, f_copied, f_empty;
-  uint64_t st_full[8], st_clean[8], st_empty[8], sums_full[8];
+  uint64_t st_full[8], st_clean[8], st_empty[8];  // st_full: the copies, and in the pass over keys the last step's rows
   uint64_t st_issued[8];  // the copies of a tile to clean are on the way (so st_full's phase is this tile's)
   uint64_t sp_full[2];
   uint64_t pd_full[2];
@@ -153,6 +161,17 @@ __device__ __forceinline__ void set_cleaning(const SeqAttnBwdArgs& a, Work& w) {
 }
 __device__ __forceinline__ bool to_clean(const Work& w, int u) { return u < w.clean_to || u >= w.clean_from; }
 
+// x as the sum of three bf16 numbers (24 bits; what is not finite is the first alone).
+__device__ __forceinline__ void cut(float x, uint32_t (&v)[3]) {
+  float left = x;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat16 b = __float2bfloat16(left);
+    v[i] = __bfloat16_as_ushort(b);
+    left = isfinite(x) ? left - __bfloat162float(b) : 0.f;
+  }
+}
+
 // The next item of the counter, by all lanes of a warp.
 __device__ __forceinline__ int take_next(uint32_t* counter, int first_next) {
   uint32_t v = 0;
@@ -172,7 +191,6 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
   const uint64_t scale2 = f32x2(a.scale_log2, a.scale_log2);
   const int row_tok = row / G, row_head = row % G;
   uint8_t* pieces = smem + C::kPieces + (warp - 4) * 32 * 64;
-  const float* sums_base = reinterpret_cast<const float*>(smem + C::kSums);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
   };
@@ -230,17 +248,6 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
     int held = -1;  // the slot of these warps' last tile
     for (int u = 0; u < w.count; ++u, next_slot()) {
       if ((u & 1) != h) continue;
-      // keys: -L of the columns, and -delta of the first 32, before the scores are there: beside the products, which read shared
-      // memory at its full rate, these loads take longer than the arithmetic (behind the scores: 1300 against 500 cycles)
-      float4 nl[16], nd[8];
-      const float4* sums = reinterpret_cast<const float4*>(sums_base + slot_u * 2 * kUnit);
-      if constexpr (KEYS) {
-        if (!wait(&sb->sums_full[slot_u], st_turn >> slot_u & 1u)) return;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) nl[e] = sums[e];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) nd[e] = sums[16 + e];
-      }
       if (!wait(&sb->sp_full[h], sp_turn)) return;
       sp_turn ^= 1u;
       tc_fence_after();
@@ -267,8 +274,9 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       for (int e = 0; e < 16; ++e) {
         uint32_t* x = s[e >> 3] + (e & 7) * 4;
         float p0, p1, p2, p3;
-        f32x2_split(ffma2(f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, KEYS ? f32x2(nl[e].x, nl[e].y) : neg_l), p0, p1);
-        f32x2_split(ffma2(f32x2(__uint_as_float(x[2]), __uint_as_float(x[3])), scale2, KEYS ? f32x2(nl[e].z, nl[e].w) : neg_l), p2, p3);
+        const uint64_t a0 = f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), a1 = f32x2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+        f32x2_split(KEYS ? fmul2(a0, scale2) : ffma2(a0, scale2, neg_l), p0, p1);
+        f32x2_split(KEYS ? fmul2(a1, scale2) : ffma2(a1, scale2, neg_l), p2, p3);
         x[0] = __float_as_uint(fast_exp2(p0)), x[1] = __float_as_uint(fast_exp2(p1));
         x[2] = __float_as_uint(fast_exp2(p2)), x[3] = __float_as_uint(fast_exp2(p3));
       }
@@ -278,8 +286,8 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
           float p0 = __uint_as_float(s[c][k]), p1 = __uint_as_float(s[c][k + 1]), z0, z1;
-          const uint64_t minus = !KEYS ? neg_d : k & 2 ? f32x2(nd[k / 4].z, nd[k / 4].w) : f32x2(nd[k / 4].x, nd[k / 4].y);
-          f32x2_split(fmul2(f32x2(p0, p1), fadd2(f32x2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), minus)), z0, z1);
+          const uint64_t g = f32x2(__uint_as_float(d[k]), __uint_as_float(d[k + 1]));
+          f32x2_split(fmul2(f32x2(p0, p1), KEYS ? g : fadd2(g, neg_d)), z0, z1);
           if constexpr (decltype(in_part)::value) {
             const int col = 32 * c + k;
             if (col < lo || col >= hi) p0 = z0 = 0.f;
@@ -300,10 +308,6 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
         columns(std::true_type{}, 0);
       else
         columns(std::false_type{}, 0);
-      if constexpr (KEYS) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) nd[e] = sums[24 + e];
-      }
       tmem_ld32_wait(t_d + 32, d);
       if (part)
         columns(std::true_type{}, 1);
@@ -377,10 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sb->f_copied, 256);
     mbar_init(&sb->f_empty, 1);
     for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(&sb->st_full[s], 1);
+      mbar_init(&sb->st_full[s], KEYS ? 1 + 32 : 1);
       mbar_init(&sb->st_clean[s], KEYS ? 32 : 64);
       mbar_init(&sb->st_empty[s], 1);
-      mbar_init(&sb->sums_full[s], 32);
       mbar_init(&sb->st_issued[s], 1);
     }
     mbar_init(&sb->done, 1);
@@ -398,6 +401,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_proxy_async_smem();
   }
+  if (KEYS && !C::kFInTmem) {
+    // the last step's F side: ones in columns 0 to 2 for S, 3 to 5 for dP (32-byte swizzle: rows 4 to 7 of 8 have their halves
+    // exchanged)
+    for (int i = threadIdx.x; i < 2 * kSeqTile * 2; i += kThreads) {
+      const int x = i / (2 * kSeqTile), r = i / 2 % kSeqTile, c = i & 1;
+      const uint4 v = c ? make_uint4(0, 0, 0, 0) : x ? make_uint4(0, 0x3F800000u, 0x3F803F80u, 0) : make_uint4(0x3F803F80u, 0x3F80u, 0, 0);
+      *reinterpret_cast<uint4*>(smem + C::kExt + C::kSlots * C::kExtM + x * C::kExtF + r * 32 + ((c ^ (r >> 2 & 1)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+  }
   if (warp == 1) {
     tmem_alloc(&sb->tmem_slot, kTmemCols);
     tmem_relinquish();
@@ -412,9 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 4) {
-    more_registers<kSoftmaxRegisters>();
+    more_registers<kBwdRows>();
+    if (KEYS && C::kFInTmem && warp < 8) {  // published with the first item's F
+      uint32_t r[16] = {0x3F803F80u, 0x3F80u, 0, 0, 0, 0, 0, 0, 0, 0x3F800000u, 0x3F803F80u, 0, 0, 0, 0, 0};
+      tmem_st16(tmem + kTmExt + (static_cast<uint32_t>((warp & 3) * 32) << 16), r);
+      tmem_st_wait();
+    }
     rows_role<D, KEYS>(sb, smem, tmem, a);
-  } else if (fewer_registers<kServiceRegisters>(), warp == 0) {
+  } else if (fewer_registers<kBwdService>(), warp == 0) {
     // ---------------- items and TMA
     if (lane == 0) tma_prefetch_desc(&tm_f0), tma_prefetch_desc(&tm_f1), tma_prefetch_desc(&tm_m0), tma_prefetch_desc(&tm_m1);
     uint32_t* counter = a.counters + (KEYS ? 0 : 1);
@@ -531,21 +549,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t k_base = sdesc_kmajor_sw128(smem_addr(m_tile(0, 0))), n_base = sdesc_mnmajor_sw128(smem_addr(m_tile(0, 0)), C::kUnitBlock);
     uint32_t f_lo = static_cast<uint32_t>(sdesc_kmajor_sw128(smem_addr(f_tile(0)))), k_lo = static_cast<uint32_t>(k_base),
              n_lo = static_cast<uint32_t>(n_base);
+    // the last step's rows of 32 bytes: 32-byte swizzle, 8 rows a group
+    constexpr uint64_t kExtDesc = static_cast<uint64_t>(1) << 16 | static_cast<uint64_t>(256 >> 4) << 32 | static_cast<uint64_t>(1) << 46 |
+                                  static_cast<uint64_t>(6) << 61;
+    uint32_t e_lo = static_cast<uint32_t>(kExtDesc) | (smem_addr(smem + C::kExt) & 0x3FFFFu) >> 4;
+    constexpr uint32_t kExtM = C::kExtM >> 4, kExtF = C::kExtF >> 4;
     constexpr uint32_t kSlot = static_cast<uint32_t>(C::kSlotBytes) >> 4, kHalf = static_cast<uint32_t>(C::kHalfSlot) >> 4,
                        kF = static_cast<uint32_t>(C::kTileBytes) >> 4;
     auto scores = [&](int sl, int h) {  // S and dP of the tile in slot sl into buffer h
       const uint32_t m_lo = k_lo + sl * kSlot;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t to = tmem + (x ? kTmD : kTmP) + 64 * h;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t to = tmem + (x ? kTmD : kTmP) + 64 * h;
           const uint64_t m = desc(k_base, m_lo + x * kHalf + koff(k, C::kUnitBlock));
           if constexpr (C::kFInTmem)
             tc_mma_ts_f16(to, tmem + kTmF + x * (D / 2) + k * 8, m, C::kIdescS, k > 0 ? 1u : 0u);
           else
             tc_mma<kKindF16>(to, desc(k_base, f_lo + x * kF + koff(k, kSeqBlock)), m, C::kIdescS, k > 0 ? 1u : 0u);
         }
+        if constexpr (KEYS) {
+          const uint64_t m = desc(kExtDesc, e_lo + sl * kExtM);
+          if constexpr (C::kFInTmem)
+            tc_mma_ts_f16(to, tmem + kTmExt + x * 8, m, C::kIdescS, 1u);
+          else
+            tc_mma<kKindF16>(to, desc(kExtDesc, e_lo + C::kSlots * kExtM + x * kExtF), m, C::kIdescS, 1u);
+        }
+      }
       tc_commit(&sb->sp_full[h]);
     };
     auto products = [&](int sl, int h, uint32_t more) {
@@ -608,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
           const int u = u0 + h;
           if (!ok || u >= w.count) break;
-          asm volatile("" : "+r"(f_lo), "+r"(k_lo), "+r"(n_lo));  // the sums below are formed here, not kept in registers
+          asm volatile("" : "+r"(f_lo), "+r"(k_lo), "+r"(n_lo), "+r"(e_lo));  // the sums below are formed here, not kept in registers
           const bool ahead = u + 2 < w.count;
           if (ahead && !cleaned(u + 2)) break;
           const bool acc_too = u == 0 && lane == 1, st_too = ahead && lane == 2;
@@ -651,21 +682,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (C::kFInRing && w.live && w.count > 0) next_slot(), next_slot();
       const int count = w.live ? w.count : 0;
       if (KEYS && warp == 2) {
-        for (int u = 0; ok && u < count; ++u, next_slot()) {
-          const int t = w.m_first + u * U, rows = G * min(U, w.seg.n - t);
-          float2 s[2];  // on their way while the slot empties
+        // the sums of three tiles are on their way (one at a time they held the pass up: 1400 cycles a tile)
+        constexpr int kAhead = 3;
+        float2 fetched[kAhead][2];
+        auto fetch = [&](int u, float2 (&to)[2]) {
+          const int t = w.m_first + u * U, rows = u < count ? G * min(U, w.seg.n - t) : 0;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = lane + 32 * e;
-            s[e] = make_float2(0.f, 0.f);
-            if (r < rows) s[e] = a.sums[(static_cast<size_t>(w.seg.q0) + t + r / G) * a.hq + w.hk * G + r % G];
+            to[e] = make_float2(0.f, 0.f);
+            if (r < rows) to[e] = a.sums[(static_cast<size_t>(w.seg.q0) + t + r / G) * a.hq + w.hk * G + r % G];
           }
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i, fetched[i]);
+        for (int u = 0; ok && u < count; ++u, next_slot()) {
+          float2 s[2] = {fetched[0][0], fetched[0][1]};
+#pragma unroll
+          for (int i = 0; i + 1 < kAhead; ++i) fetched[i][0] = fetched[i + 1][0], fetched[i][1] = fetched[i + 1][1];
+          fetch(u + kAhead, fetched[kAhead - 1]);
           ok = wait(&sb->st_empty[sl], (st_turn >> sl & 1u) ^ 1u);
           if (!ok) break;
-          float* sums = reinterpret_cast<float*>(smem + C::kSums) + sl * 2 * kUnit;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) sums[lane + 32 * e] = -s[e].x, sums[kUnit + lane + 32 * e] = -s[e].y;
-          mbar_arrive(&sb->sums_full[sl]);
+          for (int e = 0; e < 2; ++e) {
+            const int r = lane + 32 * e;
+            uint32_t x[3], y[3];
+            cut(s[e].x * a.minus_inv_scale, x), cut(-s[e].y, y);
+            uint8_t* row = smem + C::kExt + sl * C::kExtM + r * 32;
+            *reinterpret_cast<uint4*>(row + ((r >> 2 & 1) << 4)) = make_uint4(x[0] | x[1] << 16, x[2] | y[0] << 16, y[1] | y[2] << 16, 0);
+            *reinterpret_cast<uint4*>(row + (((r >> 2 & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&sb->st_full[sl]);
         }
       } else {
         for (int u = 0; ok && u < count; ++u, next_slot()) {

@@ -503,7 +503,7 @@ struct SeqAttnBwdArgs {
   int batch, tokens_q, tokens_k;
   int hq, hk, group, head_dim, causal;
   int tile_tokens, unit_tokens;  // tokens of a resident query tile (128 / group), of a moving one (64 / group)
-  float scale, scale_log2;
+  float scale, scale_log2, minus_inv_scale;  // minus_inv_scale: -1 / scale_log2
   const int *cu_q, *cu_k;
   HeadsView q, dout, out, dq, dk, dv;
   const float* lse;  // [tokens_q, hq]

@@ -2916,6 +2916,32 @@ SeqAttnArgs attention_args(int32_t batch, int32_t tokens_q, int32_t heads_q, int
   return a;
 }
 
+// The workspace of the gradients: two floats a row, and up to kPartTokens queries room for the sums of key tiles whose queries
+// are worked on in parts (as many floats as q has elements; longer calls have key tiles enough for the GPU's 152 SMs).
+constexpr int kPartTokens = 16384;
+struct AttnBwdPlan {
+  size_t sums, part, part_floats, total;
+};
+AttnBwdPlan plan_attention_bwd(int64_t tokens_q, int heads_q, int head_dim) {
+  AttnBwdPlan p = {};
+  Carver c;
+  const size_t rows = static_cast<size_t>(tokens_q) * heads_q;
+  p.sums = c.take(rows * sizeof(float2));
+  p.part_floats = tokens_q <= kPartTokens ? rows * (head_dim <= 64 ? 64 : 128) : 0;
+  p.part = c.take(p.part_floats * sizeof(float));
+  p.total = c.off;
+  return p;
+}
+// Parts of the queries of a key tile.  The tiles of 128 keys by key heads are the work items; where they are fewer than three
+// for each SM, parts of their queries are, as long as the parts' sums have room.  All three kernels for 9 documents of up to 2041
+// tokens and 8 key heads, 312 tiles: 342 us undivided (the largest tile alone takes 125), 297 in two parts; for 2 x 4608
+// tokens, 576 tiles: 959 and 1022.
+int attention_bwd_parts(const AttnBwdPlan& p, int64_t tokens_k, int heads_k, int head_dim) {
+  const int64_t items = std::max<int64_t>(1, (tokens_k + 127) / 128 * heads_k), d = head_dim <= 64 ? 64 : 128;
+  const int64_t wanted = (3 * 152 + items - 1) / items, room = static_cast<int64_t>(p.part_floats) / std::max<int64_t>(1, tokens_k * heads_k * 2 * d);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(wanted, room), 32)));
+}
+
 // How a call over a paged cache splits its work.  Keys of a sequence go to several CTAs where the sequences and key heads
 // alone are too few for the GPU's 152 SMs.
 struct PagedPlan {
@@ -2998,11 +3024,9 @@ mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t
   return MMDIT_OK;
 }
 
-size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t) {
-  if (tokens_q < 1 || heads_q < 1) return kStatusBytes;
-  Carver c;
-  c.take(static_cast<size_t>(tokens_q) * heads_q * sizeof(float2));
-  return c.off;
+size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim) {
+  if (tokens_q < 1 || heads_q < 1 || head_dim < 1) return kStatusBytes;
+  return plan_attention_bwd(tokens_q, heads_q, head_dim).total;
 }
 
 mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,
@@ -3043,7 +3067,10 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
   a.head_dim = head_dim, a.causal = causal != 0;
   a.tile_tokens = seq_tile_tokens(a.group), a.unit_tokens = 64 / a.group;
   a.scale = scale, a.scale_log2 = scale * 1.4426950408889634f, a.minus_inv_scale = -1.f / a.scale_log2;
-  a.cu_q = cu_q, a.cu_k = cu_k, a.lse = lse, a.sums = at<float2>(workspace, kStatusBytes);
+  a.cu_q = cu_q, a.cu_k = cu_k, a.lse = lse;
+  const AttnBwdPlan plan = plan_attention_bwd(std::max(tokens_q, 0), heads_q, head_dim);
+  a.sums = at<float2>(workspace, plan.sums), a.part = at<float>(workspace, plan.part);
+  a.parts = tokens_q > 0 ? attention_bwd_parts(plan, tokens_k, heads_k, head_dim) : 1;
   if (tokens_q > 0) a.q = heads_view(q), a.dout = heads_view(dout), a.out = heads_view(out), a.dq = heads_view(dq);
   if (tokens_k > 0) a.dk = heads_view(dk), a.dv = heads_view(dv);
   a.status = status_word(workspace), a.counters = a.status + 32;

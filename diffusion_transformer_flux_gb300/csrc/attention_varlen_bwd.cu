@@ -70,6 +70,7 @@ struct Work {
   int m_first;       // keys: the first token that sees a key of the tile
   int all_see;       // queries: keys that every row sees
   int clean_to, clean_from;  // tiles [0, clean_to) and [clean_from, count) have rows to clean
+  int part, parts;           // keys: which part of the moving tiles this is, of how many
   Segment seg;
 };
 
@@ -133,6 +134,26 @@ __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int ze
     }
   }
   for (int i = max(zero_from, 0) * kChunks + tid; i < kUnit * kChunks; i += THREADS) *at(i) = make_uint4(0, 0, 0, 0);
+}
+
+// The moving tiles of `first`'s key tile: the first token that sees one of its keys, and their number; and how many parts of how
+// many tiles they are worked on in (at least kPartUnits to a part, so that its sums are worth their way through memory).
+constexpr int kPartUnits = 8;
+struct KeyTile {
+  int m_first, count, per_part, parts;
+};
+__device__ __forceinline__ KeyTile key_tile(const SeqAttnBwdArgs& a, const Segment& seg, int first) {
+  KeyTile t;
+  t.m_first = a.causal ? max(first - seg.m + seg.n, 0) : 0;
+  t.count = seg.n > t.m_first ? (seg.n - t.m_first + a.unit_tokens - 1) / a.unit_tokens : 0;
+  t.per_part = max((t.count + a.parts - 1) / a.parts, kPartUnits);
+  t.parts = max((t.count + t.per_part - 1) / t.per_part, 1);
+  return t;
+}
+// Where the float32 sums of part p of key row `row` lie: dv, then dk.
+template <int D>
+__device__ __forceinline__ size_t part_at(const SeqAttnBwdArgs& a, int p, int64_t row, int hk) {
+  return ((static_cast<size_t>(p) * a.tokens_k + row) * a.hk + hk) * 2 * D;
 }
 
 // Rows of moving tile u: [0, zero_from) are of this sequence, those of [lo, hi) not seen by every row of F.
@@ -340,6 +361,11 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
         if (w.count > 0) tmem_ld32_wait(tmem + kTmAcc + (KEYS ? h * D : 0) + k * 32 + lane_off, r);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = w.count > 0 ? __uint_as_float(r[i]) * f : 0.f;
+        if (KEYS && w.parts > 1) {  // finished by seq_parts_kernel
+          if (valid)
+            store32(a.part + part_at<D>(a, w.part, static_cast<int64_t>(w.seg.k0) + w.first + row, w.hk) + h * D + k * 32, v);
+          continue;
+        }
         put_pieces32(pieces, v);
         __syncwarp();
         store_rows32(pieces, dst ? dst + k * 32 : nullptr, a.head_dim - k * 32);
@@ -442,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       order.init(a.cu_k, a.tokens_k, a.cu_q, a.tokens_q, a.batch, kSeqTile, a.causal, 0);  // the first keys have the most queries
     else
       order.init(a.cu_q, a.tokens_q, a.cu_k, a.tokens_k, a.batch, T, a.causal, 1);  // the last queries see the most keys
-    const int items = order.n * a.hk;
+    const int items = order.n * a.hk * (KEYS ? a.parts : 1);
     uint32_t f_turn = 0, st_turn = 0, st_used = 0;
     int sl = 0;
     bool ok = true, f_used = false;
@@ -459,12 +485,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.live = 0;
       for (; item < items; item = items > first_next ? take_next(counter, first_next) : items) {
         TileOrder::Found at;
-        if (!order.find(item / a.hk, at)) continue;
-        w.hk = item % a.hk, w.first = at.start;
+        if (!order.find(item / a.hk / (KEYS ? a.parts : 1), at)) continue;
+        w.hk = item % a.hk, w.first = at.start, w.part = 0, w.parts = 1;
         if constexpr (KEYS) {
           w.seg = {at.other_first, at.other_count, at.first, at.count};
-          w.m_first = a.causal ? max(w.first - w.seg.m + w.seg.n, 0) : 0;
-          w.count = w.seg.n > w.m_first ? (w.seg.n - w.m_first + U - 1) / U : 0;
+          const KeyTile t = key_tile(a, w.seg, w.first);
+          w.part = item / a.hk % a.parts, w.parts = t.parts;
+          if (w.part >= w.parts) continue;
+          w.m_first = t.m_first + w.part * t.per_part * U;
+          w.count = min(t.count - w.part * t.per_part, t.per_part);
           w.all_see = 0;
         } else {
           w.seg = {at.first, at.count, at.other_first, at.other_count};
@@ -790,9 +819,46 @@ __global__ void __launch_bounds__(256) seq_sums_kernel(const __grid_constant__ S
   }
 }
 
+// dk and dv of key rows whose queries were worked on in parts: the parts' float32 sums, added in their order.  A warp to a row
+// and key head.
+template <int D>
+__global__ void __launch_bounds__(256) seq_parts_kernel(const __grid_constant__ SeqAttnBwdArgs a) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (item >= static_cast<int64_t>(a.tokens_k) * a.hk) return;
+  const int row = static_cast<int>(item / a.hk), hk = static_cast<int>(item % a.hk);
+  const int b = find_segment(a.batch, row, [&](int i) { return min(max(a.cu_k[i], 0), a.tokens_k); });
+  Segment seg;
+  clip_segment(a.cu_k, b, a.tokens_k, seg.k0, seg.m);
+  clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
+  if (row < seg.k0 || row >= seg.k0 + seg.m) return;
+  const KeyTile t = key_tile(a, seg, (row - seg.k0) / kSeqTile * kSeqTile);
+  if (t.parts <= 1) return;
+  constexpr int kCols = D / 16;  // of dv by the lower half of the lanes, of dk by the upper
+  float sum[kCols] = {};
+  for (int p = 0; p < t.parts; ++p) {
+    const float4* v = reinterpret_cast<const float4*>(a.part + part_at<D>(a, p, row, hk) + lane * kCols);
+#pragma unroll
+    for (int i = 0; i < kCols / 4; ++i) {
+      const float4 x = v[i];
+      sum[4 * i] += x.x, sum[4 * i + 1] += x.y, sum[4 * i + 2] += x.z, sum[4 * i + 3] += x.w;
+    }
+  }
+  const HeadsView& out = lane < 16 ? a.dv : a.dk;
+  const int col = (lane & 15) * kCols;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.ptr) + row * out.stride_t + hk * out.stride_h + col;
+#pragma unroll
+  for (int i = 0; i < kCols / 4; ++i)
+    if (col + 4 * i < a.head_dim)
+      reinterpret_cast<uint2*>(dst)[i] =
+          make_uint2(pack_bf16x2(sum[4 * i], sum[4 * i + 1]), pack_bf16x2(sum[4 * i + 2], sum[4 * i + 3]));
+}
+
 template <int D, bool KEYS>
 cudaError_t launch_pass(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaStream_t stream) {
-  const int64_t items = ((KEYS ? a.tokens_k / kSeqTile : a.tokens_q / a.tile_tokens) + static_cast<int64_t>(a.batch)) * a.hk;
+  const int64_t items =
+      ((KEYS ? a.tokens_k / kSeqTile : a.tokens_q / a.tile_tokens) + static_cast<int64_t>(a.batch)) * a.hk * (KEYS ? a.parts : 1);
   if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
   using C = Cfg<D, KEYS>;
   cudaError_t e = cudaFuncSetAttribute(seq_attention_bwd_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -817,6 +883,13 @@ cudaError_t launch_seq_attention_bwd(const SeqAttnBwdArgs& a, const SeqAttnBwdMa
   if (a.tokens_k > 0) {
     e = a.head_dim <= 64 ? launch_pass<64, true>(a, m, stream) : launch_pass<128, true>(a, m, stream);
     if (e != cudaSuccess) return e;
+    if (a.parts > 1) {
+      const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tokens_k) * a.hk + 7) / 8));
+      e = a.head_dim <= 64 ? launch_pdl(seq_parts_kernel<64>, grid, dim3(256), 0, stream, a)
+                           : launch_pdl(seq_parts_kernel<128>, grid, dim3(256), 0, stream, a);
+      if (e != cudaSuccess) return e;
+      count_launch();
+    }
   }
   if (a.tokens_q > 0) {
     e = a.head_dim <= 64 ? launch_pass<64, false>(a, m, stream) : launch_pass<128, false>(a, m, stream);

@@ -510,6 +510,8 @@ struct SeqAttnBwdArgs {
   float2* sums;      // [tokens_q, hq]: lse log2(e) (NaN where q or dout is not finite), dout . out
   uint32_t* status;
   uint32_t* counters;  // of the items handed out in each pass
+  int parts;           // the queries of a key tile are worked on in up to so many
+  float* part;         // [parts, tokens_k, hk, 2, D] sums, where there are more than one
 };
 struct SeqAttnBwdMaps {
   CUtensorMap f_q, f_dout, f_k, f_v, m_q, m_dout, m_k, m_v;  // boxes of resident and of moving tiles

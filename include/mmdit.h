@@ -872,7 +872,7 @@ mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t
  * query row whose q or dout is not finite, within 64 rows (tokens by the group's heads) of one that sees fewer keys, makes
  * the gradients of the keys it sees NaN; a key row likewise those of the queries that see it.  heads_q at most 64 times
  * heads_k.
- * workspace >= mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) (two floats for each row: calls that
+ * workspace >= mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) (row sums and partial sums: calls that
  * share one are ordered on one stream). */
 size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim);
 mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,

@@ -2942,11 +2942,12 @@ int attention_bwd_parts(const AttnBwdPlan& p, int64_t tokens_k, int heads_k, int
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(wanted, room), 32)));
 }
 
-// How a call over a paged cache splits its work.  Keys of a sequence go to several CTAs where the sequences and key heads
-// alone are too few for the GPU's 152 SMs.
+// How a call over a paged cache splits its work.  Sequences of up to 16 rows (tokens by the heads of a group) are
+// paged_few_kernel's, of which two CTAs stay on each of the GPU's 152 SMs, the others the tile kernel's, whose items (two query
+// tiles of a key head) are split along the keys where they are fewer than the SMs.
 struct PagedPlan {
   int few, tiles;  // whether paged_few_kernel and the tile kernel run
-  int few_keys, few_splits, split_keys, splits;
+  int few_ctas, few_whole, few_join_rows, split_keys, splits;
   size_t few_part, few_lse, part, lse, total;
 };
 PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, int head_dim, int64_t max_q, int64_t max_kv) {
@@ -2955,25 +2956,27 @@ PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, 
   const int64_t sms = 152;
   p.tiles = max_q * group > kFewRows;
   p.few = !p.tiles || batch > 1;
-  p.few_splits = p.splits = 1;
+  p.splits = 1;
   max_kv = std::max<int64_t>(max_kv, 1);
+  Carver c;
   if (p.few) {
-    const int64_t want = std::max<int64_t>(1, 4 * sms / std::max<int64_t>(1, batch * heads_k));
-    const int64_t keys = std::max<int64_t>(256, round_up((max_kv + want - 1) / want, 64));
-    p.few_splits = static_cast<int>((max_kv + keys - 1) / keys);
-    p.few_keys = static_cast<int>(keys);
+    const int64_t steps = (max_kv + kFewStep - 1) / kFewStep, all = batch * heads_k;
+    p.few_whole = steps <= kFewLeast;
+    const int64_t runs = std::min(std::max<int64_t>(2 * sms / heads_k, 1), (batch * steps + kFewLeast - 1) / kFewLeast);
+    p.few_ctas = static_cast<int>(p.few_whole ? all : runs * heads_k);
+    p.few_join_rows = static_cast<int>(std::min<int64_t>(max_q * group, kFewRows / group * group));
+    if (!p.few_whole) {
+      const size_t rows = static_cast<size_t>(p.few_ctas) * 2 * kFewRows;
+      p.few_part = c.take(rows * d * 4), p.few_lse = c.take(rows * 4);
+    }
   }
   if (p.tiles) {
-    const int64_t items = (tokens_q / (2 * (128 / group)) + batch) * heads_k;
-    const int64_t want = items >= sms ? 1 : std::max<int64_t>(1, std::min(sms / items, max_kv / 512));
+    // beside the sequences of few rows a batch has few others: its tokens tell more of the items than its number
+    const int64_t items = (tokens_q / (2 * (128 / group)) + 1) * heads_k;
+    const int64_t want = std::max<int64_t>(1, std::min((sms + items - 1) / items, max_kv / 512));
     const int64_t keys = round_up((max_kv + want - 1) / want, 128);
     p.splits = static_cast<int>((max_kv + keys - 1) / keys);
     p.split_keys = p.splits > 1 ? static_cast<int>(keys) : 0;
-  }
-  Carver c;
-  if (p.few_splits > 1) {
-    const size_t rows = static_cast<size_t>(p.few_splits) * batch * heads_k * kFewRows;
-    p.few_part = c.take(rows * d * 4), p.few_lse = c.take(rows * 4);
   }
   if (p.splits > 1) {
     const size_t rows = static_cast<size_t>(p.splits) * tokens_q * heads_q;
@@ -3116,8 +3119,9 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
   if (reach > (1 << 30)) return fail(MMDIT_ERR_UNSUPPORTED, "%s: table_width page_size must be at most 2^30", what);
   const int most = static_cast<int>(max_kv > 0 ? std::min<int64_t>(max_kv, reach) : reach);
   const PagedPlan p = plan_paged(std::max(tokens_q, 1), std::max(batch, 1), heads_q, heads_k, head_dim, max_q, most);
-  if (tokens_q > 0 && batch > 0 && (p.few_splits > 65535 || p.splits > 65535))
-    return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many parts", what);
+  if (p.few && ((p.few_whole && static_cast<int64_t>(batch) * heads_k > INT32_MAX / 2) ||
+                batch * ((most + kFewStep - 1LL) / kFewStep + 1) > INT32_MAX))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: batch max_kv / %d must be below 2^31", what, kFewStep);
   if ((s = check_workspace(workspace, workspace_bytes, batch == 0 || tokens_q == 0 ? kStatusBytes : p.total)) != MMDIT_OK) return s;
   if (batch == 0 || tokens_q == 0 || max_q == 0) return MMDIT_OK;
   if ((s = check_heads(what, "q", q, tokens_q, heads_q, head_dim, false)) != MMDIT_OK) return s;
@@ -3133,8 +3137,9 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
   a.k_pages = pages_view(k), a.v_pages = pages_view(v);
   a.tables = tables, a.kv_lens = kv_lens, a.table_width = table_width, a.n_pages = n_pages, a.max_keys = most;
   a.page_shift = log2_of(page_size), a.page_rows = std::min(page_size, 128);
-  a.few_rows = p.few ? kFewRows : 0, a.few_keys = p.few_keys, a.split_keys = p.split_keys;
-  if (p.few_splits > 1) a.few_part = at<float>(workspace, p.few_part), a.few_lse = at<float>(workspace, p.few_lse);
+  a.few_rows = p.few ? kFewRows : 0, a.few_ctas = p.few_ctas, a.few_whole = p.few_whole, a.few_join_rows = p.few_join_rows;
+  a.split_keys = p.split_keys;
+  a.few_part = at<float>(workspace, p.few_part), a.few_lse = at<float>(workspace, p.few_lse);
   if (p.splits > 1) a.part = at<float>(workspace, p.part), a.part_lse = at<float>(workspace, p.lse);
   a.status = status_word(workspace), a.clear = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -3143,14 +3148,17 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
                   !encode_pages_map(&m.k, a.k_pages, head_dim, heads_k, n_pages, page_size, a.page_rows) ||
                   !encode_pages_map(&m.v, a.v_pages, head_dim, heads_k, n_pages, page_size, a.page_rows)))
     return fail(MMDIT_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", what);
+  if (p.few && (!encode_pages_map(&m.few_k, a.k_pages, head_dim, heads_k, n_pages, page_size, std::min(page_size, 16)) ||
+                !encode_pages_map(&m.few_v, a.v_pages, head_dim, heads_k, n_pages, page_size, std::min(page_size, 16))))
+    return fail(MMDIT_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", what);
   pdl_begin_call();
   ProfScope ps_("paged_attention", st);
   if (p.tiles) {
     MMDIT_CUDA(launch_seq_attention(a, m, 1, p.splits, status_word(workspace) + 32, st), what);
     a.clear = 0;
   }
-  if (p.few) MMDIT_CUDA(launch_paged_few(a, p.few_splits, st), "paged attention of few rows");
-  if (p.few_splits > 1 || p.splits > 1) MMDIT_CUDA(launch_paged_combine(a, st), "paged attention's join");
+  if (p.few) MMDIT_CUDA(launch_paged_few(a, m, st), "paged attention of few rows");
+  if (p.splits > 1) MMDIT_CUDA(launch_paged_join(a, st), "paged attention's join");
   return MMDIT_OK;
 }
 

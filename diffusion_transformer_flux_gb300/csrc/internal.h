@@ -474,9 +474,11 @@ struct SeqAttnArgs {
   const int *tables, *kv_lens;
   int table_width, n_pages, page_shift, page_rows, max_keys;  // page_rows: rows of a copied piece, at most 128
   int few_rows;  // sequences of at most that many rows (tokens by the group's heads) are paged_few_kernel's: kFewRows or 0
-  int few_keys, split_keys;  // keys of one CTA of paged_few_kernel, of the tile kernel (0: all)
-  // normalised parts and their log2-sums: [splits, tokens_q, hq(, D)] of the tile kernel, [splits, batch, hk, kFewRows(, D)]
-  // of paged_few_kernel
+  int few_ctas, few_whole;   // its CTAs; whether each takes one sequence and key head
+  int few_join_rows;         // rows of the sequence with most of them
+  int split_keys;            // keys of one item of the tile kernel (0: all)
+  // normalised parts and their log2-sums: [splits, tokens_q, hq(, D)] of the tile kernel, [few_ctas, 2, kFewRows(, D)] of
+  // paged_few_kernel
   float *part, *part_lse, *few_part, *few_lse;
   uint32_t* status;
   int clear;           // this kernel is the call's first and clears the status word
@@ -487,16 +489,18 @@ struct SeqAttnArgs {
   int first_next;
 };
 constexpr int kFewRows = 16;
+constexpr int kFewStep = 64, kFewLeast = 8;  // keys of a step of paged_few_kernel, the least steps of a CTA that leaves a part
 struct SeqAttnMaps {
   CUtensorMap q, k, v;
+  CUtensorMap few_k, few_v;  // paged_few_kernel's boxes: up to 16 rows
 };
 int seq_tile_tokens(int group);
 bool encode_heads_map(CUtensorMap* map, const HeadsView& v, int head_dim, int heads, int64_t tokens, int box_heads, int box_tokens);
 bool encode_pages_map(CUtensorMap* map, const PagesView& v, int head_dim, int heads, int n_pages, int page_size, int rows);
 cudaError_t launch_seq_attention(SeqAttnArgs a, const SeqAttnMaps& m, int paged, int splits, uint32_t* counter, cudaStream_t stream);
-// few rows to a sequence: `splits` CTAs of few_keys keys each; then the join of the parts of either kernel
-cudaError_t launch_paged_few(const SeqAttnArgs& a, int splits, cudaStream_t stream);
-cudaError_t launch_paged_combine(const SeqAttnArgs& a, cudaStream_t stream);
+// few rows to a sequence, with the join of their parts; the join of the tile kernel's parts
+cudaError_t launch_paged_few(const SeqAttnArgs& a, const SeqAttnMaps& m, cudaStream_t stream);
+cudaError_t launch_paged_join(const SeqAttnArgs& a, cudaStream_t stream);
 
 // gradients of the attention over packed sequences
 struct SeqAttnBwdArgs {

@@ -18,11 +18,13 @@
 // is reduced over the lanes only where one of them has a score 2^8 above it.  With the queries as the 16, copies of 16 bytes by
 // every lane and a maximum for each tile a warp had 640 instructions a tile to issue, and it was 111 us.
 //
-// What bounds it is the reading (6.9 TB/s in the loop) and, for short runs, what precedes it, where each access that waits for
+// What bounds it is the reading and, for short runs, what precedes it, where each access that waits for
 // the one before costs 2000 cycles with nothing in the caches: the lengths, the first pages (all stages' at once) and Q (16
 // bytes a thread, through shared memory: 4-byte loads of fragments took 9 us) are three such steps, and the code is kept
-// short, its rare parts out of the loop.  One token over 120000 (492 MB): 79.7 us, 6.17 TB/s; 32 tokens over up to 16384
-// (1.25 GB): 191 us, 6.51 TB/s; 4 tokens over up to 8192 of 8 sequences (160 MB): 39 us.
+// short, its rare parts out of the loop.  Pages are read once and make room first in L2, so that these stay in it (4 x 8 tokens:
+// 39 -> 34 us).  Two stages of a warp (128 KB on the way on an SM) read faster than three: 180 against 188 us for the batch.
+// One token over 120000 (492 MB): 75 us, 6.56 TB/s; 32 tokens over up to 16384 (1.25 GB): 180 us, 6.88 TB/s; 4 tokens over up
+// to 8192 of 8 sequences (160 MB): 34 us.
 #include <algorithm>
 
 #include "attention_tiles.cuh"
@@ -40,16 +42,16 @@ template <int D>
 struct FewCfg {
   static constexpr int kBlock = kFewKeys * 128;      // 16 keys of 64 columns (one 128-byte swizzle column block)
   static constexpr int kTile = (D / 64) * kBlock;    // K or V of a tile
-  static constexpr int kStages = D == 64 ? 6 : 3;
+  static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kRing = kStages * 2 * kTile;
-  static constexpr int kSmem = kFewWarps * kRing + 1024;  // 97 KB: two CTAs on an SM
+  static constexpr int kSmem = kFewWarps * kRing + 1024;  // 65 KB: two CTAs on an SM
 };
 static_assert(FewCfg<64>::kSmem >= kFewWarps * kFewRows * (64 + 2) * 4 &&
                   FewCfg<128>::kSmem >= kFewWarps * kFewRows * (128 + 2) * 4,
               "the parts of the warps lie in the rings at the end");
 
 struct FewShared {
-  uint64_t full[kFewWarps][6];
+  uint64_t full[kFewWarps][4];
   int abort_flag;
   int any_bad;
   int worst[128];
@@ -173,6 +175,7 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
   const int box_rows = min(a.page_rows, kFewKeys), pieces = kFewKeys / box_rows;
   const int piece = lane % pieces, half = lane / pieces % (D / 64), is_v = lane / (pieces * (D / 64));
   const bool copies = is_v < 2;
+  const uint64_t policy = read_once_policy();
   auto page_of = [&](int i) -> int {  // of this lane's box of tile i; -1: none
     const int key = k_begin + i * kFewKeys + piece * box_rows;
     if (!copies || i >= n_tiles || key >= k_end) return -1;
@@ -189,7 +192,7 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
     if (copies) {
       const int key = k_begin + i * kFewKeys + piece * box_rows;
       tma_load_4d(ring + (2 * stage + is_v) * C::kTile + half * C::kBlock + piece * box_rows * 128, is_v ? tm_v : tm_k,
-                  &sh->full[warp][stage], half * 64, key & ((1 << a.page_shift) - 1), hk, page < 0 ? a.n_pages : page);
+                  &sh->full[warp][stage], half * 64, key & ((1 << a.page_shift) - 1), hk, page < 0 ? a.n_pages : page, policy);
     }
   };
   int next;

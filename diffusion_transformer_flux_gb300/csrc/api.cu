@@ -2950,6 +2950,27 @@ struct PagedPlan {
   int few_ctas, few_whole, few_join_rows, split_keys, splits;
   size_t few_part, few_lse, part, lse, total;
 };
+// The keys of one part of an item of the tile kernel, where `items` over `keys` keys each are worked on by `sms` CTAs, longest
+// parts first: the length that ends first, counted in keys.  A part costs 384 keys more than its own (its start and end) and
+// the writing and adding of it `join`.  Parts of one length end in whole rounds; or, where items are fewer than CTAs, w long
+// parts of f keys take a CTA each and the CTAs left over work on c short ones of g each meanwhile: f + 384 = c (g + 384), w f + g
+// = keys.  (1000 tokens of 32 + 8 heads over 32000 keys, 128 items: whole 393 us, 2 equal parts 420, one of 6/7 and one of 1/7 364.)
+int64_t split_length(int64_t items, int64_t sms, int64_t keys, double join) {
+  const double own = 384, k = static_cast<double>(keys);
+  double best = static_cast<double>((items + sms - 1) / sms) * (k + own);
+  int64_t length = keys;
+  auto take = [&](double cost, double f) {
+    if (cost < 0.98 * best) best = cost, length = std::min(keys, static_cast<int64_t>(f) + 1);
+  };
+  for (int64_t w = 1; w <= std::min<int64_t>(keys / 512, 64); ++w) {
+    if (w > 1) take(static_cast<double>((items * w + sms - 1) / sms) * (k / w + own) + w * join, k / w);
+    const int64_t left = sms - items * w;
+    if (left <= 0) continue;
+    const double c = static_cast<double>((items + left - 1) / left), f = (c * k + (c - 1) * own) / (1 + c * w);
+    if (k - w * f >= 256) take(f + own + (w + 1) * join, f);
+  }
+  return length;
+}
 PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, int head_dim, int64_t max_q, int64_t max_kv) {
   PagedPlan p = {};
   const int group = heads_q / heads_k, d = head_dim <= 64 ? 64 : 128;
@@ -2973,8 +2994,7 @@ PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, 
   if (p.tiles) {
     // beside the sequences of few rows a batch has few others: its tokens tell more of the items than its number
     const int64_t items = (tokens_q / (2 * (128 / group)) + 1) * heads_k;
-    const int64_t want = std::max<int64_t>(1, std::min((sms + items - 1) / items, max_kv / 512));
-    const int64_t keys = round_up((max_kv + want - 1) / want, 128);
+    const int64_t keys = round_up(split_length(items, sms, max_kv, 78. * 8 / 6.7e6 * tokens_q * heads_q * d), 128);
     p.splits = static_cast<int>((max_kv + keys - 1) / keys);
     p.split_keys = p.splits > 1 ? static_cast<int>(keys) : 0;
   }
@@ -3155,7 +3175,7 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
   ProfScope ps_("paged_attention", st);
   if (p.tiles) {
     MMDIT_CUDA(launch_seq_attention(a, m, 1, p.splits, status_word(workspace) + 32, st), what);
-    a.clear = 0;
+    a.clear = 0, a.few_behind = 1;
   }
   if (p.few) MMDIT_CUDA(launch_paged_few(a, m, st), "paged attention of few rows");
   if (p.splits > 1) MMDIT_CUDA(launch_paged_join(a, st), "paged attention's join");

@@ -83,11 +83,12 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers<128>) <= 2048 && sizeof(Barriers<64>) <= 2048, "barriers");
 
-// The next item of the counter, by all lanes of a warp.
-__device__ __forceinline__ int take_next(const SeqAttnArgs& a) {
-  uint32_t v = 0;
-  if ((threadIdx.x & 31) == 0) v = atomicAdd(a.next, 1u);
-  return a.first_next + static_cast<int>(__shfl_sync(0xffffffffu, v, 0));
+// The next item of the counter, by all lanes of a warp: the first lane asks, all have the answer.
+__device__ __forceinline__ uint32_t ask_next(const SeqAttnArgs& a) {
+  return a.next && (threadIdx.x & 31) == 0 ? atomicAdd(a.next, 1u) : 0;
+}
+__device__ __forceinline__ int next_of(const SeqAttnArgs& a, uint32_t ticket) {
+  return a.first_next + static_cast<int>(__shfl_sync(0xffffffffu, ticket, 0));
 }
 
 __device__ __forceinline__ bool to_scrub(const Work& w, int j) { return (w.js + j + 1) * kSeqTile > w.all_see; }
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sb->tmem_slot;
   pdl_wait();
+  if (PAGED && a.few_rows) pdl_trigger();  // paged_few_kernel takes the SMs that run out of items
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
   };
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t it = 0; ok; ++it) {
       Work w;
       w.live = 0;
-      for (; item < items; item = a.next ? take_next(a) : items) {
+      for (; item < items; item = a.next ? next_of(a, ask_next(a)) : items) {
         const int rest = item % per_split;
         TileOrder::Found at;
         if (!order.find(rest / a.hk, at)) continue;
@@ -412,7 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (!w.live) break;
       const int n_kv = max(w.cnt[0], w.cnt[1]);
-      const int next_item = a.next ? take_next(a) : items;  // on its way while the tiles are
       if (n_kv > 0) {
         ok = wait(&sb->q_empty, q_turn ^ 1u);
         if (!ok) break;
@@ -467,7 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K runs ahead of V by a tile: it is free once its scores are formed, V when they have been multiplied
       int page = PAGED && n_kv > 0 ? page_of(0) : 0, next = PAGED && n_kv > 1 ? page_of(1) : 0, st = 0;
       if (n_kv > 0) ok = load_k(0, 0, page);
+      // The next item's number is on its way while the last two tiles are: a CTA that took it with its first ones would keep a
+      // short item waiting behind a long one.
+      uint32_t ticket = 0;
+      if (n_kv == 0) ticket = ask_next(a);
       for (int j = 0; ok && j < n_kv; ++j) {
+        if (j == max(n_kv - 2, 0)) ticket = ask_next(a);
         const int after = st + 1 == kStages ? 0 : st + 1;
         if (j + 1 < n_kv) ok = load_k(j + 1, after, next);
         ok = ok && wait(&sb->v_empty[st], (v_turn >> st & 1u) ^ 1u);
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         page = next, st = after;
         if (PAGED && j + 2 < n_kv) next = page_of(j + 2);
       }
-      item = next_item;
+      item = a.next ? next_of(a, ticket) : items;
     }
     if (!ok) {
       // give the copies already issued a bounded chance to land before the CTA exits

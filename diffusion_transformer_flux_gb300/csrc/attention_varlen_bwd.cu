@@ -193,11 +193,10 @@ __device__ __forceinline__ void cut(float x, uint32_t (&v)[3]) {
   }
 }
 
-// The next item of the counter, by all lanes of a warp.
-__device__ __forceinline__ int take_next(uint32_t* counter, int first_next) {
-  uint32_t v = 0;
-  if ((threadIdx.x & 31) == 0) v = atomicAdd(counter, 1u);
-  return first_next + static_cast<int>(__shfl_sync(0xffffffffu, v, 0));
+// The next item of the counter, by all lanes of a warp: the first lane asks, all have the answer.
+__device__ __forceinline__ uint32_t ask_next(uint32_t* counter) { return (threadIdx.x & 31) == 0 ? atomicAdd(counter, 1u) : 0; }
+__device__ __forceinline__ int next_of(int first_next, uint32_t ticket) {
+  return first_next + static_cast<int>(__shfl_sync(0xffffffffu, ticket, 0));
 }
 
 template <int D, bool KEYS>
@@ -483,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t it = 0; ok; ++it) {
       Work w;
       w.live = 0;
-      for (; item < items; item = items > first_next ? take_next(counter, first_next) : items) {
+      for (; item < items; item = items > first_next ? next_of(first_next, ask_next(counter)) : items) {
         TileOrder::Found at;
         if (!order.find(item / a.hk / (KEYS ? a.parts : 1), at)) continue;
         w.hk = item % a.hk, w.first = at.start, w.part = 0, w.parts = 1;
@@ -515,7 +514,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (!w.live) break;
-      const int next_item = items > first_next ? take_next(counter, first_next) : items;
       if (w.count > 0) {
         const int f_head = KEYS ? w.hk : w.hk * G, f_row = KEYS ? w.seg.k0 + w.first : w.seg.q0 + w.first;
         if constexpr (C::kFInRing) {
@@ -546,7 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
+      // the next item's number is on its way while the last two units are, no sooner: a short item waits behind no long one
+      const bool more = items > first_next;
+      uint32_t ticket = 0;
+      if (more && w.count == 0) ticket = ask_next(counter);
       for (int u = 0; ok && u < w.count; ++u) {
+        if (more && u == max(w.count - 2, 0)) ticket = ask_next(counter);
         if (!take_slot()) break;
         if (lane == 0) {
           const int m_head = KEYS ? w.hk * G : w.hk, row = KEYS ? w.seg.q0 + w.m_first + u * U : w.seg.k0 + u * kUnit;
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         next_slot();
       }
-      item = next_item;
+      item = more ? next_of(first_next, ticket) : items;
     }
     if (!ok) {
       // give the copies already issued a bounded chance to land before the CTA exits

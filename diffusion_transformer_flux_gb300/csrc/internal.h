@@ -475,6 +475,7 @@ struct SeqAttnArgs {
   int table_width, n_pages, page_shift, page_rows, max_keys;  // page_rows: rows of a copied piece, at most 128
   int few_rows;  // sequences of at most that many rows (tokens by the group's heads) are paged_few_kernel's: kFewRows or 0
   int few_ctas, few_whole;   // its CTAs; whether each takes one sequence and key head
+  int few_behind;            // the tile kernel runs before it
   int few_join_rows;         // rows of the sequence with most of them
   int split_keys;            // keys of one item of the tile kernel (0: all)
   // normalised parts and their log2-sums: [splits, tokens_q, hq(, D)] of the tile kernel, [few_ctas, 2, kFewRows(, D)] of

@@ -396,26 +396,11 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
   return true;
 }
 
+// A CTA's share.
 template <int D>
-__global__ void __launch_bounds__(kFewThreads, 2)
-    paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __grid_constant__ SeqAttnArgs a) {
-  extern __shared__ uint8_t few_raw[];
-  __shared__ FewShared sh;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kFewWarps; ++w)
-      for (int s = 0; s < FewCfg<D>::kStages; ++s) mbar_init(&sh.full[w][s], 1);
-    sh.abort_flag = 0;
-    fence_mbar_init();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
+__device__ __forceinline__ void few_share(const SeqAttnArgs& a, const CUtensorMap* tm_k, const CUtensorMap* tm_v, uint8_t* smem,
+                                          FewShared* sh) {
   FewTurns turns = {0};
-  __syncthreads();
-  pdl_wait();
-  pdl_trigger();
-  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
   Segment seg;
   auto segment = [&](int b) {
     clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
@@ -426,9 +411,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     segment(b);
     if (seg.n == 0 || seg.n * a.group > kFewRows) return;
     if (seg.n * a.group <= 8)
-      few_rows<D, 1>(a, &tm_k, &tm_v, smem, &sh, turns, seg, b, hk, 0, seg.m, -1);
+      few_rows<D, 1>(a, tm_k, tm_v, smem, sh, turns, seg, b, hk, 0, seg.m, -1);
     else
-      few_rows<D, 2>(a, &tm_k, &tm_v, smem, &sh, turns, seg, b, hk, 0, seg.m, -1);
+      few_rows<D, 2>(a, tm_k, tm_v, smem, sh, turns, seg, b, hk, 0, seg.m, -1);
     return;
   }
   const int lane = threadIdx.x & 31;
@@ -476,12 +461,37 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const bool whole = first == 0 && last == steps;
     const int64_t part = whole ? -1 : static_cast<int64_t>(few_row(blockIdx.x, at > begin, 0));
     const int k0 = first * kFewStep, k1 = min(seg.m, last * kFewStep);
-    const bool ok = seg.n * a.group <= 8 ? few_rows<D, 1>(a, &tm_k, &tm_v, smem, &sh, turns, seg, b, hk, k0, k1, part)
-                                         : few_rows<D, 2>(a, &tm_k, &tm_v, smem, &sh, turns, seg, b, hk, k0, k1, part);
+    const bool ok = seg.n * a.group <= 8 ? few_rows<D, 1>(a, tm_k, tm_v, smem, sh, turns, seg, b, hk, k0, k1, part)
+                                         : few_rows<D, 2>(a, tm_k, tm_v, smem, sh, turns, seg, b, hk, k0, k1, part);
     if (!ok) return;
     base += steps;
     at = base;
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ SeqAttnArgs a) {
+  extern __shared__ uint8_t few_raw[];
+  __shared__ FewShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kFewWarps; ++w)
+      for (int s = 0; s < FewCfg<D>::kStages; ++s) mbar_init(&sh.full[w][s], 1);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  __syncthreads();
+  // Behind the tile kernel, which waited for what this one reads before it let this one start: the two work beside one another,
+  // and only the end of this one waits for the other's.
+  if (!a.few_behind) pdl_wait();
+  pdl_trigger();
+  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  few_share<D>(a, &tm_k, &tm_v, smem, &sh);
+  if (a.few_behind) pdl_wait();
 }
 
 // out = sum_p 2^(L_p - L) O_p, L = log2 sum_p 2^L_p, of the parts p of a row: parts first, first + step, ... by one warp, a lane D / 32
@@ -588,26 +598,63 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_few_join_kernel(const _
   }
 }
 
-// The rows of the tile kernel whose keys were split: a warp to a token and head.
+// The rows of the tile kernel whose keys were split: a warp to four of them, so that enough reads are on their way (a warp to
+// each: 17 against 12 us for two parts of 32000 rows of 128).
+constexpr int kJoinRows = 4 * kJoinWarps;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ SeqAttnArgs a) {
-  pdl_wait();
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  if (item >= static_cast<int64_t>(a.tokens_q) * a.hq) return;
+  constexpr int kCols = D / 32;  // float4 of a lane
+  const int lane = threadIdx.x & 7;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinRows + (threadIdx.x >> 3);
   const int tok = static_cast<int>(item / a.hq), head = static_cast<int>(item % a.hq);
-  // the last sequence that starts at or before the token: empty ones before it share its start
-  const int b = find_segment(a.batch, tok, [&](int i) { return min(max(a.cu_q[i], 0), a.tokens_q); });
-  Segment seg;
-  clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
-  if (tok < seg.q0 || tok >= seg.q0 + seg.n || seg.n * a.group <= a.few_rows) return;
-  const int m = min(max(a.kv_lens[b], 0), a.max_keys), parts = (m + a.split_keys - 1) / a.split_keys;
+  // the last sequence that starts at or before the token (empty ones before it share its start), by all lanes for each token
+  int b = 0;
+  for (int r = 0, found = -1; r < 32; r += 8) {
+    const int t = __shfl_sync(0xffffffffu, tok, r);
+    if (t == found || t >= a.tokens_q) continue;
+    found = t;
+    const int x = find_segment(a.batch, t, [&](int i) { return min(max(a.cu_q[i], 0), a.tokens_q); });
+    if (tok == t) b = x;
+  }
+  int parts = 0;
+  if (tok < a.tokens_q) {
+    Segment seg;
+    clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
+    if (tok >= seg.q0 && tok < seg.q0 + seg.n && seg.n * a.group > a.few_rows)
+      parts = (min(max(a.kv_lens[b], 0), a.max_keys) + a.split_keys - 1) / a.split_keys;
+  }
+  pdl_wait();  // no thread returns without it (see paged_few_join_kernel)
   if (parts <= 1) return;
   const size_t stride = static_cast<size_t>(a.tokens_q) * a.hq;
-  auto row_of = [&](int p) { return p * stride + item; };
-  const float top = top_of(a.part_lse, threadIdx.x & 31, 32, parts, row_of);
-  float sum = 0.f, v[D / 32] = {};
-  add_parts<D>(a.part, a.part_lse, 0, 1, parts, row_of, top, sum, v);
-  write_joined<D>(a, tok, head, top, sum, v);
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_lse[p * stride + item]);
+  float sum = 0.f;
+  float4 v[kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int p = 0; p < parts; ++p) {
+    const float l = a.part_lse[p * stride + item];
+    const float4* src = reinterpret_cast<const float4*>(a.part + (p * stride + item) * D) + lane;
+    float4 u[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) u[i] = src[8 * i];
+    if (l == -INFINITY) continue;  // no keys: counts for nothing; a NaN reaches the output
+    const float e = fast_exp2(l - top);
+    sum += e;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[i].x += e * u[i].x, v[i].y += e * u[i].y, v[i].z += e * u[i].z, v[i].w += e * u[i].w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.ptr) + static_cast<int64_t>(tok) * a.out.stride_t + head * a.out.stride_h;
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) {
+    const int col = 32 * i + 4 * lane;
+    if (col < a.head_dim)
+      *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_bf16x2(v[i].x * inv, v[i].y * inv), pack_bf16x2(v[i].z * inv, v[i].w * inv));
+  }
+  if (lane == 0 && a.lse) a.lse[item] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int D>
@@ -632,7 +679,7 @@ cudaError_t launch_paged_few(const SeqAttnArgs& a, const SeqAttnMaps& m, cudaStr
 }
 
 cudaError_t launch_paged_join(const SeqAttnArgs& a, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tokens_q) * a.hq + kJoinWarps - 1) / kJoinWarps)), block(kJoinWarps * 32);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tokens_q) * a.hq + kJoinRows - 1) / kJoinRows)), block(kJoinWarps * 32);
   const cudaError_t e = a.head_dim <= 64 ? launch_pdl(paged_join_kernel<64>, grid, block, 0, stream, a)
                                          : launch_pdl(paged_join_kernel<128>, grid, block, 0, stream, a);
   if (e != cudaSuccess) return e;

@@ -3,12 +3,14 @@
 // block_tables: request b goes from before[b] to after[b] tokens, so from ceil(before / page) to ceil(after / page) pages.
 // Pages given back go onto a stack of free pages, then pages wanted come from its top, both in the order of requests and
 // of their pages within a request, so that the result is the same from call to call.  The order is a prefix sum over the
-// requests, taken by one CTA (1024 requests at a time); what each request moves is read and written by its thread, or by
-// its warp where it is more than a few pages.  The new tokens' positions and slots follow from the sums: each token
+// requests, taken by one CTA (1024 requests at a time); what each request moves is read and written by its thread, or where
+// it is more than a few pages by a warp: its own, unless a warp has more than kOwnRequests of them (64 new prompts: 15.2 us, as
+// 32 requests of a warp wait for one another; shared among the 32 warps 8.2; one finished request among 256: 8.1 us by its own
+// warp, 9.7 shared).  The new tokens' positions and slots follow from the sums: each token
 // finds its request by a binary search.  Up to kMapInPlace tokens the same CTA writes them (one launch, the step of
 // answering requests, where latency is all); more of them go to a second kernel over the whole GPU.
 //
-// kv_cache_write: bound by memory, each new key and value read and written once in 16-byte pieces, four in flight a thread.
+// kv_cache_write: bound by memory, each new key and value read and written once in 16-byte pieces, two in flight a thread.
 #include <algorithm>
 
 #include "common.cuh"
@@ -19,7 +21,9 @@ namespace {
 
 constexpr int kTableThreads = 1024;
 constexpr int kMapInPlace = 4096;
+constexpr int kTableWarps = kTableThreads / 32;
 constexpr int kOwnPages = 4;  // a request that moves at most that many pages is its thread's alone
+constexpr int kOwnRequests = 2;  // of others a warp moves as many of its own; where one has more, all warps share all of them
 
 struct Growth {
   int before, after, held, need;  // tokens, pages
@@ -35,50 +39,72 @@ __device__ __forceinline__ Growth growth_of(const BlockTableArgs& a, int b) {
   return g;
 }
 
-// Exclusive prefix sum over the CTA's threads and the total.
-template <typename T>
-__device__ __forceinline__ T scan_threads(T v, T* warp_sums, T& total) {
+// A request's entries [first, last) that change, and their place among the pages that move.
+struct Move {
+  int first, last, place;
+};
+
+// Exclusive prefix sums over the CTA's threads and the totals, of two values at once (so that they share the barriers).
+template <typename T, typename U>
+__device__ __forceinline__ void scan_threads(T& v, U& w, T* v_sums, U* w_sums, T& v_total, U& w_total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T x = v;
+  U y = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const T x1 = __shfl_up_sync(0xffffffffu, x, o);
+    const U y1 = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) x += x1, y += y1;
   }
-  if (lane == 31) warp_sums[warp] = x;
+  if (lane == 31) v_sums[warp] = x, w_sums[warp] = y;
   __syncthreads();
   if (warp == 0) {
-    T w = warp_sums[lane];
+    T p = v_sums[lane];
+    U q = w_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const T y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
+      const T p1 = __shfl_up_sync(0xffffffffu, p, o);
+      const U q1 = __shfl_up_sync(0xffffffffu, q, o);
+      if (lane >= o) p += p1, q += q1;
     }
-    warp_sums[lane] = w;
+    v_sums[lane] = p, w_sums[lane] = q;
   }
   __syncthreads();
-  total = warp_sums[31];
-  const T r = x - v + (warp ? warp_sums[warp - 1] : 0);
+  v_total = v_sums[31], w_total = w_sums[31];
+  v = x - v + (warp ? v_sums[warp - 1] : 0), w = y - w + (warp ? w_sums[warp - 1] : 0);
   __syncthreads();
-  return r;
+}
+template <typename T>
+__device__ __forceinline__ T scan_threads(T v, T* sums, T& total) {
+  __shared__ int none[32];
+  int zero = 0, zeros;
+  scan_threads(v, zero, sums, none, total, zeros);
+  return v;
 }
 
+// Where each request's tokens start, in shared memory as far as they fit: a search has no step that waits for memory (256
+// requests of one token: 8.4 us with the sums and lengths in global memory, 7.7 so).
+constexpr int kMapRequests = 2048;
+struct MapShared {
+  int cu[kMapRequests + 1], before[kMapRequests];
+};
+
 // Positions and slots of tokens first, first + step, ...
-__device__ __forceinline__ void map_tokens(const BlockTableArgs& a, int64_t first, int64_t step) {
-  const int end = a.cu[a.batch];
+__device__ __forceinline__ void map_tokens(const BlockTableArgs& a, const int* cu, const int* before, int64_t first, int64_t step) {
+  const int end = cu[a.batch];
   for (int64_t i = first; i < a.capacity; i += step) {
     int64_t pos = 0, slot = -1;
     if (i < end) {
       int lo = 0, hi = a.batch;  // cu[lo] <= i < cu[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= i)
+        if (cu[mid] <= i)
           lo = mid;
         else
           hi = mid;
       }
       const int most = a.width << a.page_shift;
-      pos = min(max(a.before[lo], 0), most) + (i - a.cu[lo]);
+      pos = min(max(before[lo], 0), most) + (i - cu[lo]);
       const int page = a.tables[static_cast<int64_t>(lo) * a.width + (pos >> a.page_shift)];
       if (page >= 0 && page < a.n_pages)
         slot = (static_cast<int64_t>(page) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
@@ -91,29 +117,62 @@ __device__ __forceinline__ void map_tokens(const BlockTableArgs& a, int64_t firs
 __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __grid_constant__ BlockTableArgs a, int map_here) {
   __shared__ int sums[32];
   __shared__ long long sums64[32];
-  const int lane = threadIdx.x & 31;
+  __shared__ MapShared map;
+  __shared__ Move moves[kTableThreads];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool fits = a.batch <= kMapRequests;
   pdl_wait();
+  pdl_trigger();
   const int n_free = min(max(*a.n_free, 0), a.n_pages);
   // ---------------- pages given back: onto the stack
   int top = n_free;
   for (int b0 = 0; b0 < a.batch; b0 += kTableThreads) {
     const int b = b0 + threadIdx.x;
+    const int here = min(a.batch - b0, kTableThreads);
     const Growth g = growth_of(a, b);
     const int* row = a.tables + static_cast<int64_t>(b) * a.width;
     const int lost = max(g.held - g.need, 0);
-    const unsigned many = __ballot_sync(0xffffffffu, lost > kOwnPages);
     int count = 0;  // entries that are pages: a request that found none free has entries without one
     if (lost <= kOwnPages)
       for (int p = g.need; p < g.held; ++p) count += static_cast<unsigned>(row[p]) < static_cast<unsigned>(a.n_pages);
-    for (unsigned m = many; m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int need = __shfl_sync(0xffffffffu, g.need, src), held = __shfl_sync(0xffffffffu, g.held, src);
-      const int* r = a.tables + static_cast<int64_t>(b - lane + src) * a.width;
+    const unsigned many = __ballot_sync(0xffffffffu, lost > kOwnPages);
+    const bool spread = __syncthreads_or(__popc(many) > kOwnRequests);
+    auto count_pages = [&](int r, int first, int last) {
+      const int* from = a.tables + static_cast<int64_t>(b0 + r) * a.width;
       int c = 0;
-      for (int p = need + lane; p < held; p += 32) c += static_cast<unsigned>(r[p]) < static_cast<unsigned>(a.n_pages);
+      for (int p = first + lane; p < last; p += 32) c += static_cast<unsigned>(from[p]) < static_cast<unsigned>(a.n_pages);
 #pragma unroll
       for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-      if (lane == src) count = c;
+      return c;
+    };
+    auto give_back = [&](int r, int first, int last, int to) {
+      const int* from = a.tables + static_cast<int64_t>(b0 + r) * a.width;
+      for (int p0 = first; p0 < last; p0 += 32) {
+        const int page = p0 + lane < last ? from[p0 + lane] : -1;
+        const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
+        const unsigned mask = __ballot_sync(0xffffffffu, there);
+        const int place = to + __popc(mask & ((1u << lane) - 1));
+        if (there && place < a.n_pages) a.free_pages[place] = page;
+        to += __popc(mask);
+      }
+    };
+    if (spread) {
+      moves[threadIdx.x] = {g.need, g.held, 0};
+      __syncthreads();
+      for (int r = warp; r < here; r += kTableWarps) {
+        const Move m = moves[r];
+        if (m.last - m.first <= kOwnPages) continue;
+        const int c = count_pages(r, m.first, m.last);
+        if (lane == 0) moves[r].place = c;
+      }
+      __syncthreads();
+      if (lost > kOwnPages) count = moves[threadIdx.x].place;
+    } else {
+      for (unsigned m = many; m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        const int c = count_pages(warp * 32 + src, __shfl_sync(0xffffffffu, g.need, src), __shfl_sync(0xffffffffu, g.held, src));
+        if (lane == src) count = c;
+      }
     }
     int total;
     int at = top + scan_threads(count, sums, total);
@@ -123,18 +182,19 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
           if (at < a.n_pages) a.free_pages[at] = row[p];
           ++at;
         }
-    for (unsigned m = many; m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int need = __shfl_sync(0xffffffffu, g.need, src), held = __shfl_sync(0xffffffffu, g.held, src);
-      int to = __shfl_sync(0xffffffffu, at, src);
-      const int* r = a.tables + static_cast<int64_t>(b - lane + src) * a.width;
-      for (int p0 = need; p0 < held; p0 += 32) {
-        const int page = p0 + lane < held ? r[p0 + lane] : -1;
-        const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
-        const unsigned mask = __ballot_sync(0xffffffffu, there);
-        const int place = to + __popc(mask & ((1u << lane) - 1));
-        if (there && place < a.n_pages) a.free_pages[place] = page;
-        to += __popc(mask);
+    if (spread) {
+      if (lost > kOwnPages) moves[threadIdx.x].place = at;
+      __syncthreads();
+      for (int r = warp; r < here; r += kTableWarps) {
+        const Move m = moves[r];
+        if (m.last - m.first > kOwnPages) give_back(r, m.first, m.last, m.place);
+      }
+      __syncthreads();
+    } else {
+      for (unsigned m = many; m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        give_back(warp * 32 + src, __shfl_sync(0xffffffffu, g.need, src), __shfl_sync(0xffffffffu, g.held, src),
+                  __shfl_sync(0xffffffffu, at, src));
       }
     }
     top += total;
@@ -146,11 +206,14 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   long long tokens = 0, left_out = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kTableThreads) {
     const int b = b0 + threadIdx.x;
+    const int here = min(a.batch - b0, kTableThreads);
     const Growth g = growth_of(a, b);
-    const int gained = max(g.need - g.held, 0);
-    int total;
-    const int rank = taken + scan_threads(gained, sums, total);
-    taken += total;
+    const int gained = max(g.need - g.held, 0), fresh = max(g.after - g.before, 0);
+    int rank = gained, total;
+    long long first = fresh, sum;
+    scan_threads(rank, first, sums, sums64, total, sum);
+    rank += taken, first += tokens;
+    taken += total, tokens += sum;
     if (gained <= kOwnPages) {
       int* row = a.tables + static_cast<int64_t>(b) * a.width;
       for (int p = g.held; p < g.need; ++p) {
@@ -158,48 +221,70 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
         row[p] = from >= 0 ? a.free_pages[from] : -1;
       }
     }
-    for (unsigned m = __ballot_sync(0xffffffffu, gained > kOwnPages); m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int need = __shfl_sync(0xffffffffu, g.need, src), held = __shfl_sync(0xffffffffu, g.held, src);
-      const int r0 = __shfl_sync(0xffffffffu, rank, src);
-      int* row = a.tables + static_cast<int64_t>(b - lane + src) * a.width;
-      for (int p = held + lane; p < need; p += 32) {
-        const int from = top - 1 - (r0 + p - held);
-        row[p] = from >= 0 ? a.free_pages[from] : -1;
+    const unsigned many = __ballot_sync(0xffffffffu, gained > kOwnPages);
+    auto hand_out = [&](int r, int first, int last, int place) {
+      int* to = a.tables + static_cast<int64_t>(b0 + r) * a.width;
+      for (int p = first + lane; p < last; p += 32) {
+        const int from = top - 1 - (place + p - first);
+        to[p] = from >= 0 ? a.free_pages[from] : -1;
+      }
+    };
+    if (__syncthreads_or(__popc(many) > kOwnRequests)) {
+      moves[threadIdx.x] = {g.held, g.need, rank};
+      __syncthreads();
+      for (int r = warp; r < here; r += kTableWarps) {
+        const Move m = moves[r];
+        if (m.last - m.first > kOwnPages) hand_out(r, m.first, m.last, m.place);
+      }
+      __syncthreads();
+    } else {
+      for (unsigned m = many; m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        hand_out(warp * 32 + src, __shfl_sync(0xffffffffu, g.held, src), __shfl_sync(0xffffffffu, g.need, src),
+                 __shfl_sync(0xffffffffu, rank, src));
       }
     }
-    const int fresh = max(g.after - g.before, 0);
-    long long sum;
-    const long long first = tokens + scan_threads(static_cast<long long>(fresh), sums64, sum);
-    tokens += sum;
     if (b < a.batch) {
-      a.cu[b] = static_cast<int>(min(first, static_cast<long long>(a.capacity)));
+      const int start = static_cast<int>(min(first, static_cast<long long>(a.capacity)));
+      a.cu[b] = start;
+      if (fits) map.cu[b] = start, map.before[b] = g.before;
       const long long asked = max(static_cast<long long>(a.after[b]) - max(a.before[b], 0), 0ll);
       left_out += max(asked - fresh, 0ll);
     }
   }
-  {
+  if (__syncthreads_or(left_out != 0)) {
     long long sum;
     scan_threads(left_out, sums64, sum);
-    left_out = sum + max(tokens - a.capacity, 0ll);
+    left_out = sum;
   }
+  left_out += max(tokens - a.capacity, 0ll);
   if (threadIdx.x == 0) {
-    a.cu[a.batch] = static_cast<int>(min(tokens, static_cast<long long>(a.capacity)));
+    const int end = static_cast<int>(min(tokens, static_cast<long long>(a.capacity)));
+    a.cu[a.batch] = end;
+    if (fits) map.cu[a.batch] = end;
     *a.n_free_out = max(top - taken, 0);
     a.missing[0] = max(taken - top, 0);
     a.missing[1] = static_cast<int>(min(left_out, static_cast<long long>(INT32_MAX)));
   }
   __syncthreads();
-  if (map_here) map_tokens(a, threadIdx.x, kTableThreads);
+  if (map_here) map_tokens(a, fits ? map.cu : a.cu, fits ? map.before : a.before, threadIdx.x, kTableThreads);
 }
 
 __global__ void __launch_bounds__(256) token_map_kernel(const __grid_constant__ BlockTableArgs a) {
+  __shared__ MapShared map;
+  const bool fits = a.batch <= kMapRequests;
   pdl_wait();
-  map_tokens(a, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, static_cast<int64_t>(gridDim.x) * 256);
+  if (fits) {
+    for (int i = threadIdx.x; i <= a.batch; i += 256) map.cu[i] = a.cu[i];
+    for (int i = threadIdx.x; i < a.batch; i += 256) map.before[i] = a.before[i];
+    __syncthreads();
+  }
+  map_tokens(a, fits ? map.cu : a.cu, fits ? map.before : a.before, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x,
+             static_cast<int64_t>(gridDim.x) * 256);
 }
 
 constexpr int kWriteThreads = 256;
-constexpr int kWriteItems = 4;  // 16-byte pieces of a thread in flight
+constexpr int kWriteItems = 2;  // 16-byte pieces of a thread in flight (32 tokens: 2.3 us, with 4 2.9, with 8 4.7; 9216: 15.4, 15.7, 19)
 
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_constant__ CacheWriteArgs a, int tokens_per_cta) {
   pdl_wait();

@@ -2904,7 +2904,7 @@ mmdit_status check_attention(const char* what, int32_t batch, int32_t tokens_q, 
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: at most 2^30 tokens and 2^20 sequences", what);
   // the CTAs: one for two tiles of 128 / group tokens and each key head
   const int64_t pairs = tokens_q / (2 * (128 / (heads_q / heads_k))) + static_cast<int64_t>(batch);
-  if (pairs * heads_k > INT32_MAX) return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
+  if (pairs * heads_k > INT32_MAX / 2) return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
   return MMDIT_OK;
 }
 
@@ -3141,7 +3141,9 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
   const PagedPlan p = plan_paged(std::max(tokens_q, 1), std::max(batch, 1), heads_q, heads_k, head_dim, max_q, most);
   if (p.few && ((p.few_whole && static_cast<int64_t>(batch) * heads_k > INT32_MAX / 2) ||
                 batch * ((most + kFewStep - 1LL) / kFewStep + 1) > INT32_MAX))
-    return fail(MMDIT_ERR_UNSUPPORTED, "%s: batch max_kv / %d must be below 2^31", what, kFewStep);
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: batch (max_kv / %d + 2) must be below 2^31", what, kFewStep);
+  if ((tokens_q / (2 * (128 / (heads_q / heads_k))) + static_cast<int64_t>(batch)) * heads_k * p.splits > INT32_MAX / 2)
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
   if ((s = check_workspace(workspace, workspace_bytes, batch == 0 || tokens_q == 0 ? kStatusBytes : p.total)) != MMDIT_OK) return s;
   if (batch == 0 || tokens_q == 0 || max_q == 0) return MMDIT_OK;
   if ((s = check_heads(what, "q", q, tokens_q, heads_q, head_dim, false)) != MMDIT_OK) return s;
@@ -3201,6 +3203,13 @@ mmdit_status mmdit_block_tables(int32_t batch, int32_t page_size, int32_t table_
     if (!aligned4(ptr)) return fail(MMDIT_ERR_INVALID_ARG, "%s: an argument is not 4-byte aligned", what);
   if ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0 || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
     return fail(MMDIT_ERR_INVALID_ARG, "%s: positions or slots is not 8-byte aligned", what);
+  const void* written[] = {tables, free_pages, n_free_out, cu, positions, slots, missing};
+  for (const void* x : written)
+    for (const void* y : {static_cast<const void*>(before), static_cast<const void*>(after), x == n_free_out ? nullptr : static_cast<const void*>(n_free)})
+      if (x && x == y) return fail(MMDIT_ERR_INVALID_ARG, "%s: an output must not be an input", what);
+  for (size_t i = 0; i < std::size(written); ++i)
+    for (size_t j = 0; j < i; ++j)
+      if (written[i] && written[i] == written[j]) return fail(MMDIT_ERR_INVALID_ARG, "%s: an output must not be another", what);
   BlockTableArgs a = {};
   a.batch = batch, a.width = table_width, a.n_pages = n_pages, a.page_shift = log2_of(page_size), a.capacity = capacity;
   a.before = before, a.after = after, a.tables = tables, a.free_pages = free_pages, a.n_free = n_free, a.n_free_out = n_free_out;

@@ -50,20 +50,29 @@ __device__ __forceinline__ int keys_seen(const Segment& s, int i, int causal) {
 //   Up to 32 sequences: a lane holds one each, sorted by the other side's length.  Where a tile's cost falls with its number
 //   (causal) the tiles of all sequences come level by level, else sequence by sequence; number x is found by counting.
 //   More: sequence b's tiles are number cu[b] / span + b and the following, which leaves each at least as many numbers as
-//   it needs without a prefix sum; those left over are of no tile, and the sequences come in their order.
+//   it needs without a prefix sum; those left over are of no tile, and the sequences come in their order.  Where sequences of
+//   up to `skip` rows have no tiles (they are another kernel's, and most of a batch) nearly all numbers would be of no
+//   tile: there the tiles are counted, 32 sequences at a time, on from where the last search ended.
 // `from_end`: a sequence's last tile is its dearest.
 struct TileOrder {
   const int *cu, *other;
-  int total, other_total, batch, span, causal, from_end;
+  int total, other_total, batch, span, causal, from_end, skip;
   int n;                                                // numbers
   int seq, first, count, other_first, other_count;      // this lane's sequence
   int tiles;
   int level, base;                                      // where the last search ended
 
   __device__ __forceinline__ void init(const int* cu_, int total_, const int* other_, int other_total_, int batch_, int span_,
-                                       int causal_, int from_end_) {
+                                       int causal_, int from_end_, int skip_ = 0) {
     cu = cu_, total = total_, other = other_, other_total = other_total_, batch = batch_, span = span_;
-    causal = causal_, from_end = from_end_, level = 0, base = 0;
+    causal = causal_, from_end = from_end_, skip = skip_, level = 0, base = 0;
+    if (batch > 32 && skip > 0) {
+      n = 0;
+      for (int b = 0; b < batch; b += 32) n += tiles_of(b + (threadIdx.x & 31));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      return;
+    }
     if (batch > 32) {
       n = total / span + batch;
       return;
@@ -84,10 +93,17 @@ struct TileOrder {
     seq = __shfl_sync(0xffffffffu, seq, from), first = __shfl_sync(0xffffffffu, first, from);
     count = __shfl_sync(0xffffffffu, count, from), other_first = __shfl_sync(0xffffffffu, other_first, from);
     other_count = __shfl_sync(0xffffffffu, other_count, from);
-    tiles = lane < batch ? (count + span - 1) / span : 0;
+    tiles = lane < batch && count > skip ? (count + span - 1) / span : 0;
     n = tiles;
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+
+  __device__ __forceinline__ int tiles_of(int b) const {
+    if (b >= batch) return 0;
+    int f, c;
+    clip_segment(cu, b, total, f, c);
+    return c > skip ? (c + span - 1) / span : 0;
   }
 
   struct Found {
@@ -97,6 +113,31 @@ struct TileOrder {
   // Number x < n; false where it is of no tile.
   __device__ __forceinline__ bool find(int x, Found& f) {
     int tile;
+    if (batch > 32 && skip > 0) {  // level: the first of 32 sequences, base: the tiles before it
+      if (x < base) level = 0, base = 0;
+      for (; level < batch; level += 32) {
+        const int mine = tiles_of(level + (threadIdx.x & 31));
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, sum, o);
+          if ((threadIdx.x & 31) >= o) sum += y;
+        }
+        const unsigned after = __ballot_sync(0xffffffffu, base + sum > x);
+        if (after) {
+          const int lane = __ffs(after) - 1;
+          f.b = level + lane;
+          tile = x - base - __shfl_sync(0xffffffffu, sum - mine, lane);
+          if (from_end) tile = __shfl_sync(0xffffffffu, mine, lane) - 1 - tile;
+          clip_segment(cu, f.b, total, f.first, f.count);
+          f.other_first = f.other_count = 0;
+          f.start = tile * span;
+          return true;
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+      }
+      return false;
+    }
     if (batch > 32) {
       const int y = from_end ? n - 1 - x : x;
       f.b = find_segment(batch, y, [&](int i) { return min(max(cu[i], 0), total) / span + i; });

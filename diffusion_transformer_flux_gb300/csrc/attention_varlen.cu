@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.clear && blockIdx.x == 0 && lane == 0) *a.status = 0;
     const int pieces = PAGED ? kSeqTile / a.page_rows : 1;
     TileOrder order;
-    order.init(a.cu_q, a.tokens_q, PAGED ? nullptr : a.cu_k, a.tokens_k, a.batch, 2 * a.tile_tokens, a.causal, 1);
+    order.init(a.cu_q, a.tokens_q, PAGED ? nullptr : a.cu_k, a.tokens_k, a.batch, 2 * a.tile_tokens, a.causal, 1,
+               PAGED ? a.few_rows / a.group : 0);
     const int per_split = order.n * a.hk, items = per_split * a.splits;
     uint32_t q_turn = 0, k_turn = 0, v_turn = 0;  // the next phases' parities; k, v: a bit for each stage
     uint32_t k_used = 0, v_used = 0;
@@ -382,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         int split_tiles = INT32_MAX;
         w.n_splits = 1, w.js = 0;
         if constexpr (PAGED) {
-          if (w.seg.n * a.group <= a.few_rows) continue;  // another kernel's
           w.seg.k0 = 0, w.seg.m = min(max(a.kv_lens[w.b], 0), a.max_keys);
           if (a.split_keys > 0) {
             split_tiles = a.split_keys / kSeqTile;
@@ -671,7 +671,6 @@ cudaError_t launch_seq_attention(SeqAttnArgs a, const SeqAttnMaps& m, int paged,
   a.tile_tokens = seq_tile_tokens(a.group);
   const int64_t pairs = a.tokens_q / (2 * a.tile_tokens) + static_cast<int64_t>(a.batch);
   const int64_t items = pairs * a.hk * splits;
-  if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
   a.splits = splits;
   const int grid = static_cast<int>(std::min<int64_t>(items, num_sms()));
   cudaError_t e;

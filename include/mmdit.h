@@ -869,9 +869,8 @@ mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t
  *   dq_i = scale sum_j dz_ij k_j,   dk_j = scale sum_i dz_ij q_i,   dv_j = sum_i p_ij dout_i,
  * dk and dv summed over the query heads of their group.  All rows of the sequences are written, rows of none left as they
  * were.  Sums in float32 in a fixed order: the same bits from call to call.  p and dz enter the products rounded to bf16.  A
- * query row whose q or dout is not finite, within 64 rows (tokens by the group's heads) of one that sees fewer keys, makes
- * the gradients of the keys it sees NaN; a key row likewise those of the queries that see it.  heads_q at most 64 times
- * heads_k.
+ * query row whose q, dout or out is not finite can make the gradients of the keys it sees NaN, a key row whose k or v is not
+ * those of the queries that see it; what a row does not see never reaches it.  heads_q at most 64 times heads_k.
  * workspace >= mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) (row sums and partial sums: calls that
  * share one are ordered on one stream). */
 size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim);
@@ -891,7 +890,7 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
  * The queries are the last tokens of their sequences (a chunk of a prompt, or one token each), so the mask is causal.
  * max_q: no sequence has more queries (one that has is not computed where max_q heads_q / heads_k <= 16); max_kv: no
  * sequence has more keys (0: table_width page_size; more keys than that are not seen).  They and the shapes alone decide how the
- * work is split; the device's lengths may change between launches of a captured graph.
+ * work is split; the device's lengths may change between launches of a captured graph.  batch (max_kv / 64 + 2) below 2^31.
  * out [tokens_q, heads_q, head_dim]; lse NULL or [tokens_q, heads_q] fp32.  The same bits from call to call.
  * workspace >= mmdit_paged_attention_workspace_size(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv), with
  * max_kv as the call takes it (parts of split sequences: calls that share one are ordered on one stream). */
@@ -919,7 +918,8 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
  *   request and page page_size + slot (-1 without a page); entries behind the last new token are 0 and -1;
  *   missing [2] int32: pages wanted that were not free, and new tokens left out (beyond capacity or the tables' width).
  * All of them on the device.  Called again with the same before, after and n_free (and n_free_out elsewhere) it gives the
- * same result.  batch table_width and batch at most 2^30, table_width page_size at most 2^30.  No workspace. */
+ * same result.  No array is another (but n_free_out n_free).  batch table_width and table_width page_size at most 2^30.  No
+ * workspace. */
 mmdit_status mmdit_block_tables(int32_t batch, int32_t page_size, int32_t table_width, int32_t n_pages,
                                 const int32_t *before, const int32_t *after, int32_t *tables, int32_t *free_pages,
                                 const int32_t *n_free, int32_t *n_free_out, int32_t *cu, int32_t capacity,

@@ -24,10 +24,11 @@
 //                rescaled in TMEM) when a row's maximum grows by more than 2^8.
 // TMEM columns: S/P of A [0,128), S/P of B [128,256), O of A [256,256+D), O of B [384,384+D).
 // V is read as it lies ([key][d], MN-major), K and Q K-major.  Heads of up to 64 run with D = 64, up to 128 with D = 128;
-// columns behind head_dim are zeros that the TMA fills in.
+// columns behind head_dim are zeros that the TMA fills in.  The products of heads of up to 96 leave out the last 32 (KD: 23
+// sequences of 25 heads of 96, 305 us with all 128 columns, 283 so).
 //
 // Over a paged cache the keys of an item may be split over several (few rows, long contexts); each then writes
-// its part normalised in float32 with its log-sum, and paged_combine_kernel joins them.
+// its part normalised in float32 with its log-sum, and paged_join_kernel joins them.
 #include <algorithm>
 
 #include "attention_tiles.cuh"
@@ -47,7 +48,6 @@ struct Cfg {
   static constexpr int kBar = kPieces + 8 * 32 * 128;
   static constexpr int kSmem = kBar + 2048 + 1024;
   static constexpr uint32_t kIdescS = make_idesc<kKindF16>(128, 128);
-  static constexpr uint32_t kIdescPV = make_idesc<kKindF16>(128, D) | kIdescBMnMajor;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -93,7 +93,7 @@ __device__ __forceinline__ int next_of(const SeqAttnArgs& a, uint32_t ticket) {
 
 __device__ __forceinline__ bool to_scrub(const Work& w, int j) { return (w.js + j + 1) * kSeqTile > w.all_see; }
 
-template <int D, bool PAGED>
+template <int D, int KD, bool PAGED>
 __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tmem, const SeqAttnArgs& a, uint8_t* pieces) {
   constexpr int kStages = Cfg<D>::kStages;
   volatile int* abort_flag = &sb->abort_flag;
@@ -204,7 +204,7 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
       // O holds sum_{t<j} P_t V_t (PV(j-1) was issued before S(j), whose completion we saw)
       if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-        for (int e = 0; e < D / 16; ++e) {
+        for (int e = 0; e < KD / 16; ++e) {
           uint32_t r[16];
           tmem_ld16_wait(o_cols + e * 16, r);
 #pragma unroll
@@ -303,12 +303,13 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
   }
 }
 
-template <int D, bool PAGED>
+template <int D, int KD, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     seq_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ SeqAttnArgs a) {
   using C = Cfg<D>;
   constexpr int kStages = C::kStages;
+  constexpr uint32_t kIdescPV = make_idesc<kKindF16>(128, KD) | kIdescBMnMajor;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Barriers<D>* sb = reinterpret_cast<Barriers<D>*>(smem + C::kBar);
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 4) {
     more_registers<kSoftmaxRegisters>();
-    softmax_role<D, PAGED>(sb, (warp - 4) >> 2, tmem, a, smem + C::kPieces + (warp - 4) * 32 * 128);
+    softmax_role<D, KD, PAGED>(sb, (warp - 4) >> 2, tmem, a, smem + C::kPieces + (warp - 4) * 32 * 128);
   } else if (fewer_registers<kServiceRegisters>(), warp == 0) {
     // ---------------- items and TMA
     if (lane == 0) tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kStep = static_cast<uint32_t>(C::kTileBytes) >> 4;
     auto mma_s = [&](int x, int st) {  // S_x = Q_x K^T into columns [128x, 128x + 128)
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
+      for (int k = 0; k < KD / 16; ++k)
         tc_mma<kKindF16>(tmem + x * 128, desc(k_base, q_lo + x * kStep + koff(k)), desc(k_base, k_lo + st * kStep + koff(k)),
                          C::kIdescS, k > 0 ? 1u : 0u);
       tc_commit(&sb->s_full[x]);
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 4 * half; k < 4 * half + 4; ++k)  // 16 keys in 8 columns of P
         tc_mma_ts_f16(tmem + 256u + x * 128, tmem + x * 128 + k * 8, desc(v_base, v_lo + st * kStep + ((k * 2048) >> 4)),
-                      C::kIdescPV, k > 0 ? 1u : more);
+                      kIdescPV, k > 0 ? 1u : more);
     };
     uint32_t q_turn = 0, k_turn = 0, v_turn = 0, clean_turn = 0, p_turn = 0;  // parities; p: a bit for each tile
     bool ok = true;
@@ -637,12 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool PAGED>
+template <int D, int KD, bool PAGED>
 cudaError_t launch_dim(const SeqAttnArgs& a, const SeqAttnMaps& m, int grid, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(seq_attention_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(seq_attention_kernel<D, KD, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(seq_attention_kernel<D, PAGED>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, stream, m.q, m.k, m.v, a);
+  return launch_pdl(seq_attention_kernel<D, KD, PAGED>, dim3(grid), dim3(kThreads), Cfg<D>::kSmem, stream, m.q, m.k, m.v, a);
 }
 
 }  // namespace
@@ -680,9 +681,11 @@ cudaError_t launch_seq_attention(SeqAttnArgs a, const SeqAttnMaps& m, int paged,
     a.next = counter, a.first_next = grid;
   }
   if (a.head_dim <= 64)
-    e = paged ? launch_dim<64, true>(a, m, grid, stream) : launch_dim<64, false>(a, m, grid, stream);
+    e = paged ? launch_dim<64, 64, true>(a, m, grid, stream) : launch_dim<64, 64, false>(a, m, grid, stream);
+  else if (a.head_dim <= 96)
+    e = paged ? launch_dim<128, 96, true>(a, m, grid, stream) : launch_dim<128, 96, false>(a, m, grid, stream);
   else
-    e = paged ? launch_dim<128, true>(a, m, grid, stream) : launch_dim<128, false>(a, m, grid, stream);
+    e = paged ? launch_dim<128, 128, true>(a, m, grid, stream) : launch_dim<128, 128, false>(a, m, grid, stream);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();

@@ -13,6 +13,11 @@
     python -m diffusion_transformer_flux_gb300.profile_case block_linear_bwd --m 4095 --n 4096 --k 4096
     python -m diffusion_transformer_flux_gb300.profile_case add_rmsnorm --m 4608 --k 4096
     python -m diffusion_transformer_flux_gb300.profile_case rope --batch 2 --seq 4608
+    python -m diffusion_transformer_flux_gb300.profile_case varlen_attention --batch 2 --seq 4608 --head-dim 128
+    python -m diffusion_transformer_flux_gb300.profile_case varlen_attention_bwd --batch 2 --seq 2304 --head-dim 128
+    python -m diffusion_transformer_flux_gb300.profile_case paged_attention --batch 16 --seq 4096 --new 1
+    python -m diffusion_transformer_flux_gb300.profile_case block_tables --batch 64 --new 2000
+    python -m diffusion_transformer_flux_gb300.profile_case kv_cache_write --seq 9216
 
 Inputs are drawn on the device (N(0,1) activations, N(0,0.02) weights); the case runs
 --iters times and exits 0 only if every kernel finished its waits.
@@ -42,7 +47,8 @@ def main():
     ap.add_argument("case", choices=["attention", "double_block", "single_block", "linear", "double_block_bwd",
                                      "fp8_attention", "head_loss", "modulation", "blockwise_linear",
                                      "mxfp8_linear", "block_linear", "block_linear_bwd", "block_cast", "add_rmsnorm",
-                                     "add_rmsnorm_bwd", "rope"])
+                                     "add_rmsnorm_bwd", "rope", "varlen_attention", "varlen_attention_bwd", "paged_attention",
+                                     "block_tables", "kv_cache_write"])
     ap.add_argument("--jobs", type=int, default=4)
     ap.add_argument("--batch", type=int, default=1)
     ap.add_argument("--seq", type=int, default=4608)
@@ -54,6 +60,8 @@ def main():
     ap.add_argument("--n", type=int, default=12288)
     ap.add_argument("--k", type=int, default=3072)
     ap.add_argument("--iters", type=int, default=3)
+    ap.add_argument("--head-dim", type=int, default=128)
+    ap.add_argument("--new", type=int, default=1)
     a = ap.parse_args()
     torch.manual_seed(0)
     L.load()
@@ -132,6 +140,39 @@ def main():
         qo, ko = torch.empty_like(q), torch.empty_like(k)
         cfg, pos = L.make_rope_cfg(128, scaling="linear", factor=4.0), torch.arange(a.seq, device="cuda")
         run = lambda: L.mmdit_rope_fwd(cfg, q, qo, k=k, k_out=ko, positions=pos)
+    elif a.case in ("varlen_attention", "varlen_attention_bwd"):  # 32 query and 8 key heads, causal
+        T, d = a.batch * a.seq, a.head_dim
+        q, k, v = _w(T, 32, d, std=1.0), _w(T, 8, d, std=1.0), _w(T, 8, d, std=1.0)
+        cu = torch.arange(0, T + 1, a.seq, device="cuda", dtype=torch.int32)
+        out, lse = torch.empty_like(q), torch.empty(T, 32, device="cuda")
+        fwd = lambda: wss.append(L.mmdit_varlen_attention_fwd(q, k, v, out, cu, lse=lse))
+        fwd()
+        dout, grads = _w(T, 32, d, std=1.0), [torch.empty_like(t) for t in (q, k, v)]
+        run = fwd if a.case == "varlen_attention" else lambda: wss.append(
+            L.mmdit_varlen_attention_bwd(dout, q, k, v, out, lse, *grads, cu))
+    elif a.case == "paged_attention":  # requests of a.seq tokens, the last a.new of them new
+        d, page = a.head_dim, 16
+        width = (a.seq + page - 1) // page
+        kc, vc = (_w(a.batch * width, page, 8, d, std=1.0) for _ in range(2))
+        tables = torch.randperm(a.batch * width, device="cuda").to(torch.int32).view(a.batch, width)
+        lens = torch.full((a.batch,), a.seq, device="cuda", dtype=torch.int32)
+        cu = torch.arange(0, a.batch * a.new + 1, a.new, device="cuda", dtype=torch.int32)
+        q = _w(a.batch * a.new, 32, d, std=1.0)
+        out = torch.empty_like(q)
+        run = lambda: wss.append(L.mmdit_paged_attention_fwd(q, kc, vc, out, tables, lens, cu, max_q=a.new))
+    elif a.case == "block_tables":  # requests of a.new tokens each
+        page, width = 64, (a.new + 63) // 64
+        i32 = lambda *s, fill=0: torch.full(s, fill, device="cuda", dtype=torch.int32)
+        before, after, tables = i32(a.batch), i32(a.batch, fill=a.new), i32(a.batch, width, fill=-1)
+        free, n = torch.arange(a.batch * width, device="cuda", dtype=torch.int32), i32(1, fill=a.batch * width)
+        pos, slots = (torch.empty(a.batch * a.new, device="cuda", dtype=torch.int64) for _ in range(2))
+        out = i32(1), i32(a.batch + 1)
+        run = lambda: L.mmdit_block_tables(before, after, tables, free, n, page, *out, pos, slots, i32(2))
+    elif a.case == "kv_cache_write":
+        k, v = (_w(a.seq, 8, a.head_dim, std=1.0) for _ in range(2))
+        kc, vc = (_w((a.seq + 63) // 64, 64, 8, a.head_dim) for _ in range(2))
+        slots = torch.arange(a.seq, device="cuda")
+        run = lambda: L.mmdit_kv_cache_write(k, v, kc, vc, slots)
     else:
         B, Si, St, D, F = a.batch, a.seq_img, a.seq_txt, a.hidden, a.mlp
         S = Si + St

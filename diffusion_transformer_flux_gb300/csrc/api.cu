@@ -2982,8 +2982,8 @@ PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, 
   Carver c;
   if (p.few) {
     const int64_t steps = (max_kv + kFewStep - 1) / kFewStep, all = batch * heads_k;
-    p.few_whole = steps <= kFewLeast;
-    const int64_t runs = std::min(std::max<int64_t>(2 * sms / heads_k, 1), (batch * steps + kFewLeast - 1) / kFewLeast);
+    p.few_whole = steps <= kFewWhole;
+    const int64_t runs = std::min(std::max<int64_t>(2 * sms / heads_k, 1), (batch * (steps + kFewStart) + kFewLeast - 1) / kFewLeast);
     p.few_ctas = static_cast<int>(p.few_whole ? all : runs * heads_k);
     p.few_join_rows = static_cast<int>(std::min<int64_t>(max_q * group, kFewRows / group * group));
     if (!p.few_whole) {
@@ -3140,8 +3140,8 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
   const int most = static_cast<int>(max_kv > 0 ? std::min<int64_t>(max_kv, reach) : reach);
   const PagedPlan p = plan_paged(std::max(tokens_q, 1), std::max(batch, 1), heads_q, heads_k, head_dim, max_q, most);
   if (p.few && ((p.few_whole && static_cast<int64_t>(batch) * heads_k > INT32_MAX / 2) ||
-                batch * ((most + kFewStep - 1LL) / kFewStep + 1) > INT32_MAX))
-    return fail(MMDIT_ERR_UNSUPPORTED, "%s: batch (max_kv / %d + 2) must be below 2^31", what, kFewStep);
+                batch * ((most + kFewStep - 1LL) / kFewStep + 1 + kFewStart) > INT32_MAX))
+    return fail(MMDIT_ERR_UNSUPPORTED, "%s: batch (max_kv / %d + 5) must be below 2^31", what, kFewStep);
   if ((tokens_q / (2 * (128 / (heads_q / heads_k))) + static_cast<int64_t>(batch)) * heads_k * p.splits > INT32_MAX / 2)
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
   if ((s = check_workspace(workspace, workspace_bytes, batch == 0 || tokens_q == 0 ? kStatusBytes : p.total)) != MMDIT_OK) return s;

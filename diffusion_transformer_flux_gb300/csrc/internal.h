@@ -490,7 +490,8 @@ struct SeqAttnArgs {
   int first_next;
 };
 constexpr int kFewRows = 16;
-constexpr int kFewStep = 64, kFewLeast = 8;  // keys of a step of paged_few_kernel, the least steps of a CTA that leaves a part
+// paged_few_kernel: keys of a step, the least steps of a run, what a sequence's start counts, the steps that one CTA takes alone
+constexpr int kFewStep = 64, kFewLeast = 4, kFewStart = 3, kFewWhole = 8;
 struct SeqAttnMaps {
   CUtensorMap q, k, v;
   CUtensorMap few_k, few_v;  // paged_few_kernel's boxes: up to 16 rows

@@ -4,11 +4,12 @@
 // The arithmetic is attention_varlen.cu's; here a sequence has at most 16 rows (new tokens by the heads of a group), so
 // the cost is reading its keys and values once.  The keys of all sequences lie behind one another as steps of 64 keys, and a
 // CTA takes an equal run of them (at least kFewLeast, so that its part is worth its join) for one key head: whatever the
-// lengths, the CTAs that the GPU holds at once end together.  The key heads' CTAs of a run are neighbours, as the key heads'
+// lengths, the CTAs that the GPU holds at once end together.  A sequence's start counts as kFewStart steps (without that, one
+// CTA worked through 8 sequences of 20 keys: 29 us).  The key heads' CTAs of a run are neighbours, as the key heads'
 // keys are in memory (each head's runs behind the last head's: 111 against 96 us for one token over 120000).  A run covers the
 // end of one sequence's steps, whole ones, and the start of another's; whole ones are written at once, the others leave
 // normalised float32 parts and their log2-sums (at most two to a CTA), which paged_few_join_kernel adds in a fixed order.
-// Where no sequence has more than kFewLeast steps a CTA takes one sequence and key head, and nothing is joined.
+// Where no sequence has more than kFewWhole steps a CTA takes one sequence and key head, and nothing is joined.
 //
 // In a step each of the four warps takes 16 keys: its own ring of TMA copies (a lane for each box: a page's rows by 64
 // columns), its own running maximum and its own float32 output, so no warp waits for another before the end.  The products
@@ -24,7 +25,7 @@
 // short, its rare parts out of the loop.  Pages are read once and make room first in L2, so that these stay in it (4 x 8 tokens:
 // 39 -> 34 us).  Two stages of a warp (128 KB on the way on an SM) read faster than three: 180 against 188 us for the batch.
 // One token over 120000 (492 MB): 75 us, 6.56 TB/s; 32 tokens over up to 16384 (1.25 GB): 180 us, 6.88 TB/s; 4 tokens over up
-// to 8192 of 8 sequences (160 MB): 34 us.
+// to 8192 of 8 sequences (160 MB): 32 us.
 #include <algorithm>
 
 #include "attention_tiles.cuh"
@@ -88,17 +89,19 @@ __device__ __forceinline__ uint32_t few_at(int r, int c) {
   return static_cast<uint32_t>((c >> 3) * FewCfg<D>::kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// The steps of a sequence of few rows for one key head.
+// The steps of a sequence of few rows for one key head, and their number in the runs: its start counts as kFewStart more, which
+// lie before them.
 __device__ __forceinline__ int steps_of(const SeqAttnArgs& a, int b) {
   const int lo = min(max(a.cu_q[b], 0), a.tokens_q), hi = min(max(a.cu_q[b + 1], 0), a.tokens_q);
   const int m = min(max(a.kv_lens[b], 0), a.max_keys);  // read beside the others, not behind their test
   const int rows = (hi - lo) * a.group;
   return rows <= 0 || rows > kFewRows ? 0 : max((m + kFewStep - 1) / kFewStep, 1);
 }
+__device__ __forceinline__ int counted(int steps) { return steps > 0 ? steps + kFewStart : 0; }
 // Their number up to sequence `until` (all: batch), by all lanes of a warp.
 __device__ __forceinline__ int steps_before(const SeqAttnArgs& a, int until) {
   int sum = 0;
-  for (int b = threadIdx.x & 31; b < until; b += 32) sum += steps_of(a, b);
+  for (int b = threadIdx.x & 31; b < until; b += 32) sum += counted(steps_of(a, b));
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
@@ -421,7 +424,7 @@ __device__ __forceinline__ void few_share(const SeqAttnArgs& a, const CUtensorMa
   // are not all
   int total = 0, mine = 0, sum = 0;
   for (int b = 0; b < a.batch; b += 32) {
-    mine = sum = b + lane < a.batch ? steps_of(a, b + lane) : 0;
+    mine = sum = b + lane < a.batch ? counted(steps_of(a, b + lane)) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, sum, o);
@@ -436,7 +439,7 @@ __device__ __forceinline__ void few_share(const SeqAttnArgs& a, const CUtensorMa
   int base = 0, b0 = 0;
   for (; b0 < a.batch; b0 += 32) {
     if (a.batch > 32) {
-      mine = sum = b0 + lane < a.batch ? steps_of(a, b0 + lane) : 0;
+      mine = sum = b0 + lane < a.batch ? counted(steps_of(a, b0 + lane)) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, sum, o);
@@ -456,16 +459,18 @@ __device__ __forceinline__ void few_share(const SeqAttnArgs& a, const CUtensorMa
   for (int b = b0; at < end && b < a.batch; ++b) {
     const int steps = steps_of(a, b);
     if (steps == 0) continue;
+    const int first = max(at - base - kFewStart, 0), last = min(end - base - kFewStart, steps);
+    const bool later = at > begin;
+    base += steps + kFewStart;
+    at = base;
+    if (first >= last) continue;  // only its start lies in this run
     segment(b);
-    const int first = at - base, last = min(steps, end - base);
     const bool whole = first == 0 && last == steps;
-    const int64_t part = whole ? -1 : static_cast<int64_t>(few_row(blockIdx.x, at > begin, 0));
+    const int64_t part = whole ? -1 : static_cast<int64_t>(few_row(blockIdx.x, later, 0));
     const int k0 = first * kFewStep, k1 = min(seg.m, last * kFewStep);
     const bool ok = seg.n * a.group <= 8 ? few_rows<D, 1>(a, tm_k, tm_v, smem, sh, turns, seg, b, hk, k0, k1, part)
                                          : few_rows<D, 2>(a, tm_k, tm_v, smem, sh, turns, seg, b, hk, k0, k1, part);
     if (!ok) return;
-    base += steps;
-    at = base;
   }
 }
 
@@ -555,11 +560,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_few_join_kernel(const _
   clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
   const int rows = seg.n * a.group, steps = steps_of(a, b);
   const int run = run_length(a, steps_before(a, a.batch)), first = steps_before(a, b);
-  const int run0 = first / run, run1 = (first + steps - 1) / run;
+  const int run0 = (first + kFewStart) / run, run1 = (first + kFewStart + steps - 1) / run;
   pdl_wait();
   if (steps == 0 || run0 == run1) return;
-  // the first run began before these steps: its last part
-  const bool behind = first != run0 * run;
+  // the first run began before this sequence: its later part
+  const bool behind = first > run0 * run;
   const int parts = run1 - run0 + 1;
   const bool alone = parts <= kJoinAlone;
   const int step = alone ? kJoinWarps * gridDim.y : gridDim.y;

@@ -890,7 +890,7 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
  * The queries are the last tokens of their sequences (a chunk of a prompt, or one token each), so the mask is causal.
  * max_q: no sequence has more queries (one that has is not computed where max_q heads_q / heads_k <= 16); max_kv: no
  * sequence has more keys (0: table_width page_size; more keys than that are not seen).  They and the shapes alone decide how the
- * work is split; the device's lengths may change between launches of a captured graph.  batch (max_kv / 64 + 2) below 2^31.
+ * work is split; the device's lengths may change between launches of a captured graph.  batch (max_kv / 64 + 5) below 2^31.
  * out [tokens_q, heads_q, head_dim]; lse NULL or [tokens_q, heads_q] fp32.  The same bits from call to call.
  * workspace >= mmdit_paged_attention_workspace_size(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv), with
  * max_kv as the call takes it (parts of split sequences: calls that share one are ordered on one stream). */

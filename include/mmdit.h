@@ -917,7 +917,7 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
  *   positions, slots [capacity] int64 (either may be NULL): of each new token in the order of requests, its position in its
  *   request and page page_size + slot (-1 without a page); entries behind the last new token are 0 and -1;
  *   missing [2] int32: pages wanted that were not free, and new tokens left out (beyond capacity or the tables' width).
- * All of them on the device.  Called again with the same before, after and n_free (and n_free_out elsewhere) it gives the
+ * All of them on the device; a page is held by one request.  Called again with the same before, after and n_free (and n_free_out elsewhere) it gives the
  * same result.  No array is another (but n_free_out n_free).  batch table_width and table_width page_size at most 2^30.  No
  * workspace. */
 mmdit_status mmdit_block_tables(int32_t batch, int32_t page_size, int32_t table_width, int32_t n_pages,

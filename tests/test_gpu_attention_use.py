@@ -52,6 +52,54 @@ def test_paged_tables_wider_than_the_requests(width):
     base.compare_paged(base.paged(rng, [40, 1, 0], [64, 3, 40], 8, 2, 128, 64, width=width))
 
 
+@pytest.mark.parametrize("d", [8, 24, 40, 72, 104, 120])
+@pytest.mark.parametrize("new,hq,hk", [([1, 1], 4, 2), ([3, 1], 5, 1), ([70, 1], 6, 3)])
+def test_paged_head_dims(d, new, hq, hk):
+    rng = np.random.default_rng(d + hq)
+    base.compare_paged(base.paged(rng, new, [900, 77], hq, hk, d, 32, pad=1))
+
+
+@pytest.mark.parametrize("new,group", [(1, 8), (1, 9), (1, 16), (1, 17), (2, 8), (3, 5), (4, 4), (16, 1), (17, 1), (1, 128)])
+def test_paged_rows_around_the_kernels_border(new, group):
+    """Sequences of up to 16 rows are one kernel's, of more another's; up to 8 rows are one column of the first's products."""
+    rng = np.random.default_rng(new + group)
+    base.compare_paged(base.paged(rng, [new, 1], [1400, 40], 2 * group, 2, 64, 16, pad=1))
+
+
+def far_apart(small, stride, offset=0):
+    """The values of `small` in a view whose first extent has stride `stride` (elements)."""
+    room = torch.empty((small.shape[0] - 1) * stride + small[0].numel() + offset, dtype=small.dtype, device="cuda")
+    view = room[offset:].as_strided(small.shape, (stride, *small.stride()[1:]))
+    view.copy_(small)
+    return view
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_paged_offsets_beyond_32_bits(new):
+    rng = np.random.default_rng(new)
+    q, kc, vc, tables, lens, cu, keys, values = base.paged(rng, [new, 1], [100, 60], 4, 2, 64, 16)
+    kc, vc = far_apart(kc, 1 << 28), far_apart(vc, 1 << 28)  # 12 pages: 6 GB
+    assert (kc.shape[0] - 1) << 28 > 2 ** 31
+    base.compare_paged((q, kc, vc, tables, lens, cu, keys, values))
+    slots = base.ints([16 * (kc.shape[0] - 1) + 5], torch.int64)
+    x = base.rand(rng, 1, 2, 64)
+    L.mmdit_kv_cache_write(x, x, kc, vc, slots)
+    assert torch.equal(kc[-1, 5], x[0]) and torch.equal(vc[-1, 5], x[0])
+
+
+def test_packed_offsets_beyond_32_bits():
+    rng = np.random.default_rng(3)
+    q, k, v, cu, _ = base.packed(rng, [30, 12], [30, 12], 2, 1, 64, layout="dense")
+    q, k, v = (far_apart(t, 1 << 26) for t in (q, k, v))
+    assert (q.shape[0] - 1) << 26 > 2 ** 31
+    base.compare_varlen(q, k, v, cu, cu, True)
+    base.compare_gradients(q, k, v, cu, cu, True)
+    out = far_apart(torch.zeros(42, 2, 64, device="cuda", dtype=B16), 1 << 26)
+    ref, _ = base.run_varlen(q, k, v, cu, cu, True)
+    base.run_varlen(q, k, v, cu, cu, True, out=out)
+    assert torch.equal(out, ref)
+
+
 # ------------------------------------------------------------------------------------- a server
 class Server:
     """Requests over a paged cache; `history` keeps what a contiguous cache would hold."""

@@ -444,7 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sb->tmem_slot;
-  pdl_wait();
+  // The pass over queries reads nothing that the one over keys writes: it takes the SMs that run out of the other's items, and
+  // only its end waits for that one's.
+  const bool behind = !KEYS && a.tokens_k > 0;
+  if (!behind) pdl_wait();
+  pdl_trigger();
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
   };
@@ -777,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (behind) pdl_wait();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -784,78 +789,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// (lse log2(e), dout . out) of every row, float32: 16 lanes to a row, four rows in flight.  A row whose q or dout is not finite
-// has NaN for the first, which tells the pass over keys to look at its tile.  Rows of no sequence are read and not used.
+// (lse log2(e), dout . out) of every row, float32: LANES lanes to a row (16 bytes of it each), four rows in flight.  A row whose q
+// or dout is not finite has NaN for the first, which tells the pass over keys to look at its tile.  Rows of no sequence are
+// read and not used.
 constexpr int kSumsRows = 4;
-__global__ void __launch_bounds__(256) seq_sums_kernel(const __grid_constant__ SeqAttnBwdArgs a) {
+template <int LANES>
+__global__ void __launch_bounds__(256) seq_sums_kernel(const __grid_constant__ SeqAttnBwdArgs a, Divisor by_heads) {
   pdl_wait();
+  pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0, a.counters[0] = 0, a.counters[1] = 0;
-  const int c = (threadIdx.x & 15) * 8;
+  constexpr int kAtOnce = 256 / LANES;
+  const int lane = threadIdx.x & (LANES - 1), c = lane * 8;
   const int64_t rows = static_cast<int64_t>(a.tokens_q) * a.hq;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 16 * kSumsRows + (threadIdx.x >> 4);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kAtOnce * kSumsRows + threadIdx.x / LANES;
   const bool there = c < a.head_dim;
   uint4 x[kSumsRows], y[kSumsRows], z[kSumsRows];
+  float lse[kSumsRows];
 #pragma unroll
   for (int e = 0; e < kSumsRows; ++e) {
-    const int64_t row = row0 + 16 * e;
-    x[e] = y[e] = z[e] = make_uint4(0, 0, 0, 0);
+    const int64_t row = row0 + kAtOnce * e;
+    x[e] = y[e] = z[e] = make_uint4(0, 0, 0, 0), lse[e] = 0.f;
     if (row < rows && there) {
-      const int64_t t = row / a.hq, h = row - t * a.hq;
+      const int t = by_heads.quotient(row), h = static_cast<int>(row - static_cast<int64_t>(t) * a.hq);
       auto at = [&](const HeadsView& v) {
         return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(v.ptr) + t * v.stride_t + h * v.stride_h + c);
       };
       x[e] = at(a.dout), y[e] = at(a.out), z[e] = at(a.q);
+      if (lane == 0) lse[e] = a.lse[row];
     }
   }
-  const unsigned half = 0xffffu << (threadIdx.x & 16);
+  const unsigned mine = (0xffffffffu >> (32 - LANES)) << (threadIdx.x & 31 & ~(LANES - 1));
 #pragma unroll
   for (int e = 0; e < kSumsRows; ++e) {
-    const int64_t row = row0 + 16 * e;
+    const int64_t row = row0 + kAtOnce * e;
     float s = bf16_lo(x[e].x) * bf16_lo(y[e].x) + bf16_hi(x[e].x) * bf16_hi(y[e].x) + bf16_lo(x[e].y) * bf16_lo(y[e].y) +
               bf16_hi(x[e].y) * bf16_hi(y[e].y) + bf16_lo(x[e].z) * bf16_lo(y[e].z) + bf16_hi(x[e].z) * bf16_hi(y[e].z) +
               bf16_lo(x[e].w) * bf16_lo(y[e].w) + bf16_hi(x[e].w) * bf16_hi(y[e].w);
 #pragma unroll
-    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const bool bad = (__ballot_sync(0xffffffffu, not_finite(x[e]) || not_finite(z[e])) & half) != 0;
-    if ((threadIdx.x & 15) == 0 && row < rows)
-      a.sums[row] = make_float2(bad ? __int_as_float(0x7FC00000) : a.lse[row] * kLog2e, s);
+    for (int o = LANES / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const bool bad = (__ballot_sync(0xffffffffu, not_finite(x[e]) || not_finite(z[e])) & mine) != 0;
+    if (lane == 0 && row < rows) a.sums[row] = make_float2(bad ? __int_as_float(0x7FC00000) : lse[e] * kLog2e, s);
   }
 }
 
-// dk and dv of key rows whose queries were worked on in parts: the parts' float32 sums, added in their order.  A warp to a row
-// and key head.
+// dk and dv of key rows whose queries were worked on in parts: the parts' float32 sums, added in their order.  A warp to a row,
+// two key heads of it at a time.
 template <int D>
 __global__ void __launch_bounds__(256) seq_parts_kernel(const __grid_constant__ SeqAttnBwdArgs a) {
-  pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (item >= static_cast<int64_t>(a.tokens_k) * a.hk) return;
-  const int row = static_cast<int>(item / a.hk), hk = static_cast<int>(item % a.hk);
-  const int b = find_segment(a.batch, row, [&](int i) { return min(max(a.cu_k[i], 0), a.tokens_k); });
-  Segment seg;
-  clip_segment(a.cu_k, b, a.tokens_k, seg.k0, seg.m);
-  clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
-  if (row < seg.k0 || row >= seg.k0 + seg.m) return;
-  const KeyTile t = key_tile(a, seg, (row - seg.k0) / kSeqTile * kSeqTile);
-  if (t.parts <= 1) return;
-  constexpr int kCols = D / 16;  // of dv by the lower half of the lanes, of dk by the upper
-  float sum[kCols] = {};
-  for (int p = 0; p < t.parts; ++p) {
-    const float4* v = reinterpret_cast<const float4*>(a.part + part_at<D>(a, p, row, hk) + lane * kCols);
-#pragma unroll
-    for (int i = 0; i < kCols / 4; ++i) {
-      const float4 x = v[i];
-      sum[4 * i] += x.x, sum[4 * i + 1] += x.y, sum[4 * i + 2] += x.z, sum[4 * i + 3] += x.w;
-    }
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  int parts = 0;
+  if (row < a.tokens_k) {
+    const int b = find_segment(a.batch, static_cast<int>(row), [&](int i) { return min(max(a.cu_k[i], 0), a.tokens_k); });
+    Segment seg;
+    clip_segment(a.cu_k, b, a.tokens_k, seg.k0, seg.m);
+    clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
+    if (row >= seg.k0 && row < seg.k0 + seg.m) parts = key_tile(a, seg, (static_cast<int>(row) - seg.k0) / kSeqTile * kSeqTile).parts;
   }
+  pdl_wait();
+  if (parts <= 1) return;
+  constexpr int kCols = D / 16;  // of dv by the lower half of the lanes, of dk by the upper
   const HeadsView& out = lane < 16 ? a.dv : a.dk;
   const int col = (lane & 15) * kCols;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.ptr) + row * out.stride_t + hk * out.stride_h + col;
+  for (int hk = 0; hk < a.hk; hk += 2) {
+    float4 sum[2][kCols / 4];
 #pragma unroll
-  for (int i = 0; i < kCols / 4; ++i)
-    if (col + 4 * i < a.head_dim)
-      reinterpret_cast<uint2*>(dst)[i] =
-          make_uint2(pack_bf16x2(sum[4 * i], sum[4 * i + 1]), pack_bf16x2(sum[4 * i + 2], sum[4 * i + 3]));
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i) sum[h][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int p = 0; p < parts; ++p)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4* v = reinterpret_cast<const float4*>(a.part + part_at<D>(a, p, row, min(hk + h, a.hk - 1)) + lane * kCols);
+#pragma unroll
+        for (int i = 0; i < kCols / 4; ++i) {
+          const float4 x = v[i];
+          sum[h][i].x += x.x, sum[h][i].y += x.y, sum[h][i].z += x.z, sum[h][i].w += x.w;
+        }
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (hk + h >= a.hk) break;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.ptr) + row * out.stride_t + (hk + h) * out.stride_h + col;
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i)
+        if (col + 4 * i < a.head_dim)
+          reinterpret_cast<uint2*>(dst)[i] =
+              make_uint2(pack_bf16x2(sum[h][i].x, sum[h][i].y), pack_bf16x2(sum[h][i].z, sum[h][i].w));
+    }
+  }
 }
 
 template <int D, bool KEYS>
@@ -879,24 +902,26 @@ cudaError_t launch_pass(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaSt
 cudaError_t launch_seq_attention_bwd(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaStream_t stream) {
   // the first kernel also clears the status word and the counters
   const int64_t rows = static_cast<int64_t>(a.tokens_q) * a.hq;
-  cudaError_t e = launch_pdl(seq_sums_kernel, dim3(static_cast<unsigned>(std::max<int64_t>((rows + 16 * kSumsRows - 1) / (16 * kSumsRows), 1))), dim3(256), 0,
-                             stream, a);
+  const int lanes = a.head_dim <= 64 ? 8 : 16, per_cta = 256 / lanes * kSumsRows;
+  const dim3 sums_grid(static_cast<unsigned>(std::max<int64_t>((rows + per_cta - 1) / per_cta, 1)));
+  cudaError_t e = lanes == 8 ? launch_pdl(seq_sums_kernel<8>, sums_grid, dim3(256), 0, stream, a, Divisor(a.hq))
+                             : launch_pdl(seq_sums_kernel<16>, sums_grid, dim3(256), 0, stream, a, Divisor(a.hq));
   if (e != cudaSuccess) return e;
   count_launch();
   if (a.tokens_k > 0) {
     e = a.head_dim <= 64 ? launch_pass<64, true>(a, m, stream) : launch_pass<128, true>(a, m, stream);
     if (e != cudaSuccess) return e;
-    if (a.parts > 1) {
-      const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tokens_k) * a.hk + 7) / 8));
-      e = a.head_dim <= 64 ? launch_pdl(seq_parts_kernel<64>, grid, dim3(256), 0, stream, a)
-                           : launch_pdl(seq_parts_kernel<128>, grid, dim3(256), 0, stream, a);
-      if (e != cudaSuccess) return e;
-      count_launch();
-    }
   }
   if (a.tokens_q > 0) {
     e = a.head_dim <= 64 ? launch_pass<64, false>(a, m, stream) : launch_pass<128, false>(a, m, stream);
     if (e != cudaSuccess) return e;
+  }
+  if (a.tokens_k > 0 && a.parts > 1) {
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tokens_k) + 7) / 8));
+    e = a.head_dim <= 64 ? launch_pdl(seq_parts_kernel<64>, grid, dim3(256), 0, stream, a)
+                         : launch_pdl(seq_parts_kernel<128>, grid, dim3(256), 0, stream, a);
+    if (e != cudaSuccess) return e;
+    count_launch();
   }
   return cudaGetLastError();
 }

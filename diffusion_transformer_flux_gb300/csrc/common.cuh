@@ -82,6 +82,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// i / d for divisors that the host knows, by the high half of a product with m = ceil(2^64 / d): exact where i d < 2^64, as
+// i (m d - 2^64) < i d.  m is 0 for d = 1.
+struct Divisor {
+  uint64_t m;
+  explicit Divisor(uint32_t d) : m(d == 1 ? 0 : ~uint64_t{0} / d + 1) {}
+  __device__ __forceinline__ int quotient(int64_t i) const {
+    return static_cast<int>(m ? __umul64hi(static_cast<uint64_t>(i), m) : static_cast<uint64_t>(i));
+  }
+};
+
 // ----------------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

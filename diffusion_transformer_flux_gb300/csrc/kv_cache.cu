@@ -287,13 +287,6 @@ __global__ void __launch_bounds__(256) token_map_kernel(const __grid_constant__ 
 constexpr int kWriteThreads = 128;
 constexpr int kWriteItems = 2;  // 16-byte pieces of a thread in flight (1, 2, 4: 1.9, 1.9, 2.7 us for 32 tokens, 16.6, 13.6, 13.5 for 9216)
 
-// i / d by the high half of a product with m = ceil(2^64 / d), exact as i (m d - 2^64) < 2^64 for 32-bit i and d; m is 0 for d = 1.
-struct Divisor {
-  uint64_t m;
-  explicit Divisor(uint32_t d) : m(d == 1 ? 0 : ~uint64_t{0} / d + 1) {}
-  __device__ __forceinline__ int quotient(int i) const { return m ? static_cast<int>(__umul64hi(static_cast<uint64_t>(i), m)) : i; }
-};
-
 __global__ void __launch_bounds__(kWriteThreads)
     kv_write_kernel(const __grid_constant__ CacheWriteArgs a, int tokens_per_cta, Divisor by_token, Divisor by_head) {
   pdl_wait();

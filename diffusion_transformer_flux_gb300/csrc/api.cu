@@ -3180,6 +3180,7 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
     a.clear = 0, a.few_behind = 1;
   }
   if (p.few) MMDIT_CUDA(launch_paged_few(a, m, st), "paged attention of few rows");
+  a.join_beside = p.few && !p.few_whole;
   if (p.splits > 1) MMDIT_CUDA(launch_paged_join(a, st), "paged attention's join");
   return MMDIT_OK;
 }

@@ -476,6 +476,7 @@ struct SeqAttnArgs {
   int few_rows;  // sequences of at most that many rows (tokens by the group's heads) are paged_few_kernel's: kFewRows or 0
   int few_ctas, few_whole;   // its CTAs; whether each takes one sequence and key head
   int few_behind;            // the tile kernel runs before it
+  int join_beside;           // paged_few_join_kernel runs before paged_join_kernel
   int few_join_rows;         // rows of the sequence with most of them
   int split_keys;            // keys of one item of the tile kernel (0: all)
   // normalised parts and their log2-sums: [splits, tokens_q, hq(, D)] of the tile kernel, [few_ctas, 2, kFewRows(, D)] of

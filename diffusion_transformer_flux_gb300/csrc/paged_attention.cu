@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_few_join_kernel(const _
   const int run = run_length(a, steps_before(a, a.batch)), first = steps_before(a, b);
   const int run0 = (first + kFewStart) / run, run1 = (first + kFewStart + steps - 1) / run;
   pdl_wait();
+  pdl_trigger();
   if (steps == 0 || run0 == run1) return;
   // the first run began before this sequence: its later part
   const bool behind = first > run0 * run;
@@ -603,33 +604,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_few_join_kernel(const _
   }
 }
 
-// The rows of the tile kernel whose keys were split: a warp to four of them, so that enough reads are on their way (a warp to
-// each: 17 against 12 us for two parts of 32000 rows of 128).
-constexpr int kJoinRows = 4 * kJoinWarps;
+// A row's parts of the tile kernel, by eight lanes.
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ SeqAttnArgs a) {
+__device__ __forceinline__ void add_tile_parts(const SeqAttnArgs& a, int64_t item, int tok, int head, int lane, int parts) {
   constexpr int kCols = D / 32;  // float4 of a lane
-  const int lane = threadIdx.x & 7;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinRows + (threadIdx.x >> 3);
-  const int tok = static_cast<int>(item / a.hq), head = static_cast<int>(item % a.hq);
-  // the last sequence that starts at or before the token (empty ones before it share its start), by all lanes for each token
-  int b = 0;
-  for (int r = 0, found = -1; r < 32; r += 8) {
-    const int t = __shfl_sync(0xffffffffu, tok, r);
-    if (t == found || t >= a.tokens_q) continue;
-    found = t;
-    const int x = find_segment(a.batch, t, [&](int i) { return min(max(a.cu_q[i], 0), a.tokens_q); });
-    if (tok == t) b = x;
-  }
-  int parts = 0;
-  if (tok < a.tokens_q) {
-    Segment seg;
-    clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
-    if (tok >= seg.q0 && tok < seg.q0 + seg.n && seg.n * a.group > a.few_rows)
-      parts = (min(max(a.kv_lens[b], 0), a.max_keys) + a.split_keys - 1) / a.split_keys;
-  }
-  pdl_wait();  // no thread returns without it (see paged_few_join_kernel)
-  if (parts <= 1) return;
   const size_t stride = static_cast<size_t>(a.tokens_q) * a.hq;
   float top = -INFINITY;
 #pragma unroll 4
@@ -660,6 +638,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
       *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_bf16x2(v[i].x * inv, v[i].y * inv), pack_bf16x2(v[i].z * inv, v[i].w * inv));
   }
   if (lane == 0 && a.lse) a.lse[item] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// The rows of the tile kernel whose keys were split: a warp to four of them, so that enough reads are on their way (a warp to
+// each: 17 against 12 us for two parts of 32000 rows of 128).
+constexpr int kJoinRows = 4 * kJoinWarps;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ SeqAttnArgs a) {
+  const int lane = threadIdx.x & 7;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinRows + (threadIdx.x >> 3);
+  const int tok = static_cast<int>(item / a.hq), head = static_cast<int>(item % a.hq);
+  // the last sequence that starts at or before the token (empty ones before it share its start), by all lanes for each token
+  int b = 0;
+  for (int r = 0, found = -1; r < 32; r += 8) {
+    const int t = __shfl_sync(0xffffffffu, tok, r);
+    if (t == found || t >= a.tokens_q) continue;
+    found = t;
+    const int x = find_segment(a.batch, t, [&](int i) { return min(max(a.cu_q[i], 0), a.tokens_q); });
+    if (tok == t) b = x;
+  }
+  int parts = 0;
+  if (tok < a.tokens_q) {
+    Segment seg;
+    clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
+    if (tok >= seg.q0 && tok < seg.q0 + seg.n && seg.n * a.group > a.few_rows)
+      parts = (min(max(a.kv_lens[b], 0), a.max_keys) + a.split_keys - 1) / a.split_keys;
+  }
+  // No thread returns without waiting (see paged_few_join_kernel).  Behind that one, which let this one start when the tile kernel
+  // had ended, the two work beside one another and the end waits.
+  if (!a.join_beside) pdl_wait();
+  if (parts > 1) add_tile_parts<D>(a, item, tok, head, lane, parts);
+  if (a.join_beside) pdl_wait();
 }
 
 template <int D>

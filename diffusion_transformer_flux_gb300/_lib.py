@@ -1133,7 +1133,7 @@ def mmdit_paged_attention_fwd(q, k_cache, v_cache, out, tables, kv_lens, cu_q, l
         raise ValueError("tables must be [B, width]")
     B, width = tables.shape
     max_q = Tq if max_q is None else int(max_q)
-    max_kv = width * page if max_kv is None else int(max_kv)
+    max_kv = int(max_kv) if max_kv else width * page
     ws = _workspace_arg(ws, dev, lambda: mmdit_paged_attention_workspace_size(Tq, B, Hq, Hk, d, max_q, min(max_kv, width * page)),
                         stream)
     _launch("mmdit_paged_attention_fwd", dev, stream, B, Tq, Hq, Hk, d, d ** -0.5 if scale is None else float(scale), vq, vk,

@@ -369,7 +369,8 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
       const float* p = parts + w * kFewRows * (D + 2);
-      const float e = p[r * 2] == -INFINITY ? 0.f : fast_exp2(p[r * 2] - top);
+      // no maximum: no keys, and zeros, or scores that are all NaN, and NaN
+      const float e = p[r * 2] == -INFINITY ? 1.f : fast_exp2(p[r * 2] - top);
       const float2 v = *reinterpret_cast<const float2*>(p + 2 * kFewRows + r * D + col);
       sum += e * p[r * 2 + 1], x += e * v.x, y += e * v.y;
     }

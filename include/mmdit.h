@@ -893,7 +893,8 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
  * work is split; the device's lengths may change between launches of a captured graph.  batch (max_kv / 64 + 5) below 2^31.
  * out [tokens_q, heads_q, head_dim]; lse NULL or [tokens_q, heads_q] fp32.  The same bits from call to call.
  * workspace >= mmdit_paged_attention_workspace_size(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv), with
- * max_kv as the call takes it (parts of split sequences: calls that share one are ordered on one stream). */
+ * the call's max_kv, or table_width page_size where that is 0 or less than it (parts of split sequences: calls that share one
+ * are ordered on one stream). */
 typedef struct mmdit_pages_view {
   void *ptr;
   int64_t stride_page, stride_t, stride_h;

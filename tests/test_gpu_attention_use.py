@@ -66,6 +66,22 @@ def test_paged_rows_around_the_kernels_border(new, group):
     base.compare_paged(base.paged(rng, [new, 1], [1400, 40], 2 * group, 2, 64, 16, pad=1))
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("new,total", [([1, 1, 1], [40, 300, 9]), ([3, 1, 4], [2000, 600, 4]), ([30, 1, 50], [2500, 600, 50])])
+def test_paged_queries_that_are_not_finite_stay_alone(new, total, bad):
+    """Their rows are NaN, whichever kernel they are of and however their keys are split; all others keep their bits."""
+    rng = np.random.default_rng(sum(total))
+    case = base.paged(rng, new, total, 4, 2, 64, 16)
+    clean, sums = base.run_paged(case)
+    for at in {0, new[0] - 1, new[0], sum(new) - 1}:
+        q = case[0].clone()
+        q[at, 1] = bad
+        out, lse = base.run_paged((q, *case[1:]))
+        assert torch.isnan(out[at, 1]).all() and torch.isnan(lse[at, 1])
+        out[at, 1], lse[at, 1] = clean[at, 1], sums[at, 1]
+        assert torch.equal(out, clean) and torch.equal(lse, sums)
+
+
 def far_apart(small, stride, offset=0):
     """The values of `small` in a view whose first extent has stride `stride` (elements)."""
     room = torch.empty((small.shape[0] - 1) * stride + small[0].numel() + offset, dtype=small.dtype, device="cuda")

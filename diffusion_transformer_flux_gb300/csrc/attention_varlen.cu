@@ -27,6 +27,11 @@
 // columns behind head_dim are zeros that the TMA fills in.  The products of heads of up to 96 leave out the last 32 (KD: 23
 // sequences of 25 heads of 96, 305 us with all 128 columns, 283 so).
 //
+// What bounds it is the chain of a tile, scores, softmax, weights, product, scores: 2950 cycles for two tiles of 128 rows by 128
+// keys, 2048 of them the tensor core's, no pipe full; and 8000 cycles where an item ends and the next begins (its last
+// product, 4500 for the rows on their way out, the first softmax).  Heads of 128, 32 + 8, causal: 2 x 4608 tokens 268 us
+// (1.30 PFLOP/s), 16384 tokens 1.41 ms (1.56); heads of 64, 2 x 4608: 214 us (0.81).
+//
 // Over a paged cache the keys of an item may be split over several (few rows, long contexts); each then writes
 // its part normalised in float32 with its log-sum, and paged_join_kernel joins them.
 #include <algorithm>

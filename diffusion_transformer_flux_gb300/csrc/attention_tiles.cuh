@@ -11,6 +11,10 @@ constexpr int kSeqTile = 128;                  // rows of a query tile, keys of 
 constexpr int kSeqBlock = kSeqTile * 128;      // bytes of 128 rows of 64 bf16 (one 128-byte swizzle column block)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// A row that sees no key is 0, its log-sum -inf.  One that sees keys whose scores are all -inf has no weights (0 / 0): it is NaN, and
+// so is its log-sum.  Where its keys are split, a part of such keys alone has this log2-sum and zeros: beside any other it weighs
+// nothing, and if it is the largest the row is NaN.
+constexpr float kNoWeights = -3.402823466e38f;
 
 // The largest b < n with start(b) <= x, for start rising with b and start(0) <= x (else 0): a search by 32 places at a
 // time, by all lanes of a warp (2 rounds of loads up to 1024 sequences).

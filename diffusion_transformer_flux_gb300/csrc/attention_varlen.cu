@@ -2,7 +2,8 @@
 //
 // Per sequence of n queries and m keys, and per query head h with its key head h / (Hq / Hk):
 //   z_ij = scale q_i . k_j over the keys j that query i sees (all, or with `causal` those up to its position m - n + i),
-//   out_i = sum_j exp(z_ij - lse_i) v_j,   lse_i = log sum_j exp(z_ij);   a row that sees no key gives 0 and -inf.
+//   out_i = sum_j exp(z_ij - lse_i) v_j,   lse_i = log sum_j exp(z_ij);   a row that sees no key gives 0 and -inf,
+// one whose scores are all -inf NaN.
 //
 // The query heads of a group read the same keys, so a tile's 128 rows are 128 / group tokens by the group's heads (row
 // r is token r / group, head r % group): a key tile is loaded once for all of them, and a short chunk of new tokens
@@ -126,6 +127,7 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
     // rows of no token compute on whatever their lines hold and are not stored
     const int lim = valid ? keys_seen(w.seg, tok, a.causal) : INT32_MAX;
     float m_run = -INFINITY, l_run = 0.f;
+    bool saw = !PAGED && lim > 0;  // a key: paged, one that has a page
     int st = 0;
     for (int j = 0; j < cnt; ++j) {
       if (!wait(&sb->s_full[X], s_turn)) return;
@@ -169,7 +171,10 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
         if (lost) {  // pieces of at least 8 keys
           whole = false;
           uint32_t eights = 0;
-          for (int e = 0; e < 16; ++e) eights |= (lost >> (e * 8 / a.page_rows) & 1u) << e;
+          for (int e = 0; e < 16; ++e) {
+            eights |= (lost >> (e * 8 / a.page_rows) & 1u) << e;
+            saw |= e * 8 < rel && !(eights >> e & 1u);
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             if (eights >> (i / 8) & 1u) r0[i] = __float_as_uint(-INFINITY);
@@ -177,6 +182,8 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
             if (eights >> (8 + i / 8) & 1u) r2[i] = __float_as_uint(-INFINITY);
             if (eights >> (12 + i / 8) & 1u) r3[i] = __float_as_uint(-INFINITY);
           }
+        } else {
+          saw |= rel > 0;
         }
       }
       if (!whole) {
@@ -263,8 +270,10 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
       tc_fence_after();
       if (last && (threadIdx.x & 127) == 0) mbar_arrive(&sb->v_empty[(cnt - 1) % kStages]);
     }
-    const float inv_l = l_run == 0.f ? 0.f : 1.f / l_run;
-    const float lse2 = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
+    // no sum: no keys, or scores that are all -inf (see kNoWeights)
+    const float nan = __int_as_float(0x7FC00000);
+    const float inv_l = l_run == 0.f ? (saw && w.n_splits == 1 ? nan : 0.f) : 1.f / l_run;
+    const float lse2 = l_run == 0.f ? (!saw ? -INFINITY : w.n_splits == 1 ? nan : kNoWeights) : m_run + log2f(l_run);
     const int head = w.hk * a.group + row_head;
     const size_t out_row = valid ? (static_cast<size_t>(w.seg.q0) + tok) * a.hq + head : 0;
     const bool any_bad = *reinterpret_cast<volatile int*>(&sb->any_bad[slot]) != 0;

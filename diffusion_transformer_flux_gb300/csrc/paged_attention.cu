@@ -234,6 +234,7 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
   }
   float o[N][D / 16][4];
   float m_run[N][2], l_run[N][2];
+  uint32_t saw = 0;  // a bit for each of this lane's 2 N rows: it sees one of this lane's keys (that has a page)
 #pragma unroll
   for (int n = 0; n < N; ++n) {
 #pragma unroll
@@ -278,8 +279,13 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = key0 + g + 8 * (e >> 1);
-          if (key >= lim[n][e & 1] || (lost >> (e >> 1) & 1u)) s[n][e] = -INFINITY;
+          if (key >= lim[n][e & 1] || (lost >> (e >> 1) & 1u))
+            s[n][e] = -INFINITY;
+          else
+            saw |= 1u << (2 * n + (e & 1));
         }
+    } else {
+      saw = ~0u;
     }
     bool up = false;
 #pragma unroll
@@ -343,6 +349,13 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], x);
+#pragma unroll
+  for (int x = 4; x < 32; x <<= 1) saw |= __shfl_xor_sync(0xffffffffu, saw, x);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (m_run[n][e] == -INFINITY && l_run[n][e] == 0.f && (saw >> (2 * n + e) & 1u)) m_run[n][e] = kNoWeights;
   __syncthreads();
   if (*reinterpret_cast<volatile int*>(&sh->abort_flag)) return false;
   float* parts = reinterpret_cast<float*>(smem);
@@ -369,12 +382,13 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
       const float* p = parts + w * kFewRows * (D + 2);
-      // no maximum: no keys, and zeros, or scores that are all NaN, and NaN
+      // no maximum: no keys, and zeros, or scores that are all NaN, and NaN (all -inf: kNoWeights and zeros)
       const float e = p[r * 2] == -INFINITY ? 1.f : fast_exp2(p[r * 2] - top);
       const float2 v = *reinterpret_cast<const float2*>(p + 2 * kFewRows + r * D + col);
       sum += e * p[r * 2 + 1], x += e * v.x, y += e * v.y;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const bool no_weights = sum == 0.f && top == kNoWeights;
+    const float inv = sum == 0.f ? (no_weights && part < 0 ? __int_as_float(0x7FC00000) : 0.f) : 1.f / sum;
     x *= inv, y *= inv;
     if (sh->any_bad) {
       const int l = keys_seen(seg, r / a.group, a.causal);
@@ -383,7 +397,7 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
     }
     const int64_t tok = static_cast<int64_t>(seg.q0) + r / a.group;
     const int head = hk * a.group + r % a.group;
-    const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+    const float lse2 = sum == 0.f ? (!no_weights ? -INFINITY : part < 0 ? __int_as_float(0x7FC00000) : kNoWeights) : top + log2f(sum);
     if (part >= 0) {
       const size_t at = static_cast<size_t>(part) + r;
       *reinterpret_cast<float2*>(a.few_part + at * D + col) = make_float2(x, y);
@@ -531,6 +545,7 @@ template <int D>
 __device__ __forceinline__ void write_joined(const SeqAttnArgs& a, int64_t tok, int head, float top, float sum, const float (&v)[D / 32]) {
   constexpr int kCols = D / 32;
   const int lane = threadIdx.x & 31, col = lane * kCols;
+  if (top == kNoWeights) sum = __int_as_float(0x7FC00000);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.ptr) + tok * a.out.stride_t + head * a.out.stride_h + col;
   if (col < a.head_dim)
@@ -630,6 +645,7 @@ __device__ __forceinline__ void add_tile_parts(const SeqAttnArgs& a, int64_t ite
 #pragma unroll
     for (int i = 0; i < kCols; ++i) v[i].x += e * u[i].x, v[i].y += e * u[i].y, v[i].z += e * u[i].z, v[i].w += e * u[i].w;
   }
+  if (top == kNoWeights) sum = __int_as_float(0x7FC00000);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.ptr) + static_cast<int64_t>(tok) * a.out.stride_t + head * a.out.stride_h;
 #pragma unroll

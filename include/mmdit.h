@@ -840,7 +840,8 @@ mmdit_status mmdit_rope_bwd(int32_t act, const mmdit_rope_cfg *cfg, int32_t batc
  * were.  Query i of a sequence of n queries and m keys stands at position m - n + i; with causal != 0 it sees the keys up to
  * its own position, else all:
  *   z_ij = scale q_i . k_j,   lse_i = log sum_j exp(z_ij),   out_i = sum_j exp(z_ij - lse_i) v_j   over the keys it sees;
- * a row that sees none gives zeros and lse -inf.  Query head h reads key head h / (heads_q / heads_k).  Nothing of a key
+ * a row that sees none gives zeros and lse -inf, one whose scores are all -inf (0 / 0) NaN and lse NaN.  Query head h reads
+ * key head h / (heads_q / heads_k).  Nothing of a key
  * that a row does not see reaches it; a non-finite element of a v that it sees, within 128 keys of the first that it does not,
  * makes that column NaN.
  *

@@ -1,0 +1,127 @@
+"""Rows of the text model's attention whose scores are infinite, and calls at the ends of the documented ranges."""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_attention as base
+from diffusion_transformer_flux_gb300 import _lib as L
+
+pytestmark = pytest.mark.gpu
+B16 = torch.bfloat16
+INF = float("inf")
+
+
+def row_reference(q, k, v, keys):
+    """(out, lse, bounds) [1, 1, d] of one row of one head over the keys in `keys`."""
+    return base.attention_reference(base.f64(q)[None, None], base.f64(k)[keys][:, None], base.f64(v)[keys][:, None], False)
+
+
+def check_row(out, lse, q, k, v, keys, seen, what):
+    """A row that sees no key: 0 and -inf.  Scores that are all -inf have no weights (0 / 0): NaN.  Else the -inf ones weigh 0."""
+    if not seen:
+        assert (out == 0).all() and lse == -INF, what
+    elif not len(keys):
+        assert torch.isnan(out).all() and torch.isnan(lse), what
+    else:
+        ref, rl, tol, tl = row_reference(q, k, v, keys)
+        # parts of a split row are joined in float32, as in base.compare_paged
+        base.check(base.f64(out)[None, None], ref, tol * (1 + 2.0 ** -12), what)
+        base.check(base.f64(lse)[None, None], rl, tl + 2.0 ** -20, what)
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 128), (3, 1, 96), (2, 2, 64)])
+def test_packed_rows_whose_scores_are_all_minus_infinity(hq, hk, d, causal, sign):
+    """One infinite element of q against keys of the opposite sign: the row is NaN, all others keep their bits."""
+    rng = np.random.default_rng(d + causal)
+    q, k, v, cu, _ = base.packed(rng, [5, 300, 1], [5, 300, 1], hq, hk, d, layout="dense")
+    k[:, :, 0] = -sign * (k[:, :, 0].abs() + 0.125)
+    clean, sums = base.run_varlen(q, k, v, cu, cu, causal)
+    rows = [0, 3, 5, 5 + 140, 304, 305]  # first tokens, with one key each where the mask is causal; rows of one tile and of three
+    bad = q.clone()
+    bad[rows, 1, 0] = sign * INF
+    out, lse = base.run_varlen(bad, k, v, cu, cu, causal)
+    assert torch.isnan(out[rows, 1]).all() and torch.isnan(lse[rows, 1]).all()
+    out[rows, 1], lse[rows, 1] = clean[rows, 1], sums[rows, 1]
+    assert torch.equal(out, clean) and torch.equal(lse, sums)
+
+
+def test_packed_keys_of_minus_infinity():
+    """Keys whose score is -inf weigh nothing; a row that sees only such keys is NaN, one that sees none at all is 0."""
+    rng = np.random.default_rng(7)
+    n, m, dead = 300, 290, 150  # the first ten rows see no key
+    q, k, v, cq, ck = base.packed(rng, [n], [m], 2, 1, 64, layout="dense")
+    q[:, :, 0] = q[:, :, 0].abs() + 0.125
+    k[:dead, :, 0] = -INF
+    out, lse = base.run_varlen(q, k, v, cq, ck, True)
+    for i in (0, 9, 10, 11, 100, 137, 138, 139, 159, 160, 161, 200, 299):
+        see = m - n + i + 1
+        for h in range(2):
+            check_row(out[i, h], lse[i, h], q[i, h], k[:, 0], v[:, 0], np.arange(dead, max(see, dead)), see > 0, (i, h))
+
+
+# new tokens and cached ones: few rows in one CTA, over several; a tile, a tile whose keys are split, and both kernels at once
+PAGED = {"few": ([1, 3], [40, 9]), "few_runs": ([1, 4], [20000, 700]), "tile": ([30], [300]), "tile_parts": ([130], [20000]),
+         "mixed": ([1, 40, 2], [6000, 5000, 33])}
+
+
+@pytest.mark.parametrize("name", list(PAGED))
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_rows_whose_scores_are_all_minus_infinity(name, d):
+    new, total = PAGED[name]
+    rng = np.random.default_rng(len(name) + d)
+    case = base.paged(rng, new, total, 4, 2, d, 16)
+    q, kc = case[0], case[1]
+    kc[..., 0] = kc[..., 0].abs() + 0.125
+    clean, sums = base.run_paged(case)
+    starts = base.sums(new)
+    rows = sorted({r for b in range(len(new)) for r in (starts[b], starts[b + 1] - 1)})
+    bad = q.clone()
+    bad[rows, 2, 0] = -INF
+    out, lse = base.run_paged((bad, *case[1:]))
+    assert torch.isnan(out[rows, 2]).all() and torch.isnan(lse[rows, 2]).all()
+    out[rows, 2], lse[rows, 2] = clean[rows, 2], sums[rows, 2]
+    assert torch.equal(out, clean) and torch.equal(lse, sums)
+
+
+@pytest.mark.parametrize("name", list(PAGED))
+@pytest.mark.parametrize("share", [0.4, 1.0])
+def test_paged_keys_of_minus_infinity(name, share):
+    """The first `share` of each request's keys have a score of -inf: parts of nothing else weigh nothing beside others; where
+    all keys are such, rows are NaN."""
+    new, total = PAGED[name]
+    rng = np.random.default_rng(len(name))
+    q, kc, vc, tables, lens, cu, keys, values = base.paged(rng, new, total, 4, 2, 64, 16)
+    q[..., 0] = q[..., 0].abs() + 0.125
+    dead = [round(share * t) for t in total]
+    for b, n in enumerate(dead):
+        at = torch.arange(n, device="cuda")
+        kc[tables[b, at // 16].long(), at % 16, :, 0] = -INF
+    out, lse = base.run_paged((q, kc, vc, tables, lens, cu, keys, values))
+    starts = base.sums(new)
+    for b, (n, t) in enumerate(zip(new, total)):
+        for i in sorted({0, n // 2, n - 1}):
+            see = t - n + i + 1
+            for h in (0, 3):
+                r, g = starts[b] + i, h // 2
+                check_row(out[r, h], lse[r, h], q[r, h], keys[b][:, g], values[b][:, g], np.arange(dead[b], max(see, dead[b])), True,
+                          (b, i, h))
+
+
+@pytest.mark.parametrize("new,total", [([1], [64]), ([1], [9000]), ([40], [300]), ([130], [9000])])
+def test_paged_rows_without_a_page_stay_zero(new, total):
+    """Without any page a row sees no key; with one, whose scores are -inf, it is NaN."""
+    rng = np.random.default_rng(new[0])
+    page, count = 16, -(-total[0] // 16)
+    case = base.paged(rng, new, total, 4, 2, 64, page, dead=[(0, p) for p in range(count)])
+    out, lse = base.run_paged(case)
+    assert (out == 0).all() and (lse == -INF).all()
+    q, kc, _, tables = case[:4]
+    q[..., 0] = -INF
+    kc[0, :, :, 0] = 1.0
+    tables[0, 1] = 0
+    case[2][0] = 1.0
+    kc[0, :, :, 1:] = 1.0
+    out, lse = base.run_paged(case)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()

@@ -276,6 +276,30 @@ __device__ __forceinline__ void store_rows32(const uint8_t* pieces, const __nv_b
   }
 }
 
+// mbar_wait for what lasts as long as a work item does (its tiles are others' work): of 2^28 keys some seconds.  The limit
+// counts from the last change of `*progress`, which the warp that hands out items and loads tiles changes with each.
+__device__ __forceinline__ bool mbar_wait_item(uint64_t* bar, uint32_t parity, volatile uint32_t* progress, volatile int* abort,
+                                               uint32_t* status, uint32_t err_bit) {
+  if (mbar_test(bar, parity)) return true;
+  uint64_t t0 = global_timer_ns();
+  uint32_t before = *progress;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_test(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      const uint32_t now = *progress;
+      if (now == before) {
+        *abort = 1;
+        atomicOr(status, err_bit);
+        return false;
+      }
+      before = now, t0 = global_timer_ns();
+    }
+  }
+}
+
 // One lane of a converged warp.  What is computed before it stays uniform, so that the operands of the instructions behind
 // it need no moves out of a lane's registers.
 __device__ __forceinline__ bool one_lane() {

@@ -80,6 +80,7 @@ struct Barriers {
   uint64_t drain;
   uint32_t tmem_slot;
   int abort_flag;
+  uint32_t progress;  // see mbar_wait_item
   int any_bad[2];
   // paged: pieces of an item's tile j whose page does not exist; two rounds of the ring for each of the two items, as a K tile
   // is free before all rows have read this
@@ -117,7 +118,8 @@ __device__ __forceinline__ void softmax_role(Barriers<D>* sb, int X, uint32_t tm
   };
   for (uint32_t it = 0;; ++it) {
     const int slot = it & 1;
-    if (!wait(&sb->work_full[slot], it >> 1 & 1u)) return;
+    // an item of one tile is the other tile's warps' alone
+    if (!__all_sync(0xffffffffu, mbar_wait_item(&sb->work_full[slot], it >> 1 & 1u, &sb->progress, abort_flag, a.status, kErrAttnWait))) return;
     const Work w = sb->work[slot];
     if (!w.live) return;
     const int cnt = X ? w.cnt[1] : w.cnt[0];
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sb->drain, 1);
     sb->abort_flag = 0;
+    sb->progress = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -368,6 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (PAGED && a.few_rows) pdl_trigger();  // paged_few_kernel takes the SMs that run out of items
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
+  };
+  auto wait_item = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_item(bar, parity, &sb->progress, abort_flag, a.status, kErrAttnWait)) != 0;
   };
 
   if (warp >= 4) {
@@ -386,10 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t k_used = 0, v_used = 0;
     bool ok = true, q_used = false;
     int item = blockIdx.x;
+    uint32_t steps = 0;
+    auto progress = [&]() {
+      if (lane == 0) *const_cast<volatile uint32_t*>(&sb->progress) = ++steps;
+    };
     for (uint32_t it = 0; ok; ++it) {
       Work w;
       w.live = 0;
       for (; item < items; item = a.next ? next_of(a, ask_next(a)) : items) {
+        progress();
         const int rest = item % per_split;
         TileOrder::Found at;
         if (!order.find(rest / a.hk, at)) continue;
@@ -488,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ticket = 0;
       if (n_kv == 0) ticket = ask_next(a);
       for (int j = 0; ok && j < n_kv; ++j) {
+        progress();
         if (j == max(n_kv - 2, 0)) ticket = ask_next(a);
         const int after = st + 1 == kStages ? 0 : st + 1;
         if (j + 1 < n_kv) ok = load_k(j + 1, after, next);
@@ -540,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int slot = it & 1;
-      ok = wait(&sb->work_full[slot], it >> 1 & 1u);
+      ok = wait_item(&sb->work_full[slot], it >> 1 & 1u);
       if (!ok) break;
       const int cnt0 = sb->work[slot].cnt[0], cnt1 = sb->work[slot].cnt[1], live = sb->work[slot].live;
       // tiles from here on are to be cleaned
@@ -621,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int slot = it & 1;
-      ok = wait(&sb->work_full[slot], it >> 1 & 1u);
+      ok = wait_item(&sb->work_full[slot], it >> 1 & 1u);
       if (!ok) break;
       const Work w = sb->work[slot];
       if (w.live) {
@@ -631,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t parity = v_turn >> st & 1u;
           v_turn ^= 1u << st;
           if (!to_scrub(w, j)) continue;
-          ok = wait(&sb->v_issued[st], clean_turn >> st & 1u) && wait(&sb->v_full[st], parity);
+          ok = wait_item(&sb->v_issued[st], clean_turn >> st & 1u) && wait(&sb->v_full[st], parity);
           clean_turn ^= 1u << st;
           if (!ok) break;
           const int key = (w.js + j) * kSeqTile;

@@ -87,6 +87,7 @@ struct Barriers {
   uint64_t drain;
   uint32_t tmem_slot;
   int abort_flag;
+  uint32_t progress;  // see mbar_wait_item
   int worst[2];  // per item: the row of M that is not finite and that most rows of F see (keys: the last query row, queries: the first key)
   Work work[2];
 };
@@ -224,7 +225,7 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
   };
   for (uint32_t it = 0;; ++it) {
     const int slot = it & 1;
-    if (!wait(&sb->work_full[slot], it >> 1 & 1u)) return;
+    if (!__all_sync(0xffffffffu, mbar_wait_item(&sb->work_full[slot], it >> 1 & 1u, &sb->progress, abort_flag, a.status, kErrAttnWait))) return;
     const Work w = sb->work[slot];
     if (!w.live) return;
     const int lag = w.seg.m - w.seg.n;  // query i stands at lag + i
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sb->acc_free, 8);
     mbar_init(&sb->drain, 1);
     sb->abort_flag = 0;
+    sb->progress = 0;
     fence_mbar_init();
   }
   if (KEYS && G * U < kUnit) {
@@ -454,6 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status, kErrAttnWait)) != 0;
   };
+  auto wait_item = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_item(bar, parity, &sb->progress, abort_flag, a.status, kErrAttnWait)) != 0;
+  };
 
   if (warp >= 4) {
     more_registers<kBwdRows>();
@@ -485,10 +490,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto next_slot = [&]() { sl = sl + 1 == C::kSlots ? 0 : sl + 1; };
     int item = blockIdx.x;
+    uint32_t steps = 0;
+    auto progress = [&]() {
+      if (lane == 0) *const_cast<volatile uint32_t*>(&sb->progress) = ++steps;
+    };
     for (uint32_t it = 0; ok; ++it) {
       Work w;
       w.live = 0;
       for (; item < items; item = items > first_next ? next_of(first_next, ask_next(counter)) : items) {
+        progress();
         TileOrder::Found at;
         if (!order.find(item / a.hk / (KEYS ? a.parts : 1), at)) continue;
         w.hk = item % a.hk, w.first = at.start, w.part = 0, w.parts = 1;
@@ -555,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ticket = 0;
       if (more && w.count == 0) ticket = ask_next(counter);
       for (int u = 0; ok && u < w.count; ++u) {
+        progress();
         if (more && u == max(w.count - 2, 0)) ticket = ask_next(counter);
         if (!take_slot()) break;
         if (lane == 0) {
@@ -632,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int slot = it & 1;
-      ok = wait(&sb->work_full[slot], it >> 1 & 1u);
+      ok = wait_item(&sb->work_full[slot], it >> 1 & 1u);
       if (!ok) break;
       const Work w = sb->work[slot];
       __syncwarp();
@@ -714,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int slot = it & 1;
-      ok = wait(&sb->work_full[slot], it >> 1 & 1u);
+      ok = wait_item(&sb->work_full[slot], it >> 1 & 1u);
       if (!ok) break;
       const Work w = sb->work[slot];
       if (C::kFInRing && w.live && w.count > 0) next_slot(), next_slot();
@@ -767,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!__any_sync(0xffffffffu, bad)) hi = 0;
           }
-          ok = wait(&sb->st_issued[sl], clean_turn >> sl & 1u) && wait(&sb->st_full[sl], st_turn >> sl & 1u);
+          ok = wait_item(&sb->st_issued[sl], clean_turn >> sl & 1u) && wait(&sb->st_full[sl], st_turn >> sl & 1u);
           clean_turn ^= 1u << sl;
           if (!ok) break;
           const int at = KEYS ? G * (w.m_first + u * U) : u * kUnit;

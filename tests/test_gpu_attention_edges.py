@@ -125,3 +125,36 @@ def test_paged_rows_without_a_page_stay_zero(new, total):
     kc[0, :, :, 1:] = 1.0
     out, lse = base.run_paged(case)
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def test_items_that_take_seconds():
+    """One query over 4 x 10^8 keys: the warps that clean the last tile, and those of the item's absent second tile, wait longer for it
+    than a wait may stand still."""
+    if torch.cuda.mem_get_info()[0] < 50 << 30:
+        pytest.skip("needs 50 GB")
+    m, d, half = (3 << 27) - 5, 8, 3 << 26
+    kv = torch.ones(m, 1, d, dtype=B16, device="cuda")
+    kv[half:] = -1
+    q, dout, one = torch.zeros(1, 1, d, dtype=B16, device="cuda"), *(torch.ones(1, 1, d, dtype=B16, device="cuda") for _ in range(2))
+    cu_q, cu_k = base.ints([0, 1]), base.ints([0, m])
+    out, lse = base.run_varlen(q, kv, kv, cu_q, cu_k, True)
+    mean = (half - (m - half)) / m
+    # all weights are 1.  A product adds a few keys' terms at a time to a float32 sum, which takes none of them any more once they are
+    # below its last place (of terms of 8, at 2^27): a sum of m terms is off by up to m 2^-23 of the sum of their magnitudes
+    assert (out.double() - mean).abs().max() <= 2.0 ** -8 * mean + m * 2.0 ** -23
+    assert abs(lse.item() - np.log(m)) <= 2.0 ** -22 * np.log(m)
+    v = torch.zeros_like(kv)
+    v[-1000:] = 3
+    out, _ = base.run_varlen(q, kv, v, cu_q, cu_k, True)
+    assert (out.double() * m / 3000 - 1).abs().max() <= 2.0 ** -8 + 2.0 ** -16
+    # gradients: with out = 1 and v = 1, dz = p (dout . v - dout . out) is 0 but for the last 1000 keys, where it is 16 p
+    v = torch.ones_like(kv)
+    v[-1000:] = 3
+    dk, dv, dq = torch.full_like(kv, 7), torch.full_like(kv, 7), torch.full_like(q, 7)
+    ws = L.mmdit_varlen_attention_bwd(dout, q, kv, v, one, lse, dq, dk, dv, cu_q, cu_k)
+    torch.cuda.synchronize()
+    assert L.mmdit_workspace_status(ws) == 0
+    # p is off by 2^-16 (its exponent is 29, in float32), and dz or p and the result are rounded to bf16
+    tol = 2.0 ** -7 + 2.0 ** -15
+    assert (dq.double() * m / (-16000 * d ** -0.5) - 1).abs().max() <= tol
+    assert not dk.any() and all((x.double() * m - 1).abs() <= tol for x in (dv.amax(), dv.amin()))

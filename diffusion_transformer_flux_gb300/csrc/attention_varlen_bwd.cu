@@ -88,7 +88,7 @@ struct Barriers {
   uint32_t tmem_slot;
   int abort_flag;
   uint32_t progress;  // see mbar_wait_item
-  int worst[2];  // per item: the row of M that is not finite and that most rows of F see (keys: the last query row, queries: the first key)
+  int worst[2];  // per item: the row of M that is not finite and that most rows of F see (keys: the last token, queries: the first key)
   Work work[2];
 };
 static_assert(sizeof(Barriers) <= 1024, "barriers");
@@ -110,10 +110,11 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Rows [lo, hi) of a moving tile that hold a non-finite element have it zeroed and are noted, rows [zero_from, 64) become zeros.
+// Rows [lo, hi) of a moving tile that hold a non-finite element have it zeroed and are noted (queries: by their token first + r / group,
+// keys: first + r), rows [zero_from, 64) become zeros.
 // Called by THREADS threads; eight pieces are in flight in each.
 template <int D, bool KEYS, int THREADS>
-__device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int zero_from, int first, int* worst, int tid) {
+__device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int zero_from, int first, int group, int* worst, int tid) {
   constexpr int kChunks = D / 8;
   auto at = [&](int i) {
     const int r = i / kChunks, c = i % kChunks;
@@ -131,7 +132,7 @@ __device__ __forceinline__ void scrub_pair(uint8_t* tile, int lo, int hi, int ze
       const int i = i0 + THREADS * (__ffs(bad) - 1);
       *at(i) = make_uint4(0, 0, 0, 0);
       if (KEYS)
-        atomicMax(worst, first + i / kChunks);
+        atomicMax(worst, first + i / kChunks / group);
       else
         atomicMin(worst, first + i / kChunks);
     }
@@ -229,11 +230,11 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
     const Work w = sb->work[slot];
     if (!w.live) return;
     const int lag = w.seg.m - w.seg.n;  // query i stands at lag + i
-    // queries: this row's sums and the keys it sees; keys: the first query row (tokens by group) that sees it
+    // queries: this row's sums and the keys it sees; keys: the first token that sees it
     const int tok = w.first + row_tok;
     const bool valid = KEYS ? w.first + row < w.seg.m : row < G * T && tok < w.seg.n;
     const int lim = KEYS || !valid ? 0 : keys_seen(w.seg, tok, a.causal);
-    const int from = !KEYS ? 0 : !valid ? INT32_MAX : a.causal ? G * max(w.first + row - lag, 0) : 0;
+    const int from = !KEYS ? 0 : !valid ? INT32_MAX : a.causal ? max(w.first + row - lag, 0) : 0;
     uint64_t neg_l = 0, neg_d = 0;
     if constexpr (!KEYS) {
       float2 s = make_float2(0.f, 0.f);
@@ -283,8 +284,9 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
       // columns [lo, hi) of the tile are seen by this row
       int lo, hi;
       if constexpr (KEYS) {
+        // in tokens first: a sequence's rows (tokens by the group) may be more than 32 bits count
         const int t = w.m_first + u * a.unit_tokens;
-        hi = G * min(a.unit_tokens, w.seg.n - t), lo = from == INT32_MAX ? kUnit : max(from - G * t, 0);
+        hi = G * min(a.unit_tokens, w.seg.n - t), lo = G * min(max(from - t, 0), a.unit_tokens);
       } else {
         lo = 0, hi = lim - u * kUnit;
       }
@@ -781,9 +783,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_item(&sb->st_issued[sl], clean_turn >> sl & 1u) && wait(&sb->st_full[sl], st_turn >> sl & 1u);
           clean_turn ^= 1u << sl;
           if (!ok) break;
-          const int at = KEYS ? G * (w.m_first + u * U) : u * kUnit;
-          scrub_pair<D, KEYS, KEYS ? 32 : 64>(m_tile(sl, 0), lo, hi, zero_from, at, &sb->worst[slot], tid);
-          if (KEYS) scrub_pair<D, KEYS, 32>(m_tile(sl, 1), lo, hi, zero_from, at, &sb->worst[slot], tid);
+          const int at = KEYS ? w.m_first + u * U : u * kUnit;
+          scrub_pair<D, KEYS, KEYS ? 32 : 64>(m_tile(sl, 0), lo, hi, zero_from, at, KEYS ? G : 1, &sb->worst[slot], tid);
+          if (KEYS) scrub_pair<D, KEYS, 32>(m_tile(sl, 1), lo, hi, zero_from, at, G, &sb->worst[slot], tid);
           fence_proxy_async_smem();
           mbar_arrive(&sb->st_clean[sl]);
         }

@@ -158,3 +158,46 @@ def test_items_that_take_seconds():
     tol = 2.0 ** -7 + 2.0 ** -15
     assert (dq.double() * m / (-16000 * d ** -0.5) - 1).abs().max() <= tol
     assert not dk.any() and all((x.double() * m - 1).abs() <= tol for x in (dv.amax(), dv.amin()))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_gradients_of_more_rows_than_31_bits_count(causal):
+    """One sequence whose queries by the heads of a group pass 2^31.  All rows but the last tokens' have dout = 0 and add nothing;
+    q, dout and out are read through views that overlap, dq needs its 34 GB."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    rng = np.random.default_rng(causal)
+    group, d, m, n, last = 64, 8, 100, (1 << 25) + 1024, 128
+    k, v = base.rand(rng, m, 1, d), base.rand(rng, m, 1, d)
+    q, dout = (torch.zeros(n + group, d, dtype=B16, device="cuda") for _ in range(2))
+    # element (token, head) is row token + head: the last 64 and the group's rows behind them are of the last 127 tokens
+    q[n - 64:], dout[n - 64:] = base.rand(rng, 64 + group, d), base.rand(rng, 64 + group, d)
+    view = [t.as_strided((n, group, d), (d, d, 1)) for t in (q, dout, torch.zeros_like(q))]
+    lse = torch.zeros(n, group, device="cuda")
+    end = slice(n - last, n)
+    see = base.lm.seen(last, m, causal)
+    ql, gl = (base.f64(t[end]) for t in view[:2])
+    kl, vl, scale = base.f64(k), base.f64(v), d ** -0.5
+    # rows of the last tokens may have any out and lse: the formula takes them as they are
+    lse[end] = torch.logsumexp(torch.einsum("ihd,jd->ihj", view[0][end].float(), k[:, 0].float()) * scale, -1)
+    cu_q, cu_k = base.ints([0, n]), base.ints([0, m])
+    dq = torch.empty(n, group, d, dtype=B16, device="cuda")
+    dq.fill_(7)
+    dk, dv = torch.full_like(k, 7), torch.full_like(v, 7)
+    ws = L.mmdit_varlen_attention_bwd(view[1], view[0], k, v, view[2], lse, dq, dk, dv, cu_q, cu_k, causal=causal)
+    torch.cuda.synchronize()
+    assert L.mmdit_workspace_status(ws) == 0
+    ll = base.f64(lse[end])
+    p = np.where(see[:, None, :], np.exp(scale * np.einsum("ihd,jd->ihj", ql, kl[:, 0]) - ll[:, :, None]), 0)
+    z = p * np.einsum("ihd,jd->ihj", gl, vl[:, 0])
+    refs = scale * np.einsum("ihj,jd->ihd", z, kl[:, 0]), scale * np.einsum("ihj,ihd->jd", z, ql), np.einsum("ihj,ihd->jd", p, gl)
+    # each weight is off by its score's and the lse's error and two roundings to bf16 (of p or dz and of the result); zeros add nothing
+    w = 4 * ((2 * d + 8) * base.U * np.abs(scale * np.einsum("ihd,jd->ihj", np.abs(ql), np.abs(kl[:, 0]))).max() + 2.0 ** -21)
+    size = p * np.einsum("ihd,jd->ihj", np.abs(gl), np.abs(vl[:, 0]))
+    each = 2.0 ** -8 + w + 2 * (last * group + m + d + 32) * base.U
+    tols = (scale * np.einsum("ihj,jd->ihd", size, np.abs(kl[:, 0])) * each, scale * np.einsum("ihj,ihd->jd", size, np.abs(ql)) * each,
+            np.einsum("ihj,ihd->jd", p, np.abs(gl)) * each)
+    for name, got, ref, tol in zip(("dq", "dk", "dv"), (dq[end], dk[:, 0], dv[:, 0]), refs, tols):
+        base.check(base.f64(got), ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref) + 1e-30, name)
+    for i in range(0, n - last, 1 << 22):
+        assert not dq[i:min(i + (1 << 22), n - last)].any()

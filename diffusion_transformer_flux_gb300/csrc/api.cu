@@ -3159,7 +3159,8 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
   a.k_pages = pages_view(k), a.v_pages = pages_view(v);
   a.tables = tables, a.kv_lens = kv_lens, a.table_width = table_width, a.n_pages = n_pages, a.max_keys = most;
   a.page_shift = log2_of(page_size), a.page_rows = std::min(page_size, 128);
-  a.few_rows = p.few ? kFewRows : 0, a.few_ctas = p.few_ctas, a.few_whole = p.few_whole, a.few_join_rows = p.few_join_rows;
+  a.few_rows = p.few ? kFewRows : 0, a.few_tokens = a.few_rows / a.group;
+  a.few_ctas = p.few_ctas, a.few_whole = p.few_whole, a.few_join_rows = p.few_join_rows;
   a.split_keys = p.split_keys;
   a.few_part = at<float>(workspace, p.few_part), a.few_lse = at<float>(workspace, p.few_lse);
   if (p.splits > 1) a.part = at<float>(workspace, p.part), a.part_lse = at<float>(workspace, p.lse);

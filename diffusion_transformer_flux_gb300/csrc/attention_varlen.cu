@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pieces = PAGED ? kSeqTile / a.page_rows : 1;
     TileOrder order;
     order.init(a.cu_q, a.tokens_q, PAGED ? nullptr : a.cu_k, a.tokens_k, a.batch, 2 * a.tile_tokens, a.causal, 1,
-               PAGED ? a.few_rows / a.group : 0);
+               PAGED ? a.few_tokens : 0);
     const int per_split = order.n * a.hk, items = per_split * a.splits;
     uint32_t q_turn = 0, k_turn = 0, v_turn = 0;  // the next phases' parities; k, v: a bit for each stage
     uint32_t k_used = 0, v_used = 0;

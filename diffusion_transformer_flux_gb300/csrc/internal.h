@@ -474,6 +474,7 @@ struct SeqAttnArgs {
   const int *tables, *kv_lens;
   int table_width, n_pages, page_shift, page_rows, max_keys;  // page_rows: rows of a copied piece, at most 128
   int few_rows;  // sequences of at most that many rows (tokens by the group's heads) are paged_few_kernel's: kFewRows or 0
+  int few_tokens;  // the same in tokens, few_rows / group: a sequence's rows may be more than 32 bits count
   int few_ctas, few_whole;   // its CTAs; whether each takes one sequence and key head
   int few_behind;            // the tile kernel runs before it
   int join_beside;           // paged_few_join_kernel runs before paged_join_kernel

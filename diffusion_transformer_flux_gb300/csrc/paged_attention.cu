@@ -94,8 +94,7 @@ __device__ __forceinline__ uint32_t few_at(int r, int c) {
 __device__ __forceinline__ int steps_of(const SeqAttnArgs& a, int b) {
   const int lo = min(max(a.cu_q[b], 0), a.tokens_q), hi = min(max(a.cu_q[b + 1], 0), a.tokens_q);
   const int m = min(max(a.kv_lens[b], 0), a.max_keys);  // read beside the others, not behind their test
-  const int rows = (hi - lo) * a.group;
-  return rows <= 0 || rows > kFewRows ? 0 : max((m + kFewStep - 1) / kFewStep, 1);
+  return hi <= lo || hi - lo > a.few_tokens ? 0 : max((m + kFewStep - 1) / kFewStep, 1);
 }
 __device__ __forceinline__ int counted(int steps) { return steps > 0 ? steps + kFewStart : 0; }
 // Their number up to sequence `until` (all: batch), by all lanes of a warp.
@@ -427,7 +426,7 @@ __device__ __forceinline__ void few_share(const SeqAttnArgs& a, const CUtensorMa
   if (a.few_whole) {
     const int hk = blockIdx.x % a.hk, b = blockIdx.x / a.hk;
     segment(b);
-    if (seg.n == 0 || seg.n * a.group > kFewRows) return;
+    if (seg.n == 0 || seg.n > a.few_tokens) return;
     if (seg.n * a.group <= 8)
       few_rows<D, 1>(a, tm_k, tm_v, smem, sh, turns, seg, b, hk, 0, seg.m, -1);
     else
@@ -574,7 +573,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_few_join_kernel(const _
   const int b = blockIdx.x / a.hk, hk = blockIdx.x % a.hk;
   Segment seg;
   clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
-  const int rows = seg.n * a.group, steps = steps_of(a, b);
+  const int steps = steps_of(a, b), rows = steps > 0 ? seg.n * a.group : 0;
   const int run = run_length(a, steps_before(a, a.batch)), first = steps_before(a, b);
   const int run0 = (first + kFewStart) / run, run1 = (first + kFewStart + steps - 1) / run;
   pdl_wait();
@@ -678,7 +677,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   if (tok < a.tokens_q) {
     Segment seg;
     clip_segment(a.cu_q, b, a.tokens_q, seg.q0, seg.n);
-    if (tok >= seg.q0 && tok < seg.q0 + seg.n && seg.n * a.group > a.few_rows)
+    if (tok >= seg.q0 && tok < seg.q0 + seg.n && seg.n > a.few_tokens)
       parts = (min(max(a.kv_lens[b], 0), a.max_keys) + a.split_keys - 1) / a.split_keys;
   }
   // No thread returns without waiting (see paged_few_join_kernel).  Behind that one, which let this one start when the tile kernel

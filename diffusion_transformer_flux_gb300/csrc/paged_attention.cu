@@ -233,7 +233,6 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
   }
   float o[N][D / 16][4];
   float m_run[N][2], l_run[N][2];
-  uint32_t saw = 0;  // a bit for each of this lane's 2 N rows: it sees one of this lane's keys (that has a page)
 #pragma unroll
   for (int n = 0; n < N; ++n) {
 #pragma unroll
@@ -278,13 +277,8 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = key0 + g + 8 * (e >> 1);
-          if (key >= lim[n][e & 1] || (lost >> (e >> 1) & 1u))
-            s[n][e] = -INFINITY;
-          else
-            saw |= 1u << (2 * n + (e & 1));
+          if (key >= lim[n][e & 1] || (lost >> (e >> 1) & 1u)) s[n][e] = -INFINITY;
         }
-    } else {
-      saw = ~0u;
     }
     bool up = false;
 #pragma unroll
@@ -348,13 +342,6 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], x);
-#pragma unroll
-  for (int x = 4; x < 32; x <<= 1) saw |= __shfl_xor_sync(0xffffffffu, saw, x);
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (m_run[n][e] == -INFINITY && l_run[n][e] == 0.f && (saw >> (2 * n + e) & 1u)) m_run[n][e] = kNoWeights;
   __syncthreads();
   if (*reinterpret_cast<volatile int*>(&sh->abort_flag)) return false;
   float* parts = reinterpret_cast<float*>(smem);
@@ -381,12 +368,20 @@ __device__ __forceinline__ bool few_rows(const SeqAttnArgs& a, const CUtensorMap
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
       const float* p = parts + w * kFewRows * (D + 2);
-      // no maximum: no keys, and zeros, or scores that are all NaN, and NaN (all -inf: kNoWeights and zeros)
+      // no maximum: no keys or scores that are all -inf, and zeros, or scores that are all NaN, and NaN
       const float e = p[r * 2] == -INFINITY ? 1.f : fast_exp2(p[r * 2] - top);
       const float2 v = *reinterpret_cast<const float2*>(p + 2 * kFewRows + r * D + col);
       sum += e * p[r * 2 + 1], x += e * v.x, y += e * v.y;
     }
-    const bool no_weights = sum == 0.f && top == kNoWeights;
+    bool no_weights = false;  // no sum: does the row see a key that has a page?  (A warp's lanes work on one row.)
+    if (sum == 0.f) {
+      const int end = min(keys_seen(seg, r / a.group, a.causal), k_end);
+      for (int p0 = k_begin >> a.page_shift; end > k_begin && (p0 << a.page_shift) < end; p0 += 32) {
+        const int p = p0 + lane;
+        no_weights |= (p << a.page_shift) < end && static_cast<unsigned>(table[p]) < static_cast<unsigned>(a.n_pages);
+      }
+      no_weights = __any_sync(0xffffffffu, no_weights);
+    }
     const float inv = sum == 0.f ? (no_weights && part < 0 ? __int_as_float(0x7FC00000) : 0.f) : 1.f / sum;
     x *= inv, y *= inv;
     if (sh->any_bad) {

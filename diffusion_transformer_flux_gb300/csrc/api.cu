@@ -2932,13 +2932,17 @@ AttnBwdPlan plan_attention_bwd(int64_t tokens_q, int heads_q, int head_dim) {
   p.total = c.off;
   return p;
 }
-// Parts of the queries of a key tile.  The tiles of 128 keys by key heads are the work items; where they are fewer than two
-// for each SM, parts of their queries are, as long as the parts' sums have room.  All kernels together: 4096 tokens of 16 + 1
-// heads, 32 tiles, 986 us undivided and 229 in eight parts; 2048 of 32 + 8 heads, 128 tiles, 172 and 142; 9 documents of up to
-// 2041, 312 tiles, 254 and 285 (the pass over queries fills the SMs that run out of key tiles).
+// Parts of the queries of a key tile.  The tiles of 128 keys by key heads are the work items; where they are few for the GPU's
+// 152 SMs, parts of their queries are, about two for each SM, as long as the parts' sums have room.  All kernels together, undivided
+// and in parts, causal: 4096 tokens of 16 + 1 heads, 32 tiles, 986 us and 229 (eight parts); 2048 of 32 + 8 heads, 128 tiles, 172
+// and 142; 2560, 160 tiles, 216 and 207; 5632 of 16 + 4 heads, 176 tiles, 410 and 389; 2816 of 32 + 8, 176 tiles, 232 and 237; 3056,
+// 192 tiles, 248 and 268; 3328, 208 tiles, 280 and 305; 4096, 256 tiles, 397 and 430: from 192 on they are not cut, as the pass
+// over queries fills the SMs that run out of key tiles.
+constexpr int64_t kPartItems = 192;
 int attention_bwd_parts(const AttnBwdPlan& p, int64_t tokens_k, int heads_k, int head_dim) {
   const int64_t items = std::max<int64_t>(1, (tokens_k + 127) / 128 * heads_k), d = head_dim <= 64 ? 64 : 128;
   const int64_t wanted = (2 * 152 + items - 1) / items, room = static_cast<int64_t>(p.part_floats) / std::max<int64_t>(1, tokens_k * heads_k * 2 * d);
+  if (items >= kPartItems) return 1;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(wanted, room), 32)));
 }
 

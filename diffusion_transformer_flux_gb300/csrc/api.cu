@@ -2916,9 +2916,12 @@ SeqAttnArgs attention_args(int32_t batch, int32_t tokens_q, int32_t heads_q, int
   return a;
 }
 
-// The workspace of the gradients: two floats a row, and up to kPartTokens queries room for the sums of key tiles whose queries
-// are worked on in parts (as many floats as q has elements; longer calls have key tiles enough for the GPU's 152 SMs).
-constexpr int kPartTokens = 16384;
+// The gradients' pass over keys has tiles of 128 keys by key heads for its work items; below kPartItems of them the queries of a
+// tile are worked on in parts, about kPartTarget in all (see attention_bwd_parts).
+constexpr int64_t kPartItems = 192, kPartTarget = 2 * 152;
+// The workspace of the gradients: two floats a row, and room for the parts' sums: 128 keys by 2 d floats each, and with the last
+// round of them fewer than kPartTarget + kPartItems parts; calls of fewer rows have room for as many floats as q has elements.  It
+// never shrinks as a call grows, so that a workspace serves all calls of fewer queries, and parts depend on the keys alone.
 struct AttnBwdPlan {
   size_t sums, part, part_floats, total;
 };
@@ -2927,7 +2930,7 @@ AttnBwdPlan plan_attention_bwd(int64_t tokens_q, int heads_q, int head_dim) {
   Carver c;
   const size_t rows = static_cast<size_t>(tokens_q) * heads_q;
   p.sums = c.take(rows * sizeof(float2));
-  p.part_floats = tokens_q <= kPartTokens ? rows * (head_dim <= 64 ? 64 : 128) : 0;
+  p.part_floats = std::min<size_t>(rows, (kPartTarget + kPartItems) * 256) * (head_dim <= 64 ? 64 : 128);
   p.part = c.take(p.part_floats * sizeof(float));
   p.total = c.off;
   return p;
@@ -2937,11 +2940,10 @@ AttnBwdPlan plan_attention_bwd(int64_t tokens_q, int heads_q, int head_dim) {
 // and in parts, causal: 4096 tokens of 16 + 1 heads, 32 tiles, 986 us and 229 (eight parts); 2048 of 32 + 8 heads, 128 tiles, 172
 // and 142; 2560, 160 tiles, 216 and 207; 5632 of 16 + 4 heads, 176 tiles, 410 and 389; 2816 of 32 + 8, 176 tiles, 232 and 237; 3056,
 // 192 tiles, 248 and 268; 3328, 208 tiles, 280 and 305; 4096, 256 tiles, 397 and 430: from 192 on they are not cut, as the pass
-// over queries fills the SMs that run out of key tiles.
-constexpr int64_t kPartItems = 192;
+// over queries fills the SMs that run out of key tiles.  Without a mask, 20000 queries over 512 keys, 32 tiles: 1273 and 639.
 int attention_bwd_parts(const AttnBwdPlan& p, int64_t tokens_k, int heads_k, int head_dim) {
   const int64_t items = std::max<int64_t>(1, (tokens_k + 127) / 128 * heads_k), d = head_dim <= 64 ? 64 : 128;
-  const int64_t wanted = (2 * 152 + items - 1) / items, room = static_cast<int64_t>(p.part_floats) / std::max<int64_t>(1, tokens_k * heads_k * 2 * d);
+  const int64_t wanted = (kPartTarget + items - 1) / items, room = static_cast<int64_t>(p.part_floats) / std::max<int64_t>(1, tokens_k * heads_k * 2 * d);
   if (items >= kPartItems) return 1;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(wanted, room), 32)));
 }

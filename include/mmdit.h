@@ -873,7 +873,7 @@ mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t
  * query row whose q, dout or out is not finite can make the gradients of the keys it sees NaN, a key row whose k or v is not
  * those of the queries that see it; what a row does not see never reaches it.  heads_q at most 64 times heads_k.
  * workspace >= mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) (row sums and partial sums: calls that
- * share one are ordered on one stream). */
+ * share one are ordered on one stream); one that is enough for a call is for every call of fewer queries. */
 size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim);
 mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,
                                         int32_t head_dim, int32_t causal, float scale, const mmdit_heads_view *dout,

@@ -189,3 +189,14 @@ def test_view_checks():
         L._heads_view("x", c, dev)
     with pytest.raises(ValueError, match="meta"):
         L._heads_view("x", x, torch.device("meta"))
+
+
+def test_varlen_bwd_workspace_serves_smaller_calls(lib):
+    """It never shrinks as a call grows, also past 16384 queries."""
+    size = L.mmdit_varlen_attention_bwd_workspace_size
+    for heads, d in ((1, 64), (4, 8), (32, 128), (24, 64), (128, 128)):
+        sizes = [size(t, heads, d) for t in (0, 1, 7, 128, 1000, 2048, 4096, 8191, 8192, 16383, 16384, 16385, 20000, 65536, 1 << 20)]
+        assert sizes == sorted(sizes)
+        assert sizes[1] >= 256 + 8 * heads
+    assert [size(5000, h, 64) for h in (1, 2, 3, 16)] == sorted(size(5000, h, 64) for h in (1, 2, 3, 16))
+    assert size(5000, 8, 64) <= size(5000, 8, 72) == size(5000, 8, 128)

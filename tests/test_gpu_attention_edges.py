@@ -201,3 +201,9 @@ def test_gradients_of_more_rows_than_31_bits_count(causal):
         base.check(base.f64(got), ref, tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref) + 1e-30, name)
     for i in range(0, n - last, 1 << 22):
         assert not dq[i:min(i + (1 << 22), n - last)].any()
+
+
+def test_gradients_of_many_queries_over_few_keys():
+    """More than 16384 queries: their key tiles are worked on in parts as those of fewer are."""
+    rng = np.random.default_rng(5)
+    base.compare_gradients(*base.packed(rng, [17000, 40], [200, 40], 2, 1, 64, layout="dense"), False)

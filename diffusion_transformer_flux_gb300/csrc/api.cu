@@ -2954,30 +2954,40 @@ int attention_bwd_parts(const AttnBwdPlan& p, int64_t tokens_k, int heads_k, int
 struct PagedPlan {
   int few, tiles;  // whether paged_few_kernel and the tile kernel run
   int few_ctas, few_whole, few_join_rows, split_keys, splits;
-  size_t few_part, few_lse, part, lse, total;
+  size_t few_part, few_lse, part, lse;
+  size_t least, total;  // bytes without which the call cannot be made; those asked for
 };
 // The keys of one part of an item of the tile kernel, where `items` over `keys` keys each are worked on by `sms` CTAs, longest
 // parts first: the length that ends first, counted in keys.  A part costs 384 keys more than its own (its start and end) and
 // the writing and adding of it `join`.  Parts of one length end in whole rounds; or, where items are fewer than CTAs, w long
 // parts of f keys take a CTA each and the CTAs left over work on c short ones of g each meanwhile: f + 384 = c (g + 384), w f + g
 // = keys.  (1000 tokens of 32 + 8 heads over 32000 keys, 128 items: whole 393 us, 2 equal parts 420, one of 6/7 and one of 1/7 364.)
-int64_t split_length(int64_t items, int64_t sms, int64_t keys, double join) {
+// `parts`: at most so many; how many it is.
+int64_t split_length(int64_t items, int64_t sms, int64_t keys, double join, int64_t* parts) {
   const double own = 384, k = static_cast<double>(keys);
   double best = static_cast<double>((items + sms - 1) / sms) * (k + own);
   int64_t length = keys;
-  auto take = [&](double cost, double f) {
-    if (cost < 0.98 * best) best = cost, length = std::min(keys, static_cast<int64_t>(f) + 1);
+  const int64_t most = *parts;
+  *parts = 1;
+  auto take = [&](double cost, double f, int64_t n) {
+    if (cost < 0.98 * best) best = cost, length = std::min(keys, static_cast<int64_t>(f) + 1), *parts = n;
   };
   for (int64_t w = 1; w <= std::min<int64_t>(keys / 512, 64); ++w) {
-    if (w > 1) take(static_cast<double>((items * w + sms - 1) / sms) * (k / w + own) + w * join, k / w);
+    if (w > 1 && w <= most) take(static_cast<double>((items * w + sms - 1) / sms) * (k / w + own) + w * join, k / w, w);
     const int64_t left = sms - items * w;
-    if (left <= 0) continue;
+    if (left <= 0 || w + 1 > most) continue;
     const double c = static_cast<double>((items + left - 1) / left), f = (c * k + (c - 1) * own) / (1 + c * w);
-    if (k - w * f >= 256) take(f + own + (w + 1) * join, f);
+    if (k - w * f >= 256) take(f + own + (w + 1) * join, f, w + 1);
   }
   return length;
 }
-PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, int head_dim, int64_t max_q, int64_t max_kv) {
+// A workspace of `have` bytes: the parts of the tile kernel's items are as many as it has room for, so that one made for a call serves
+// every call of fewer tokens, requests and keys, whose own wish may be larger (4096 tokens over 32000 keys are worked on in two parts,
+// 8192 in one).  What is asked for has room for kLeastRows rows of parts: two for each of the 152 pairs of tiles that a full round
+// has, which is about what calls of fewer items than SMs want.
+constexpr int64_t kLeastRows = 2 * 152 * 256;
+PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, int head_dim, int64_t max_q, int64_t max_kv,
+                     size_t have = SIZE_MAX) {
   PagedPlan p = {};
   const int group = heads_q / heads_k, d = head_dim <= 64 ? 64 : 128;
   const int64_t sms = 152;
@@ -2986,7 +2996,7 @@ PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, 
   p.splits = 1;
   max_kv = std::max<int64_t>(max_kv, 1);
   Carver c;
-  if (p.few) {
+  {  // where the call has no sequences of few rows a smaller one may
     const int64_t steps = (max_kv + kFewStep - 1) / kFewStep, all = batch * heads_k;
     p.few_whole = steps <= kFewWhole;
     const int64_t runs = std::min(std::max<int64_t>(2 * sms / heads_k, 1), (batch * (steps + kFewStart) + kFewLeast - 1) / kFewLeast);
@@ -2997,18 +3007,25 @@ PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, 
       p.few_part = c.take(rows * d * 4), p.few_lse = c.take(rows * 4);
     }
   }
+  p.total = c.off;
+  if (!p.few) c = Carver();
+  p.least = c.off;
   if (p.tiles) {
     // beside the sequences of few rows a batch has few others: its tokens tell more of the items than its number
-    const int64_t items = (tokens_q / (2 * (128 / group)) + 1) * heads_k;
-    const int64_t keys = round_up(split_length(items, sms, max_kv, 78. * 8 / 6.7e6 * tokens_q * heads_q * d), 128);
+    const int64_t items = (tokens_q / (2 * (128 / group)) + 1) * heads_k, rows = tokens_q * heads_q, row_bytes = 4 * (d + 1);
+    const size_t room = have > c.off + 512 ? have - c.off - 512 : 0;
+    int64_t parts = static_cast<int64_t>(std::min<size_t>(room / (static_cast<size_t>(rows) * row_bytes), 65));
+    const int64_t keys = round_up(split_length(items, sms, max_kv, 78. * 8 / 6.7e6 * rows * d, &parts), 128);
     p.splits = static_cast<int>((max_kv + keys - 1) / keys);
     p.split_keys = p.splits > 1 ? static_cast<int>(keys) : 0;
+    const int64_t least_rows = max_kv < 512 ? 0 : std::min(tokens_q * group * (sms + heads_k), kLeastRows);
+    p.total = std::max(p.total + round_up(static_cast<size_t>(least_rows * row_bytes) + 512, 256),
+                       p.least + round_up(static_cast<size_t>(parts > 1 ? parts * rows * row_bytes : 0) + 512, 256));
+    if (p.splits > 1) {
+      const size_t all = static_cast<size_t>(p.splits) * rows;
+      p.part = c.take(all * d * 4), p.lse = c.take(all * 4);
+    }
   }
-  if (p.splits > 1) {
-    const size_t rows = static_cast<size_t>(p.splits) * tokens_q * heads_q;
-    p.part = c.take(rows * d * 4), p.lse = c.take(rows * 4);
-  }
-  p.total = c.off;
   return p;
 }
 }  // namespace
@@ -3144,13 +3161,13 @@ mmdit_status mmdit_paged_attention_fwd(int32_t batch, int32_t tokens_q, int32_t 
   const int64_t reach = static_cast<int64_t>(table_width) * page_size;
   if (reach > (1 << 30)) return fail(MMDIT_ERR_UNSUPPORTED, "%s: table_width page_size must be at most 2^30", what);
   const int most = static_cast<int>(max_kv > 0 ? std::min<int64_t>(max_kv, reach) : reach);
-  const PagedPlan p = plan_paged(std::max(tokens_q, 1), std::max(batch, 1), heads_q, heads_k, head_dim, max_q, most);
+  const PagedPlan p = plan_paged(std::max(tokens_q, 1), std::max(batch, 1), heads_q, heads_k, head_dim, max_q, most, workspace_bytes);
   if (p.few && ((p.few_whole && static_cast<int64_t>(batch) * heads_k > INT32_MAX / 2) ||
                 batch * ((most + kFewStep - 1LL) / kFewStep + 1 + kFewStart) > INT32_MAX))
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: batch (max_kv / %d + 5) must be below 2^31", what, kFewStep);
   if ((tokens_q / (2 * (128 / (heads_q / heads_k))) + static_cast<int64_t>(batch)) * heads_k * p.splits > INT32_MAX / 2)
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
-  if ((s = check_workspace(workspace, workspace_bytes, batch == 0 || tokens_q == 0 ? kStatusBytes : p.total)) != MMDIT_OK) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, batch == 0 || tokens_q == 0 ? kStatusBytes : p.least)) != MMDIT_OK) return s;
   if (batch == 0 || tokens_q == 0 || max_q == 0) return MMDIT_OK;
   if ((s = check_heads(what, "q", q, tokens_q, heads_q, head_dim, false)) != MMDIT_OK) return s;
   if ((s = check_pages(what, "k", k, n_pages, page_size, heads_k, head_dim, false)) != MMDIT_OK) return s;

@@ -895,7 +895,8 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
  * out [tokens_q, heads_q, head_dim]; lse NULL or [tokens_q, heads_q] fp32.  The same bits from call to call.
  * workspace >= mmdit_paged_attention_workspace_size(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv), with
  * the call's max_kv, or table_width page_size where that is 0 or less than it (parts of split sequences: calls that share one
- * are ordered on one stream). */
+ * are ordered on one stream).  One made for a call of as many tokens, requests and keys or more (of the same heads, tables as wide)
+ * also serves; where it is less than the call's own, sequences are split into fewer parts. */
 typedef struct mmdit_pages_view {
   void *ptr;
   int64_t stride_page, stride_t, stride_h;

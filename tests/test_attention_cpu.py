@@ -200,3 +200,26 @@ def test_varlen_bwd_workspace_serves_smaller_calls(lib):
         assert sizes[1] >= 256 + 8 * heads
     assert [size(5000, h, 64) for h in (1, 2, 3, 16)] == sorted(size(5000, h, 64) for h in (1, 2, 3, 16))
     assert size(5000, 8, 64) <= size(5000, 8, 72) == size(5000, 8, 128)
+
+
+# (tokens, batch, heads_q, heads_k, head_dim, max_q, max_kv) of calls that grow; each serves all before it
+GROWING = [
+    [(1, 1, 32, 8, 128, 1, 100), (1, 1, 32, 8, 128, 1, 32000), (300, 1, 32, 8, 128, 300, 32000), (1000, 1, 32, 8, 128, 1000, 32000),
+     (4096, 1, 32, 8, 128, 4096, 32000), (8192, 1, 32, 8, 128, 8192, 32000), (8192, 1, 32, 8, 128, 8192, 200000)],
+    [(8, 8, 28, 4, 64, 1, 500), (40, 40, 28, 4, 64, 1, 5000), (371, 40, 28, 4, 64, 333, 5000), (6000, 40, 28, 4, 64, 6000, 5000)],
+    [(64, 64, 16, 1, 96, 1, 600), (64, 64, 16, 1, 96, 64, 16384), (2600, 64, 16, 1, 96, 700, 16384), (20000, 64, 16, 1, 96, 20000, 16384)],
+]
+
+
+@pytest.mark.parametrize("calls", GROWING)
+def test_paged_workspace_serves_smaller_calls(lib, calls):
+    """What a call asks for is enough for every call of fewer tokens, requests and keys, whatever these would ask for."""
+    size = L.mmdit_paged_attention_workspace_size
+    for i, large in enumerate(calls):
+        for t, b, hq, hk, d, max_q, max_kv in calls[:i + 1]:
+            kw = dict(batch=b, tq=t, hq=hq, hk=hk, d=d, max_q=max_q, max_kv=max_kv, width=1 << 14, ws_bytes=size(*large))
+            # the check of q comes behind the workspace's
+            assert _paged(lib, q=None, **kw) == INVALID and "q is NULL" in L.last_error(), (large, kw)
+    for t, b, hq, hk, d, max_q, max_kv in calls:
+        kw = dict(batch=b, tq=t, hq=hq, hk=hk, d=d, max_q=max_q, max_kv=max_kv, width=1 << 14)
+        assert _paged(lib, q=None, ws_bytes=0, **kw) == WORKSPACE

@@ -207,3 +207,33 @@ def test_gradients_of_many_queries_over_few_keys():
     """More than 16384 queries: their key tiles are worked on in parts as those of fewer are."""
     rng = np.random.default_rng(5)
     base.compare_gradients(*base.packed(rng, [17000, 40], [200, 40], 2, 1, 64, layout="dense"), False)
+
+
+@pytest.mark.parametrize("new,total,large", [([130], [9000], (1500, 1, 9000)), ([1, 40, 2], [6000, 5000, 33], (6000, 3, 6000)),
+                                             ([130], [9000], None), ([1, 4], [20000, 700], (300, 2, 20000))])
+def test_paged_workspaces_of_other_calls(new, total, large):
+    """One made for a larger call, or with no room for parts of the tiles (large: None), serves: no byte behind it is touched, and
+    with its own or more the bits are the same."""
+    rng = np.random.default_rng(len(new))
+    hq, hk, d = 16, 4, 64
+    case = base.paged(rng, new, total, hq, hk, d, 16)
+    tables = torch.cat((case[3], torch.full((len(new), 2000 - case[3].shape[1]), -1, dtype=torch.int32, device="cuda")), 1)
+    case = (*case[:3], tables, *case[4:])
+    kv = max(total)
+    own = L.mmdit_paged_attention_workspace_size(sum(new), len(new), hq, hk, d, max(new), kv)
+    other = 256 if large is None else L.mmdit_paged_attention_workspace_size(large[0], large[1], hq, hk, d, large[0], large[2])
+
+    def run(size):
+        ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        out = base.run_paged(case, max_q=max(new), max_kv=kv, ws=ws[:size])
+        assert (ws[size:] == 0xA5).all()
+        return out
+
+    ref = run(own)
+    again = run(own + (1 << 20))
+    assert torch.equal(ref[0], again[0]) and torch.equal(ref[1], again[1])
+    out, lse = run(other)
+    # both are within the bounds that base.compare_paged checks; here one against the other: roundings of the weights and of the result
+    assert ((out.double() - ref[0].double()).abs() <= 2.0 ** -6 * ref[0].double().abs() + 2.0 ** -6).all()
+    assert ((lse - ref[1]).abs() <= 2.0 ** -8).all()  # twice the sums of up to 20000 terms, 2^-24 each
+    base.compare_paged(case, max_q=max(new), max_kv=kv)

@@ -238,7 +238,7 @@ __device__ __forceinline__ void rows_role(Barriers* sb, uint8_t* smem, uint32_t 
     uint64_t neg_l = 0, neg_d = 0;
     if constexpr (!KEYS) {
       float2 s = make_float2(0.f, 0.f);
-      if (valid) s = a.sums[(static_cast<size_t>(w.seg.q0) + tok) * a.hq + w.hk * G + row_head];
+      if (valid) s = __ldcg(&a.sums[(static_cast<size_t>(w.seg.q0) + tok) * a.hq + w.hk * G + row_head]);  // see `behind` below
       neg_l = f32x2(-s.x, -s.x), neg_d = f32x2(-s.y, -s.y);
     }
     if (C::kFInTmem && w.count > 0) {
@@ -451,7 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sb->tmem_slot;
   // The pass over queries reads nothing that the one over keys writes: it takes the SMs that run out of the other's items, and
-  // only its end waits for that one's.
+  // only its end waits for that one's.  What it reads of this call's, the row sums and the counter, was complete when that one's CTAs
+  // let this one start; it reads them in L2 (__ldcg, an atomic), where they are, as no wait of its own makes them visible to an SM.
   const bool behind = !KEYS && a.tokens_k > 0;
   if (!behind) pdl_wait();
   pdl_trigger();

@@ -453,7 +453,7 @@ __device__ __forceinline__ void store32(float* p, const float (&v)[32]) {
 // Kernels are launched with programmatic stream serialization (launch_pdl in internal.h), so a
 // kernel's CTAs may be scheduled, and run their set-up, while the previous kernel in the stream
 // finishes.  pdl_wait() blocks until that kernel has completed and its memory is visible (a
-// no-op when there is none); every kernel calls it before it touches global memory.
+// no-op when there is none); every kernel calls it before it touches global memory, but for those named at launch_pdl.
 // pdl_trigger() lets the next kernel in the stream begin launching.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {

@@ -95,7 +95,11 @@ struct GemmProblem {
 // wait for whatever the caller enqueued before it: copies, memsets, other libraries' kernels),
 // and each later kernel of the call launches with programmatic stream serialization, so it may
 // be scheduled while the call's previous kernel finishes.  Every kernel calls pdl_wait()
-// (common.cuh) before it touches global memory, so results are those of ordinary launches.
+// (common.cuh) before it touches what a kernel of its call wrote, so results are those of ordinary launches.  Two read such
+// data ahead of their wait, in L2, after a chain of waits by the kernels between (seq_attention_bwd_kernel over queries,
+// paged_join_kernel); they and paged_few_kernel, paged_few_join_kernel and seq_parts_kernel read the call's inputs ahead of it,
+// which were there before the call's first kernel, an ordinary launch.  No kernel ends without waiting: the one behind it
+// may rely on all before.
 void pdl_begin_call();
 bool pdl_next_launch();  // false for the call's first launch, true afterwards
 

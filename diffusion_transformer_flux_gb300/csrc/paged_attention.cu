@@ -614,25 +614,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_few_join_kernel(const _
   }
 }
 
-// A row's parts of the tile kernel, by eight lanes.
+// A row's parts of the tile kernel, by eight lanes.  Read in L2: see paged_join_kernel.
 template <int D>
 __device__ __forceinline__ void add_tile_parts(const SeqAttnArgs& a, int64_t item, int tok, int head, int lane, int parts) {
   constexpr int kCols = D / 32;  // float4 of a lane
   const size_t stride = static_cast<size_t>(a.tokens_q) * a.hq;
   float top = -INFINITY;
 #pragma unroll 4
-  for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_lse[p * stride + item]);
+  for (int p = 0; p < parts; ++p) top = fmaxf(top, __ldcg(&a.part_lse[p * stride + item]));
   float sum = 0.f;
   float4 v[kCols];
 #pragma unroll
   for (int i = 0; i < kCols; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
   for (int p = 0; p < parts; ++p) {
-    const float l = a.part_lse[p * stride + item];
+    const float l = __ldcg(&a.part_lse[p * stride + item]);
     const float4* src = reinterpret_cast<const float4*>(a.part + (p * stride + item) * D) + lane;
     float4 u[kCols];
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) u[i] = src[8 * i];
+    for (int i = 0; i < kCols; ++i) u[i] = __ldcg(src + 8 * i);
     if (l == -INFINITY) continue;  // no keys: counts for nothing; a NaN reaches the output
     const float e = fast_exp2(l - top);
     sum += e;
@@ -676,7 +676,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
       parts = (min(max(a.kv_lens[b], 0), a.max_keys) + a.split_keys - 1) / a.split_keys;
   }
   // No thread returns without waiting (see paged_few_join_kernel).  Behind that one, which let this one start when the tile kernel
-  // had ended, the two work beside one another and the end waits.
+  // had ended, the two work beside one another and the end waits: the parts are complete, and are read in L2, as no wait of this
+  // kernel's has made them visible to its SM.
   if (!a.join_beside) pdl_wait();
   if (parts > 1) add_tile_parts<D>(a, item, tok, head, lane, parts);
   if (a.join_beside) pdl_wait();

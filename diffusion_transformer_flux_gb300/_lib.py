@@ -1074,7 +1074,8 @@ def mmdit_varlen_attention_workspace_size(tokens_q, heads_q, head_dim) -> int:
 def mmdit_varlen_attention_fwd(q, k, v, out, cu_q, cu_k=None, lse=None, causal=True, scale=None, ws=None, stream=None):
     """Attention over packed sequences: q, out [Tq, Hq, d], k, v [Tk, Hk, d] bf16 (views with adjacent head elements);
     sequence b's queries are rows cu_q[b] .. cu_q[b + 1] (int32 [B + 1]), its keys rows cu_k[b] .. (cu_q's without cu_k).
-    lse [Tq, Hq] fp32 for the backward; scale 1 / sqrt(d) by default."""
+    lse [Tq, Hq] fp32 for the backward; scale 1 / sqrt(d) by default.  Calls that share a ws must be ordered on one stream
+    (as for the gradients and mmdit_paged_attention_fwd): it holds the counter that hands out the work."""
     dev = _device(q)
     vq = _heads_view("q", q, dev)
     Tq, Hq, d = q.shape

@@ -857,8 +857,8 @@ typedef struct mmdit_heads_view {
 } mmdit_heads_view;
 
 /* out [tokens_q, heads_q, head_dim]; lse NULL, or [tokens_q, heads_q] fp32 (for the backward).
- * workspace >= mmdit_varlen_attention_workspace_size(tokens_q, heads_q, head_dim) (the status word).
- * The same bits from call to call. */
+ * workspace >= mmdit_varlen_attention_workspace_size(tokens_q, heads_q, head_dim) (256 bytes: the status word and the counter that
+ * hands out the work; calls that share one are ordered on one stream, or rows are left out).  The same bits from call to call. */
 size_t mmdit_varlen_attention_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim);
 mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,
                                         int32_t head_dim, int32_t causal, float scale, const mmdit_heads_view *q,
@@ -872,8 +872,8 @@ mmdit_status mmdit_varlen_attention_fwd(int32_t batch, int32_t tokens_q, int32_t
  * were.  Sums in float32 in a fixed order: the same bits from call to call.  p and dz enter the products rounded to bf16.  A
  * query row whose q, dout or out is not finite can make the gradients of the keys it sees NaN, a key row whose k or v is not
  * those of the queries that see it; what a row does not see never reaches it.  heads_q at most 64 times heads_k.
- * workspace >= mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) (row sums and partial sums: calls that
- * share one are ordered on one stream); one that is enough for a call is for every call of fewer queries. */
+ * workspace >= mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim) (row sums, partial sums and counters: calls
+ * that share one are ordered on one stream); one that is enough for a call is for every call of fewer queries. */
 size_t mmdit_varlen_attention_bwd_workspace_size(int32_t tokens_q, int32_t heads_q, int32_t head_dim);
 mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t tokens_k, int32_t heads_q, int32_t heads_k,
                                         int32_t head_dim, int32_t causal, float scale, const mmdit_heads_view *dout,
@@ -894,8 +894,8 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
  * work is split; the device's lengths may change between launches of a captured graph.  batch (max_kv / 64 + 5) below 2^31.
  * out [tokens_q, heads_q, head_dim]; lse NULL or [tokens_q, heads_q] fp32.  The same bits from call to call.
  * workspace >= mmdit_paged_attention_workspace_size(tokens_q, batch, heads_q, heads_k, head_dim, max_q, max_kv), with
- * the call's max_kv, or table_width page_size where that is 0 or less than it (parts of split sequences: calls that share one
- * are ordered on one stream).  One made for a call of as many tokens, requests and keys or more (of the same heads, tables as wide)
+ * the call's max_kv, or table_width page_size where that is 0 or less than it (parts of split sequences and the counter: calls that
+ * share one are ordered on one stream).  One made for a call of as many tokens, requests and keys or more (of the same heads, tables as wide)
  * also serves; where it is less than the call's own, sequences are split into fewer parts. */
 typedef struct mmdit_pages_view {
   void *ptr;

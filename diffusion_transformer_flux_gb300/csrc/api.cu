@@ -2900,6 +2900,8 @@ mmdit_status check_attention(const char* what, int32_t batch, int32_t tokens_q, 
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: at most 128 query heads to a key head and 65535 in all (got %d, %d)", what,
                 heads_q / heads_k, heads_q);
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MMDIT_ERR_INVALID_ARG, "%s: scale must be positive and finite", what);
+  // its reciprocal times a row's log-sum (gradients) and its product with log2(e) are to stay within float32
+  if (scale < 0x1p-100f || scale > 0x1p100f) return fail(MMDIT_ERR_UNSUPPORTED, "%s: scale must be from 2^-100 to 2^100", what);
   if (tokens_q > (1 << 30) || tokens_k > (1 << 30) || batch > (1 << 20))
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: at most 2^30 tokens and 2^20 sequences", what);
   // the CTAs: one for two tiles of 128 / group tokens and each key head

@@ -849,7 +849,7 @@ mmdit_status mmdit_rope_bwd(int32_t act, const mmdit_rope_cfg *cfg, int32_t batc
  * bf16.  A view is element (token, head, i) at ptr + token stride_t + head stride_h + i (elements; multiples of 8, at most
  * 2^36, not below head_dim where the extent is above one; ptr 16-byte aligned); a view that is written must not overlap
  * itself or another view of the call.  The views are host memory.  head_dim a multiple of 8, at most 128; heads_q a
- * multiple of heads_k, at most 128 times it and at most 65535; scale positive and finite; tokens at most 2^30, batch at
+ * multiple of heads_k, at most 128 times it and at most 65535; scale from 2^-100 to 2^100; tokens at most 2^30, batch at
  * most 2^20. */
 typedef struct mmdit_heads_view {
   void *ptr;

@@ -223,3 +223,12 @@ def test_paged_workspace_serves_smaller_calls(lib, calls):
     for t, b, hq, hk, d, max_q, max_kv in calls:
         kw = dict(batch=b, tq=t, hq=hq, hk=hk, d=d, max_q=max_q, max_kv=max_kv, width=1 << 14)
         assert _paged(lib, q=None, ws_bytes=0, **kw) == WORKSPACE
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd, _paged])
+def test_scales_outside_float32_reach(lib, call):
+    """1 / (scale log2(e)) times a log-sum, as the gradients form it, would overflow; 2^-100 and 2^100 pass to the next check."""
+    for scale in (1e-40, 1e-38, 2.0 ** -101, 2.0 ** 101, 3e38):
+        assert call(lib, scale=scale) == UNSUPPORTED and "2^-100" in L.last_error()
+    for scale in (2.0 ** -100, 2.0 ** 100):
+        assert call(lib, scale=scale, q=None) == INVALID and "q is NULL" in L.last_error()

@@ -323,11 +323,12 @@ __global__ void __launch_bounds__(kWriteThreads)
 }  // namespace
 
 cudaError_t launch_block_tables(const BlockTableArgs& a, cudaStream_t stream) {
-  const int map_here = a.capacity <= kMapInPlace || !(a.positions || a.slots) ? 1 : 0;
+  const bool places = a.positions || a.slots;
+  const int map_here = places && a.capacity <= kMapInPlace ? 1 : 0;
   cudaError_t e = launch_pdl(block_tables_kernel, dim3(1), dim3(kTableThreads), 0, stream, a, map_here);
   if (e != cudaSuccess) return e;
   count_launch();
-  if (!map_here) {
+  if (places && !map_here) {
     const int grid = static_cast<int>(std::min<int64_t>((a.capacity + 255) / 256, 8 * num_sms()));
     e = launch_pdl(token_map_kernel, dim3(grid), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;

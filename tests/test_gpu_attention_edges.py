@@ -237,3 +237,25 @@ def test_paged_workspaces_of_other_calls(new, total, large):
     assert ((out.double() - ref[0].double()).abs() <= 2.0 ** -6 * ref[0].double().abs() + 2.0 ** -6).all()
     assert ((lse - ref[1]).abs() <= 2.0 ** -8).all()  # twice the sums of up to 20000 terms, 2^-24 each
     base.compare_paged(case, max_q=max(new), max_kv=kv)
+
+
+def test_block_tables_whose_places_nobody_asks_for():
+    """The entry point without positions and slots, of a capacity that counts: prefix sums and pages, and no walk over the tokens."""
+    batch, page, capacity = 64, 1 << 14, 1 << 24
+    width = capacity // batch // page
+    before, after = base.ints([0] * batch), base.ints([capacity // batch - 3] * batch)
+    tables, free = torch.full((batch, width), -1, dtype=torch.int32, device="cuda"), torch.arange(batch * width, dtype=torch.int32, device="cuda")
+    n_free, after_n, cu, missing = base.ints([batch * width]), base.ints([7]), base.ints([7] * (batch + 1)), base.ints([7, 7])
+    best = float("inf")
+    for _ in range(4):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        L._launch("mmdit_block_tables", before.device, None, batch, page, width, batch * width, before.data_ptr(), after.data_ptr(),
+                  tables.data_ptr(), free.data_ptr(), n_free.data_ptr(), after_n.data_ptr(), cu.data_ptr(), capacity, None, None,
+                  missing.data_ptr())
+        end.record()
+        torch.cuda.synchronize()
+        best = min(best, start.elapsed_time(end))
+    assert cu.tolist() == [i * (capacity // batch - 3) for i in range(batch + 1)] and missing.tolist() == [0, 0] and after_n.tolist() == [0]
+    assert tables.flatten().tolist() == list(range(batch * width - 1, -1, -1))
+    assert best < 2.0, f"{best} ms"  # one CTA's few reads; the walk over the tokens took 13

@@ -3088,8 +3088,12 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
   if (s != MMDIT_OK) return s;
   if (heads_q / heads_k > kBwdMaxGroup)
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: at most 64 query heads to a key head (got %d)", what, heads_q / heads_k);
-  const int64_t tiles = std::max(tokens_k / 128, tokens_q / (128 / (heads_q / heads_k))) + static_cast<int64_t>(batch);
-  if (tiles * heads_k > INT32_MAX || static_cast<int64_t>(tokens_q) * heads_q > (int64_t{1} << 34))
+  const AttnBwdPlan plan = plan_attention_bwd(tokens_q, heads_q, head_dim);
+  const int parts = tokens_q > 0 ? attention_bwd_parts(plan, tokens_k, heads_k, head_dim) : 1;
+  // the passes' items, over keys and over queries
+  const int64_t items_k = (tokens_k / 128 + static_cast<int64_t>(batch)) * heads_k * parts,
+                items_q = (tokens_q / (128 / (heads_q / heads_k)) + static_cast<int64_t>(batch)) * heads_k;
+  if (std::max(items_k, items_q) > INT32_MAX / 2 || static_cast<int64_t>(tokens_q) * heads_q > (int64_t{1} << 34))
     return fail(MMDIT_ERR_UNSUPPORTED, "%s: too many tiles", what);
   if ((s = check_workspace(workspace, workspace_bytes, mmdit_varlen_attention_bwd_workspace_size(tokens_q, heads_q, head_dim))) !=
       MMDIT_OK)
@@ -3116,9 +3120,8 @@ mmdit_status mmdit_varlen_attention_bwd(int32_t batch, int32_t tokens_q, int32_t
   a.tile_tokens = seq_tile_tokens(a.group), a.unit_tokens = 64 / a.group;
   a.scale = scale, a.scale_log2 = scale * 1.4426950408889634f, a.minus_inv_scale = -1.f / a.scale_log2;
   a.cu_q = cu_q, a.cu_k = cu_k, a.lse = lse;
-  const AttnBwdPlan plan = plan_attention_bwd(std::max(tokens_q, 0), heads_q, head_dim);
   a.sums = at<float2>(workspace, plan.sums), a.part = at<float>(workspace, plan.part);
-  a.parts = tokens_q > 0 ? attention_bwd_parts(plan, tokens_k, heads_k, head_dim) : 1;
+  a.parts = parts;
   if (tokens_q > 0) a.q = heads_view(q), a.dout = heads_view(dout), a.out = heads_view(out), a.dq = heads_view(dq);
   if (tokens_k > 0) a.dk = heads_view(dk), a.dv = heads_view(dv);
   a.status = status_word(workspace), a.counters = a.status + 32;

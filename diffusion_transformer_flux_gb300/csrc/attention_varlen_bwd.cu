@@ -901,7 +901,6 @@ template <int D, bool KEYS>
 cudaError_t launch_pass(const SeqAttnBwdArgs& a, const SeqAttnBwdMaps& m, cudaStream_t stream) {
   const int64_t items =
       ((KEYS ? a.tokens_k / kSeqTile : a.tokens_q / a.tile_tokens) + static_cast<int64_t>(a.batch)) * a.hk * (KEYS ? a.parts : 1);
-  if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
   using C = Cfg<D, KEYS>;
   cudaError_t e = cudaFuncSetAttribute(seq_attention_bwd_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;

@@ -232,3 +232,15 @@ def test_scales_outside_float32_reach(lib, call):
         assert call(lib, scale=scale) == UNSUPPORTED and "2^-100" in L.last_error()
     for scale in (2.0 ** -100, 2.0 ** 100):
         assert call(lib, scale=scale, q=None) == INVALID and "q is NULL" in L.last_error()
+
+
+def test_varlen_bwd_refuses_too_many_items_before_it_starts(lib):
+    """Tiles of 128 rows of queries or of keys by key heads, counted in 31 bits with room for one more of each sequence."""
+    for tq, tk in ((1 << 24, 128), (128, 1 << 24)):
+        kw = dict(batch=1 << 20, tq=tq, tk=tk, hq=960, hk=960, d=8)
+        views = dict(dout=heads(A, 8 * kw["hq"], 8), q=heads(B_, 8 * kw["hq"], 8), k=heads(C_, 8 * kw["hk"], 8), v=heads(D_, 8 * kw["hk"], 8),
+                     out=heads(E_, 8 * kw["hq"], 8), dq=heads(H_, 8 * kw["hq"], 8), dk=heads(I_, 8 * kw["hk"], 8), dv=heads(J_, 8 * kw["hk"], 8))
+        # lse NULL is refused behind the shapes: this call never starts
+        few = dict(kw, batch=1 << 10)
+        assert _bwd(lib, ws_bytes=1 << 40, lse=None, **few, **views) == INVALID
+        assert _bwd(lib, ws_bytes=1 << 40, lse=None, **kw, **views) == UNSUPPORTED and "too many tiles" in L.last_error()

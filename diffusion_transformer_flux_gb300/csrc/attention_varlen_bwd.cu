@@ -6,8 +6,8 @@
 // recompute z and dout . v: seven products where one pass would need five, but that one has to add its dq into
 // memory from every key tile, in an order that changes the bits, through float32 traffic of several times the tensors' size.
 // Here every sum stays in tensor memory and is written once, in bf16.  The pass over queries starts on the SMs that the one over
-// keys leaves.  2 x 4608 tokens of 32 + 8 heads of 128: 948 us (918 TFLOP/s of the five products), of 24 heads of 64: 508 us
-// (642); 9 documents of up to 2041 tokens of 32 + 8 heads of 128: 254 us (680).
+// keys leaves.  2 x 4608 tokens of 32 + 8 heads of 128: 943 us (923 TFLOP/s of the five products), of 24 heads of 64: 510 us
+// (640); 9 documents of up to 2041 tokens of 32 + 8 heads of 128: 255 us (677).
 //
 // Both passes are one kernel, whose work items have a resident tile pair F (of 128 rows) and moving tile pairs M:
 //   keys:    F = K, V;     M = Q, dO;   S = K Q^T, dP = V dO^T;   dV += P dO,  dK += dS Q     (rows of S are keys)

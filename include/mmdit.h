@@ -846,7 +846,8 @@ mmdit_status mmdit_rope_bwd(int32_t act, const mmdit_rope_cfg *cfg, int32_t batc
  * makes that column NaN.
  *
  * bf16 tensors, products on the tensor cores with float32 sums; the weights exp(z - max) enter the second product rounded to
- * bf16.  A view is element (token, head, i) at ptr + token stride_t + head stride_h + i (elements; multiples of 8, at most
+ * bf16.  A sum over a row's keys in one go is cut, not rounded, as it grows: of weights and values of like size it is 0.5% low
+ * at 2^20 keys, within the rounding of the result up to 2^18.  Scores beyond 2^30 in magnitude may give NaN.  A view is element (token, head, i) at ptr + token stride_t + head stride_h + i (elements; multiples of 8, at most
  * 2^36, not below head_dim where the extent is above one; ptr 16-byte aligned); a view that is written must not overlap
  * itself or another view of the call.  The views are host memory.  head_dim a multiple of 8, at most 128; heads_q a
  * multiple of heads_k, at most 128 times it and at most 65535; scale from 2^-100 to 2^100; tokens at most 2^30, batch at

@@ -3020,7 +3020,9 @@ PagedPlan plan_paged(int64_t tokens_q, int64_t batch, int heads_q, int heads_k, 
     const int64_t keys = round_up(split_length(items, sms, max_kv, 78. * 8 / 6.7e6 * rows * d, &parts), 128);
     p.splits = static_cast<int>((max_kv + keys - 1) / keys);
     p.split_keys = p.splits > 1 ? static_cast<int>(keys) : 0;
-    const int64_t least_rows = max_kv < 512 ? 0 : std::min(tokens_q * group * (sms + heads_k), kLeastRows);
+    // never more than a full round of a smaller call's items takes, nor than its keys give (parts of 512 and a shorter one)
+    const int64_t least_rows =
+        max_kv < 512 ? 0 : std::min({tokens_q * group * (sms + heads_k), rows * (max_kv / 512 + 1), kLeastRows});
     p.total = std::max(p.total + round_up(static_cast<size_t>(least_rows * row_bytes) + 512, 256),
                        p.least + round_up(static_cast<size_t>(parts > 1 ? parts * rows * row_bytes : 0) + 512, 256));
     if (p.splits > 1) {
